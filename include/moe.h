@@ -56,7 +56,8 @@ typedef enum {
     MOE_ERR_DEVICE_CHECK = 7   /* a kernel recorded an error in the workspace (see below) */
 } moe_status;
 
-typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_RELU2 = 1 } moe_act;
+/* NONE: moe_mxfp4_matmul only (a layer has an activation). */
+typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_RELU2 = 1, MOE_ACT_NONE = 2 } moe_act;
 /* Expert weight formats.  INT8PC: per-channel int8 (the Inferentia page, "Squeezing a 26B MoE
  * onto the cheapest Inferentia instance", section "Wall 1: the memory math": experts in int8
  * with one scale per output channel): per row s = amax/127 (fp32), q = round-half-away(x / s). */
@@ -172,6 +173,107 @@ moe_status moe_quantize_int8pc(const float* src, int64_t n_mat, int64_t rows, in
  */
 moe_status moe_quantize_act_q8_0(const void* x, moe_dtype xt, int64_t rows, int64_t cols, float* out,
                                  moe_stream_t stream);
+
+/*
+ * MXFP4 matrices (OCP microscaling: E2M1 codes, one E8M0 scale per 32 consecutive values of a row),
+ * for weights and expert inputs alike.  [rows, cols], cols a multiple of 32, any number of rows:
+ *   all codes row-major, two per byte (even column in the low nibble), rows*cols/2 bytes;
+ *   then panel q = columns 128q .. 128q+127, ceil(cols/128) of them: the 4 scale bytes (blocks 4q ..
+ *   4q+3) of every row; the blocks of the last panel past cols hold 127 (2^0);
+ *   then zero to 15 bytes up to a multiple of 16 (not read, not written).
+ * A stack of matrices is the matrices back to back, moe_mxfp4_bytes(rows, cols) apart.
+ * moe_mxfp4_bytes returns 0 for sizes that are not positive, not a multiple or too large.
+ */
+size_t moe_mxfp4_bytes(int64_t rows, int64_t cols);
+
+/*
+ * moe_quantize_mxfp4 -- the MXFP4 quantiser.  Per block of 32 along a row:
+ *   X = max(floor(log2 amax) - 2, -127), scale byte X + 127;  code = E2M1(x * 2^-X), nearest even,
+ *   saturating at 6; a zero magnitude is coded +0.  A block that holds a NaN or an infinity gets
+ *   scale byte 255 (NaN) and zero codes: all its 32 values stand for NaN.
+ * x         device, fp32 or bf16 (xt): [n_mat][rows][cols], or [x_rows][cols] when src_rows is given.
+ * src_rows  device int32 [rows], or NULL: row r of the result is row src_rows[r] of x (n_mat 1), so
+ *           that the tokens of every expert come out side by side.  An index outside [0, x_rows)
+ *           gives a row of zeros.  x_rows is not read without src_rows.
+ * dst       device, n_mat * moe_mxfp4_bytes(rows, cols) bytes.
+ * rows = 0 or n_mat = 0 returns MOE_OK, launches nothing and touches no buffer (they may be NULL).
+ * Errors: INVALID_ARG (NULL, bad dtype, src_rows with n_mat > 1), SHAPE (cols a positive multiple of
+ * 32 up to 65536, rows up to 2^25, n_mat up to 65535), ALIGNMENT, CUDA.
+ */
+moe_status moe_quantize_mxfp4(const void* x, moe_dtype xt, int64_t x_rows, const int32_t* src_rows, int64_t n_mat,
+                              int64_t rows, int64_t cols, void* dst, moe_stream_t stream);
+
+/*
+ * moe_dequantize_mxfp4 -- the values that the codes of n_mat MXFP4 matrices stand for, [n_mat][rows]
+ * [cols] in fp32 or bf16 (ot), exact in both.  Errors: as moe_quantize_mxfp4.
+ */
+moe_status moe_dequantize_mxfp4(const void* src, int64_t n_mat, int64_t rows, int64_t cols, void* out, moe_dtype ot,
+                                moe_stream_t stream);
+
+/*
+ * moe_mxfp4_matmul -- the expert-indexed product with both operands in MXFP4 (the `mul_mat_id` of
+ * "Running Gemma 4 26B at 5 tokens/s on a 13-year-old Xeon without a GPU", section "A three-step
+ * fix", on 4-bit rows and weights), the activation fused:
+ *   z[r][n] = sum_i xq[r][i] * wq[e(r)][n][i]: every block's 32 code products summed and scaled
+ *   by both scales, the blocks summed in fp32;
+ *   NONE: out = z;  SWIGLU: out[r][j] = silu(z[r][j]) * z[r][N/2 + j] (N/2 columns);
+ *   RELU2: out = max(z, 0)^2.
+ * xq       device, one MXFP4 matrix [P][K]: the rows sorted by expert.
+ * wq       device, E MXFP4 matrices [N][K] back to back (SWIGLU: rows 0..N/2-1 gate, the rest up).
+ * offsets  device int32 [E+1]: expert e owns rows offsets[e] .. offsets[e+1]-1 (the moe_trace field),
+ *          or NULL with E = 1: every row.  Values are clamped to [0, P], and a reversed range is
+ *          empty; with increasing offsets no row has two experts.  Rows outside [offsets[0],
+ *          offsets[E]) are left as they were.
+ * out      device, [P][N] or [P][N/2], fp32 or bf16 (ot; rounded once).
+ * workspace  device, moe_mxfp4_matmul_workspace_bytes() bytes, zero-filled before its first use: an
+ *          error word that moe_get_device_status() reads and clears (2: a wait ran past its
+ *          limit, out is not valid).  Calls that may overlap can share it.
+ * The same inputs give the same bits.  P = 0 returns MOE_OK, launches nothing and touches no buffer.
+ * Errors: INVALID_ARG (NULL, bad enum, offsets NULL with E > 1), SHAPE (K a positive multiple of 32 up
+ * to 65536; P up to 2^25; N from 1 to 131072, for SWIGLU a multiple of 64; E up to 1024), ALIGNMENT,
+ * WORKSPACE, CUDA.
+ */
+size_t moe_mxfp4_matmul_workspace_bytes(void);
+moe_status moe_mxfp4_matmul(const void* xq, int64_t P, const void* wq, int64_t E, int64_t N, int64_t K,
+                            const int32_t* offsets, moe_act act, void* out, moe_dtype ot, void* workspace,
+                            size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_balance_loss -- how evenly the router loads its experts, over n_seq sequences of seq_len tokens
+ * (token t = s * seq_len + i).  A token counts when mask[t] != 0 (every token when mask is NULL); for
+ * the n_s counted tokens of sequence s:
+ *   counts[s][e] = entries of their idx rows equal to e (entries outside [0, E), e.g. -1 for a dropped
+ *   slot, are not counted);  prob[s][e] = mean of softmax(logits[t])[e];  tokens[s] = n_s;
+ *   loss = mean over the sequences with n_s > 0 of  E * sum_e counts[s][e] / (k n_s) * prob[s][e].
+ * A sequence without a counted token has zero counts and prob; when there is no counted token at all
+ * the loss is 0.  A row of -inf logits has no probability (all p are 0).  Logits of tokens that do
+ * not count are not looked at.  The same inputs give the same bits.
+ * logits     device [T][E], fp32 or bf16 (lt).   idx  device int32 [T][k].   mask  device uint8 [T]
+ *            or NULL.
+ * loss       device fp32 [1];  counts  int32 [n_seq][E];  prob  fp32 [n_seq][E];  tokens  int32
+ *            [n_seq] (all written).
+ * workspace  device, moe_balance_workspace_bytes(n_seq, seq_len, E) bytes, 256-byte aligned; needs no
+ *            clearing.  Calls that may overlap need workspaces of their own.
+ * T = 0 returns MOE_OK, launches nothing and touches no buffer.
+ * Errors: INVALID_ARG (NULL, bad dtype, k outside 1 .. min(E, 32)), SHAPE (E from 1 to 1024, T up to
+ * 2^20), ALIGNMENT, WORKSPACE, CUDA.
+ */
+size_t moe_balance_workspace_bytes(int64_t n_seq, int64_t seq_len, int64_t E);
+moe_status moe_balance_loss(const void* logits, moe_dtype lt, const int32_t* idx, const uint8_t* mask, int64_t n_seq,
+                            int64_t seq_len, int64_t E, int k, float* loss, int32_t* counts, float* prob,
+                            int32_t* tokens, void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_balance_loss_backward -- the gradient of moe_balance_loss's loss (the counts have none):
+ *   grad[t][e] = g * E / (S' n_s) * p_e * (f_e - sum_j f_j p_j),  f = counts[s] / (k n_s),
+ * S' the number of sequences with n_s > 0; exactly 0 for tokens that do not count.
+ * counts, tokens  device, as moe_balance_loss wrote them.   grad_loss  device fp32 [1]: g.
+ * grad            device [T][E] in the logits' type (written, rounded once).
+ * Errors: as moe_balance_loss, without a workspace.
+ */
+moe_status moe_balance_loss_backward(const void* logits, moe_dtype lt, const int32_t* counts, const int32_t* tokens,
+                                     const uint8_t* mask, const float* grad_loss, int64_t n_seq, int64_t seq_len,
+                                     int64_t E, int k, void* grad, moe_stream_t stream);
 
 /*
  * moe_router_topk -- router projection, top-k and softmax over the selected logits

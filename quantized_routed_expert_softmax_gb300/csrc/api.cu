@@ -3,7 +3,7 @@
 #include <algorithm>
 #include <mutex>
 
-#include "common.cuh"
+#include "mxfp4.cuh"
 
 namespace moe {
 
@@ -38,7 +38,17 @@ size_t decode_smem_plan(int, int, int, int, int, int, int, int*, int*);
 size_t decode_ring_bytes();
 size_t decode_max_smem();
 cudaError_t launch_decode_layer(const DecodeArgs&, int, int, size_t, int, cudaStream_t);
-
+// (mxfp4.cu, balance.cu)
+cudaError_t launch_mxfp4_quantize(const void*, int, int64_t, const int32_t*, int, int64_t, int64_t, int64_t, void*, int,
+                                  cudaStream_t);
+cudaError_t launch_mxfp4_dequantize(const void*, int64_t, int64_t, int64_t, void*, int, int, cudaStream_t);
+cudaError_t launch_mxfp4_matmul(const void*, int64_t, const void*, int64_t, int64_t, int64_t, const int32_t*, int, void*,
+                                int, int32_t*, int, cudaStream_t);
+size_t balance_workspace_bytes(int64_t, int64_t, int64_t);
+cudaError_t launch_balance_loss(const void*, int, const int32_t*, const uint8_t*, int64_t, int64_t, int64_t, int, float*,
+                                int32_t*, float*, int32_t*, void*, cudaStream_t);
+cudaError_t launch_balance_backward(const void*, int, const int32_t*, const int32_t*, const uint8_t*, const float*,
+                                    int64_t, int64_t, int64_t, int, void*, int, cudaStream_t);
 
 namespace {
 
@@ -89,6 +99,21 @@ cudaError_t ensure_configured(int* num_sms) {
 }
 
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+constexpr size_t kMxWorkspaceBytes = 256;   // the MXFP4 product's error word
+
+bool dtype_ok(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16; }
+
+bool mx_shape_ok(int64_t rows, int64_t cols) {
+    return rows >= 0 && rows <= kMaxTokens * kMaxK && cols > 0 && cols % 32 == 0 && cols <= kMaxDim;
+}
+
+// n_seq sequences of seq_len tokens over E experts (each factor bounded before the product is taken).
+moe_status balance_shape(int64_t n_seq, int64_t seq_len, int64_t E) {
+    if (n_seq < 0 || seq_len < 0 || n_seq > kMaxTokens || seq_len > kMaxTokens || n_seq * seq_len > kMaxTokens)
+        return MOE_ERR_SHAPE;
+    return E < 1 || E > kMaxE ? MOE_ERR_SHAPE : MOE_OK;
+}
 
 struct Plan {
     int64_t T, P;
@@ -557,6 +582,97 @@ moe_status moe_quantize_act_q8_0(const void* x, moe_dtype xt, int64_t rows, int6
     if (ensure_configured(&num_sms) != cudaSuccess) return MOE_ERR_CUDA;
     return cuda_status(launch_act_q8_0(x, xt, rows, cols, out, nullptr, nullptr, num_sms,
                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_mxfp4_bytes(int64_t rows, int64_t cols) {
+    return mx_shape_ok(rows, cols) && rows > 0 ? static_cast<size_t>(mx_bytes(rows, cols)) : 0;
+}
+
+moe_status moe_quantize_mxfp4(const void* x, moe_dtype xt, int64_t x_rows, const int32_t* src_rows, int64_t n_mat,
+                              int64_t rows, int64_t cols, void* dst, moe_stream_t stream) {
+    if (n_mat < 0 || !dtype_ok(xt)) return MOE_ERR_INVALID_ARG;
+    if (src_rows && (n_mat > 1 || x_rows < 0)) return MOE_ERR_INVALID_ARG;
+    if (!mx_shape_ok(rows, cols) || n_mat > 65535) return MOE_ERR_SHAPE;
+    if (n_mat == 0 || rows == 0) return MOE_OK;
+    if (!x || !dst) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(dst) || (reinterpret_cast<uintptr_t>(src_rows) & 3u)) return MOE_ERR_ALIGNMENT;
+    int num_sms = 0;
+    if (ensure_configured(&num_sms) != cudaSuccess) return MOE_ERR_CUDA;
+    return cuda_status(launch_mxfp4_quantize(x, xt, x_rows, src_rows, 1, n_mat, rows, cols, dst, num_sms,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_dequantize_mxfp4(const void* src, int64_t n_mat, int64_t rows, int64_t cols, void* out, moe_dtype ot,
+                                moe_stream_t stream) {
+    if (n_mat < 0 || !dtype_ok(ot)) return MOE_ERR_INVALID_ARG;
+    if (!mx_shape_ok(rows, cols) || n_mat > 65535) return MOE_ERR_SHAPE;
+    if (n_mat == 0 || rows == 0) return MOE_OK;
+    if (!src || !out) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(src) || !aligned16(out)) return MOE_ERR_ALIGNMENT;
+    int num_sms = 0;
+    if (ensure_configured(&num_sms) != cudaSuccess) return MOE_ERR_CUDA;
+    return cuda_status(launch_mxfp4_dequantize(src, n_mat, rows, cols, out, ot, num_sms,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_mxfp4_matmul_workspace_bytes(void) { return kMxWorkspaceBytes; }
+
+moe_status moe_mxfp4_matmul(const void* xq, int64_t P, const void* wq, int64_t E, int64_t N, int64_t K,
+                            const int32_t* offsets, moe_act act, void* out, moe_dtype ot, void* workspace,
+                            size_t ws_bytes, moe_stream_t stream) {
+    if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU && act != MOE_ACT_RELU2) return MOE_ERR_INVALID_ARG;
+    if (!dtype_ok(ot) || E < 1) return MOE_ERR_INVALID_ARG;
+    if (!mx_shape_ok(P, K) || E > kMaxE || N < 1 || N > 2 * kMaxDim) return MOE_ERR_SHAPE;
+    if (act == MOE_ACT_SWIGLU && N % 64 != 0) return MOE_ERR_SHAPE;
+    if (P == 0) return MOE_OK;
+    if (!xq || !wq || !out || (!offsets && E != 1)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(xq) || !aligned16(wq) || !aligned16(out) || (reinterpret_cast<uintptr_t>(offsets) & 3u))
+        return MOE_ERR_ALIGNMENT;
+    if (!workspace || ws_bytes < kMxWorkspaceBytes) return MOE_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MOE_ERR_ALIGNMENT;
+    int num_sms = 0;
+    if (ensure_configured(&num_sms) != cudaSuccess) return MOE_ERR_CUDA;
+    return cuda_status(launch_mxfp4_matmul(xq, P, wq, E, N, K, offsets, act, out, ot, static_cast<int32_t*>(workspace),
+                                           num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_balance_workspace_bytes(int64_t n_seq, int64_t seq_len, int64_t E) {
+    if (balance_shape(n_seq, seq_len, E) != MOE_OK || n_seq * seq_len == 0) return 0;
+    return balance_workspace_bytes(n_seq, seq_len, E);
+}
+
+moe_status moe_balance_loss(const void* logits, moe_dtype lt, const int32_t* idx, const uint8_t* mask, int64_t n_seq,
+                            int64_t seq_len, int64_t E, int k, float* loss, int32_t* counts, float* prob,
+                            int32_t* tokens, void* workspace, size_t ws_bytes, moe_stream_t stream) {
+    if (!dtype_ok(lt) || k < 1 || k > kMaxK || k > E) return MOE_ERR_INVALID_ARG;
+    const moe_status st = balance_shape(n_seq, seq_len, E);
+    if (st != MOE_OK) return st;
+    if (n_seq * seq_len == 0) return MOE_OK;
+    if (!logits || !idx || !loss || !counts || !prob || !tokens) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(logits) || !aligned16(idx) || !aligned16(counts) || !aligned16(prob) || !aligned16(tokens) ||
+        (reinterpret_cast<uintptr_t>(loss) & 3u))
+        return MOE_ERR_ALIGNMENT;
+    if (!workspace || ws_bytes < balance_workspace_bytes(n_seq, seq_len, E)) return MOE_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MOE_ERR_ALIGNMENT;
+    return cuda_status(launch_balance_loss(logits, lt, idx, mask, n_seq, seq_len, E, k, loss, counts, prob, tokens,
+                                           workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_balance_loss_backward(const void* logits, moe_dtype lt, const int32_t* counts, const int32_t* tokens,
+                                     const uint8_t* mask, const float* grad_loss, int64_t n_seq, int64_t seq_len,
+                                     int64_t E, int k, void* grad, moe_stream_t stream) {
+    if (!dtype_ok(lt) || k < 1 || k > kMaxK || k > E) return MOE_ERR_INVALID_ARG;
+    const moe_status st = balance_shape(n_seq, seq_len, E);
+    if (st != MOE_OK) return st;
+    if (n_seq * seq_len == 0) return MOE_OK;
+    if (!logits || !counts || !tokens || !grad_loss || !grad) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(logits) || !aligned16(counts) || !aligned16(tokens) || !aligned16(grad) ||
+        (reinterpret_cast<uintptr_t>(grad_loss) & 3u))
+        return MOE_ERR_ALIGNMENT;
+    int num_sms = 0;
+    if (ensure_configured(&num_sms) != cudaSuccess) return MOE_ERR_CUDA;
+    return cuda_status(launch_balance_backward(logits, lt, counts, tokens, mask, grad_loss, n_seq, seq_len, E, k, grad,
+                                               num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_router_workspace_bytes(int64_t T, int64_t E) {

@@ -17,6 +17,7 @@ MOE_OK = 0
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_SHAPE", 3: "MOE_ERR_ALIGNMENT",
                 4: "MOE_ERR_WORKSPACE", 5: "MOE_ERR_UNSUPPORTED", 6: "MOE_ERR_CUDA", 7: "MOE_ERR_DEVICE_CHECK"}
 ACT = {"swiglu": 0, "relu2": 1}
+MATMUL_ACT = {**ACT, "none": 2}
 WFMT = {"q8_0": 0, "nvfp4": 1, "int8pc": 2}
 DTYPE_F32, DTYPE_BF16 = 0, 1
 LAYOUT = {"canonical": 0, "device": 1, "neuron": 2}
@@ -31,7 +32,9 @@ EXPORTS = ["moe_q8_0_bytes", "moe_nvfp4_bytes", "moe_int8pc_bytes", "moe_quantiz
            "moe_router_topk", "moe_layer_workspace_bytes", "moe_layer_forward", "moe_rmsnorm_bf16",
            "moe_get_device_status", "moe_status_string", "moe_abi_version", "moe_layer_forward_launches",
            "moe_layer_forward_noalloc", "moe_layer_forward_noalloc_status", "moe_stack_forward",
-           "moe_stack_forward_launches"]
+           "moe_stack_forward_launches",
+           "moe_mxfp4_bytes", "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_mxfp4_matmul_workspace_bytes",
+           "moe_mxfp4_matmul", "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward"]
 
 
 class MoeError(RuntimeError):
@@ -89,6 +92,14 @@ def lib() -> ctypes.CDLL:
             "moe_layer_forward_noalloc_status": (I32, [P, ctypes.POINTER(I32)]),
             "moe_stack_forward": (I32, [ctypes.POINTER(LayerDesc), I32, P, I32, ctypes.c_float, P, P, P, P, P, SZ, P]),
             "moe_stack_forward_launches": (I32, [ctypes.POINTER(LayerDesc), I32, I32]),
+            "moe_mxfp4_bytes": (SZ, [I64, I64]),
+            "moe_quantize_mxfp4": (I32, [P, I32, I64, P, I64, I64, I64, P, P]),
+            "moe_dequantize_mxfp4": (I32, [P, I64, I64, I64, P, I32, P]),
+            "moe_mxfp4_matmul_workspace_bytes": (SZ, []),
+            "moe_mxfp4_matmul": (I32, [P, I64, P, I64, I64, I64, P, I32, P, I32, P, SZ, P]),
+            "moe_balance_workspace_bytes": (SZ, [I64, I64, I64]),
+            "moe_balance_loss": (I32, [P, I32, P, P, I64, I64, I64, I32, P, P, P, P, P, SZ, P]),
+            "moe_balance_loss_backward": (I32, [P, I32, P, P, P, P, I64, I64, I64, I32, P, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -172,6 +183,137 @@ def quantize_act_q8_0(x, out=None, stream=None):
         out = torch.empty(x.shape, dtype=torch.float32, device=x.device)
     _check("moe_quantize_act_q8_0", lib().moe_quantize_act_q8_0(_ptr(x), _x_dtype(x), x.shape[0], x.shape[1],
                                                                  _ptr(out), _stream(stream)))
+    return out
+
+
+def mxfp4_bytes(rows: int, cols: int) -> int:
+    return int(lib().moe_mxfp4_bytes(rows, cols))
+
+
+def _operand(name: str, t, dtype, numel: int | None = None) -> int | None:
+    """The pointer of an operand, checked: contiguous device memory of the type and size that the
+    entry point reads or writes (the C side sees only a pointer)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on the GPU")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must hold {numel} values, not {t.numel()}")
+    return t.data_ptr()
+
+
+def quantize_mxfp4(x, rows=None, out=None, stream=None):
+    """moe_quantize_mxfp4: x [..., rows, cols] fp32 or bf16 -> uint8 [n_mat, bytes].
+
+    rows: int32 [n] row indices; the result is then one matrix of x's rows in that order (an index
+    outside x gives a row of zeros)."""
+    import torch
+    xt = _x_dtype(x)
+    x_rows, cols = x.shape[-2], x.shape[-1]
+    n_rows = x_rows if rows is None else rows.numel()
+    n = x.numel() // max(1, x_rows * cols)
+    if rows is not None and x.dim() != 2:
+        raise ValueError("rows needs one matrix x [rows, cols]")
+    if rows is not None:
+        n = 1
+    per = mxfp4_bytes(max(1, n_rows), cols)
+    if out is None:
+        out = torch.empty((n, per if n_rows else 0), dtype=torch.uint8, device=x.device)
+    _check("moe_quantize_mxfp4", lib().moe_quantize_mxfp4(
+        _operand("x", x, x.dtype), xt, x_rows, _operand("rows", rows, torch.int32), n, n_rows, cols,
+        _operand("out", out, torch.uint8, n * per if n_rows else 0), _stream(stream)))
+    return out
+
+
+def dequantize_mxfp4(q, rows: int, cols: int, dtype=None, out=None, stream=None):
+    """moe_dequantize_mxfp4: uint8 [bytes] -> [rows, cols], or uint8 [n_mat, bytes] -> [n_mat, rows, cols];
+    dtype float32 (the default) or bfloat16."""
+    import torch
+    n = q.shape[0] if q.dim() == 2 else 1
+    shape = (n, rows, cols) if q.dim() == 2 else (rows, cols)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype or torch.float32, device=q.device)
+    _check("moe_dequantize_mxfp4", lib().moe_dequantize_mxfp4(
+        _operand("q", q, torch.uint8, n * mxfp4_bytes(rows, cols)), n, rows, cols,
+        _operand("out", out, out.dtype, n * rows * cols), _x_dtype(out), _stream(stream)))
+    return out
+
+
+def mxfp4_workspace(device="cuda"):
+    """A zero-filled workspace of moe_mxfp4_matmul (device_status reads its error word)."""
+    import torch
+    return torch.zeros(int(lib().moe_mxfp4_matmul_workspace_bytes()), dtype=torch.uint8, device=device)
+
+
+def mxfp4_matmul(xq, wq, offsets, rows: int, n: int, cols: int, act: str = "none", dtype=None, out=None,
+                 workspace=None, stream=None):
+    """moe_mxfp4_matmul: xq one MXFP4 matrix [rows, cols] sorted by expert, wq uint8 [E, bytes] of MXFP4
+    matrices [n, cols], offsets int32 [E + 1] (None with one matrix) -> [rows, n], or [rows, n / 2] for
+    act "swiglu"; dtype float32 (the default) or bfloat16.  Without a workspace the call makes one."""
+    import torch
+    E = wq.shape[0] if wq.dim() == 2 else 1
+    width = n // 2 if act == "swiglu" else n
+    if out is None:
+        out = torch.empty((rows, width), dtype=dtype or torch.float32, device=xq.device)
+    if workspace is None:
+        workspace = mxfp4_workspace(xq.device)
+    _check("moe_mxfp4_matmul", lib().moe_mxfp4_matmul(
+        _operand("xq", xq, torch.uint8, mxfp4_bytes(rows, cols)), rows,
+        _operand("wq", wq, torch.uint8, E * mxfp4_bytes(n, cols)), E, n, cols,
+        _operand("offsets", offsets, torch.int32, E + 1), MATMUL_ACT[act],
+        _operand("out", out, out.dtype, rows * width), _x_dtype(out),
+        _operand("workspace", workspace, torch.uint8), workspace.numel(), _stream(stream)))
+    return out
+
+
+def _mask_operand(mask, T: int):
+    import torch
+    if mask is None:
+        return None
+    return _operand("mask", mask, torch.bool if mask.dtype is torch.bool else torch.uint8, T)
+
+
+def balance_loss(logits, idx, mask=None, n_seq: int = 1, workspace=None, stream=None):
+    """moe_balance_loss: logits [T, E] fp32 or bf16, idx int32 [T, k], mask bool or uint8 [T], T = n_seq
+    sequences of one (padded) length -> (loss fp32 [1], counts int32 [n_seq, E], prob fp32 [n_seq, E],
+    tokens int32 [n_seq])."""
+    import torch
+    (T, E), k = logits.shape, idx.shape[-1]
+    if n_seq < 1 or T % n_seq:
+        raise ValueError(f"{T} tokens are not {n_seq} sequences of one length")
+    dev = logits.device
+    # zeros where the library launches nothing
+    new = torch.empty if T else torch.zeros
+    loss = new(1, dtype=torch.float32, device=dev)
+    counts = new((n_seq, E), dtype=torch.int32, device=dev)
+    prob = new((n_seq, E), dtype=torch.float32, device=dev)
+    tokens = new(n_seq, dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(int(lib().moe_balance_workspace_bytes(n_seq, T // n_seq, E)), dtype=torch.uint8,
+                                device=dev)
+    _check("moe_balance_loss", lib().moe_balance_loss(
+        _operand("logits", logits, logits.dtype), _x_dtype(logits), _operand("idx", idx, torch.int32, T * k),
+        _mask_operand(mask, T), n_seq, T // n_seq, E, k, _ptr(loss), _ptr(counts), _ptr(prob), _ptr(tokens),
+        _operand("workspace", workspace, torch.uint8), workspace.numel(), _stream(stream)))
+    return loss, counts, prob, tokens
+
+
+def balance_loss_backward(logits, counts, tokens, grad_loss, k: int, mask=None, out=None, stream=None):
+    """moe_balance_loss_backward: the logits' gradient [T, E] from balance_loss's counts and tokens and
+    the loss's gradient (fp32 [1])."""
+    import torch
+    T, E = logits.shape
+    n_seq = tokens.numel()
+    if n_seq < 1 or T % n_seq:
+        raise ValueError(f"{T} tokens are not {n_seq} sequences of one length")
+    if out is None:
+        out = torch.empty_like(logits)
+    _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
+        _operand("logits", logits, logits.dtype), _x_dtype(logits), _operand("counts", counts, torch.int32, n_seq * E),
+        _operand("tokens", tokens, torch.int32), _mask_operand(mask, T), _operand("grad_loss", grad_loss, torch.float32, 1),
+        n_seq, T // n_seq, E, k, _operand("out", out, logits.dtype, T * E), _stream(stream)))
     return out
 
 
