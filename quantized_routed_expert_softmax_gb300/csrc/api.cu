@@ -30,6 +30,7 @@ cudaError_t launch_combine(const float*, const int32_t*, const float*, int64_t, 
 cudaError_t launch_rmsnorm_bf16(const float*, int64_t, int64_t, float, uint16_t*, cudaStream_t);
 cudaError_t configure_gemm_kernels();
 cudaError_t configure_route_kernels();
+cudaError_t configure_mxfp4_kernels();
 cudaError_t launch_expert_gemm(const ExpertArgs&, int, int, int, int, int, int, cudaStream_t);
 cudaError_t launch_gather_x_f16(const ExpertArgs&, int, cudaStream_t);
 cudaError_t configure_decode_kernel(int, int);
@@ -38,7 +39,7 @@ size_t decode_smem_plan(int, int, int, int, int, int, int, int*, int*);
 size_t decode_ring_bytes();
 size_t decode_max_smem();
 cudaError_t launch_decode_layer(const DecodeArgs&, int, int, size_t, int, cudaStream_t);
-// (mxfp4.cu, balance.cu)
+// (mxfp4.cu, mxfp4_gemm.cu, balance.cu)
 cudaError_t launch_mxfp4_quantize(const void*, int, int64_t, const int32_t*, int, int64_t, int64_t, int64_t, void*, int,
                                   cudaStream_t);
 cudaError_t launch_mxfp4_dequantize(const void*, int64_t, int64_t, int64_t, void*, int, int, cudaStream_t);
@@ -89,6 +90,7 @@ cudaError_t ensure_configured(int* num_sms) {
         e = configure_gemv_kernels();
         if (e == cudaSuccess) e = configure_gemm_kernels();
         if (e == cudaSuccess) e = configure_route_kernels();
+        if (e == cudaSuccess) e = configure_mxfp4_kernels();
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&g_num_sms[dev], cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess) e = configure_decode_kernel(dev, g_num_sms[dev]);
         if (e != cudaSuccess) return e;

@@ -127,50 +127,6 @@ __global__ void __launch_bounds__(256) mxfp4_dequantize_kernel(const uint8_t* __
     }
 }
 
-// The expert product, one thread per output value, in order of the columns.
-__global__ void __launch_bounds__(256) mxfp4_matmul_kernel(const uint8_t* __restrict__ xq, int P,
-                                                            const uint8_t* __restrict__ wq, int E, int64_t N, int64_t K,
-                                                            const int32_t* __restrict__ offsets, int act,
-                                                            void* __restrict__ out, int ot) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t nout = act == MOE_ACT_SWIGLU ? N / 2 : N;
-    const int64_t r = blockIdx.y + static_cast<int64_t>(blockIdx.z) * 65535;
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (r >= P || n >= nout) return;
-    int e = -1;
-    for (int i = 0; i < E; ++i) {
-        int a, b;
-        mx_expert_rows(offsets, i, P, &a, &b);
-        if (r >= a && r < b) {
-            e = i;
-            break;
-        }
-    }
-    if (e < 0) return;
-    const uint8_t* w = wq + e * mx_bytes(N, K);
-    auto dot = [&](int64_t row) {
-        float acc = 0.0f;
-        for (int64_t b = 0; b < K / 32; ++b) {
-            const float sx = mx_scale(xq[mx_code_bytes(P, K) + 4 * ((b / 4) * P + r) + b % 4]);
-            const float sw = mx_scale(w[mx_code_bytes(N, K) + 4 * ((b / 4) * N + row) + b % 4]);
-            float s = 0.0f;
-            for (int i = 0; i < 16; ++i) {
-                const float2 u = e2m1x2_to_f32x2(xq[r * (K / 2) + b * 16 + i]);
-                const float2 v = e2m1x2_to_f32x2(w[row * (K / 2) + b * 16 + i]);
-                s += u.x * v.x + u.y * v.y;   // exact: multiples of 1/4 below 2^11
-            }
-            acc += s * sx * sw;
-        }
-        return acc;
-    };
-    float y = dot(n);
-    if (act == MOE_ACT_SWIGLU) y = silu(y) * dot(nout + n);
-    else if (act == MOE_ACT_RELU2) y = y > 0.0f ? y * y : (y <= 0.0f ? 0.0f : y);
-    if (ot == MOE_F32) static_cast<float*>(out)[r * nout + n] = y;
-    else static_cast<__nv_bfloat16*>(out)[r * nout + n] = __float2bfloat16_rn(y);
-}
-
 // ------------------------------------------------------------------------------- launchers
 namespace {
 unsigned grid_for(int64_t threads, int num_sms) {   // CTAs of 256, grid-stride beyond 8 per SM
@@ -190,19 +146,6 @@ cudaError_t launch_mxfp4_dequantize(const void* src, int64_t n_mat, int64_t rows
     const int64_t items = n_mat * rows * (cols / 8);
     return launch_pdl(mxfp4_dequantize_kernel, dim3(grid_for(items, num_sms)), dim3(256), 0, s,
                       static_cast<const uint8_t*>(src), items, rows, cols, out, ot);
-}
-
-cudaError_t launch_mxfp4_matmul(const void* xq, int64_t P, const void* wq, int64_t E, int64_t N, int64_t K,
-                                const int32_t* offsets, int act, void* out, int ot, int32_t* err, int num_sms,
-                                cudaStream_t s) {
-    (void)err;
-    (void)num_sms;
-    const int64_t nout = act == MOE_ACT_SWIGLU ? N / 2 : N;
-    const dim3 grid(static_cast<unsigned>((nout + 255) / 256), static_cast<unsigned>(std::min<int64_t>(P, 65535)),
-                    static_cast<unsigned>((P + 65534) / 65535));
-    return launch_pdl(mxfp4_matmul_kernel, grid, dim3(256), 0, s, static_cast<const uint8_t*>(xq),
-                      static_cast<int>(P), static_cast<const uint8_t*>(wq), static_cast<int>(E), N, K, offsets, act, out,
-                      ot);
 }
 
 }  // namespace moe

@@ -1,0 +1,531 @@
+// mxfp4_gemm.cu -- the expert-indexed product of MXFP4 rows with MXFP4 weights on the 5th-generation
+// tensor cores: block-scaled 4-bit MMAs (tcgen05 kind::mxf4), accumulators in tensor memory.
+//
+//   z[r][n] = sum over blocks b of 32:  2^(sx[r][b] + sw[n][b]) * sum_{i in b} x[r][i] w[n][i]
+//
+// The MMA takes the codes as they lie in memory and both scales per block, so nothing is dequantised:
+// the kernel moves bytes and issues instructions.  Weight rows fill the MMA's M = 128 and an expert's
+// rows its N = 16 .. 128, so a decode batch pads its few rows to 16 and not to 128.
+//
+// A persistent grid (one CTA per SM) walks the (expert, row tile of x, tile of weight rows) items that
+// every CTA derives from the offsets.  Warps have fixed roles, linked by mbarriers:
+//   warp 0     TMA: per K step of 256, 128 weight rows and up to NT rows of x, 128 bytes each, into
+//              128-byte-swizzled tiles;
+//   warp 1     one thread copies the step's scales into tensor memory (tcgen05.cp) and issues its four
+//              K = 64 MMAs;
+//   warp 2, 3  the scales of the weight rows / of the rows of x: a panel's 4-byte words (128 columns)
+//              by asynchronous copies into the 512-byte form that tcgen05.cp reads (row r's word at
+//              (r % 32) * 16 + (r / 32) * 4).  Rows of x start anywhere, and SwiGLU interleaves gate and
+//              up rows, so no bulk copy makes that form;
+//   warps 4-7  epilogue: accumulators to registers, activation, stores.  Two accumulators alternate.
+// SwiGLU tiles hold 16 gate rows and the same neurons' 16 up rows in every 32 lanes, so one shuffle
+// pairs them.
+//
+// Rows past a matrix or past K arrive as zero codes; stale words in the scale tiles meet rows whose
+// results are not stored, and the last panel's blocks past K hold 2^0.
+#include <cuda.h>   // CUtensorMap and its enums; the encoder is looked up in the driver at run time
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "mxfp4.cuh"
+#include "tc.cuh"
+
+namespace moe {
+
+constexpr int kMxThreads = 256;
+constexpr int kMxTileM = 128;            // weight rows of an item (SwiGLU: 64 gate and 64 up rows)
+constexpr int kMxStepK = 256;            // one 128-byte swizzle row of 4-bit codes
+constexpr int kMxABytes = kMxTileM * 128;
+constexpr int kMxSfBytes = 512;          // a panel's scale words of 128 rows
+constexpr int kMxLag = 3;                // K steps between issuing and publishing the scale copies
+constexpr uint32_t kMxTmemCols = 512;
+constexpr uint32_t kMxSfCol = 256;       // scale columns behind the two accumulators
+constexpr int kMxMaxBoxes = 4;
+constexpr long long kMxMaxItems = 1ll << 30;
+
+// Shared memory: the ring, and its depth, by the width of the row tile.
+template <int NT>
+struct MxCfg {
+    static constexpr int kBBytes = NT * 128;
+    static constexpr int kStage = kMxABytes + kBBytes + 4 * kMxSfBytes;
+    static constexpr int kStages = NT >= 128 ? 6 : (NT >= 64 ? 7 : 9);
+    static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage;
+    static_assert(kSmem <= 220 * 1024, "ring fits beside the item table");
+    static_assert(kMxLag < kStages - 1, "a scale copy is published before its stage is needed again");
+};
+
+struct MxArgs {
+    CUtensorMap tw;                  // weights: {bytes, rows, matrix}, SwiGLU {bytes, 16, half, block, matrix}
+    CUtensorMap tx[kMxMaxBoxes];     // rows of x: {bytes, rows}, boxes of boxh[i] rows
+    int boxh[kMxMaxBoxes];
+    int nbox;
+    const uint8_t* xs;               // scale panels of x
+    const uint8_t* ws;               // scale panels of the first weight matrix
+    int64_t w_mat;                   // bytes between weight matrices
+    const int32_t* offsets;
+    int E, P, N, K;
+    int act, ot;
+    void* out;
+    int32_t* err;
+};
+
+struct MxItem {
+    int e, r_first, nt, mtile;
+};
+
+// The items in order: experts, then row tiles, then weight tiles.  Every role walks them in increasing
+// order, so the expert is found by stepping on from the last one.
+template <int NT>
+struct MxWalk {
+    const int* prefix;
+    const int* first;
+    int E, mtiles;
+    int e = 0;
+    __device__ MxItem at(int item) {
+        while (prefix[e + 1] <= item) ++e;
+        const int local = item - prefix[e];
+        const int ntile = local / mtiles;
+        MxItem it;
+        it.e = e;
+        it.mtile = local - ntile * mtiles;
+        it.r_first = first[e] + ntile * NT;
+        // (the rows of the expert end where its tiles do: first[E + e] is its last row + 1)
+        it.nt = min(NT, first[E + e] - it.r_first);
+        return it;
+    }
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_constant__ MxArgs g) {
+    using Cfg = MxCfg<NT>;
+    extern __shared__ __align__(16) unsigned char dsm_raw[];
+    unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) &
+                                                           ~static_cast<uintptr_t>(1023));
+    __shared__ uint64_t full[Cfg::kStages], sf_full[Cfg::kStages], empty[Cfg::kStages];
+    __shared__ uint64_t acc_full[2], acc_empty[2];
+    __shared__ uint32_t issued[Cfg::kStages], commits[Cfg::kStages];
+    __shared__ uint32_t tmem_base;
+    __shared__ int prefix[kMaxE + 1], rows_of[2 * kMaxE];
+    __shared__ long long warp_tot[kMxThreads / 32];
+    __shared__ volatile int s_fail;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::s_addr(&tmem_base)),
+                     "r"(kMxTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid == 0) {
+        for (int s = 0; s < Cfg::kStages; ++s) {
+            tc::mbar_init(&full[s], 1);
+            tc::mbar_init(&sf_full[s], 2);
+            tc::mbar_init(&empty[s], 1);
+            issued[s] = commits[s] = 0;
+        }
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(&acc_full[s], 1);
+            tc::mbar_init(&acc_empty[s], 4);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        s_fail = 0;
+    }
+    pdl_wait();
+    pdl_trigger();
+    const bool swiglu = g.act == MOE_ACT_SWIGLU;
+    const int mtiles = (g.N + kMxTileM - 1) / kMxTileM;
+    {   // the item table: exclusive prefix over the experts of (row tiles) x (weight tiles).  Offsets
+        // that overlap could count past 32 bits: the table is cut at kMxMaxItems, which increasing
+        // offsets stay far below
+        constexpr int kPer = kMaxE / kMxThreads;
+        int cnt[kPer];
+        long long local = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = tid * kPer + i;
+            cnt[i] = 0;
+            if (e < g.E) {
+                int a, b;
+                mx_expert_rows(g.offsets, e, g.P, &a, &b);
+                rows_of[e] = a;
+                rows_of[g.E + e] = b;
+                cnt[i] = ((b - a + NT - 1) / NT) * mtiles;
+            }
+            local += cnt[i];
+        }
+        long long incl = local;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) warp_tot[warp] = incl;
+        __syncthreads();
+        long long run = incl - local;
+        for (int w = 0; w < warp; ++w) run += warp_tot[w];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = tid * kPer + i;
+            if (e <= g.E) prefix[e] = static_cast<int>(min(run, kMxMaxItems));
+            run += cnt[i];
+        }
+        if (g.E == kMaxE && tid == kMxThreads - 1) prefix[kMaxE] = static_cast<int>(min(run, kMxMaxItems));
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = tmem_base;
+    const int total = prefix[g.E];
+    const int ksteps = (g.K + kMxStepK - 1) / kMxStepK, npan = static_cast<int>(mx_panels(g.K));
+    MxWalk<NT> walk{prefix, rows_of, g.E, mtiles};
+
+    if (warp == 0) {
+        // -------------------------------------------------------------------- TMA producer
+        if (lane == 0) {
+            uint32_t gs = 0;
+            bool ok = true;
+            for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+                const MxItem it = walk.at(item);
+                int bi = 0;
+                while (bi + 1 < g.nbox && g.boxh[bi] < it.nt) ++bi;   // smallest box covering the rows
+                const uint32_t bytes = static_cast<uint32_t>(kMxABytes + g.boxh[bi] * 128);
+                for (int ks = 0; ks < ksteps; ++ks, ++gs) {
+                    const int st = gs % Cfg::kStages;
+                    const uint32_t use = gs / Cfg::kStages;
+                    if ((use > 0 && !tc::mbar_wait(&empty[st], use - 1)) || s_fail) {
+                        ok = false;
+                        break;
+                    }
+                    tc::mbar_arrive_expect_tx(&full[st], bytes);
+                    issued[st] = use + 1;
+                    const uint32_t dst = tc::s_addr(ring + st * Cfg::kStage);
+                    if (swiglu) tc::tma_5d(dst, &g.tw, ks * 128, 0, 0, it.mtile * 4, it.e, &full[st]);
+                    else tc::tma_3d(dst, &g.tw, ks * 128, it.mtile * kMxTileM, it.e, &full[st]);
+                    tc::tma_2d(dst + kMxABytes, &g.tx[bi], ks * 128, it.r_first, &full[st]);
+                }
+            }
+            if (!ok) {
+                s_fail = 1;
+                set_error(g.err, tc::kErrTimeout);
+            }
+        }
+    } else if (warp == 1) {
+        // -------------------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            uint32_t gs = 0, n_item = 0;
+            bool ok = true;
+            const uint32_t ring0 = tc::s_addr(ring);
+            for (int item = blockIdx.x; item < total && ok; item += gridDim.x, ++n_item) {
+                const MxItem it = walk.at(item);
+                const uint32_t idesc = tc::idesc_mxf4((it.nt + 15) & ~15);
+                const int buf = n_item & 1;
+                const uint32_t ub = n_item >> 1;
+                if ((ub > 0 && !tc::mbar_wait(&acc_empty[buf], ub - 1)) || s_fail) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                const uint32_t dt = tmem + static_cast<uint32_t>(buf * 128);
+                for (int ks = 0; ks < ksteps; ++ks, ++gs) {
+                    const int st = gs % Cfg::kStages;
+                    const uint32_t use = gs / Cfg::kStages;
+                    if (!tc::mbar_wait(&full[st], use) || !tc::mbar_wait(&sf_full[st], use) || s_fail) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    const uint32_t a = ring0 + st * Cfg::kStage, b = a + kMxABytes, sa = b + Cfg::kBBytes,
+                                   sb = sa + 2 * kMxSfBytes;
+                    // (alternate columns, so that a step's scales do not replace the ones in use)
+                    const uint32_t ta = tmem + kMxSfCol + (gs & 1u) * 16, tb = ta + 8;
+                    const uint64_t da = tc::sdesc_k128(a), db = tc::sdesc_k128(b);
+                    const int panels = min(2, npan - 2 * ks), slices = min(4, (g.K - ks * kMxStepK + 63) / 64);
+                    for (int p = 0; p < panels; ++p) {
+                        tc::cp_scales(ta + 4 * p, tc::sdesc_scales(sa + p * kMxSfBytes));
+                        tc::cp_scales(tb + 4 * p, tc::sdesc_scales(sb + p * kMxSfBytes));
+                    }
+                    for (int kk = 0; kk < slices; ++kk)   // 32 bytes of codes; blocks 2 (kk % 2), + 1 of panel kk / 2
+                        tc::umma_mxf4(dt, da + 2 * kk, db + 2 * kk, idesc | tc::idesc_sf((kk & 1) * 2),
+                                      ta + 4 * (kk >> 1), tb + 4 * (kk >> 1), ks > 0 || kk > 0);
+                    tc::commit(&empty[st]);
+                    commits[st] = use + 1;
+                }
+                if (ok) tc::commit(&acc_full[buf]);
+            }
+            if (!ok) {
+                s_fail = 1;
+                set_error(g.err, tc::kErrTimeout);
+            }
+        }
+    } else if (warp < 4) {
+        // -------------------------------------------------------------------- scale loaders
+        const bool weights = warp == 2;
+        const int f = g.N / 2;
+        uint32_t gs = 0;
+        bool ok = true;
+        auto publish = [&](uint32_t step) {   // this warp's words of `step` are in shared memory: the tensor core may read them
+            tc::proxy_fence_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sf_full[step % Cfg::kStages]);
+        };
+        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+            const MxItem it = walk.at(item);
+            const uint8_t* src[4];   // the words of tile rows lane, lane + 32, .. in panel 0
+            bool in[4];
+            int64_t pitch;           // bytes between panels
+            if (weights) {
+                const uint8_t* base = g.ws + it.e * g.w_mat;
+                pitch = 4ll * g.N;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    int n = it.mtile * kMxTileM + 32 * j + lane;
+                    in[j] = n < g.N;
+                    if (swiglu) {
+                        const int neuron = it.mtile * 64 + 16 * j + (lane & 15);
+                        in[j] = neuron < f;
+                        n = (lane >> 4) * f + neuron;
+                    }
+                    src[j] = base + 4ll * n;
+                }
+            } else {
+                pitch = 4ll * g.P;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    in[j] = 32 * j + lane < it.nt;
+                    src[j] = g.xs + 4ll * (it.r_first + 32 * j + lane);
+                }
+            }
+            for (int ks = 0; ks < ksteps; ++ks, ++gs) {
+                const int st = gs % Cfg::kStages;
+                const uint32_t use = gs / Cfg::kStages;
+                bool w_ok = use == 0 || tc::mbar_wait(&empty[st], use - 1);
+                w_ok = __all_sync(0xffffffffu, w_ok && !s_fail);
+                if (!w_ok) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = tc::s_addr(ring + st * Cfg::kStage) + kMxABytes + Cfg::kBBytes +
+                                     (weights ? 0 : 2 * kMxSfBytes) + 16 * lane;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    if (2 * ks + p < npan) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (in[j]) tc::cp_async4(dst + p * kMxSfBytes + 4 * j, src[j] + (2 * ks + p) * pitch);
+                    }
+                }
+                tc::cp_async_commit();
+                if (gs >= kMxLag) {
+                    tc::cp_async_wait<kMxLag>();
+                    publish(gs - kMxLag);
+                }
+            }
+        }
+        tc::cp_async_wait<0>();
+        if (ok)
+            for (uint32_t step = gs >= kMxLag ? gs - kMxLag : 0; step < gs; ++step) publish(step);
+        if (!ok && lane == 0) {
+            s_fail = 1;
+            set_error(g.err, tc::kErrTimeout);
+        }
+    } else {
+        // -------------------------------------------------------------------- epilogue
+        const int q = warp & 3;                       // lane quadrant of tensor memory
+        const int nout = swiglu ? g.N / 2 : g.N;
+        const bool pairs = g.ot == MOE_BF16 && nout % 2 == 0;
+        float* of = static_cast<float*>(g.out);
+        __nv_bfloat16* oh = static_cast<__nv_bfloat16*>(g.out);
+        uint32_t n_item = 0;
+        bool ok = true;
+        for (int item = blockIdx.x; item < total; item += gridDim.x, ++n_item) {
+            const MxItem it = walk.at(item);
+            const int buf = n_item & 1;
+            bool w_ok = tc::mbar_wait(&acc_full[buf], n_item >> 1);
+            w_ok = __all_sync(0xffffffffu, w_ok && !s_fail);
+            if (!w_ok) {
+                ok = false;
+                break;
+            }
+            tc::fence_after();
+            const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * 128);
+            for (int c0 = 0; c0 < it.nt; c0 += 16) {
+                float v[16];
+                tc::tmem_ld16(tb + c0, v);
+                if (swiglu) {
+                    // lanes 0-15 hold gate rows, 16-31 the same neurons' up rows: of every two rows of
+                    // x the low half takes the first and the high half the second
+                    const bool up = lane >= 16;
+                    const int col = it.mtile * 64 + 16 * q + (lane & 15);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float other = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 16);
+                        const float y = up ? silu(other) * v[j + 1] : silu(v[j]) * other;
+                        const int n = c0 + j + (up ? 1 : 0);
+                        if (n < it.nt && col < nout) {
+                            const int64_t o = static_cast<int64_t>(it.r_first + n) * nout + col;
+                            if (g.ot == MOE_F32) of[o] = y;
+                            else oh[o] = __float2bfloat16_rn(y);
+                        }
+                    }
+                    continue;
+                }
+                if (g.act == MOE_ACT_RELU2) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = v[j] > 0.0f ? v[j] * v[j] : (v[j] <= 0.0f ? 0.0f : v[j]);
+                }
+                const int col = it.mtile * kMxTileM + 32 * q + lane;
+                if (pairs) {   // two columns a store: of every two rows of x, even lanes store the first
+                    const bool odd = lane & 1;
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+                        const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(other, v[j + 1])
+                                                     : __floats2bfloat162_rn(v[j], other);
+                        const int n = c0 + j + (odd ? 1 : 0);
+                        if (n < it.nt && col < nout)
+                            *reinterpret_cast<__nv_bfloat162*>(oh + static_cast<int64_t>(it.r_first + n) * nout +
+                                                               (col & ~1)) = h;
+                    }
+                } else if (col < nout) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (c0 + j < it.nt) {
+                            const int64_t o = static_cast<int64_t>(it.r_first + c0 + j) * nout + col;
+                            if (g.ot == MOE_F32) of[o] = v[j];
+                            else oh[o] = __float2bfloat16_rn(v[j]);
+                        }
+                    }
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
+        }
+        if (!ok && lane == 0) {
+            s_fail = 1;
+            set_error(g.err, tc::kErrTimeout);
+        }
+    }
+
+    // every copy and MMA this CTA issued has landed before its memories are given back (immediate
+    // on the normal path; bounded after a timeout)
+    __syncthreads();
+    if (tid == 0) {
+        bool ok = true;
+        for (int s = 0; s < Cfg::kStages; ++s) {
+            if (issued[s]) ok &= tc::mbar_wait(&full[s], issued[s] - 1);
+            if (commits[s]) ok &= tc::mbar_wait(&empty[s], commits[s] - 1);
+        }
+        if (!ok) set_error(g.err, tc::kErrTimeout);
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kMxTmemCols));
+}
+
+// ------------------------------------------------------------------------------- host side
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 g_mx_encode = nullptr;
+
+cudaError_t mx_encoder() {
+    static std::once_flag once;
+    static cudaError_t status = cudaSuccess;
+    std::call_once(once, [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        status = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+        if (status == cudaSuccess && (q != cudaDriverEntryPointSuccess || fn == nullptr)) status = cudaErrorNotSupported;
+        if (status == cudaSuccess) g_mx_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    });
+    return status;
+}
+
+// Bytes in 128-byte-swizzled boxes; what lies outside the tensor reads as zero.
+cudaError_t mx_map(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+                   const cuuint32_t* box) {
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    const CUresult r = g_mx_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank),
+                                   const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int NT>
+cudaError_t mx_launch(MxArgs& g, const void* xq, int num_sms, cudaStream_t s) {
+    // boxes of x: the powers of two from 16 below the tile, so that a short group does not load a tile
+    const cuuint64_t xd[2] = {static_cast<cuuint64_t>(g.K / 2), static_cast<cuuint64_t>(g.P)};
+    const cuuint64_t xst[1] = {static_cast<cuuint64_t>(g.K / 2)};
+    g.nbox = 0;
+    for (int h = 16; h <= NT; h *= 2) {
+        const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(h)};
+        const cudaError_t e = mx_map(&g.tx[g.nbox], 2, xq, xd, xst, box);
+        if (e != cudaSuccess) return e;
+        g.boxh[g.nbox++] = h;
+    }
+    const int64_t mtiles = (g.N + kMxTileM - 1) / kMxTileM;
+    const int64_t bound = mtiles * (std::min(g.E, g.P) + g.P / NT);
+    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms, bound)));
+    return launch_pdl(mxfp4_gemm_kernel<NT>, dim3(grid), dim3(kMxThreads), MxCfg<NT>::kSmem, s, g);
+}
+
+}  // namespace
+
+cudaError_t configure_mxfp4_kernels() {
+    cudaError_t e = mx_encoder();
+    auto set = [&](const void* fn, size_t smem) {
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    };
+    set(reinterpret_cast<const void*>(mxfp4_gemm_kernel<16>), MxCfg<16>::kSmem);
+    set(reinterpret_cast<const void*>(mxfp4_gemm_kernel<32>), MxCfg<32>::kSmem);
+    set(reinterpret_cast<const void*>(mxfp4_gemm_kernel<64>), MxCfg<64>::kSmem);
+    set(reinterpret_cast<const void*>(mxfp4_gemm_kernel<128>), MxCfg<128>::kSmem);
+    return e;
+}
+
+cudaError_t launch_mxfp4_matmul(const void* xq, int64_t P, const void* wq, int64_t E, int64_t N, int64_t K,
+                                const int32_t* offsets, int act, void* out, int ot, int32_t* err, int num_sms,
+                                cudaStream_t s) {
+    MxArgs g;
+    std::memset(&g, 0, sizeof(g));
+    g.xs = static_cast<const uint8_t*>(xq) + mx_code_bytes(P, K);
+    g.ws = static_cast<const uint8_t*>(wq) + mx_code_bytes(N, K);
+    g.w_mat = mx_bytes(N, K);
+    g.offsets = offsets;
+    g.E = static_cast<int>(E);
+    g.P = static_cast<int>(P);
+    g.N = static_cast<int>(N);
+    g.K = static_cast<int>(K);
+    g.act = act;
+    g.ot = ot;
+    g.out = out;
+    g.err = err;
+    const cuuint64_t kb = static_cast<cuuint64_t>(K / 2), mat = static_cast<cuuint64_t>(g.w_mat);
+    cudaError_t e;
+    if (act == MOE_ACT_SWIGLU) {   // 16 gate rows, the same neurons' 16 up rows, four times
+        const cuuint64_t f = static_cast<cuuint64_t>(N / 2);
+        const cuuint64_t d[5] = {kb, 16, 2, f / 16, static_cast<cuuint64_t>(E)};
+        const cuuint64_t st[4] = {kb, f * kb, 16 * kb, mat};
+        const cuuint32_t box[5] = {128, 16, 2, 4, 1};
+        e = mx_map(&g.tw, 5, wq, d, st, box);
+    } else {
+        const cuuint64_t d[3] = {kb, static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(E)};
+        const cuuint64_t st[2] = {kb, mat};
+        const cuuint32_t box[3] = {128, kMxTileM, 1};
+        e = mx_map(&g.tw, 3, wq, d, st, box);
+    }
+    if (e != cudaSuccess) return e;
+    const int64_t avg = P / std::min(E, P);
+    if (avg <= 8) return mx_launch<16>(g, xq, num_sms, s);
+    if (avg <= 24) return mx_launch<32>(g, xq, num_sms, s);
+    if (avg <= 64) return mx_launch<64>(g, xq, num_sms, s);
+    return mx_launch<128>(g, xq, num_sms, s);
+}
+
+}  // namespace moe
