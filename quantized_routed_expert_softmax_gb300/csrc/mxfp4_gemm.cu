@@ -11,18 +11,21 @@
 // every CTA derives from the offsets.  Warps have fixed roles, linked by mbarriers:
 //   warp 0     TMA: per K step of 256, 128 weight rows and up to NT rows of x, 128 bytes each, into
 //              128-byte-swizzled tiles;
-//   warp 1     one thread copies the step's scales into tensor memory (tcgen05.cp) and issues its four
-//              K = 64 MMAs;
-//   warp 2, 3  the scales of the weight rows / of the rows of x: a panel's 4-byte words (128 columns)
-//              by asynchronous copies into the 512-byte form that tcgen05.cp reads (row r's word at
-//              (r % 32) * 16 + (r / 32) * 4).  Rows of x start anywhere, and SwiGLU interleaves gate and
-//              up rows, so no bulk copy makes that form;
-//   warps 4-7  epilogue: accumulators to registers, activation, stores.  Two accumulators alternate.
+//   warp 1     one thread issues the step's four K = 64 MMAs, operands in shared memory, scales in
+//              tensor memory;
+//   warps 4-7  epilogue: accumulators to registers, activation, stores.  Two accumulators alternate;
+//   warps 8-11 the scales: a panel's 4-byte words (128 columns) of the weight rows and of the rows of x,
+//              read kMxAhead steps ahead into registers and written straight into the form that the MMA
+//              takes them from tensor memory in: row r's word in lane r % 32 of every quadrant of 32
+//              lanes, column r / 32 (a warp writes the quadrant warp % 4).  Rows of x start anywhere and
+//              SwiGLU interleaves gate and up rows, so no bulk copy makes that form; asynchronous copies
+//              into shared memory for tcgen05.cp took 0.8 us a step, as the proxy fence that publishes
+//              one step's words also waits for the later steps' copies (512-expert up, 32 tokens: 179 us).
 // SwiGLU tiles hold 16 gate rows and the same neurons' 16 up rows in every 32 lanes, so one shuffle
 // pairs them.
 //
-// Rows past a matrix or past K arrive as zero codes; stale words in the scale tiles meet rows whose
-// results are not stored, and the last panel's blocks past K hold 2^0.
+// Codes past a matrix or past K arrive as zero; rows of the tile that are no rows of the item are computed
+// and not stored, and the last panel's blocks past K hold 2^0.
 #include <cuda.h>   // CUtensorMap and its enums; the encoder is looked up in the driver at run time
 #include <cudaTypedefs.h>
 
@@ -35,14 +38,14 @@
 
 namespace moe {
 
-constexpr int kMxThreads = 256;
+constexpr int kMxThreads = 384;
 constexpr int kMxTileM = 128;            // weight rows of an item (SwiGLU: 64 gate and 64 up rows)
 constexpr int kMxStepK = 256;            // one 128-byte swizzle row of 4-bit codes
 constexpr int kMxABytes = kMxTileM * 128;
-constexpr int kMxSfBytes = 512;          // a panel's scale words of 128 rows
-constexpr int kMxLag = 3;                // K steps between issuing and publishing the scale copies
+constexpr int kMxAhead = 4;               // K steps that the scale words are read ahead
 constexpr uint32_t kMxTmemCols = 512;
-constexpr uint32_t kMxSfCol = 256;       // scale columns behind the two accumulators
+constexpr uint32_t kMxSfCol = 256;       // scale columns behind the two accumulators, 16 a stage:
+                                         // weights panel 0, panel 1, rows of x panel 0, panel 1
 constexpr int kMxMaxBoxes = 4;
 constexpr long long kMxMaxItems = 1ll << 30;
 
@@ -50,17 +53,17 @@ constexpr long long kMxMaxItems = 1ll << 30;
 template <int NT>
 struct MxCfg {
     static constexpr int kBBytes = NT * 128;
-    static constexpr int kStage = kMxABytes + kBBytes + 4 * kMxSfBytes;
-    static constexpr int kStages = NT >= 128 ? 6 : (NT >= 64 ? 7 : 9);
+    static constexpr int kStage = kMxABytes + kBBytes;
+    static constexpr int kStages = NT >= 128 ? 6 : (NT >= 64 ? 8 : 10);
+    static constexpr int kXWords = (NT + 31) / 32;   // columns of a panel's scales of x
     static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage;
-    static_assert(kSmem <= 220 * 1024, "ring fits beside the item table");
-    static_assert(kMxLag < kStages - 1, "a scale copy is published before its stage is needed again");
+    static_assert(kSmem <= 214 * 1024, "ring fits beside the item table");
+    static_assert(kMxSfCol + 16 * kStages <= kMxTmemCols, "scale columns of every stage");
 };
 
 struct MxArgs {
     CUtensorMap tw;                  // weights: {bytes, rows, matrix}, SwiGLU {bytes, 16, half, block, matrix}
-    CUtensorMap tx[kMxMaxBoxes];     // rows of x: {bytes, rows}, boxes of boxh[i] rows
-    int boxh[kMxMaxBoxes];
+    CUtensorMap tx[kMxMaxBoxes];     // rows of x: {bytes, rows}, boxes of 16 << i rows
     int nbox;
     const uint8_t* xs;               // scale panels of x
     const uint8_t* ws;               // scale panels of the first weight matrix
@@ -111,7 +114,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     __shared__ int prefix[kMaxE + 1], rows_of[2 * kMaxE];
     __shared__ long long warp_tot[kMxThreads / 32];
     __shared__ volatile int s_fail;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the warp number through a shuffle, so that the compiler takes the roles' branches as uniform and
+    // keeps descriptors and coordinates in uniform registers, where the tensor core and the copy engine
+    // take them from (read out of divergent code, a step's four MMAs took 800 cycles to issue)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::s_addr(&tmem_base)),
@@ -121,7 +127,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     if (tid == 0) {
         for (int s = 0; s < Cfg::kStages; ++s) {
             tc::mbar_init(&full[s], 1);
-            tc::mbar_init(&sf_full[s], 2);
+            tc::mbar_init(&sf_full[s], 4);
             tc::mbar_init(&empty[s], 1);
             issued[s] = commits[s] = 0;
         }
@@ -139,7 +145,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     {   // the item table: exclusive prefix over the experts of (row tiles) x (weight tiles).  Offsets
         // that overlap could count past 32 bits: the table is cut at kMxMaxItems, which increasing
         // offsets stay far below
-        constexpr int kPer = kMaxE / kMxThreads;
+        constexpr int kPer = (kMaxE + kMxThreads) / kMxThreads;   // with a thread for the entry behind the last
         int cnt[kPer];
         long long local = 0;
 #pragma unroll
@@ -171,166 +177,169 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             if (e <= g.E) prefix[e] = static_cast<int>(min(run, kMxMaxItems));
             run += cnt[i];
         }
-        if (g.E == kMaxE && tid == kMxThreads - 1) prefix[kMaxE] = static_cast<int>(min(run, kMxMaxItems));
     }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = tmem_base;
     const int total = prefix[g.E];
-    const int ksteps = (g.K + kMxStepK - 1) / kMxStepK, npan = static_cast<int>(mx_panels(g.K));
+    const int ksteps = (g.K + kMxStepK - 1) / kMxStepK;
     MxWalk<NT> walk{prefix, rows_of, g.E, mtiles};
 
     if (warp == 0) {
         // -------------------------------------------------------------------- TMA producer
-        if (lane == 0) {
-            uint32_t gs = 0;
-            bool ok = true;
-            for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-                const MxItem it = walk.at(item);
-                int bi = 0;
-                while (bi + 1 < g.nbox && g.boxh[bi] < it.nt) ++bi;   // smallest box covering the rows
-                const uint32_t bytes = static_cast<uint32_t>(kMxABytes + g.boxh[bi] * 128);
-                for (int ks = 0; ks < ksteps; ++ks, ++gs) {
-                    const int st = gs % Cfg::kStages;
-                    const uint32_t use = gs / Cfg::kStages;
-                    if ((use > 0 && !tc::mbar_wait(&empty[st], use - 1)) || s_fail) {
-                        ok = false;
-                        break;
-                    }
+        const bool leader = tc::elect_one();
+        const uint32_t ring0 = tc::s_addr(ring);
+        uint32_t st = 0, use = 0;
+        bool ok = true;
+        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+            const MxItem it = walk.at(item);
+            int bi = 0;
+            while (bi + 1 < g.nbox && (16 << bi) < it.nt) ++bi;   // smallest box covering the rows
+            const uint32_t bytes = static_cast<uint32_t>(kMxABytes + (16 << bi) * 128);
+            for (int ks = 0; ks < ksteps; ++ks) {
+                const bool w_ok = use == 0 || tc::mbar_wait(&empty[st], use - 1);
+                if (!__all_sync(0xffffffffu, w_ok && !s_fail)) {
+                    ok = false;
+                    break;
+                }
+                if (leader) {
                     tc::mbar_arrive_expect_tx(&full[st], bytes);
                     issued[st] = use + 1;
-                    const uint32_t dst = tc::s_addr(ring + st * Cfg::kStage);
+                    const uint32_t dst = ring0 + st * Cfg::kStage;
                     if (swiglu) tc::tma_5d(dst, &g.tw, ks * 128, 0, 0, it.mtile * 4, it.e, &full[st]);
                     else tc::tma_3d(dst, &g.tw, ks * 128, it.mtile * kMxTileM, it.e, &full[st]);
                     tc::tma_2d(dst + kMxABytes, &g.tx[bi], ks * 128, it.r_first, &full[st]);
                 }
+                if (++st == Cfg::kStages) st = 0, ++use;
             }
-            if (!ok) {
-                s_fail = 1;
-                set_error(g.err, tc::kErrTimeout);
-            }
+        }
+        if (!ok && leader) {
+            s_fail = 1;
+            set_error(g.err, tc::kErrTimeout);
         }
     } else if (warp == 1) {
         // -------------------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            uint32_t gs = 0, n_item = 0;
-            bool ok = true;
-            const uint32_t ring0 = tc::s_addr(ring);
-            for (int item = blockIdx.x; item < total && ok; item += gridDim.x, ++n_item) {
-                const MxItem it = walk.at(item);
-                const uint32_t idesc = tc::idesc_mxf4((it.nt + 15) & ~15);
-                const int buf = n_item & 1;
-                const uint32_t ub = n_item >> 1;
-                if ((ub > 0 && !tc::mbar_wait(&acc_empty[buf], ub - 1)) || s_fail) {
+        const bool leader = tc::elect_one();
+        const uint64_t da0 = tc::sdesc_k128(tc::s_addr(ring)), db0 = tc::sdesc_k128(tc::s_addr(ring + kMxABytes));
+        uint32_t st = 0, use = 0, n_item = 0;
+        bool ok = true;
+        for (int item = blockIdx.x; item < total && ok; item += gridDim.x, ++n_item) {
+            const MxItem it = walk.at(item);
+            const uint32_t idesc = tc::idesc_mxf4((it.nt + 15) & ~15);
+            const uint32_t buf = n_item & 1, ub = n_item >> 1;
+            const bool a_ok = ub == 0 || tc::mbar_wait(&acc_empty[buf], ub - 1);
+            if (!__all_sync(0xffffffffu, a_ok && !s_fail)) {
+                ok = false;
+                break;
+            }
+            const uint32_t dt = tmem + buf * 128;
+            for (int ks = 0; ks < ksteps; ++ks) {
+                const bool w_ok = tc::mbar_wait(&full[st], use) && tc::mbar_wait(&sf_full[st], use);
+                if (!__all_sync(0xffffffffu, w_ok && !s_fail)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after();
-                const uint32_t dt = tmem + static_cast<uint32_t>(buf * 128);
-                for (int ks = 0; ks < ksteps; ++ks, ++gs) {
-                    const int st = gs % Cfg::kStages;
-                    const uint32_t use = gs / Cfg::kStages;
-                    if (!tc::mbar_wait(&full[st], use) || !tc::mbar_wait(&sf_full[st], use) || s_fail) {
-                        ok = false;
-                        break;
-                    }
-                    tc::fence_after();
-                    const uint32_t a = ring0 + st * Cfg::kStage, b = a + kMxABytes, sa = b + Cfg::kBBytes,
-                                   sb = sa + 2 * kMxSfBytes;
-                    // (alternate columns, so that a step's scales do not replace the ones in use)
-                    const uint32_t ta = tmem + kMxSfCol + (gs & 1u) * 16, tb = ta + 8;
-                    const uint64_t da = tc::sdesc_k128(a), db = tc::sdesc_k128(b);
-                    const int panels = min(2, npan - 2 * ks), slices = min(4, (g.K - ks * kMxStepK + 63) / 64);
-                    for (int p = 0; p < panels; ++p) {
-                        tc::cp_scales(ta + 4 * p, tc::sdesc_scales(sa + p * kMxSfBytes));
-                        tc::cp_scales(tb + 4 * p, tc::sdesc_scales(sb + p * kMxSfBytes));
-                    }
-                    for (int kk = 0; kk < slices; ++kk)   // 32 bytes of codes; blocks 2 (kk % 2), + 1 of panel kk / 2
-                        tc::umma_mxf4(dt, da + 2 * kk, db + 2 * kk, idesc | tc::idesc_sf((kk & 1) * 2),
-                                      ta + 4 * (kk >> 1), tb + 4 * (kk >> 1), ks > 0 || kk > 0);
+                if (leader) {
+                    // (the descriptors' start address, bytes / 16, is linear in the address)
+                    const uint64_t da = da0 + st * (Cfg::kStage >> 4), db = db0 + st * (Cfg::kStage >> 4);
+                    const uint32_t ta = tmem + kMxSfCol + st * 16, tb = ta + 8;
+                    const int slices = (g.K - ks * kMxStepK + 63) / 64;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)   // 32 bytes of codes; blocks 2 (kk % 2), + 1 of panel kk / 2
+                        if (kk < slices)
+                            tc::umma_mxf4(dt, da + 2 * kk, db + 2 * kk, idesc | tc::idesc_sf((kk & 1) * 2),
+                                          ta + 4 * (kk >> 1), tb + 4 * (kk >> 1), ks > 0 || kk > 0);
                     tc::commit(&empty[st]);
                     commits[st] = use + 1;
+                    if (ks + 1 == ksteps) tc::commit(&acc_full[buf]);
                 }
-                if (ok) tc::commit(&acc_full[buf]);
-            }
-            if (!ok) {
-                s_fail = 1;
-                set_error(g.err, tc::kErrTimeout);
+                if (++st == Cfg::kStages) st = 0, ++use;
             }
         }
-    } else if (warp < 4) {
-        // -------------------------------------------------------------------- scale loaders
-        const bool weights = warp == 2;
-        const int f = g.N / 2;
-        uint32_t gs = 0;
-        bool ok = true;
-        auto publish = [&](uint32_t step) {   // this warp's words of `step` are in shared memory: the tensor core may read them
-            tc::proxy_fence_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sf_full[step % Cfg::kStages]);
-        };
-        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-            const MxItem it = walk.at(item);
-            const uint8_t* src[4];   // the words of tile rows lane, lane + 32, .. in panel 0
-            bool in[4];
-            int64_t pitch;           // bytes between panels
-            if (weights) {
+        if (!ok && leader) {
+            s_fail = 1;
+            set_error(g.err, tc::kErrTimeout);
+        }
+    } else if (warp >= 8) {
+        // -------------------------------------------------------------------- scales
+        // Two walks over the steps: `ld` reads words kMxAhead steps before `st` writes them.
+        constexpr int kXW = Cfg::kXWords;
+        struct Words {
+            uint32_t w[2][4], x[2][kXW];
+        } buf[kMxAhead];
+        const int f = g.N / 2, npan = static_cast<int>(mx_panels(g.K));
+        const int64_t w_pitch = 4ll * g.N, x_pitch = 4ll * g.P;
+        int ld_item = blockIdx.x, ld_ks = 0;
+        // This lane's words in panel 0 of the item.  Rows past the end read another row's word, and
+        // panels past the end the last one's: nothing that is stored or multiplied depends on them, and a
+        // read that always happens is not waited for until its word is used.
+        const uint8_t *wp[4], *xp[kXW];
+        auto read = [&](Words& b) {
+            if (ld_item >= total) return;
+            if (ld_ks == 0) {
+                const MxItem it = walk.at(ld_item);
                 const uint8_t* base = g.ws + it.e * g.w_mat;
-                pitch = 4ll * g.N;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    int n = it.mtile * kMxTileM + 32 * j + lane;
-                    in[j] = n < g.N;
-                    if (swiglu) {
-                        const int neuron = it.mtile * 64 + 16 * j + (lane & 15);
-                        in[j] = neuron < f;
-                        n = (lane >> 4) * f + neuron;
-                    }
-                    src[j] = base + 4ll * n;
+                    int n = min(it.mtile * kMxTileM + 32 * j + lane, g.N - 1);
+                    if (swiglu) n = (lane >> 4) * f + min(it.mtile * 64 + 16 * j + (lane & 15), f - 1);
+                    wp[j] = base + 4ll * n;
                 }
-            } else {
-                pitch = 4ll * g.P;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    in[j] = 32 * j + lane < it.nt;
-                    src[j] = g.xs + 4ll * (it.r_first + 32 * j + lane);
-                }
+                for (int j = 0; j < kXW; ++j)
+                    xp[j] = g.xs + 4ll * (it.r_first + min(32 * j + lane, it.nt - 1));
             }
-            for (int ks = 0; ks < ksteps; ++ks, ++gs) {
-                const int st = gs % Cfg::kStages;
-                const uint32_t use = gs / Cfg::kStages;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int q = min(2 * ld_ks + p, npan - 1);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b.w[p][j] = __ldg(reinterpret_cast<const uint32_t*>(wp[j] + q * w_pitch));
+#pragma unroll
+                for (int j = 0; j < kXW; ++j) b.x[p][j] = __ldg(reinterpret_cast<const uint32_t*>(xp[j] + q * x_pitch));
+            }
+            if (++ld_ks == ksteps) {
+                ld_ks = 0;
+                ld_item += gridDim.x;
+            }
+        };
+        const uint32_t t0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kMxSfCol;
+        const int items = total > static_cast<int>(blockIdx.x) ? (total - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+        const int64_t steps = static_cast<int64_t>(items) * ksteps;
+        uint32_t st = 0, use = 0;
+        bool ok = true;
+#pragma unroll
+        for (int i = 0; i < kMxAhead; ++i) read(buf[i]);
+        for (int64_t g0 = 0; g0 < steps && ok; g0 += kMxAhead) {
+#pragma unroll
+            for (int i = 0; i < kMxAhead; ++i) {
+                if (g0 + i >= steps || !ok) break;
                 bool w_ok = use == 0 || tc::mbar_wait(&empty[st], use - 1);
                 w_ok = __all_sync(0xffffffffu, w_ok && !s_fail);
                 if (!w_ok) {
                     ok = false;
                     break;
                 }
-                const uint32_t dst = tc::s_addr(ring + st * Cfg::kStage) + kMxABytes + Cfg::kBBytes +
-                                     (weights ? 0 : 2 * kMxSfBytes) + 16 * lane;
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    if (2 * ks + p < npan) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (in[j]) tc::cp_async4(dst + p * kMxSfBytes + 4 * j, src[j] + (2 * ks + p) * pitch);
-                    }
-                }
-                tc::cp_async_commit();
-                if (gs >= kMxLag) {
-                    tc::cp_async_wait<kMxLag>();
-                    publish(gs - kMxLag);
-                }
+                tc::fence_after();
+                const uint32_t t = t0 + st * 16;
+                tc::tmem_st4(t, buf[i].w[0]);
+                tc::tmem_st4(t + 4, buf[i].w[1]);
+                tc::tmem_st<kXW>(t + 8, buf[i].x[0]);
+                tc::tmem_st<kXW>(t + 12, buf[i].x[1]);
+                read(buf[i]);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sf_full[st]);
+                if (++st == Cfg::kStages) st = 0, ++use;
             }
         }
-        tc::cp_async_wait<0>();
-        if (ok)
-            for (uint32_t step = gs >= kMxLag ? gs - kMxLag : 0; step < gs; ++step) publish(step);
         if (!ok && lane == 0) {
             s_fail = 1;
             set_error(g.err, tc::kErrTimeout);
         }
-    } else {
+    } else if (warp >= 4) {
         // -------------------------------------------------------------------- epilogue
         const int q = warp & 3;                       // lane quadrant of tensor memory
         const int nout = swiglu ? g.N / 2 : g.N;
@@ -465,7 +474,7 @@ cudaError_t mx_launch(MxArgs& g, const void* xq, int num_sms, cudaStream_t s) {
         const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(h)};
         const cudaError_t e = mx_map(&g.tx[g.nbox], 2, xq, xd, xst, box);
         if (e != cudaSuccess) return e;
-        g.boxh[g.nbox++] = h;
+        ++g.nbox;
     }
     const int64_t mtiles = (g.N + kMxTileM - 1) / kMxTileM;
     const int64_t bound = mtiles * (std::min(g.E, g.P) + g.P / NT);
