@@ -14,8 +14,8 @@
 //   warp 1     one thread issues the step's four K = 64 MMAs, operands in shared memory, scales in
 //              tensor memory;
 //   warps 4-7  epilogue: accumulators to registers, activation, stores.  Two accumulators alternate;
-//   warps 8-11 the scales: a panel's 4-byte words (128 columns) of the weight rows and of the rows of x,
-//              read kMxAhead steps ahead into registers and written straight into the form that the MMA
+//   warps 8-15 the scales, every other step by each group of four: a panel's 4-byte words (128 columns) of the weight rows and of the rows of x,
+//              read some steps ahead into registers and written straight into the form that the MMA
 //              takes them from tensor memory in: row r's word in lane r % 32 of every quadrant of 32
 //              lanes, column r / 32 (a warp writes the quadrant warp % 4).  Rows of x start anywhere and
 //              SwiGLU interleaves gate and up rows, so no bulk copy makes that form; asynchronous copies
@@ -38,14 +38,15 @@
 
 namespace moe {
 
-constexpr int kMxThreads = 384;
+constexpr int kMxThreads = 512;
 constexpr int kMxTileM = 128;            // weight rows of an item (SwiGLU: 64 gate and 64 up rows)
 constexpr int kMxStepK = 256;            // one 128-byte swizzle row of 4-bit codes
 constexpr int kMxABytes = kMxTileM * 128;
-constexpr int kMxAhead = 4;               // K steps that the scale words are read ahead
+constexpr int kMxAhead = 3;              // own K steps that a group of scale warps reads ahead
 constexpr uint32_t kMxTmemCols = 512;
 constexpr uint32_t kMxSfCol = 256;       // scale columns behind the two accumulators, 16 a stage:
                                          // weights panel 0, panel 1, rows of x panel 0, panel 1
+constexpr int kMxTransChunks = 3 * 31 + 2 * 3 + 2;   // 16-byte chunks of an epilogue warp's transposition
 constexpr int kMxMaxBoxes = 4;
 constexpr long long kMxMaxItems = 1ll << 30;
 
@@ -58,6 +59,7 @@ struct MxCfg {
     static constexpr int kXWords = (NT + 31) / 32;   // columns of a panel's scales of x
     static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage;
     static_assert(kSmem <= 214 * 1024, "ring fits beside the item table");
+    static_assert(kStages % 2 == 0, "the two groups of scale warps alternate");
     static_assert(kMxSfCol + 16 * kStages <= kMxTmemCols, "scale columns of every stage");
 };
 
@@ -113,12 +115,17 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     __shared__ uint32_t tmem_base;
     __shared__ int prefix[kMaxE + 1], rows_of[2 * kMaxE];
     __shared__ long long warp_tot[kMxThreads / 32];
+    __shared__ uint4 trans[4][kMxTransChunks];
     __shared__ volatile int s_fail;
     // the warp number through a shuffle, so that the compiler takes the roles' branches as uniform and
     // keeps descriptors and coordinates in uniform registers, where the tensor core and the copy engine
     // take them from (read out of divergent code, a step's four MMAs took 800 cycles to issue)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
+    if (warp == 1) {
+        tc::prefetch_map(&g.tw);
+        tc::prefetch_map(&g.tx[0]);
+    }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::s_addr(&tmem_base)),
                      "r"(kMxTmemCols));
@@ -264,51 +271,73 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         }
     } else if (warp >= 8) {
         // -------------------------------------------------------------------- scales
-        // Two walks over the steps: `ld` reads words kMxAhead steps before `st` writes them.
+        // Group grp takes the steps whose number has parity grp, so that one group's waits overlap the
+        // other's.  Words are read kMxAhead own steps before they are written.
         constexpr int kXW = Cfg::kXWords;
         struct Words {
             uint32_t w[2][4], x[2][kXW];
         } buf[kMxAhead];
+        const int grp = (warp - 8) >> 2;
         const int f = g.N / 2, npan = static_cast<int>(mx_panels(g.K));
         const int64_t w_pitch = 4ll * g.N, x_pitch = 4ll * g.P;
-        int ld_item = blockIdx.x, ld_ks = 0;
-        // This lane's words in panel 0 of the item.  Rows past the end read another row's word, and
-        // panels past the end the last one's: nothing that is stored or multiplied depends on them, and a
-        // read that always happens is not waited for until its word is used.
+        // This lane's words in the step's first panel.  Rows past the end read another row's word, and
+        // panels past the end the one before: nothing that is stored or multiplied depends on them, and
+        // a read that always happens is not waited for until its word is used.
         const uint8_t *wp[4], *xp[kXW];
-        auto read = [&](Words& b) {
-            if (ld_item >= total) return;
-            if (ld_ks == 0) {
-                const MxItem it = walk.at(ld_item);
-                const uint8_t* base = g.ws + it.e * g.w_mat;
+        int ld_item = blockIdx.x, ld_ks = 0;
+        auto point = [&](int ks) {   // the pointers at step ks of ld_item
+            const MxItem it = walk.at(ld_item);
+            const uint8_t* base = g.ws + it.e * g.w_mat + 2 * ks * w_pitch;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    int n = min(it.mtile * kMxTileM + 32 * j + lane, g.N - 1);
-                    if (swiglu) n = (lane >> 4) * f + min(it.mtile * 64 + 16 * j + (lane & 15), f - 1);
-                    wp[j] = base + 4ll * n;
-                }
-#pragma unroll
-                for (int j = 0; j < kXW; ++j)
-                    xp[j] = g.xs + 4ll * (it.r_first + min(32 * j + lane, it.nt - 1));
+            for (int j = 0; j < 4; ++j) {
+                int n = min(it.mtile * kMxTileM + 32 * j + lane, g.N - 1);
+                if (swiglu) n = (lane >> 4) * f + min(it.mtile * 64 + 16 * j + (lane & 15), f - 1);
+                wp[j] = base + 4ll * n;
             }
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int q = min(2 * ld_ks + p, npan - 1);
+            for (int j = 0; j < kXW; ++j)
+                xp[j] = g.xs + 4ll * (it.r_first + min(32 * j + lane, it.nt - 1)) + 2 * ks * x_pitch;
+        };
+        auto advance = [&](int by) {   // on to the group's next step
+            ld_ks += by;
+            if (ld_ks < ksteps) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) b.w[p][j] = __ldg(reinterpret_cast<const uint32_t*>(wp[j] + q * w_pitch));
+                for (int j = 0; j < 4; ++j) wp[j] += 2 * by * w_pitch;
 #pragma unroll
-                for (int j = 0; j < kXW; ++j) b.x[p][j] = __ldg(reinterpret_cast<const uint32_t*>(xp[j] + q * x_pitch));
+                for (int j = 0; j < kXW; ++j) xp[j] += 2 * by * x_pitch;
+                return;
             }
-            if (++ld_ks == ksteps) {
-                ld_ks = 0;
+            while (ld_ks >= ksteps && ld_item < total) {
+                ld_ks -= ksteps;
                 ld_item += gridDim.x;
             }
+            if (ld_item < total) point(ld_ks);
+        };
+        auto read = [&](Words& b) {
+            if (ld_item >= total) return;
+            const bool two = 2 * ld_ks + 1 < npan;
+            const int64_t wq = two ? w_pitch : 0, xq = two ? x_pitch : 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                b.w[0][j] = __ldg(reinterpret_cast<const uint32_t*>(wp[j]));
+                b.w[1][j] = __ldg(reinterpret_cast<const uint32_t*>(wp[j] + wq));
+            }
+#pragma unroll
+            for (int j = 0; j < kXW; ++j) {
+                b.x[0][j] = __ldg(reinterpret_cast<const uint32_t*>(xp[j]));
+                b.x[1][j] = __ldg(reinterpret_cast<const uint32_t*>(xp[j] + xq));
+            }
+            advance(2);
         };
         const uint32_t t0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kMxSfCol;
         const int items = total > static_cast<int>(blockIdx.x) ? (total - 1 - blockIdx.x) / gridDim.x + 1 : 0;
-        const int64_t steps = static_cast<int64_t>(items) * ksteps;
-        uint32_t st = 0, use = 0;
+        const int64_t steps = (static_cast<int64_t>(items) * ksteps - grp + 1) / 2;   // of this group
+        uint32_t st = grp, use = 0;
         bool ok = true;
+        if (ld_item < total) {
+            point(0);
+            if (grp) advance(1);
+        }
 #pragma unroll
         for (int i = 0; i < kMxAhead; ++i) read(buf[i]);
         for (int64_t g0 = 0; g0 < steps && ok; g0 += kMxAhead) {
@@ -332,7 +361,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&sf_full[st]);
-                if (++st == Cfg::kStages) st = 0, ++use;
+                st += 2;
+                if (st >= Cfg::kStages) st -= Cfg::kStages, ++use;
             }
         }
         if (!ok && lane == 0) {
@@ -343,9 +373,36 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         // -------------------------------------------------------------------- epilogue
         const int q = warp & 3;                       // lane quadrant of tensor memory
         const int nout = swiglu ? g.N / 2 : g.N;
-        const bool pairs = g.ot == MOE_BF16 && nout % 2 == 0;
-        float* of = static_cast<float*>(g.out);
         __nv_bfloat16* oh = static_cast<__nv_bfloat16*>(g.out);
+        auto put = [&](int64_t o, float y) {
+            if (g.ot == MOE_F32) static_cast<float*>(g.out)[o] = y;
+            else oh[o] = __float2bfloat16_rn(y);
+        };
+        // A lane has one column of the output and 16 rows of x, so a bf16 store of a warp would be 64
+        // bytes of one row (32 for SwiGLU).  Where 16 bytes of a row are aligned, 16 rows go through
+        // shared memory instead, packed by rows, and come back transposed (ldmatrix) as 16 bytes (8)
+        // of a row a lane, 8 rows a store.  Column f's 32 bytes start at 16-byte chunk 3 f + 2 (f / 8):
+        // both the writes and the gathered reads of 8 lanes then meet 8 different chunks mod 8.
+        const bool wide = g.ot == MOE_BF16 && nout % 8 == 0;
+        auto pos = [](int f) { return 3 * f + 2 * (f >> 3); };
+        const uint32_t tr = tc::s_addr(&trans[q][0]);
+        auto store8 = [](uint32_t base, int chunk, const float* y) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(base + 16 * chunk), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                         "r"(w[3])
+                         : "memory");
+        };
+        auto ldsm4_t = [](uint32_t w[4], uint32_t addr) {
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(addr)
+                         : "memory");
+        };
         uint32_t n_item = 0;
         bool ok = true;
         for (int item = blockIdx.x; item < total; item += gridDim.x, ++n_item) {
@@ -359,53 +416,79 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             }
             tc::fence_after();
             const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * 128);
-            for (int c0 = 0; c0 < it.nt; c0 += 16) {
-                float v[16];
-                tc::tmem_ld16(tb + c0, v);
-                if (swiglu) {
-                    // lanes 0-15 hold gate rows, 16-31 the same neurons' up rows: of every two rows of
-                    // x the low half takes the first and the high half the second
-                    const bool up = lane >= 16;
-                    const int col = it.mtile * 64 + 16 * q + (lane & 15);
+            const int col0 = swiglu ? it.mtile * 64 + 16 * q : it.mtile * kMxTileM + 32 * q;   // the warp's first column
+            const int64_t row0 = static_cast<int64_t>(it.r_first) * nout;
+            float v[16];
+            tc::tmem_ld16(tb, v);
+            for (int c0 = 0; c0 < it.nt; c0 += 16) {   // 16 rows of x
+                const int nt = it.nt - c0;             // of which this many are the item's
+                float y[16];
+                tc::tmem_ld_wait(v);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float other = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 16);
-                        const float y = up ? silu(other) * v[j + 1] : silu(v[j]) * other;
-                        const int n = c0 + j + (up ? 1 : 0);
-                        if (n < it.nt && col < nout) {
-                            const int64_t o = static_cast<int64_t>(it.r_first + n) * nout + col;
-                            if (g.ot == MOE_F32) of[o] = y;
-                            else oh[o] = __float2bfloat16_rn(y);
+                for (int j = 0; j < 16; ++j) y[j] = v[j];
+                if (c0 + 16 < it.nt) tc::tmem_ld16(tb + c0 + 16, v);
+                if (swiglu) {
+                    // lanes 0-15 hold gate rows, 16-31 the same neurons' up rows: the low half takes
+                    // the first 8 rows of x and the high half the others
+                    const bool up = lane >= 16;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float other = __shfl_xor_sync(0xffffffffu, up ? y[j] : y[j + 8], 16);
+                        y[j] = up ? silu(other) * y[j + 8] : silu(y[j]) * other;
+                    }
+                    if (wide) {
+                        store8(tr, pos(lane & 15) + (up ? 1 : 0), y);
+                        __syncwarp();
+                        // matrix m of row block t / 2: the pairs (4 u + 2 (m % 2), + 1) of its 16 columns
+                        const int c = lane & 7, m = lane >> 3;
+                        uint32_t w[4];
+                        ldsm4_t(w, tr + 16 * (pos(4 * (c >> 1) + 2 * (m & 1) + (c & 1)) + (m >> 1)));
+                        __syncwarp();
+                        const int u = lane & 3;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const int n = 8 * t + (lane >> 2);
+                            if (n < nt && col0 + 4 * u < nout)
+                                *reinterpret_cast<uint2*>(oh + row0 + static_cast<int64_t>(c0 + n) * nout + col0 + 4 * u) =
+                                    make_uint2(w[2 * t], w[2 * t + 1]);
+                        }
+                    } else {
+                        const int col = col0 + (lane & 15);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int n = j + (up ? 8 : 0);
+                            if (n < nt && col < nout) put(row0 + static_cast<int64_t>(c0 + n) * nout + col, y[j]);
                         }
                     }
                     continue;
                 }
                 if (g.act == MOE_ACT_RELU2) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = v[j] > 0.0f ? v[j] * v[j] : (v[j] <= 0.0f ? 0.0f : v[j]);
+                    for (int j = 0; j < 16; ++j) y[j] = y[j] > 0.0f ? y[j] * y[j] : (y[j] <= 0.0f ? 0.0f : y[j]);
                 }
-                const int col = it.mtile * kMxTileM + 32 * q + lane;
-                if (pairs) {   // two columns a store: of every two rows of x, even lanes store the first
-                    const bool odd = lane & 1;
+                if (wide) {
+                    store8(tr, pos(lane), y);
+                    store8(tr, pos(lane) + 1, y + 8);
+                    __syncwarp();
+                    // matrix m: the pairs (8 u + 2 m, + 1) of the 32 columns, so that the four registers
+                    // of lane 4 n + u are columns 8 u .. 8 u + 7 of row n
+                    const int c = lane & 7, m = lane >> 3, u = lane & 3;
+                    const uint32_t at = tr + 16 * pos(8 * (c >> 1) + 2 * m + (c & 1));
+                    uint32_t w[2][4];
+                    ldsm4_t(w[0], at);
+                    ldsm4_t(w[1], at + 16);
+                    __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-                        const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(other, v[j + 1])
-                                                     : __floats2bfloat162_rn(v[j], other);
-                        const int n = c0 + j + (odd ? 1 : 0);
-                        if (n < it.nt && col < nout)
-                            *reinterpret_cast<__nv_bfloat162*>(oh + static_cast<int64_t>(it.r_first + n) * nout +
-                                                               (col & ~1)) = h;
+                    for (int t = 0; t < 2; ++t) {
+                        const int n = 8 * t + (lane >> 2);
+                        if (n < nt && col0 + 8 * u < nout)
+                            *reinterpret_cast<uint4*>(oh + row0 + static_cast<int64_t>(c0 + n) * nout + col0 + 8 * u) =
+                                make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
                     }
-                } else if (col < nout) {
+                } else if (col0 + lane < nout) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (c0 + j < it.nt) {
-                            const int64_t o = static_cast<int64_t>(it.r_first + c0 + j) * nout + col;
-                            if (g.ot == MOE_F32) of[o] = v[j];
-                            else oh[o] = __float2bfloat16_rn(v[j]);
-                        }
-                    }
+                    for (int j = 0; j < 16; ++j)
+                        if (j < nt) put(row0 + static_cast<int64_t>(c0 + j) * nout + col0 + lane, y[j]);
                 }
             }
             tc::fence_before();
