@@ -38,7 +38,7 @@
 
 namespace moe {
 
-constexpr int kMxThreads = 512;
+constexpr int kMxThreads = 512, kMxWarps = kMxThreads / 32;
 constexpr int kMxTileM = 128;            // weight rows of an item (SwiGLU: 64 gate and 64 up rows)
 constexpr int kMxStepK = 256;            // one 128-byte swizzle row of 4-bit codes
 constexpr int kMxABytes = kMxTileM * 128;
@@ -50,6 +50,8 @@ constexpr int kMxTransChunks = 3 * 31 + 2 * 3 + 2;   // 16-byte chunks of an epi
 constexpr int kMxMaxBoxes = 4;
 constexpr long long kMxMaxItems = 1ll << 30;
 
+__device__ const uint32_t kMxOne = 0x7f7f7f7fu;   // scales of 2^0
+
 // Shared memory: the ring, and its depth, by the width of the row tile.
 template <int NT>
 struct MxCfg {
@@ -58,7 +60,7 @@ struct MxCfg {
     static constexpr int kStages = NT >= 128 ? 6 : (NT >= 64 ? 8 : 10);
     static constexpr int kXWords = (NT + 31) / 32;   // columns of a panel's scales of x
     static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage;
-    static_assert(kSmem <= 214 * 1024, "ring fits beside the item table");
+    static_assert(kSmem + 22 * 1024 <= 227 * 1024, "ring fits beside the item table");
     static_assert(kStages % 2 == 0, "the two groups of scale warps alternate");
     static_assert(kMxSfCol + 16 * kStages <= kMxTmemCols, "scale columns of every stage");
 };
@@ -77,28 +79,38 @@ struct MxArgs {
     int32_t* err;
 };
 
+__device__ __forceinline__ void mx_fail(const MxArgs& g, volatile int* s_fail) {
+    *s_fail = 1;
+    set_error(g.err, tc::kErrTimeout);
+}
+
 struct MxItem {
     int e, r_first, nt, mtile;
 };
 
-// The items in order: experts, then row tiles, then weight tiles.  Every role walks them in increasing
-// order, so the expert is found by stepping on from the last one.
+// The items in order: experts with rows (slots), then row tiles, then weight tiles.  Every role walks
+// them in increasing order, so a warp looks for an item's slot from the last one on, 32 slots at a time.
 template <int NT>
 struct MxWalk {
-    const int* prefix;
-    const int* first;
-    int E, mtiles;
-    int e = 0;
-    __device__ MxItem at(int item) {
-        while (prefix[e + 1] <= item) ++e;
-        const int local = item - prefix[e];
-        const int ntile = local / mtiles;
+    const int* prefix;    // [slots + 1] first item of a slot
+    const int2* rows;     // first row, last row + 1
+    const uint16_t* expert;
+    int n_slots, mtiles, lane;
+    int slot = 0;
+    __device__ MxItem at(int item) {   // the whole warp
+        for (;;) {
+            const int i = slot + 1 + lane;
+            const int n = __popc(__ballot_sync(0xffffffffu, i < n_slots && prefix[i] <= item));
+            slot += n;
+            if (n < 32) break;
+        }
+        const int2 r = rows[slot];
+        const int local = item - prefix[slot], ntile = local / mtiles;
         MxItem it;
-        it.e = e;
+        it.e = expert[slot];
         it.mtile = local - ntile * mtiles;
-        it.r_first = first[e] + ntile * NT;
-        // (the rows of the expert end where its tiles do: first[E + e] is its last row + 1)
-        it.nt = min(NT, first[E + e] - it.r_first);
+        it.r_first = r.x + ntile * NT;
+        it.nt = min(NT, r.y - it.r_first);
         return it;
     }
 };
@@ -109,12 +121,15 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     extern __shared__ __align__(16) unsigned char dsm_raw[];
     unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) &
                                                            ~static_cast<uintptr_t>(1023));
-    __shared__ uint64_t full[Cfg::kStages], sf_full[Cfg::kStages], empty[Cfg::kStages];
+    __shared__ uint64_t full[Cfg::kStages], empty[Cfg::kStages];
     __shared__ uint64_t acc_full[2], acc_empty[2];
-    __shared__ uint32_t issued[Cfg::kStages], commits[Cfg::kStages];
+    __shared__ uint32_t issued, committed;   // steps whose loads / MMAs this CTA has issued
     __shared__ uint32_t tmem_base;
-    __shared__ int prefix[kMaxE + 1], rows_of[2 * kMaxE];
-    __shared__ long long warp_tot[kMxThreads / 32];
+    __shared__ int prefix[kMaxE];
+    __shared__ int2 rows[kMaxE];
+    __shared__ uint16_t expert[kMaxE];
+    __shared__ long long warp_tiles[kMxWarps];
+    __shared__ int warp_live[kMxWarps], n_slots, n_items;
     __shared__ uint4 trans[4][kMxTransChunks];
     __shared__ volatile int s_fail;
     // the warp number through a shuffle, so that the compiler takes the roles' branches as uniform and
@@ -133,10 +148,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     }
     if (tid == 0) {
         for (int s = 0; s < Cfg::kStages; ++s) {
-            tc::mbar_init(&full[s], 1);
-            tc::mbar_init(&sf_full[s], 4);
+            tc::mbar_init(&full[s], 5);   // the TMA's arrival and bytes, four scale warps
             tc::mbar_init(&empty[s], 1);
-            issued[s] = commits[s] = 0;
         }
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&acc_full[s], 1);
@@ -144,54 +157,67 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_fail = 0;
+        issued = committed = 0;
     }
     pdl_wait();
     pdl_trigger();
     const bool swiglu = g.act == MOE_ACT_SWIGLU;
     const int mtiles = (g.N + kMxTileM - 1) / kMxTileM;
-    {   // the item table: exclusive prefix over the experts of (row tiles) x (weight tiles).  Offsets
-        // that overlap could count past 32 bits: the table is cut at kMxMaxItems, which increasing
-        // offsets stay far below
-        constexpr int kPer = (kMaxE + kMxThreads) / kMxThreads;   // with a thread for the entry behind the last
-        int cnt[kPer];
-        long long local = 0;
+    {   // the slots and an exclusive prefix over them of (row tiles) x (weight tiles).  Offsets that
+        // overlap could count past 32 bits: the prefix is cut at kMxMaxItems, which increasing offsets
+        // stay far below
+        constexpr int kPer = kMaxE / kMxThreads;
+        int first[kPer], last[kPer];
+        long long tiles = 0;
+        int live = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int e = tid * kPer + i;
-            cnt[i] = 0;
-            if (e < g.E) {
-                int a, b;
-                mx_expert_rows(g.offsets, e, g.P, &a, &b);
-                rows_of[e] = a;
-                rows_of[g.E + e] = b;
-                cnt[i] = ((b - a + NT - 1) / NT) * mtiles;
-            }
-            local += cnt[i];
+            first[i] = last[i] = 0;
+            if (tid * kPer + i < g.E) mx_expert_rows(g.offsets, tid * kPer + i, g.P, &first[i], &last[i]);
+            tiles += (last[i] - first[i] + NT - 1) / NT;
+            live += last[i] > first[i];
         }
-        long long incl = local;
+        long long t_incl = tiles;
+        int l_incl = live;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+            const long long t = __shfl_up_sync(0xffffffffu, t_incl, o);
+            const int l = __shfl_up_sync(0xffffffffu, l_incl, o);
+            if (lane >= o) t_incl += t, l_incl += l;
         }
-        if (lane == 31) warp_tot[warp] = incl;
+        if (lane == 31) warp_tiles[warp] = t_incl, warp_live[warp] = l_incl;
         __syncthreads();
-        long long run = incl - local;
-        for (int w = 0; w < warp; ++w) run += warp_tot[w];
+        long long t_before = lane < warp ? warp_tiles[lane & (kMxWarps - 1)] : 0;
+        int l_before = lane < warp ? warp_live[lane & (kMxWarps - 1)] : 0;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            t_before += __shfl_xor_sync(0xffffffffu, t_before, o);
+            l_before += __shfl_xor_sync(0xffffffffu, l_before, o);
+        }
+        long long run = t_before + t_incl - tiles;
+        int slot = l_before + l_incl - live;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int e = tid * kPer + i;
-            if (e <= g.E) prefix[e] = static_cast<int>(min(run, kMxMaxItems));
-            run += cnt[i];
+            if (last[i] > first[i]) {
+                prefix[slot] = static_cast<int>(min(run * mtiles, kMxMaxItems));
+                rows[slot] = make_int2(first[i], last[i]);
+                expert[slot] = static_cast<uint16_t>(tid * kPer + i);
+                ++slot;
+                run += (last[i] - first[i] + NT - 1) / NT;
+            }
+        }
+        if (tid == kMxThreads - 1) {
+            n_slots = slot;
+            n_items = static_cast<int>(min(run * mtiles, kMxMaxItems));
         }
     }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = tmem_base;
-    const int total = prefix[g.E];
+    const int total = n_items;
     const int ksteps = (g.K + kMxStepK - 1) / kMxStepK;
-    MxWalk<NT> walk{prefix, rows_of, g.E, mtiles};
+    MxWalk<NT> walk{prefix, rows, expert, n_slots, mtiles, lane};
 
     if (warp == 0) {
         // -------------------------------------------------------------------- TMA producer
@@ -205,14 +231,12 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             while (bi + 1 < g.nbox && (16 << bi) < it.nt) ++bi;   // smallest box covering the rows
             const uint32_t bytes = static_cast<uint32_t>(kMxABytes + (16 << bi) * 128);
             for (int ks = 0; ks < ksteps; ++ks) {
-                const bool w_ok = use == 0 || tc::mbar_wait(&empty[st], use - 1);
-                if (!__all_sync(0xffffffffu, w_ok && !s_fail)) {
+                if (use > 0 && !tc::mbar_wait_warp(&empty[st], use - 1, &s_fail)) {
                     ok = false;
                     break;
                 }
                 if (leader) {
                     tc::mbar_arrive_expect_tx(&full[st], bytes);
-                    issued[st] = use + 1;
                     const uint32_t dst = ring0 + st * Cfg::kStage;
                     if (swiglu) tc::tma_5d(dst, &g.tw, ks * 128, 0, 0, it.mtile * 4, it.e, &full[st]);
                     else tc::tma_3d(dst, &g.tw, ks * 128, it.mtile * kMxTileM, it.e, &full[st]);
@@ -221,9 +245,9 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                 if (++st == Cfg::kStages) st = 0, ++use;
             }
         }
-        if (!ok && leader) {
-            s_fail = 1;
-            set_error(g.err, tc::kErrTimeout);
+        if (leader) {
+            issued = use * Cfg::kStages + st;
+            if (!ok) mx_fail(g, &s_fail);
         }
     } else if (warp == 1) {
         // -------------------------------------------------------------------- MMA issuer
@@ -235,15 +259,13 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             const MxItem it = walk.at(item);
             const uint32_t idesc = tc::idesc_mxf4((it.nt + 15) & ~15);
             const uint32_t buf = n_item & 1, ub = n_item >> 1;
-            const bool a_ok = ub == 0 || tc::mbar_wait(&acc_empty[buf], ub - 1);
-            if (!__all_sync(0xffffffffu, a_ok && !s_fail)) {
+            if (ub > 0 && !tc::mbar_wait_warp(&acc_empty[buf], ub - 1, &s_fail)) {
                 ok = false;
                 break;
             }
             const uint32_t dt = tmem + buf * 128;
             for (int ks = 0; ks < ksteps; ++ks) {
-                const bool w_ok = tc::mbar_wait(&full[st], use) && tc::mbar_wait(&sf_full[st], use);
-                if (!__all_sync(0xffffffffu, w_ok && !s_fail)) {
+                if (!tc::mbar_wait_warp(&full[st], use, &s_fail)) {
                     ok = false;
                     break;
                 }
@@ -252,22 +274,20 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                     // (the descriptors' start address, bytes / 16, is linear in the address)
                     const uint64_t da = da0 + st * (Cfg::kStage >> 4), db = db0 + st * (Cfg::kStage >> 4);
                     const uint32_t ta = tmem + kMxSfCol + st * 16, tb = ta + 8;
-                    const int slices = (g.K - ks * kMxStepK + 63) / 64;
+                    // (slices past K multiply zero codes by scales of 2^0)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)   // 32 bytes of codes; blocks 2 (kk % 2), + 1 of panel kk / 2
-                        if (kk < slices)
-                            tc::umma_mxf4(dt, da + 2 * kk, db + 2 * kk, idesc | tc::idesc_sf((kk & 1) * 2),
-                                          ta + 4 * (kk >> 1), tb + 4 * (kk >> 1), ks > 0 || kk > 0);
+                        tc::umma_mxf4(dt, da + 2 * kk, db + 2 * kk, idesc | tc::idesc_sf((kk & 1) * 2),
+                                      ta + 4 * (kk >> 1), tb + 4 * (kk >> 1), ks > 0 || kk > 0);
                     tc::commit(&empty[st]);
-                    commits[st] = use + 1;
                     if (ks + 1 == ksteps) tc::commit(&acc_full[buf]);
                 }
                 if (++st == Cfg::kStages) st = 0, ++use;
             }
         }
-        if (!ok && leader) {
-            s_fail = 1;
-            set_error(g.err, tc::kErrTimeout);
+        if (leader) {
+            committed = use * Cfg::kStages + st;
+            if (!ok) mx_fail(g, &s_fail);
         }
     } else if (warp >= 8) {
         // -------------------------------------------------------------------- scales
@@ -280,9 +300,9 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         const int grp = (warp - 8) >> 2;
         const int f = g.N / 2, npan = static_cast<int>(mx_panels(g.K));
         const int64_t w_pitch = 4ll * g.N, x_pitch = 4ll * g.P;
-        // This lane's words in the step's first panel.  Rows past the end read another row's word, and
-        // panels past the end the one before: nothing that is stored or multiplied depends on them, and
-        // a read that always happens is not waited for until its word is used.
+        // This lane's words in the step's first panel.  Rows past the end read another row's word, and a
+        // panel past the end reads kMxOne: a read that always happens is not waited for until its word is
+        // used.
         const uint8_t *wp[4], *xp[kXW];
         int ld_item = blockIdx.x, ld_ks = 0;
         auto point = [&](int ks) {   // the pointers at step ks of ld_item
@@ -316,16 +336,17 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         auto read = [&](Words& b) {
             if (ld_item >= total) return;
             const bool two = 2 * ld_ks + 1 < npan;
-            const int64_t wq = two ? w_pitch : 0, xq = two ? x_pitch : 0;
+            auto word = [](const void* p) { return __ldg(static_cast<const uint32_t*>(p)); };
+            const void* one = &kMxOne;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                b.w[0][j] = __ldg(reinterpret_cast<const uint32_t*>(wp[j]));
-                b.w[1][j] = __ldg(reinterpret_cast<const uint32_t*>(wp[j] + wq));
+                b.w[0][j] = word(wp[j]);
+                b.w[1][j] = word(two ? wp[j] + w_pitch : one);
             }
 #pragma unroll
             for (int j = 0; j < kXW; ++j) {
-                b.x[0][j] = __ldg(reinterpret_cast<const uint32_t*>(xp[j]));
-                b.x[1][j] = __ldg(reinterpret_cast<const uint32_t*>(xp[j] + xq));
+                b.x[0][j] = word(xp[j]);
+                b.x[1][j] = word(two ? xp[j] + x_pitch : one);
             }
             advance(2);
         };
@@ -344,9 +365,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
 #pragma unroll
             for (int i = 0; i < kMxAhead; ++i) {
                 if (g0 + i >= steps || !ok) break;
-                bool w_ok = use == 0 || tc::mbar_wait(&empty[st], use - 1);
-                w_ok = __all_sync(0xffffffffu, w_ok && !s_fail);
-                if (!w_ok) {
+                if (use > 0 && !tc::mbar_wait_warp(&empty[st], use - 1, &s_fail)) {
                     ok = false;
                     break;
                 }
@@ -360,15 +379,12 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&sf_full[st]);
+                if (lane == 0) tc::mbar_arrive(&full[st]);
                 st += 2;
                 if (st >= Cfg::kStages) st -= Cfg::kStages, ++use;
             }
         }
-        if (!ok && lane == 0) {
-            s_fail = 1;
-            set_error(g.err, tc::kErrTimeout);
-        }
+        if (!ok && lane == 0) mx_fail(g, &s_fail);
     } else if (warp >= 4) {
         // -------------------------------------------------------------------- epilogue
         const int q = warp & 3;                       // lane quadrant of tensor memory
@@ -408,9 +424,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         for (int item = blockIdx.x; item < total; item += gridDim.x, ++n_item) {
             const MxItem it = walk.at(item);
             const int buf = n_item & 1;
-            bool w_ok = tc::mbar_wait(&acc_full[buf], n_item >> 1);
-            w_ok = __all_sync(0xffffffffu, w_ok && !s_fail);
-            if (!w_ok) {
+            if (!tc::mbar_wait_warp(&acc_full[buf], n_item >> 1, &s_fail)) {
                 ok = false;
                 break;
             }
@@ -495,25 +509,22 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
         }
-        if (!ok && lane == 0) {
-            s_fail = 1;
-            set_error(g.err, tc::kErrTimeout);
-        }
+        if (!ok && lane == 0) mx_fail(g, &s_fail);
     }
 
-    // every copy and MMA this CTA issued has landed before its memories are given back (immediate
-    // on the normal path; bounded after a timeout)
-    __syncthreads();
-    if (tid == 0) {
-        bool ok = true;
-        for (int s = 0; s < Cfg::kStages; ++s) {
-            if (issued[s]) ok &= tc::mbar_wait(&full[s], issued[s] - 1);
-            if (commits[s]) ok &= tc::mbar_wait(&empty[s], commits[s] - 1);
-        }
-        if (!ok) set_error(g.err, tc::kErrTimeout);
-    }
+    // Every copy and MMA this CTA issued has landed before its memories are given back: the MMAs waited
+    // for every copy and the epilogue for every MMA, unless a wait ran out.
     tc::fence_before();
     __syncthreads();
+    if (s_fail) {
+        if (tid == 0) {
+            for (uint32_t n = issued > Cfg::kStages ? issued - Cfg::kStages : 0; n < issued; ++n)
+                tc::mbar_wait(&full[n % Cfg::kStages], n / Cfg::kStages);
+            for (uint32_t n = committed > Cfg::kStages ? committed - Cfg::kStages : 0; n < committed; ++n)
+                tc::mbar_wait(&empty[n % Cfg::kStages], n / Cfg::kStages);
+        }
+        __syncthreads();
+    }
     tc::fence_after();
     if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kMxTmemCols));
 }

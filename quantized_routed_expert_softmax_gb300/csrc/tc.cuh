@@ -57,6 +57,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t n) {
     }
 }
 
+// The same by a whole warp, all lanes with one answer; also gives up once *fail is set.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t n, const volatile int* fail) {
+    const uint32_t parity = n & 1u;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const long long t0 = global_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((i & 63u) == 0 && __any_sync(0xffffffffu, *fail || global_ns() - t0 > kWaitLimitNs)) return false;
+    }
+}
+
 // ------------------------------------------------------------------------------ loads
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
