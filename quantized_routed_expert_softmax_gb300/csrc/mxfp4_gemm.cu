@@ -57,10 +57,10 @@ template <int NT>
 struct MxCfg {
     static constexpr int kBBytes = NT * 128;
     static constexpr int kStage = kMxABytes + kBBytes;
-    static constexpr int kStages = NT >= 128 ? 6 : (NT >= 64 ? 8 : 10);
+    static constexpr int kStages = NT >= 128 ? 6 : (NT >= 32 ? 8 : 10);
     static constexpr int kXWords = (NT + 31) / 32;   // columns of a panel's scales of x
     static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage;
-    static_assert(kSmem + 22 * 1024 <= 227 * 1024, "ring fits beside the item table");
+    static_assert(kSmem + 32 * 1024 <= 227 * 1024, "ring fits beside the item table");
     static_assert(kStages % 2 == 0, "the two groups of scale warps alternate");
     static_assert(kMxSfCol + 16 * kStages <= kMxTmemCols, "scale columns of every stage");
 };
@@ -74,7 +74,6 @@ struct MxArgs {
     int64_t w_mat;                   // bytes between weight matrices
     const int32_t* offsets;
     int E, P, N, K;
-    int act, ot;
     void* out;
     int32_t* err;
 };
@@ -115,9 +114,32 @@ struct MxWalk {
     }
 };
 
-template <int NT>
+// Output forms: fp32; bf16 where 16 bytes of a row are aligned; other bf16.
+enum { kOutF32 = 0, kOutWide = 1, kOutBf16 = 2 };
+
+// The epilogue's transposition: column f's 16 values (32 bytes) start at this 16-byte chunk.  Both the
+// writes and the gathered reads of 8 lanes then meet 8 different chunks mod 8.
+__device__ __forceinline__ int mx_chunk(int f) { return 3 * f + 2 * (f >> 3); }
+__device__ __forceinline__ void mx_store8(uint32_t addr, const float* y) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+__device__ __forceinline__ void mx_ldsm4_t(uint32_t* w, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <int NT, int ACT, int OUT>
 __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_constant__ MxArgs g) {
     using Cfg = MxCfg<NT>;
+    constexpr bool kSwiglu = ACT == MOE_ACT_SWIGLU;
     extern __shared__ __align__(16) unsigned char dsm_raw[];
     unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) &
                                                            ~static_cast<uintptr_t>(1023));
@@ -130,7 +152,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     __shared__ uint16_t expert[kMaxE];
     __shared__ long long warp_tiles[kMxWarps];
     __shared__ int warp_live[kMxWarps], n_slots, n_items;
-    __shared__ uint4 trans[4][kMxTransChunks];
+    __shared__ uint4 trans[4][2][kMxTransChunks];
     __shared__ volatile int s_fail;
     // the warp number through a shuffle, so that the compiler takes the roles' branches as uniform and
     // keeps descriptors and coordinates in uniform registers, where the tensor core and the copy engine
@@ -161,7 +183,6 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     }
     pdl_wait();
     pdl_trigger();
-    const bool swiglu = g.act == MOE_ACT_SWIGLU;
     const int mtiles = (g.N + kMxTileM - 1) / kMxTileM;
     {   // the slots and an exclusive prefix over them of (row tiles) x (weight tiles).  Offsets that
         // overlap could count past 32 bits: the prefix is cut at kMxMaxItems, which increasing offsets
@@ -238,7 +259,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                 if (leader) {
                     tc::mbar_arrive_expect_tx(&full[st], bytes);
                     const uint32_t dst = ring0 + st * Cfg::kStage;
-                    if (swiglu) tc::tma_5d(dst, &g.tw, ks * 128, 0, 0, it.mtile * 4, it.e, &full[st]);
+                    if (kSwiglu) tc::tma_5d(dst, &g.tw, ks * 128, 0, 0, it.mtile * 4, it.e, &full[st]);
                     else tc::tma_3d(dst, &g.tw, ks * 128, it.mtile * kMxTileM, it.e, &full[st]);
                     tc::tma_2d(dst + kMxABytes, &g.tx[bi], ks * 128, it.r_first, &full[st]);
                 }
@@ -311,7 +332,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 int n = min(it.mtile * kMxTileM + 32 * j + lane, g.N - 1);
-                if (swiglu) n = (lane >> 4) * f + min(it.mtile * 64 + 16 * j + (lane & 15), f - 1);
+                if (kSwiglu) n = (lane >> 4) * f + min(it.mtile * 64 + 16 * j + (lane & 15), f - 1);
                 wp[j] = base + 4ll * n;
             }
 #pragma unroll
@@ -387,38 +408,20 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         if (!ok && lane == 0) mx_fail(g, &s_fail);
     } else if (warp >= 4) {
         // -------------------------------------------------------------------- epilogue
+        // (activation and output form are template parameters: the loop over 16 rows of x has to stay
+        // short, as a warp that runs alone on its scheduler pays for every instruction it fetches)
         const int q = warp & 3;                       // lane quadrant of tensor memory
-        const int nout = swiglu ? g.N / 2 : g.N;
-        __nv_bfloat16* oh = static_cast<__nv_bfloat16*>(g.out);
-        auto put = [&](int64_t o, float y) {
-            if (g.ot == MOE_F32) static_cast<float*>(g.out)[o] = y;
-            else oh[o] = __float2bfloat16_rn(y);
-        };
-        // A lane has one column of the output and 16 rows of x, so a bf16 store of a warp would be 64
-        // bytes of one row (32 for SwiGLU).  Where 16 bytes of a row are aligned, 16 rows go through
-        // shared memory instead, packed by rows, and come back transposed (ldmatrix) as 16 bytes (8)
-        // of a row a lane, 8 rows a store.  Column f's 32 bytes start at 16-byte chunk 3 f + 2 (f / 8):
-        // both the writes and the gathered reads of 8 lanes then meet 8 different chunks mod 8.
-        const bool wide = g.ot == MOE_BF16 && nout % 8 == 0;
-        auto pos = [](int f) { return 3 * f + 2 * (f >> 3); };
-        const uint32_t tr = tc::s_addr(&trans[q][0]);
-        auto store8 = [](uint32_t base, int chunk, const float* y) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(base + 16 * chunk), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                         "r"(w[3])
-                         : "memory");
-        };
-        auto ldsm4_t = [](uint32_t w[4], uint32_t addr) {
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(addr)
-                         : "memory");
-        };
+        const int nout = kSwiglu ? g.N / 2 : g.N;
+        const bool up = kSwiglu && lane >= 16;
+        const int wcol = kSwiglu ? 16 * q : 32 * q;   // the warp's first column in the tile
+        // kOutWide: where this lane writes, and reads back, the transposition, and the column it stores
+        const uint32_t tr = tc::s_addr(&trans[q][0][0]);
+        const uint32_t tr_st = tr + 16 * (kSwiglu ? mx_chunk(lane & 15) + (up ? 1 : 0) : mx_chunk(lane));
+        const int c8 = lane & 7, m4 = lane >> 3;
+        const uint32_t tr_ld = tr + 16 * (kSwiglu ? mx_chunk(4 * (c8 >> 1) + 2 * (m4 & 1) + (c8 & 1)) + (m4 >> 1)
+                                                  : mx_chunk(8 * (c8 >> 1) + 2 * m4 + (c8 & 1)));
+        const int lcol = wcol + (OUT == kOutWide ? (kSwiglu ? 4 : 8) * (lane & 3) : (kSwiglu ? lane & 15 : lane));
+        const int lrow = OUT == kOutWide ? lane >> 2 : (up ? 8 : 0);   // this lane's first row of 16
         uint32_t n_item = 0;
         bool ok = true;
         for (int item = blockIdx.x; item < total; item += gridDim.x, ++n_item) {
@@ -430,80 +433,63 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             }
             tc::fence_after();
             const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * 128);
-            const int col0 = swiglu ? it.mtile * 64 + 16 * q : it.mtile * kMxTileM + 32 * q;   // the warp's first column
-            const int64_t row0 = static_cast<int64_t>(it.r_first) * nout;
+            const int col = it.mtile * (kSwiglu ? 64 : kMxTileM) + lcol;
+            const bool in = col < nout;
+            int left = it.nt - lrow;   // rows of the item from this lane's first on
+            char* o = static_cast<char*>(g.out) +
+                      (static_cast<int64_t>(it.r_first + lrow) * nout + col) * (OUT == kOutF32 ? 4 : 2);
+            const int64_t pitch = static_cast<int64_t>(nout) * (OUT == kOutF32 ? 4 : 2);
+            uint32_t flip = 0;
             float v[16];
             tc::tmem_ld16(tb, v);
+#pragma unroll 1
             for (int c0 = 0; c0 < it.nt; c0 += 16) {   // 16 rows of x
-                const int nt = it.nt - c0;             // of which this many are the item's
                 float y[16];
                 tc::tmem_ld_wait(v);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) y[j] = v[j];
                 if (c0 + 16 < it.nt) tc::tmem_ld16(tb + c0 + 16, v);
-                if (swiglu) {
+                if (kSwiglu) {
                     // lanes 0-15 hold gate rows, 16-31 the same neurons' up rows: the low half takes
                     // the first 8 rows of x and the high half the others
-                    const bool up = lane >= 16;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float other = __shfl_xor_sync(0xffffffffu, up ? y[j] : y[j + 8], 16);
                         y[j] = up ? silu(other) * y[j + 8] : silu(y[j]) * other;
                     }
-                    if (wide) {
-                        store8(tr, pos(lane & 15) + (up ? 1 : 0), y);
-                        __syncwarp();
-                        // matrix m of row block t / 2: the pairs (4 u + 2 (m % 2), + 1) of its 16 columns
-                        const int c = lane & 7, m = lane >> 3;
-                        uint32_t w[4];
-                        ldsm4_t(w, tr + 16 * (pos(4 * (c >> 1) + 2 * (m & 1) + (c & 1)) + (m >> 1)));
-                        __syncwarp();
-                        const int u = lane & 3;
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            const int n = 8 * t + (lane >> 2);
-                            if (n < nt && col0 + 4 * u < nout)
-                                *reinterpret_cast<uint2*>(oh + row0 + static_cast<int64_t>(c0 + n) * nout + col0 + 4 * u) =
-                                    make_uint2(w[2 * t], w[2 * t + 1]);
-                        }
-                    } else {
-                        const int col = col0 + (lane & 15);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int n = j + (up ? 8 : 0);
-                            if (n < nt && col < nout) put(row0 + static_cast<int64_t>(c0 + n) * nout + col, y[j]);
-                        }
-                    }
-                    continue;
-                }
-                if (g.act == MOE_ACT_RELU2) {
+                } else if (ACT == MOE_ACT_RELU2) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) y[j] = y[j] > 0.0f ? y[j] * y[j] : (y[j] <= 0.0f ? 0.0f : y[j]);
                 }
-                if (wide) {
-                    store8(tr, pos(lane), y);
-                    store8(tr, pos(lane) + 1, y + 8);
+                if (OUT == kOutWide) {
+                    // A lane has one column of the output and 16 rows of x, so that a store of a warp would
+                    // be 64 bytes of one row (32 for SwiGLU).  The 16 rows go through shared memory, packed
+                    // by rows, and come back transposed: lane 4 n + u has columns 8 u .. 8 u + 7 (4 u ..) of
+                    // rows n and n + 8.  Two buffers, so that one barrier orders a pass after the last.
+                    mx_store8(tr_st + flip, y);
+                    if (!kSwiglu) mx_store8(tr_st + 16 + flip, y + 8);
                     __syncwarp();
-                    // matrix m: the pairs (8 u + 2 m, + 1) of the 32 columns, so that the four registers
-                    // of lane 4 n + u are columns 8 u .. 8 u + 7 of row n
-                    const int c = lane & 7, m = lane >> 3, u = lane & 3;
-                    const uint32_t at = tr + 16 * pos(8 * (c >> 1) + 2 * m + (c & 1));
-                    uint32_t w[2][4];
-                    ldsm4_t(w[0], at);
-                    ldsm4_t(w[1], at + 16);
-                    __syncwarp();
+                    uint32_t w[8];
+                    mx_ldsm4_t(w, tr_ld + flip);
+                    if (!kSwiglu) mx_ldsm4_t(w + 4, tr_ld + 16 + flip);
+                    flip ^= 16 * kMxTransChunks;
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const int n = 8 * t + (lane >> 2);
-                        if (n < nt && col0 + 8 * u < nout)
-                            *reinterpret_cast<uint4*>(oh + row0 + static_cast<int64_t>(c0 + n) * nout + col0 + 8 * u) =
-                                make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+                        if (!in || 8 * t >= left) continue;
+                        if (kSwiglu) *reinterpret_cast<uint2*>(o + 8 * t * pitch) = make_uint2(w[2 * t], w[2 * t + 1]);
+                        else *reinterpret_cast<uint4*>(o + 8 * t * pitch) = make_uint4(w[4 * t], w[4 * t + 1], w[4 * t + 2], w[4 * t + 3]);
                     }
-                } else if (col0 + lane < nout) {
+                } else {
+                    char* p = o;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (j < nt) put(row0 + static_cast<int64_t>(c0 + j) * nout + col0 + lane, y[j]);
+                    for (int j = 0; j < (kSwiglu ? 8 : 16); ++j, p += pitch) {
+                        if (!in || j >= left) continue;
+                        if (OUT == kOutF32) *reinterpret_cast<float*>(p) = y[j];
+                        else *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(y[j]);
+                    }
                 }
+                o += 16 * pitch;
+                left -= 16;
             }
             tc::fence_before();
             __syncwarp();
@@ -558,37 +544,42 @@ cudaError_t mx_map(CUtensorMap* m, int rank, const void* base, const cuuint64_t*
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+using MxKernel = void (*)(MxArgs);
+
+template <int NT, int ACT>
+MxKernel mx_kernel(int out) {
+    if (out == kOutF32) return mxfp4_gemm_kernel<NT, ACT, kOutF32>;
+    if (out == kOutWide || ACT == MOE_ACT_SWIGLU) return mxfp4_gemm_kernel<NT, ACT, kOutWide>;   // (N / 2 is a multiple of 32)
+    return mxfp4_gemm_kernel<NT, ACT, ACT == MOE_ACT_SWIGLU ? kOutWide : kOutBf16>;
+}
 template <int NT>
-cudaError_t mx_launch(MxArgs& g, const void* xq, int num_sms, cudaStream_t s) {
-    // boxes of x: the powers of two from 16 below the tile, so that a short group does not load a tile
-    const cuuint64_t xd[2] = {static_cast<cuuint64_t>(g.K / 2), static_cast<cuuint64_t>(g.P)};
-    const cuuint64_t xst[1] = {static_cast<cuuint64_t>(g.K / 2)};
-    g.nbox = 0;
-    for (int h = 16; h <= NT; h *= 2) {
-        const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(h)};
-        const cudaError_t e = mx_map(&g.tx[g.nbox], 2, xq, xd, xst, box);
-        if (e != cudaSuccess) return e;
-        ++g.nbox;
+MxKernel mx_kernel(int act, int out) {
+    if (act == MOE_ACT_SWIGLU) return mx_kernel<NT, MOE_ACT_SWIGLU>(out);
+    if (act == MOE_ACT_RELU2) return mx_kernel<NT, MOE_ACT_RELU2>(out);
+    return mx_kernel<NT, MOE_ACT_NONE>(out);
+}
+MxKernel mx_kernel(int nt, int act, int out, size_t* smem) {
+    switch (nt) {
+        case 16: *smem = MxCfg<16>::kSmem; return mx_kernel<16>(act, out);
+        case 32: *smem = MxCfg<32>::kSmem; return mx_kernel<32>(act, out);
+        case 64: *smem = MxCfg<64>::kSmem; return mx_kernel<64>(act, out);
+        default: *smem = MxCfg<128>::kSmem; return mx_kernel<128>(act, out);
     }
-    const int64_t mtiles = (g.N + kMxTileM - 1) / kMxTileM;
-    const int64_t bound = mtiles * (std::min(g.E, g.P) + g.P / NT);
-    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms, bound)));
-    return launch_pdl(mxfp4_gemm_kernel<NT>, dim3(grid), dim3(kMxThreads), MxCfg<NT>::kSmem, s, g);
 }
 
 }  // namespace
 
 cudaError_t configure_mxfp4_kernels() {
     cudaError_t e = mx_encoder();
-    auto set = [&](const void* fn, size_t smem) {
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-    };
-    set(reinterpret_cast<const void*>(mxfp4_gemm_kernel<16>), MxCfg<16>::kSmem);
-    set(reinterpret_cast<const void*>(mxfp4_gemm_kernel<32>), MxCfg<32>::kSmem);
-    set(reinterpret_cast<const void*>(mxfp4_gemm_kernel<64>), MxCfg<64>::kSmem);
-    set(reinterpret_cast<const void*>(mxfp4_gemm_kernel<128>), MxCfg<128>::kSmem);
+    for (int nt : {16, 32, 64, 128})
+        for (int act : {MOE_ACT_SWIGLU, MOE_ACT_RELU2, MOE_ACT_NONE})
+            for (int out : {kOutF32, kOutWide, kOutBf16}) {
+                size_t smem = 0;
+                const void* fn = reinterpret_cast<const void*>(mx_kernel(nt, act, out, &smem));
+                if (e == cudaSuccess)
+                    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+                if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+            }
     return e;
 }
 
@@ -605,8 +596,6 @@ cudaError_t launch_mxfp4_matmul(const void* xq, int64_t P, const void* wq, int64
     g.P = static_cast<int>(P);
     g.N = static_cast<int>(N);
     g.K = static_cast<int>(K);
-    g.act = act;
-    g.ot = ot;
     g.out = out;
     g.err = err;
     const cuuint64_t kb = static_cast<cuuint64_t>(K / 2), mat = static_cast<cuuint64_t>(g.w_mat);
@@ -625,10 +614,19 @@ cudaError_t launch_mxfp4_matmul(const void* xq, int64_t P, const void* wq, int64
     }
     if (e != cudaSuccess) return e;
     const int64_t avg = P / std::min(E, P);
-    if (avg <= 8) return mx_launch<16>(g, xq, num_sms, s);
-    if (avg <= 24) return mx_launch<32>(g, xq, num_sms, s);
-    if (avg <= 64) return mx_launch<64>(g, xq, num_sms, s);
-    return mx_launch<128>(g, xq, num_sms, s);
+    const int nt = avg <= 8 ? 16 : (avg <= 24 ? 32 : (avg <= 64 ? 64 : 128));
+    // boxes of x: the powers of two from 16 up to the tile, so that a short group does not load a tile
+    const cuuint64_t xd[2] = {kb, static_cast<cuuint64_t>(P)}, xst[1] = {kb};
+    for (int h = 16; h <= nt; h *= 2) {
+        const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(h)};
+        if ((e = mx_map(&g.tx[g.nbox++], 2, xq, xd, xst, box)) != cudaSuccess) return e;
+    }
+    const int64_t nout = act == MOE_ACT_SWIGLU ? N / 2 : N, mtiles = (N + kMxTileM - 1) / kMxTileM;
+    const int64_t bound = mtiles * (std::min(E, P) + P / nt);
+    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms, bound)));
+    size_t smem = 0;
+    const MxKernel kernel = mx_kernel(nt, act, ot == MOE_F32 ? kOutF32 : (nout % 8 == 0 ? kOutWide : kOutBf16), &smem);
+    return launch_pdl(kernel, dim3(grid), dim3(kMxThreads), smem, s, g);
 }
 
 }  // namespace moe
