@@ -44,31 +44,34 @@ constexpr int kMxStepK = 256;            // one 128-byte swizzle row of 4-bit co
 constexpr int kMxABytes = kMxTileM * 128;
 constexpr int kMxAhead = 3;              // own K steps that a group of scale warps reads ahead
 constexpr uint32_t kMxTmemCols = 512;
-constexpr uint32_t kMxSfCol = 256;       // scale columns behind the two accumulators, 16 a stage:
-                                         // weights panel 0, panel 1, rows of x panel 0, panel 1
 constexpr int kMxTransChunks = 3 * 31 + 2 * 3 + 2;   // 16-byte chunks of an epilogue warp's transposition
-constexpr int kMxMaxBoxes = 4;
+constexpr int kMxMaxBoxes = 5;
 constexpr long long kMxMaxItems = 1ll << 30;
 
 __device__ const uint32_t kMxOne = 0x7f7f7f7fu;   // scales of 2^0
 
-// Shared memory: the ring, and its depth, by the width of the row tile.
+// Shared memory and tensor memory by the width of the row tile.  Tensor memory: two accumulators of
+// kAccCols columns, then per stage 8 columns of the weights' scale words (panel 0, panel 1) and two times
+// kXCols of those of x.
 template <int NT>
 struct MxCfg {
-    static constexpr int kBBytes = NT * 128;
-    static constexpr int kStage = kMxABytes + kBBytes;
-    static constexpr int kStages = NT >= 128 ? 6 : (NT >= 32 ? 8 : 10);
+    static constexpr int kStage = kMxABytes + NT * 128;
+    static constexpr int kStages = NT > 128 ? 4 : (NT > 64 ? 6 : (NT >= 32 ? 8 : 10));
     static constexpr int kXWords = (NT + 31) / 32;   // columns of a panel's scales of x
+    static constexpr int kXCols = NT > 128 ? 8 : 4;
+    static constexpr uint32_t kAccCols = NT > 128 ? NT : 128;
+    static constexpr uint32_t kSfCol = 2 * kAccCols, kSfStage = 8 + 2 * kXCols;
+    static constexpr int kBoxes = NT > 128 ? 5 : (NT > 64 ? 4 : (NT > 32 ? 3 : (NT > 16 ? 2 : 1)));
     static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage;
     static_assert(kSmem + 32 * 1024 <= 227 * 1024, "ring fits beside the item table");
-    static_assert(kStages % 2 == 0, "the two groups of scale warps alternate");
-    static_assert(kMxSfCol + 16 * kStages <= kMxTmemCols, "scale columns of every stage");
+    static_assert(kSfCol + kSfStage * kStages <= kMxTmemCols, "scale columns of every stage");
 };
+// Rows of box i of x: 16, 32, 64, 128, 192.
+__host__ __device__ constexpr int mx_box(int i) { return i == 4 ? 192 : 16 << i; }
 
 struct MxArgs {
     CUtensorMap tw;                  // weights: {bytes, rows, matrix}, SwiGLU {bytes, 16, half, block, matrix}
-    CUtensorMap tx[kMxMaxBoxes];     // rows of x: {bytes, rows}, boxes of 16 << i rows
-    int nbox;
+    CUtensorMap tx[kMxMaxBoxes];     // rows of x: {bytes, rows}, boxes of mx_box(i) rows
     const uint8_t* xs;               // scale panels of x
     const uint8_t* ws;               // scale panels of the first weight matrix
     int64_t w_mat;                   // bytes between weight matrices
@@ -88,28 +91,42 @@ struct MxItem {
 };
 
 // The items in order: experts with rows (slots), then row tiles, then weight tiles.  Every role walks
-// them in increasing order, so a warp looks for an item's slot from the last one on, 32 slots at a time.
+// them in increasing order: the row tile and the weight tile advance by the quotient and the rest of the
+// stride (a division an item would be on the MMA warp's path), and a warp looks for the row tile's slot
+// from the last one on, 32 slots at a time.
 template <int NT>
 struct MxWalk {
-    const int* prefix;    // [slots + 1] first item of a slot
+    const int* prefix;    // [slots] first row tile of a slot
     const int2* rows;     // first row, last row + 1
+    const uint16_t* height;   // rows of a row tile, at most NT
     const uint16_t* expert;
     int n_slots, mtiles, lane;
-    int slot = 0;
-    __device__ MxItem at(int item) {   // the whole warp
+    int stride_t, stride_m;   // stride / mtiles, stride % mtiles
+    int tile, mtile;          // of the item that `at` describes
+    int slot;
+    __device__ MxWalk(const int* prefix_, const int2* rows_, const uint16_t* height_, const uint16_t* expert_, int n_slots_,
+                      int mtiles_, int lane_, int item, int stride)
+        : prefix(prefix_), rows(rows_), height(height_), expert(expert_), n_slots(n_slots_), mtiles(mtiles_), lane(lane_),
+          stride_t(stride / mtiles_), stride_m(stride % mtiles_), tile(item / mtiles_), mtile(item % mtiles_), slot(0) {}
+    __device__ void next() {
+        tile += stride_t;
+        mtile += stride_m;
+        if (mtile >= mtiles) mtile -= mtiles, ++tile;
+    }
+    __device__ MxItem at() {   // the whole warp
         for (;;) {
             const int i = slot + 1 + lane;
-            const int n = __popc(__ballot_sync(0xffffffffu, i < n_slots && prefix[i] <= item));
+            const int n = __popc(__ballot_sync(0xffffffffu, i < n_slots && prefix[i] <= tile));
             slot += n;
             if (n < 32) break;
         }
         const int2 r = rows[slot];
-        const int local = item - prefix[slot], ntile = local / mtiles;
         MxItem it;
         it.e = expert[slot];
-        it.mtile = local - ntile * mtiles;
-        it.r_first = r.x + ntile * NT;
-        it.nt = min(NT, r.y - it.r_first);
+        it.mtile = mtile;
+        const int h = height[slot];
+        it.r_first = r.x + (tile - prefix[slot]) * h;
+        it.nt = min(h, r.y - it.r_first);
         return it;
     }
 };
@@ -149,7 +166,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     __shared__ uint32_t tmem_base;
     __shared__ int prefix[kMaxE];
     __shared__ int2 rows[kMaxE];
-    __shared__ uint16_t expert[kMaxE];
+    __shared__ uint16_t height[kMaxE], expert[kMaxE];
     __shared__ long long warp_tiles[kMxWarps];
     __shared__ int warp_live[kMxWarps], n_slots, n_items;
     __shared__ uint4 trans[4][2][kMxTransChunks];
@@ -184,9 +201,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     pdl_wait();
     pdl_trigger();
     const int mtiles = (g.N + kMxTileM - 1) / kMxTileM;
-    {   // the slots and an exclusive prefix over them of (row tiles) x (weight tiles).  Offsets that
-        // overlap could count past 32 bits: the prefix is cut at kMxMaxItems, which increasing offsets
-        // stay far below
+    {   // the slots and an exclusive prefix over them of the row tiles.  Offsets that overlap could count
+        // past 32 bits: counts are cut at kMxMaxItems, which increasing offsets stay far below
         constexpr int kPer = kMaxE / kMxThreads;
         int first[kPer], last[kPer];
         long long tiles = 0;
@@ -220,7 +236,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             if (last[i] > first[i]) {
-                prefix[slot] = static_cast<int>(min(run * mtiles, kMxMaxItems));
+                prefix[slot] = static_cast<int>(min(run, kMxMaxItems));
+                // an expert's row tiles are equally high, up to the 16 that the MMA's N is a multiple of
+                const int n = last[i] - first[i], n_tiles = (n + NT - 1) / NT;
+                height[slot] = static_cast<uint16_t>(((n + n_tiles - 1) / n_tiles + 15) & ~15);
                 rows[slot] = make_int2(first[i], last[i]);
                 expert[slot] = static_cast<uint16_t>(tid * kPer + i);
                 ++slot;
@@ -238,7 +257,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     const uint32_t tmem = tmem_base;
     const int total = n_items;
     const int ksteps = (g.K + kMxStepK - 1) / kMxStepK;
-    MxWalk<NT> walk{prefix, rows, expert, n_slots, mtiles, lane};
+    constexpr uint32_t stages = Cfg::kStages;
+    MxWalk<NT> walk(prefix, rows, height, expert, n_slots, mtiles, lane, blockIdx.x, gridDim.x);
 
     if (warp == 0) {
         // -------------------------------------------------------------------- TMA producer
@@ -246,11 +266,11 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         const uint32_t ring0 = tc::s_addr(ring);
         uint32_t st = 0, use = 0;
         bool ok = true;
-        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-            const MxItem it = walk.at(item);
+        for (int item = blockIdx.x; item < total && ok; item += gridDim.x, walk.next()) {
+            const MxItem it = walk.at();
             int bi = 0;
-            while (bi + 1 < g.nbox && (16 << bi) < it.nt) ++bi;   // smallest box covering the rows
-            const uint32_t bytes = static_cast<uint32_t>(kMxABytes + (16 << bi) * 128);
+            while (bi + 1 < Cfg::kBoxes && mx_box(bi) < it.nt) ++bi;   // smallest box covering the rows
+            const uint32_t bytes = static_cast<uint32_t>(kMxABytes + mx_box(bi) * 128);
             for (int ks = 0; ks < ksteps; ++ks) {
                 if (use > 0 && !tc::mbar_wait_warp(&empty[st], use - 1, &s_fail)) {
                     ok = false;
@@ -263,51 +283,57 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                     else tc::tma_3d(dst, &g.tw, ks * 128, it.mtile * kMxTileM, it.e, &full[st]);
                     tc::tma_2d(dst + kMxABytes, &g.tx[bi], ks * 128, it.r_first, &full[st]);
                 }
-                if (++st == Cfg::kStages) st = 0, ++use;
+                if (++st == stages) st = 0, ++use;
             }
         }
         if (leader) {
-            issued = use * Cfg::kStages + st;
+            issued = use * stages + st;
             if (!ok) mx_fail(g, &s_fail);
         }
     } else if (warp == 1) {
         // -------------------------------------------------------------------- MMA issuer
         const bool leader = tc::elect_one();
-        const uint64_t da0 = tc::sdesc_k128(tc::s_addr(ring)), db0 = tc::sdesc_k128(tc::s_addr(ring + kMxABytes));
+        const uint64_t da0 = tc::sdesc_k128(tc::s_addr(ring));
+        const uint64_t db0 = tc::sdesc_k128(tc::s_addr(ring + kMxABytes));
         uint32_t st = 0, use = 0, n_item = 0;
         bool ok = true;
-        for (int item = blockIdx.x; item < total && ok; item += gridDim.x, ++n_item) {
-            const MxItem it = walk.at(item);
+        bool ready = false;   // the step's stage was already full when the step before was issued
+        for (int item = blockIdx.x; item < total && ok; item += gridDim.x, ++n_item, walk.next()) {
+            const MxItem it = walk.at();
             const uint32_t idesc = tc::idesc_mxf4((it.nt + 15) & ~15);
             const uint32_t buf = n_item & 1, ub = n_item >> 1;
             if (ub > 0 && !tc::mbar_wait_warp(&acc_empty[buf], ub - 1, &s_fail)) {
                 ok = false;
                 break;
             }
-            const uint32_t dt = tmem + buf * 128;
+            const uint32_t dt = tmem + buf * Cfg::kAccCols;
             for (int ks = 0; ks < ksteps; ++ks) {
-                if (!tc::mbar_wait_warp(&full[st], use, &s_fail)) {
+                if (!__all_sync(0xffffffffu, ready) && !tc::mbar_wait_warp(&full[st], use, &s_fail)) {
                     ok = false;
                     break;
                 }
+                const uint32_t st1 = st + 1 == stages ? 0 : st + 1, use1 = use + (st1 == 0);
+                ready = tc::mbar_test_wait(&full[st1], use1 & 1u);
                 tc::fence_after();
                 if (leader) {
                     // (the descriptors' start address, bytes / 16, is linear in the address)
-                    const uint64_t da = da0 + st * (Cfg::kStage >> 4), db = db0 + st * (Cfg::kStage >> 4);
-                    const uint32_t ta = tmem + kMxSfCol + st * 16, tb = ta + 8;
+                    const uint64_t da = da0 + st * (Cfg::kStage >> 4);
+                    const uint64_t db = db0 + st * (Cfg::kStage >> 4);
+                    const uint32_t ta = tmem + Cfg::kSfCol + st * Cfg::kSfStage, tb = ta + 8;
                     // (slices past K multiply zero codes by scales of 2^0)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)   // 32 bytes of codes; blocks 2 (kk % 2), + 1 of panel kk / 2
                         tc::umma_mxf4(dt, da + 2 * kk, db + 2 * kk, idesc | tc::idesc_sf((kk & 1) * 2),
-                                      ta + 4 * (kk >> 1), tb + 4 * (kk >> 1), ks > 0 || kk > 0);
+                                      ta + 4 * (kk >> 1), tb + Cfg::kXCols * (kk >> 1), ks > 0 || kk > 0);
                     tc::commit(&empty[st]);
                     if (ks + 1 == ksteps) tc::commit(&acc_full[buf]);
                 }
-                if (++st == Cfg::kStages) st = 0, ++use;
+                st = st1;
+                use = use1;
             }
         }
         if (leader) {
-            committed = use * Cfg::kStages + st;
+            committed = use * stages + st;
             if (!ok) mx_fail(g, &s_fail);
         }
     } else if (warp >= 8) {
@@ -327,7 +353,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         const uint8_t *wp[4], *xp[kXW];
         int ld_item = blockIdx.x, ld_ks = 0;
         auto point = [&](int ks) {   // the pointers at step ks of ld_item
-            const MxItem it = walk.at(ld_item);
+            const MxItem it = walk.at();
             const uint8_t* base = g.ws + it.e * g.w_mat + 2 * ks * w_pitch;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -351,6 +377,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             while (ld_ks >= ksteps && ld_item < total) {
                 ld_ks -= ksteps;
                 ld_item += gridDim.x;
+                walk.next();
             }
             if (ld_item < total) point(ld_ks);
         };
@@ -371,7 +398,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             }
             advance(2);
         };
-        const uint32_t t0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kMxSfCol;
+        const uint32_t t0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + Cfg::kSfCol;
         const int items = total > static_cast<int>(blockIdx.x) ? (total - 1 - blockIdx.x) / gridDim.x + 1 : 0;
         const int64_t steps = (static_cast<int64_t>(items) * ksteps - grp + 1) / 2;   // of this group
         uint32_t st = grp, use = 0;
@@ -391,18 +418,18 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                     break;
                 }
                 tc::fence_after();
-                const uint32_t t = t0 + st * 16;
+                const uint32_t t = t0 + st * Cfg::kSfStage;
                 tc::tmem_st4(t, buf[i].w[0]);
                 tc::tmem_st4(t + 4, buf[i].w[1]);
                 tc::tmem_st<kXW>(t + 8, buf[i].x[0]);
-                tc::tmem_st<kXW>(t + 12, buf[i].x[1]);
+                tc::tmem_st<kXW>(t + 8 + Cfg::kXCols, buf[i].x[1]);
                 read(buf[i]);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&full[st]);
                 st += 2;
-                if (st >= Cfg::kStages) st -= Cfg::kStages, ++use;
+                if (st >= stages) st -= stages, ++use;
             }
         }
         if (!ok && lane == 0) mx_fail(g, &s_fail);
@@ -424,15 +451,15 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         const int lrow = OUT == kOutWide ? lane >> 2 : (up ? 8 : 0);   // this lane's first row of 16
         uint32_t n_item = 0;
         bool ok = true;
-        for (int item = blockIdx.x; item < total; item += gridDim.x, ++n_item) {
-            const MxItem it = walk.at(item);
-            const int buf = n_item & 1;
+        for (int item = blockIdx.x; item < total; item += gridDim.x, ++n_item, walk.next()) {
+            const MxItem it = walk.at();
+            const uint32_t buf = n_item & 1;
             if (!tc::mbar_wait_warp(&acc_full[buf], n_item >> 1, &s_fail)) {
                 ok = false;
                 break;
             }
             tc::fence_after();
-            const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * 128);
+            const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * Cfg::kAccCols;
             const int col = it.mtile * (kSwiglu ? 64 : kMxTileM) + lcol;
             const bool in = col < nout;
             int left = it.nt - lrow;   // rows of the item from this lane's first on
@@ -504,10 +531,9 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     __syncthreads();
     if (s_fail) {
         if (tid == 0) {
-            for (uint32_t n = issued > Cfg::kStages ? issued - Cfg::kStages : 0; n < issued; ++n)
-                tc::mbar_wait(&full[n % Cfg::kStages], n / Cfg::kStages);
-            for (uint32_t n = committed > Cfg::kStages ? committed - Cfg::kStages : 0; n < committed; ++n)
-                tc::mbar_wait(&empty[n % Cfg::kStages], n / Cfg::kStages);
+            for (uint32_t n = issued > stages ? issued - stages : 0; n < issued; ++n) tc::mbar_wait(&full[n % stages], n / stages);
+            for (uint32_t n = committed > stages ? committed - stages : 0; n < committed; ++n)
+                tc::mbar_wait(&empty[n % stages], n / stages);
         }
         __syncthreads();
     }
@@ -553,17 +579,19 @@ MxKernel mx_kernel(int out) {
     return mxfp4_gemm_kernel<NT, ACT, ACT == MOE_ACT_SWIGLU ? kOutWide : kOutBf16>;
 }
 template <int NT>
-MxKernel mx_kernel(int act, int out) {
+MxKernel mx_kernel(int act, int out, size_t* smem) {
+    *smem = MxCfg<NT>::kSmem;
     if (act == MOE_ACT_SWIGLU) return mx_kernel<NT, MOE_ACT_SWIGLU>(out);
     if (act == MOE_ACT_RELU2) return mx_kernel<NT, MOE_ACT_RELU2>(out);
     return mx_kernel<NT, MOE_ACT_NONE>(out);
 }
 MxKernel mx_kernel(int nt, int act, int out, size_t* smem) {
     switch (nt) {
-        case 16: *smem = MxCfg<16>::kSmem; return mx_kernel<16>(act, out);
-        case 32: *smem = MxCfg<32>::kSmem; return mx_kernel<32>(act, out);
-        case 64: *smem = MxCfg<64>::kSmem; return mx_kernel<64>(act, out);
-        default: *smem = MxCfg<128>::kSmem; return mx_kernel<128>(act, out);
+        case 16: return mx_kernel<16>(act, out, smem);
+        case 32: return mx_kernel<32>(act, out, smem);
+        case 64: return mx_kernel<64>(act, out, smem);
+        case 128: return mx_kernel<128>(act, out, smem);
+        default: return mx_kernel<192>(act, out, smem);
     }
 }
 
@@ -571,7 +599,7 @@ MxKernel mx_kernel(int nt, int act, int out, size_t* smem) {
 
 cudaError_t configure_mxfp4_kernels() {
     cudaError_t e = mx_encoder();
-    for (int nt : {16, 32, 64, 128})
+    for (int nt : {16, 32, 64, 128, 192})
         for (int act : {MOE_ACT_SWIGLU, MOE_ACT_RELU2, MOE_ACT_NONE})
             for (int out : {kOutF32, kOutWide, kOutBf16}) {
                 size_t smem = 0;
@@ -614,12 +642,12 @@ cudaError_t launch_mxfp4_matmul(const void* xq, int64_t P, const void* wq, int64
     }
     if (e != cudaSuccess) return e;
     const int64_t avg = P / std::min(E, P);
-    const int nt = avg <= 8 ? 16 : (avg <= 24 ? 32 : (avg <= 64 ? 64 : 128));
+    const int nt = avg <= 8 ? 16 : (avg <= 24 ? 32 : (avg <= 64 ? 64 : (avg <= 128 ? 128 : 192)));
     // boxes of x: the powers of two from 16 up to the tile, so that a short group does not load a tile
     const cuuint64_t xd[2] = {kb, static_cast<cuuint64_t>(P)}, xst[1] = {kb};
-    for (int h = 16; h <= nt; h *= 2) {
-        const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(h)};
-        if ((e = mx_map(&g.tx[g.nbox++], 2, xq, xd, xst, box)) != cudaSuccess) return e;
+    for (int i = 0; i < kMxMaxBoxes && mx_box(i) <= nt; ++i) {
+        const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(mx_box(i))};
+        if ((e = mx_map(&g.tx[i], 2, xq, xd, xst, box)) != cudaSuccess) return e;
     }
     const int64_t nout = act == MOE_ACT_SWIGLU ? N / 2 : N, mtiles = (N + kMxTileM - 1) / kMxTileM;
     const int64_t bound = mtiles * (std::min(E, P) + P / nt);

@@ -46,6 +46,16 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// The same without the suspension that try_wait may take while the phase is not complete.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(s_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // Wait for completion number n (0-based) of a barrier's phases, for at most kWaitLimitNs.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t n) {
     const uint32_t parity = n & 1u;
@@ -127,7 +137,7 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
                  : "memory");
 }
 
-// Registers into 4 (1, 2) columns of the warp's 32 lanes of tensor memory.
+// Registers into 4 (1, 2, 6) columns of the warp's 32 lanes of tensor memory.
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                  "r"(v[3])
@@ -135,11 +145,12 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t* v) {
 }
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* v) {
-    static_assert(N == 1 || N == 2 || N == 4, "columns");
-    if constexpr (N == 4) tmem_st4(taddr, v);
-    else if constexpr (N == 2)
+    static_assert(N == 1 || N == 2 || N == 4 || N == 6, "columns");
+    if constexpr (N >= 4) tmem_st4(taddr, v);
+    if constexpr (N == 6) tmem_st<2>(taddr + 4, v + 4);
+    if constexpr (N == 2)
         asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(taddr), "r"(v[0]), "r"(v[1]) : "memory");
-    else asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v[0]) : "memory");
+    if constexpr (N == 1) asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v[0]) : "memory");
 }
 
 // 16 columns of the warp's 32 lanes of tensor memory; v holds them after tmem_ld_wait.
