@@ -13,8 +13,8 @@
 //              128-byte-swizzled tiles;
 //   warp 1     one thread issues the step's four K = 64 MMAs, operands in shared memory, scales in
 //              tensor memory;
-//   warps 4-7  epilogue: accumulators to registers, activation, stores.  Two accumulators alternate;
-//   warps 8-15 the scales, every other step by each group of four: a panel's 4-byte words (128 columns) of the weight rows and of the rows of x,
+//   warps 4-11 epilogue: accumulators to registers, activation, stores.  Two accumulators alternate;
+//   warps 12-19 the scales, every other step by each group of four: a panel's 4-byte words (128 columns) of the weight rows and of the rows of x,
 //              read some steps ahead into registers and written straight into the form that the MMA
 //              takes them from tensor memory in: row r's word in lane r % 32 of every quadrant of 32
 //              lanes, column r / 32 (a warp writes the quadrant warp % 4).  Rows of x start anywhere and
@@ -38,11 +38,12 @@
 
 namespace moe {
 
-constexpr int kMxThreads = 512, kMxWarps = kMxThreads / 32;
+constexpr int kMxThreads = 640, kMxWarps = kMxThreads / 32;
+constexpr int kMxEpi0 = 4, kMxSf0 = 12;   // first epilogue and first scale warp (the MMA warps' neighbours idle)
 constexpr int kMxTileM = 128;            // weight rows of an item (SwiGLU: 64 gate and 64 up rows)
 constexpr int kMxStepK = 256;            // one 128-byte swizzle row of 4-bit codes
 constexpr int kMxABytes = kMxTileM * 128;
-constexpr int kMxAhead = 3;              // own K steps that a group of scale warps reads ahead
+constexpr int kMxAhead = 2;              // own K steps that a group of scale warps reads ahead
 constexpr uint32_t kMxTmemCols = 512;
 constexpr int kMxTransChunks = 3 * 31 + 2 * 3 + 2;   // 16-byte chunks of an epilogue warp's transposition
 constexpr int kMxMaxBoxes = 5;
@@ -51,19 +52,18 @@ constexpr long long kMxMaxItems = 1ll << 30;
 __device__ const uint32_t kMxOne = 0x7f7f7f7fu;   // scales of 2^0
 
 // Shared memory and tensor memory by the width of the row tile.  Tensor memory: two accumulators of
-// kAccCols columns, then per stage 8 columns of the weights' scale words (panel 0, panel 1) and two times
+// NT columns, then per stage 8 columns of the weights' scale words (panel 0, panel 1) and two times
 // kXCols of those of x.
 template <int NT>
 struct MxCfg {
     static constexpr int kStage = kMxABytes + NT * 128;
-    static constexpr int kStages = NT > 128 ? 4 : (NT > 64 ? 6 : (NT >= 32 ? 8 : 10));
+    static constexpr int kStages = NT > 128 ? 4 : 6;
     static constexpr int kXWords = (NT + 31) / 32;   // columns of a panel's scales of x
     static constexpr int kXCols = NT > 128 ? 8 : 4;
-    static constexpr uint32_t kAccCols = NT > 128 ? NT : 128;
-    static constexpr uint32_t kSfCol = 2 * kAccCols, kSfStage = 8 + 2 * kXCols;
-    static constexpr int kBoxes = NT > 128 ? 5 : (NT > 64 ? 4 : (NT > 32 ? 3 : (NT > 16 ? 2 : 1)));
+    static constexpr uint32_t kSfCol = 2 * NT, kSfStage = 8 + 2 * kXCols;
+    static constexpr int kBoxes = NT > 128 ? 5 : 4;
     static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage;
-    static_assert(kSmem + 32 * 1024 <= 227 * 1024, "ring fits beside the item table");
+    static_assert(kSmem + 30 * 1024 <= 227 * 1024, "ring fits beside the item table");
     static_assert(kSfCol + kSfStage * kStages <= kMxTmemCols, "scale columns of every stage");
 };
 // Rows of box i of x: 16, 32, 64, 128, 192.
@@ -134,6 +134,11 @@ struct MxWalk {
 // Output forms: fp32; bf16 where 16 bytes of a row are aligned; other bf16.
 enum { kOutF32 = 0, kOutWide = 1, kOutBf16 = 2 };
 
+// SiLU by the fast exponential and division (2 units in the last place each; a divisor past fp32 gives 0,
+// as -88 and below should).  With the correctly rounded ones the SwiGLU epilogue of 128 x 128 results took
+// 10,000 cycles.
+__device__ __forceinline__ float mx_silu(float g) { return g * __fdividef(1.0f, 1.0f + __expf(-g)); }
+
 // The epilogue's transposition: column f's 16 values (32 bytes) start at this 16-byte chunk.  Both the
 // writes and the gathered reads of 8 lanes then meet 8 different chunks mod 8.
 __device__ __forceinline__ int mx_chunk(int f) { return 3 * f + 2 * (f >> 3); }
@@ -169,7 +174,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     __shared__ uint16_t height[kMaxE], expert[kMaxE];
     __shared__ long long warp_tiles[kMxWarps];
     __shared__ int warp_live[kMxWarps], n_slots, n_items;
-    __shared__ uint4 trans[4][2][kMxTransChunks];
+    __shared__ uint4 trans[8][kMxTransChunks];
     __shared__ volatile int s_fail;
     // the warp number through a shuffle, so that the compiler takes the roles' branches as uniform and
     // keeps descriptors and coordinates in uniform registers, where the tensor core and the copy engine
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         }
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&acc_full[s], 1);
-            tc::mbar_init(&acc_empty[s], 4);
+            tc::mbar_init(&acc_empty[s], 8);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_fail = 0;
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     const int mtiles = (g.N + kMxTileM - 1) / kMxTileM;
     {   // the slots and an exclusive prefix over them of the row tiles.  Offsets that overlap could count
         // past 32 bits: counts are cut at kMxMaxItems, which increasing offsets stay far below
-        constexpr int kPer = kMaxE / kMxThreads;
+        constexpr int kPer = (kMaxE + kMxThreads - 1) / kMxThreads;
         int first[kPer], last[kPer];
         long long tiles = 0;
         int live = 0;
@@ -224,8 +229,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         }
         if (lane == 31) warp_tiles[warp] = t_incl, warp_live[warp] = l_incl;
         __syncthreads();
-        long long t_before = lane < warp ? warp_tiles[lane & (kMxWarps - 1)] : 0;
-        int l_before = lane < warp ? warp_live[lane & (kMxWarps - 1)] : 0;
+        long long t_before = lane < warp ? warp_tiles[lane] : 0;
+        int l_before = lane < warp ? warp_live[lane] : 0;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) {
             t_before += __shfl_xor_sync(0xffffffffu, t_before, o);
@@ -306,7 +311,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                 ok = false;
                 break;
             }
-            const uint32_t dt = tmem + buf * Cfg::kAccCols;
+            const uint32_t dt = tmem + buf * NT;
             for (int ks = 0; ks < ksteps; ++ks) {
                 if (!__all_sync(0xffffffffu, ready) && !tc::mbar_wait_warp(&full[st], use, &s_fail)) {
                     ok = false;
@@ -336,7 +341,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             committed = use * stages + st;
             if (!ok) mx_fail(g, &s_fail);
         }
-    } else if (warp >= 8) {
+    } else if (warp >= kMxSf0) {
         // -------------------------------------------------------------------- scales
         // Group grp takes the steps whose number has parity grp, so that one group's waits overlap the
         // other's.  Words are read kMxAhead own steps before they are written.
@@ -344,7 +349,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         struct Words {
             uint32_t w[2][4], x[2][kXW];
         } buf[kMxAhead];
-        const int grp = (warp - 8) >> 2;
+        const int grp = (warp - kMxSf0) >> 2;
         const int f = g.N / 2, npan = static_cast<int>(mx_panels(g.K));
         const int64_t w_pitch = 4ll * g.N, x_pitch = 4ll * g.P;
         // This lane's words in the step's first panel.  Rows past the end read another row's word, and a
@@ -433,22 +438,22 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             }
         }
         if (!ok && lane == 0) mx_fail(g, &s_fail);
-    } else if (warp >= 4) {
+    } else if (warp >= kMxEpi0) {
         // -------------------------------------------------------------------- epilogue
         // (activation and output form are template parameters: the loop over 16 rows of x has to stay
         // short, as a warp that runs alone on its scheduler pays for every instruction it fetches)
-        const int q = warp & 3;                       // lane quadrant of tensor memory
+        const int q = warp & 3, half = (warp - kMxEpi0) >> 2;   // lane quadrant of tensor memory; which 16 rows of 32
         const int nout = kSwiglu ? g.N / 2 : g.N;
         const bool up = kSwiglu && lane >= 16;
         const int wcol = kSwiglu ? 16 * q : 32 * q;   // the warp's first column in the tile
         // kOutWide: where this lane writes, and reads back, the transposition, and the column it stores
-        const uint32_t tr = tc::s_addr(&trans[q][0][0]);
+        const uint32_t tr = tc::s_addr(&trans[warp - kMxEpi0][0]);
         const uint32_t tr_st = tr + 16 * (kSwiglu ? mx_chunk(lane & 15) + (up ? 1 : 0) : mx_chunk(lane));
         const int c8 = lane & 7, m4 = lane >> 3;
         const uint32_t tr_ld = tr + 16 * (kSwiglu ? mx_chunk(4 * (c8 >> 1) + 2 * (m4 & 1) + (c8 & 1)) + (m4 >> 1)
                                                   : mx_chunk(8 * (c8 >> 1) + 2 * m4 + (c8 & 1)));
         const int lcol = wcol + (OUT == kOutWide ? (kSwiglu ? 4 : 8) * (lane & 3) : (kSwiglu ? lane & 15 : lane));
-        const int lrow = OUT == kOutWide ? lane >> 2 : (up ? 8 : 0);   // this lane's first row of 16
+        const int lrow = 16 * half + (OUT == kOutWide ? lane >> 2 : (up ? 8 : 0));   // this lane's first row of the tile
         uint32_t n_item = 0;
         bool ok = true;
         for (int item = blockIdx.x; item < total; item += gridDim.x, ++n_item, walk.next()) {
@@ -459,30 +464,29 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                 break;
             }
             tc::fence_after();
-            const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * Cfg::kAccCols;
+            const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * NT;
             const int col = it.mtile * (kSwiglu ? 64 : kMxTileM) + lcol;
             const bool in = col < nout;
             int left = it.nt - lrow;   // rows of the item from this lane's first on
             char* o = static_cast<char*>(g.out) +
                       (static_cast<int64_t>(it.r_first + lrow) * nout + col) * (OUT == kOutF32 ? 4 : 2);
             const int64_t pitch = static_cast<int64_t>(nout) * (OUT == kOutF32 ? 4 : 2);
-            uint32_t flip = 0;
             float v[16];
-            tc::tmem_ld16(tb, v);
+            if (16 * half < it.nt) tc::tmem_ld16(tb + 16 * half, v);
 #pragma unroll 1
-            for (int c0 = 0; c0 < it.nt; c0 += 16) {   // 16 rows of x
+            for (int c0 = 16 * half; c0 < it.nt; c0 += 32) {   // 16 rows of x
                 float y[16];
                 tc::tmem_ld_wait(v);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) y[j] = v[j];
-                if (c0 + 16 < it.nt) tc::tmem_ld16(tb + c0 + 16, v);
+                if (c0 + 32 < it.nt) tc::tmem_ld16(tb + c0 + 32, v);
                 if (kSwiglu) {
                     // lanes 0-15 hold gate rows, 16-31 the same neurons' up rows: the low half takes
                     // the first 8 rows of x and the high half the others
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float other = __shfl_xor_sync(0xffffffffu, up ? y[j] : y[j + 8], 16);
-                        y[j] = up ? silu(other) * y[j + 8] : silu(y[j]) * other;
+                        y[j] = up ? mx_silu(other) * y[j + 8] : mx_silu(y[j]) * other;
                     }
                 } else if (ACT == MOE_ACT_RELU2) {
 #pragma unroll
@@ -492,14 +496,14 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                     // A lane has one column of the output and 16 rows of x, so that a store of a warp would
                     // be 64 bytes of one row (32 for SwiGLU).  The 16 rows go through shared memory, packed
                     // by rows, and come back transposed: lane 4 n + u has columns 8 u .. 8 u + 7 (4 u ..) of
-                    // rows n and n + 8.  Two buffers, so that one barrier orders a pass after the last.
-                    mx_store8(tr_st + flip, y);
-                    if (!kSwiglu) mx_store8(tr_st + 16 + flip, y + 8);
+                    // rows n and n + 8.
+                    __syncwarp();
+                    mx_store8(tr_st, y);
+                    if (!kSwiglu) mx_store8(tr_st + 16, y + 8);
                     __syncwarp();
                     uint32_t w[8];
-                    mx_ldsm4_t(w, tr_ld + flip);
-                    if (!kSwiglu) mx_ldsm4_t(w + 4, tr_ld + 16 + flip);
-                    flip ^= 16 * kMxTransChunks;
+                    mx_ldsm4_t(w, tr_ld);
+                    if (!kSwiglu) mx_ldsm4_t(w + 4, tr_ld + 16);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (!in || 8 * t >= left) continue;
@@ -515,8 +519,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                         else *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(y[j]);
                     }
                 }
-                o += 16 * pitch;
-                left -= 16;
+                o += 32 * pitch;
+                left -= 32;
             }
             tc::fence_before();
             __syncwarp();
@@ -586,20 +590,14 @@ MxKernel mx_kernel(int act, int out, size_t* smem) {
     return mx_kernel<NT, MOE_ACT_NONE>(out);
 }
 MxKernel mx_kernel(int nt, int act, int out, size_t* smem) {
-    switch (nt) {
-        case 16: return mx_kernel<16>(act, out, smem);
-        case 32: return mx_kernel<32>(act, out, smem);
-        case 64: return mx_kernel<64>(act, out, smem);
-        case 128: return mx_kernel<128>(act, out, smem);
-        default: return mx_kernel<192>(act, out, smem);
-    }
+    return nt == 128 ? mx_kernel<128>(act, out, smem) : mx_kernel<192>(act, out, smem);
 }
 
 }  // namespace
 
 cudaError_t configure_mxfp4_kernels() {
     cudaError_t e = mx_encoder();
-    for (int nt : {16, 32, 64, 128, 192})
+    for (int nt : {128, 192})
         for (int act : {MOE_ACT_SWIGLU, MOE_ACT_RELU2, MOE_ACT_NONE})
             for (int out : {kOutF32, kOutWide, kOutBf16}) {
                 size_t smem = 0;
@@ -642,7 +640,10 @@ cudaError_t launch_mxfp4_matmul(const void* xq, int64_t P, const void* wq, int64
     }
     if (e != cudaSuccess) return e;
     const int64_t avg = P / std::min(E, P);
-    const int nt = avg <= 8 ? 16 : (avg <= 24 ? 32 : (avg <= 64 ? 64 : (avg <= 128 ? 128 : 192)));
+    // Row tiles of 128, or of 192 from 160 rows an expert on, where the loads of weights and x from L2 bound
+    // the kernel: down (704 -> 2816) of 128 experts, us: 64 rows an expert 33.5 (192: 35.2), 128: 44.1
+    // (43.6), 256: 72.0 (66.7).  Tiles of 16, 32 and 64 rows are no faster at any number of rows.
+    const int nt = avg <= 160 ? 128 : 192;
     // boxes of x: the powers of two from 16 up to the tile, so that a short group does not load a tile
     const cuuint64_t xd[2] = {kb, static_cast<cuuint64_t>(P)}, xst[1] = {kb};
     for (int i = 0; i < kMxMaxBoxes && mx_box(i) <= nt; ++i) {
