@@ -49,7 +49,7 @@ size_t balance_workspace_bytes(int64_t, int64_t, int64_t);
 cudaError_t launch_balance_loss(const void*, int, const int32_t*, const uint8_t*, int64_t, int64_t, int64_t, int, float*,
                                 int32_t*, float*, int32_t*, void*, cudaStream_t);
 cudaError_t launch_balance_backward(const void*, int, const int32_t*, const int32_t*, const uint8_t*, const float*,
-                                    int64_t, int64_t, int64_t, int, void*, int, cudaStream_t);
+                                    int64_t, int64_t, int64_t, int, void*, cudaStream_t);
 
 namespace {
 
@@ -671,10 +671,8 @@ moe_status moe_balance_loss_backward(const void* logits, moe_dtype lt, const int
     if (!aligned16(logits) || !aligned16(counts) || !aligned16(tokens) || !aligned16(grad) ||
         (reinterpret_cast<uintptr_t>(grad_loss) & 3u))
         return MOE_ERR_ALIGNMENT;
-    int num_sms = 0;
-    if (ensure_configured(&num_sms) != cudaSuccess) return MOE_ERR_CUDA;
     return cuda_status(launch_balance_backward(logits, lt, counts, tokens, mask, grad_loss, n_seq, seq_len, E, k, grad,
-                                               num_sms, reinterpret_cast<cudaStream_t>(stream)));
+                                               reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_router_workspace_bytes(int64_t T, int64_t E) {

@@ -10,8 +10,16 @@
 // numbers.  As sum p = 1 a constant may be taken off f first: with f_e - 1/E, which is formed from
 // the integer counts, (E counts_e - k n_s) / (E k n_s), nothing cancels.
 //
-// No floating-point atomics: every chunk of a sequence's tokens writes its own partial sums, and
-// they are added in chunk order.
+// One wave of CTAs, each with an equal run of the batch's tokens, whatever the sequences' length (chunks of
+// one sequence left up to a third of the SMs idle in the last wave: 16 x 4096 x 512 fp32 forward 43 us).
+// No floating-point atomics: every part of a run that lies in one sequence writes a record of partial sums,
+// and the records of a sequence are added in order.
+//
+// Both directions read the logits once and are bound by that (backward also by writing the gradient).
+// A row is held by kLanes lanes, 4 consecutive experts at a time, so that loads are 16 (bf16: 8) bytes
+// a lane and a warp takes up to 16 rows of a small router at once.  The next row's logits and expert
+// indices are read before this row's softmax, and the mask of the row after it, so that no read waits for
+// another.
 #include <algorithm>
 
 #include "common.cuh"
@@ -20,124 +28,183 @@ namespace moe {
 
 constexpr int kBalThreads = 256, kBalWarps = kBalThreads / 32;
 
-__device__ __forceinline__ float bal_logit(const void* x, int lt, int64_t off) {
-    return lt == MOE_F32 ? __ldg(static_cast<const float*>(x) + off)
-                         : bf16_bits_to_f32(__ldg(static_cast<const uint16_t*>(x) + off));
-}
+// The runs: CTA b of n has tokens [start(b), start(b + 1)), multiples of 8 up to the end.  Run b's part of
+// sequence s is record b + s: both grow along the tokens, one at a time.  (T is at most 2^20 and n 608:
+// 32 bits hold the products.)
+struct BalRuns {
+    int T, n;
+    __host__ __device__ int start(int b) const {
+        const int t = (T + 7) / 8 * b / n * 8;
+        return t < T ? t : T;
+    }
+    // the last run that starts at or before token t < T
+    __device__ int run_of(int t) const {
+        int b = t / 8 * n / ((T + 7) / 8);   // start(b) <= t, and the answer is at most a step away
+        while (b + 1 < n && start(b + 1) <= t) ++b;
+        return b;
+    }
+};
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
+// How a warp holds rows of E logits.  Vector form (E a multiple of 4): element i of lane l of a group of
+// LANES is expert 4 (l + LANES (i / 4)) + i % 4.  Scalar form: expert l + 32 i.
+template <int LANES, int N, bool VEC>
+struct BalRow {
+    static constexpr int kLanes = LANES, kN = N, kGroups = 32 / LANES;
+    static_assert(VEC ? N % 4 == 0 : LANES == 32, "forms");
+    static __device__ __forceinline__ int expert(int l, int i) { return VEC ? 4 * (l + LANES * (i / 4)) + i % 4 : l + 32 * i; }
 
-// The softmax of one row by a warp: lane holds experts lane + 32 i.  A row of -inf has no
-// probability at all (p = 0); a NaN or +inf logit makes the row NaN.
-template <int NE>
-__device__ __forceinline__ void row_softmax(const void* logits, int lt, int64_t t, int E, int lane, float p[NE]) {
-    float m = -INFINITY;
+    // Logits of row t, -inf past E (E is a multiple of 4 in the vector form: a quad is in or out).
+    static __device__ __forceinline__ void load(const void* x, int lt, int64_t t, int E, int l, float v[N]) {
+        if (VEC) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        const int e = lane + 32 * i;
-        p[i] = e < E ? bal_logit(logits, lt, t * E + e) : -INFINITY;
-        m = fmaxf(m, p[i]);
-    }
-    m = warp_max(m);
-    if (m == -INFINITY) m = 0.0f;
-    float s = 0.0f;
+            for (int q = 0; q < N / 4; ++q) {
+                const int e = expert(l, 4 * q);
+                float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                if (e < E) {
+                    if (lt == MOE_F32) {
+                        f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(x) + t * E + e));
+                    } else {
+                        const uint2 b = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x) + t * E + e));
+                        f = make_float4(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
+                                        __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u));
+                    }
+                }
+                v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
+            }
+        } else {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        p[i] = expf(p[i] - m);
-        s += p[i];
-    }
-    s = warp_sum(s);
-    const float inv = s == 0.0f ? 0.0f : 1.0f / s;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) p[i] *= inv;
-}
-
-// One CTA per (sequence, chunk of tokens): part[s][chunk][E] sums of p, cnt[s][chunk][E + 1] counts
-// and, last, the chunk's counted tokens.
-template <int NE>
-__global__ void __launch_bounds__(kBalThreads) balance_partial_kernel(
-    const void* __restrict__ logits, int lt, const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask,
-    int64_t L, int chunks, int chunk_tokens, int E, int k, float* __restrict__ part, int32_t* __restrict__ cnt) {
-    pdl_wait();
-    pdl_trigger();
-    extern __shared__ float red[];                                  // [kBalWarps][E]
-    int32_t* hist = reinterpret_cast<int32_t*>(red + kBalWarps * E);   // [E + 1]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t s = blockIdx.x / chunks, c = blockIdx.x - s * chunks;
-    const int64_t t0 = s * L + c * chunk_tokens, t1 = s * L + min(L, (c + 1) * chunk_tokens);
-    for (int e = threadIdx.x; e <= E; e += kBalThreads) hist[e] = 0;
-    __syncthreads();
-    for (int64_t i = t0 * k + threadIdx.x; i < t1 * k; i += kBalThreads) {
-        const int e = __ldg(idx + i);
-        if (e >= 0 && e < E && (!mask || __ldg(mask + i / k))) atomicAdd(hist + e, 1);
-    }
-    float acc[NE];
-#pragma unroll
-    for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
-    int n = 0;
-    for (int64_t t = t0 + warp; t < t1; t += kBalWarps) {
-        if (mask && !__ldg(mask + t)) continue;
-        float p[NE];
-        row_softmax<NE>(logits, lt, t, E, lane, p);
-#pragma unroll
-        for (int i = 0; i < NE; ++i) acc[i] += p[i];
-        ++n;
-    }
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-        if (lane + 32 * i < E) red[warp * E + lane + 32 * i] = acc[i];
-    if (lane == 0) atomicAdd(hist + E, n);
-    __syncthreads();
-    float* po = part + static_cast<int64_t>(blockIdx.x) * E;
-    int32_t* co = cnt + static_cast<int64_t>(blockIdx.x) * (E + 1);
-    for (int e = threadIdx.x; e < E; e += kBalThreads) {
-        float v = 0.0f;
-        for (int w = 0; w < kBalWarps; ++w) v += red[w * E + e];
-        po[e] = v;
-    }
-    for (int e = threadIdx.x; e <= E; e += kBalThreads) co[e] = hist[e];
-}
-
-// One CTA per sequence: the chunks in order; counts, tokens, prob and the sequence's loss.
-__global__ void __launch_bounds__(kBalThreads) balance_sequence_kernel(const float* __restrict__ part,
-                                                                        const int32_t* __restrict__ cnt, int chunks,
-                                                                        int E, int k, int32_t* __restrict__ counts,
-                                                                        float* __restrict__ prob,
-                                                                        int32_t* __restrict__ tokens,
-                                                                        double* __restrict__ seq_loss) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t s = blockIdx.x;
-    __shared__ double red[kBalWarps];
-    int n = 0;
-    for (int c = 0; c < chunks; ++c) n += cnt[(s * chunks + c) * (E + 1) + E];
-    const double rn = n > 0 ? 1.0 / n : 0.0;
-    double dot = 0.0;
-    for (int e = threadIdx.x; e < E; e += kBalThreads) {
-        double p = 0.0;
-        int count = 0;
-        for (int c = 0; c < chunks; ++c) {
-            p += part[(s * chunks + c) * E + e];
-            count += cnt[(s * chunks + c) * (E + 1) + e];
+            for (int i = 0; i < N; ++i) v[i] = expert(l, i) < E ? load_x(x, lt, t * E + expert(l, i)) : -INFINITY;
         }
-        p *= rn;
-        counts[s * E + e] = count;
-        prob[s * E + e] = static_cast<float>(p);
-        dot += p * count;
     }
+    static __device__ __forceinline__ void store(void* g, int lt, int64_t t, int E, int l, const float v[N]) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double v = 0.0;
-        for (int w = 0; w < kBalWarps; ++w) v += red[w];
-        tokens[s] = n;
-        seq_loss[s] = v * rn * E / k;
+        for (int i = 0; i < N; i += VEC ? 4 : 1) {
+            const int e = expert(l, i);
+            if (e >= E) continue;
+            if (lt == MOE_F32) {
+                float* o = static_cast<float*>(g) + t * E + e;
+                if (VEC) *reinterpret_cast<float4*>(o) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                else *o = v[i];
+            } else {
+                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(g) + t * E + e;
+                if (VEC) {
+                    const __nv_bfloat162 a = __floats2bfloat162_rn(v[i], v[i + 1]), b = __floats2bfloat162_rn(v[i + 2], v[i + 3]);
+                    *reinterpret_cast<uint2*>(o) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+                } else {
+                    *o = __float2bfloat16_rn(v[i]);
+                }
+            }
+        }
+    }
+    // Over the group's lanes; every lane of the warp takes part.
+    static __device__ __forceinline__ float sum(float v) {
+#pragma unroll
+        for (int o = LANES / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+    // Logits -> probabilities, exp(x - m) by the hardware's 2^x (2 units in the last place; the largest
+    // logit's is exactly 1).  A row of -inf has no probability at all (p = 0); a NaN or +inf logit makes the
+    // row NaN.
+    static __device__ __forceinline__ void softmax(float v[N]) {
+        constexpr float kLog2e = 1.44269504f;
+        float m = v[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+#pragma unroll
+        for (int o = LANES / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (m == -INFINITY) m = 0.0f;
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"((v[i] - m) * kLog2e));
+            s += v[i];
+        }
+        s = sum(s);
+        const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] *= inv;
+    }
+};
+
+// CTAs that share an SM, by the registers that N logits of a lane take.
+constexpr int bal_ctas_forward(int n) { return n <= 8 ? 4 : (n <= 16 ? 3 : 1); }
+constexpr int bal_ctas_backward(int n) { return n <= 8 ? 4 : (n <= 16 ? 2 : 1); }
+
+// One CTA per run.  A record is part[E], the sums of p, and cnt[E + 1], the experts' counts and, last, the
+// counted tokens.
+template <typename Row>
+__global__ void __launch_bounds__(kBalThreads, bal_ctas_forward(Row::kN)) balance_partial_kernel(
+    const void* __restrict__ logits, int lt, const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask,
+    int L, BalRuns runs, int E, int k, float* __restrict__ part, int32_t* __restrict__ cnt,
+    uint32_t* __restrict__ done) {
+    pdl_wait();
+    pdl_trigger();
+    constexpr int N = Row::kN;
+    extern __shared__ float red[];                                     // [kBalWarps][E]
+    int32_t* hist = reinterpret_cast<int32_t*>(red + kBalWarps * E);   // [E + 1]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % Row::kLanes, grp = lane / Row::kLanes;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *done = 0;   // the next kernel's counter
+    constexpr int kStep = kBalWarps * Row::kGroups;
+    const int end = runs.start(blockIdx.x + 1);
+    for (int t0 = runs.start(blockIdx.x); t0 < end;) {   // the run's part of one sequence
+        const int s = t0 / L, t1 = min(end, (s + 1) * L);
+        for (int e = threadIdx.x; e <= E; e += kBalThreads) hist[e] = 0;
+        __syncthreads();
+        float acc[N], v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = v[i] = 0.0f;
+        int n = 0;
+        int t = t0 + warp * Row::kGroups + grp;
+        auto counted = [&](int u) -> bool { return u < t1 && (!mask || __ldg(mask + u)); };
+        int e_next = -1;   // this lane's first index of the next row
+        auto load = [&](int u) {
+            Row::load(logits, lt, u, E, l, v);
+            if (l < k) e_next = __ldg(idx + static_cast<int64_t>(u) * k + l);
+        };
+        bool live = counted(t), live2 = counted(t + kStep);
+        if (live) load(t);
+        for (int tw = t0 + warp * Row::kGroups; tw < t1; tw += kStep, t += kStep) {
+            const bool now = live;
+            const int e = e_next;
+            float p[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) p[i] = v[i];
+            live = live2;
+            live2 = counted(t + 2 * kStep);
+            if (live) load(t + kStep);
+            if (now) {
+                if (e >= 0 && e < E) atomicAdd(hist + e, 1);   // (-1 on lanes without an index)
+                for (int j = l + Row::kLanes; j < k; j += Row::kLanes) {
+                    const int e2 = __ldg(idx + static_cast<int64_t>(t) * k + j);
+                    if (e2 >= 0 && e2 < E) atomicAdd(hist + e2, 1);
+                }
+                n += l == 0;
+            }
+            Row::softmax(p);
+            if (now) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc[i] += p[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int o = Row::kLanes; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+            if (grp == 0 && Row::expert(l, i) < E) red[warp * E + Row::expert(l, i)] = acc[i];
+        }
+        if (n) atomicAdd(hist + E, n);
+        __syncthreads();
+        const int64_t rec = static_cast<int64_t>(blockIdx.x) + s;
+        for (int e = threadIdx.x; e < E; e += kBalThreads) {
+            float a = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kBalWarps; ++w) a += red[w * E + e];
+            part[rec * E + e] = a;
+        }
+        for (int e = threadIdx.x; e <= E; e += kBalThreads) cnt[rec * (E + 1) + e] = hist[e];
+        __syncthreads();
+        t0 = t1;
     }
 }
 
@@ -150,157 +217,210 @@ __device__ __forceinline__ T block_sum(T v, T* red) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     T t = 0;
+#pragma unroll
     for (int w = 0; w < kBalWarps; ++w) t += red[w];
     return t;
 }
 
-__global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const double* __restrict__ seq_loss,
-                                                                    const int32_t* __restrict__ tokens, int64_t S,
-                                                                    float* __restrict__ loss) {
+// One CTA per (sequence, 32 experts): warp w adds the sequence's records w, w + 8, ..; counts, tokens, prob and the
+// block's part of the sequence's loss.  The last CTA adds those up, in order.
+__global__ void __launch_bounds__(kBalThreads) balance_sequence_kernel(
+    const float* __restrict__ part, const int32_t* __restrict__ cnt, int S, int L, BalRuns runs, int E, int k,
+    int32_t* __restrict__ counts, float* __restrict__ prob, int32_t* tokens, float* seq_loss, uint32_t* done,
+    float* __restrict__ loss) {
     pdl_wait();
     pdl_trigger();
-    __shared__ double rd[kBalWarps];
-    __shared__ int ri[kBalWarps];
-    double v = 0.0;
-    int live = 0;
-    for (int64_t s = threadIdx.x; s < S; s += kBalThreads) {
-        if (tokens[s] > 0) {   // a sequence without a counted token is not part of the mean
-            v += seq_loss[s];
-            ++live;
+    __shared__ float sp[kBalWarps][32], rd[kBalWarps];
+    __shared__ int sc[kBalWarps][33], ri[kBalWarps];
+    __shared__ bool last;
+    const int blocks = (E + 31) / 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t s = blockIdx.x / blocks;
+    const int e = (blockIdx.x % blocks) * 32 + lane;
+    const int b0 = runs.run_of(static_cast<int>(s) * L);
+    const int chunks = runs.run_of(static_cast<int>(s + 1) * L - 1) - b0 + 1;
+    const float* ps = part + (b0 + s) * E + e;
+    const int32_t* cs = cnt + (b0 + s) * (E + 1);
+    float p = 0.0f;
+    int count = 0, n = 0;
+#pragma unroll 4
+    for (int c = warp; c < chunks; c += kBalWarps) {
+        if (e < E) {
+            p += __ldcg(ps + static_cast<int64_t>(c) * E);
+            count += __ldcg(cs + static_cast<int64_t>(c) * (E + 1) + e);
+        }
+        n += lane == 0 ? __ldcg(cs + static_cast<int64_t>(c) * (E + 1) + E) : 0;
+    }
+    sp[warp][lane] = p;
+    sc[warp][lane] = count;
+    if (lane == 0) sc[warp][32] = n;
+    __syncthreads();
+    if (warp == 0) {
+        p = 0.0f, count = n = 0;
+#pragma unroll
+        for (int w = 0; w < kBalWarps; ++w) p += sp[w][lane], count += sc[w][lane], n += sc[w][32];
+        const float rn = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
+        p *= rn;
+        float dot = e < E ? p * (static_cast<float>(count) * rn) : 0.0f;
+        if (e < E) {
+            counts[s * E + e] = count;
+            prob[s * E + e] = p;
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) {
+            if (e < 32) tokens[s] = n;
+            seq_loss[blockIdx.x] = dot * (static_cast<float>(E) / static_cast<float>(k));
+            __threadfence();
+            last = atomicAdd(done, 1u) == gridDim.x - 1;
         }
     }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    float v = 0.0f;
+    int live = 0;
+    for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += kBalThreads) v += __ldcg(seq_loss + i);   // 0 where n_s = 0
+    for (int i = threadIdx.x; i < S; i += kBalThreads) live += __ldcg(tokens + i) > 0;
     v = block_sum(v, rd);
     live = block_sum(live, ri);
-    if (threadIdx.x == 0) *loss = live > 0 ? static_cast<float>(v / live) : 0.0f;
+    if (threadIdx.x == 0) *loss = live > 0 ? v / static_cast<float>(live) : 0.0f;
 }
 
-// A persistent grid over (sequence, chunk): the chunk's f_e - 1/E times E / (S' n_s) times the
-// incoming gradient in shared memory, then one warp per token.
-template <int NE>
-__global__ void __launch_bounds__(kBalThreads) balance_backward_kernel(
+// One CTA per run: per sequence f_e - 1/E times E / (S' n_s) times the incoming gradient in registers, then
+// the rows.
+template <typename Row>
+__global__ void __launch_bounds__(kBalThreads, bal_ctas_backward(Row::kN)) balance_backward_kernel(
     const void* __restrict__ logits, int lt, const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens,
-    const uint8_t* __restrict__ mask, const float* __restrict__ grad_loss, int64_t S, int64_t L, int chunks,
-    int chunk_tokens, int E, int k, void* __restrict__ grad) {
+    const uint8_t* __restrict__ mask, const float* __restrict__ grad_loss, int S, int L, BalRuns runs, int E,
+    int k, void* __restrict__ grad) {
     pdl_wait();
     pdl_trigger();
-    extern __shared__ float sf[];   // [E]
+    constexpr int N = Row::kN;
     __shared__ int ri[kBalWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int live = 0;
-    for (int64_t s = threadIdx.x; s < S; s += kBalThreads) live += tokens[s] > 0;
-    live = block_sum(live, ri);
-    const double g = __ldg(grad_loss);
-    for (int64_t b = blockIdx.x; b < S * chunks; b += gridDim.x) {
-        const int64_t s = b / chunks, c = b - s * chunks;
-        const int n = tokens[s];
-        __syncthreads();
-        for (int e = threadIdx.x; e < E; e += kBalThreads) {
-            // (E counts - k n) / (E k n) * g E / (S' n)
-            const int64_t num = static_cast<int64_t>(E) * counts[s * E + e] - static_cast<int64_t>(k) * n;
-            sf[e] = n > 0 ? static_cast<float>(g * static_cast<double>(num) /
-                                               (static_cast<double>(k) * n * (static_cast<double>(live) * n)))
-                          : 0.0f;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % Row::kLanes, grp = lane / Row::kLanes;
+    const float g = __ldg(grad_loss);
+    constexpr int kStep = kBalWarps * Row::kGroups;
+    const int64_t end = runs.start(blockIdx.x + 1);
+    int live_seq = -1;
+    for (int64_t t0 = runs.start(blockIdx.x); t0 < end;) {   // the run's part of one sequence
+        const int64_t s = t0 / L, t1 = min(end, (s + 1) * L);
+        float v[N], f[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = 0.0f;
+        int t = t0 + warp * Row::kGroups + grp;
+        auto counted = [&](int u) -> bool { return u < t1 && (!mask || __ldg(mask + u)); };
+        bool live = counted(t), live2 = counted(t + kStep);
+        if (live) Row::load(logits, lt, t, E, l, v);
+        if (live_seq < 0) {   // (behind the first row's loads)
+            int c = 0;
+            for (int i = threadIdx.x; i < S; i += kBalThreads) c += __ldg(tokens + i) > 0;
+            live_seq = block_sum(c, ri);
         }
-        __syncthreads();
-        float f[NE];
+        // (E counts - k n) / (E k n) * g E / (S' n), the difference in integers
+        const int n = __ldg(tokens + s);
+        const int64_t kn = static_cast<int64_t>(k) * n;
+        const float scale =
+            n > 0 ? g / (static_cast<float>(kn) * (static_cast<float>(live_seq) * static_cast<float>(n))) : 0.0f;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) f[i] = lane + 32 * i < E ? sf[lane + 32 * i] : 0.0f;
-        const int64_t t0 = s * L + c * chunk_tokens, t1 = s * L + min(L, (c + 1) * chunk_tokens);
-        for (int64_t t = t0 + warp; t < t1; t += kBalWarps) {
-            float p[NE];
-            if (mask && !__ldg(mask + t)) {
-#pragma unroll
-                for (int i = 0; i < NE; ++i) p[i] = 0.0f;
-            } else {
-                row_softmax<NE>(logits, lt, t, E, lane, p);
-                float dot = 0.0f;
-#pragma unroll
-                for (int i = 0; i < NE; ++i) dot += p[i] * f[i];
-                dot = warp_sum(dot);
-#pragma unroll
-                for (int i = 0; i < NE; ++i) p[i] *= f[i] - dot;
-            }
-#pragma unroll
-            for (int i = 0; i < NE; ++i) {
-                const int e = lane + 32 * i;
-                if (e >= E) continue;
-                if (lt == MOE_F32) static_cast<float*>(grad)[t * E + e] = p[i];
-                else static_cast<__nv_bfloat16*>(grad)[t * E + e] = __float2bfloat16_rn(p[i]);
-            }
+        for (int i = 0; i < N; ++i) {
+            const int e = Row::expert(l, i);
+            f[i] = e < E ? scale * static_cast<float>(static_cast<int64_t>(E) * __ldg(counts + static_cast<int64_t>(s) * E + e) - kn) : 0.0f;
         }
+        for (int tw = t0 + warp * Row::kGroups; tw < t1; tw += kStep, t += kStep) {
+            const bool now = live;
+            float p[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) p[i] = v[i];
+            live = live2;
+            live2 = counted(t + 2 * kStep);
+            if (live) Row::load(logits, lt, t + kStep, E, l, v);
+            Row::softmax(p);
+            float dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) dot += p[i] * f[i];
+            dot = Row::sum(dot);
+#pragma unroll
+            for (int i = 0; i < N; ++i) p[i] = now ? p[i] * (f[i] - dot) : 0.0f;
+            if (t < t1) Row::store(grad, lt, t, E, l, p);
+        }
+        t0 = t1;
     }
 }
 
 // ------------------------------------------------------------------------------- launchers
 namespace {
 
-struct BalPlan {
-    int chunk_tokens, chunks;
-};
+constexpr int64_t kBalSms = 152;   // the runs depend on the shapes alone, and so does the workspace
 
-// Chunks of whole warps' tokens, about 600 of them (4 CTAs per SM), none across two sequences.
-BalPlan bal_plan(int64_t S, int64_t L) {
-    int64_t per = (S * L + 607) / 608;
-    per = std::max<int64_t>(kBalWarps, (per + kBalWarps - 1) / kBalWarps * kBalWarps);
-    per = std::min<int64_t>(per, (L + kBalWarps - 1) / kBalWarps * kBalWarps);
-    return {static_cast<int>(per), static_cast<int>((L + per - 1) / per)};
+BalRuns bal_runs(int64_t T, int ctas_per_sm) {
+    return {static_cast<int>(T), static_cast<int>(std::min<int64_t>((T + 15) / 16, kBalSms * ctas_per_sm))};
 }
 
 template <typename F>
-cudaError_t with_ne(int64_t E, F f) {
-    if (E <= 32) return f(std::integral_constant<int, 1>{});
-    if (E <= 64) return f(std::integral_constant<int, 2>{});
-    if (E <= 128) return f(std::integral_constant<int, 4>{});
-    if (E <= 256) return f(std::integral_constant<int, 8>{});
-    if (E <= 512) return f(std::integral_constant<int, 16>{});
-    return f(std::integral_constant<int, 32>{});
+cudaError_t with_row(int64_t E, F f) {
+    if (E % 4 == 0) {
+        if (E <= 8) return f(BalRow<2, 4, true>{});
+        if (E <= 16) return f(BalRow<4, 4, true>{});
+        if (E <= 32) return f(BalRow<8, 4, true>{});
+        if (E <= 64) return f(BalRow<16, 4, true>{});
+        if (E <= 128) return f(BalRow<32, 4, true>{});
+        if (E <= 256) return f(BalRow<32, 8, true>{});
+        if (E <= 512) return f(BalRow<32, 16, true>{});
+        return f(BalRow<32, 32, true>{});
+    }
+    if (E <= 64) return f(BalRow<32, 2, false>{});
+    if (E <= 128) return f(BalRow<32, 4, false>{});
+    if (E <= 256) return f(BalRow<32, 8, false>{});
+    if (E <= 512) return f(BalRow<32, 16, false>{});
+    return f(BalRow<32, 32, false>{});
 }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+int64_t expert_blocks(int64_t E) { return (E + 31) / 32; }
 
 }  // namespace
 
 size_t balance_workspace_bytes(int64_t S, int64_t L, int64_t E) {
-    const int64_t n = S * bal_plan(S, L).chunks;
-    return align256(sizeof(float) * n * E) + align256(sizeof(int32_t) * n * (E + 1)) + align256(sizeof(double) * S);
+    const int64_t n = bal_runs(S * L, 4).n + S;   // records, at most
+    return 256 + align256(sizeof(float) * n * E) + align256(sizeof(int32_t) * n * (E + 1)) +
+           align256(sizeof(float) * S * expert_blocks(E));
 }
 
 cudaError_t launch_balance_loss(const void* logits, int lt, const int32_t* idx, const uint8_t* mask, int64_t S,
                                 int64_t L, int64_t E, int k, float* loss, int32_t* counts, float* prob, int32_t* tokens,
                                 void* workspace, cudaStream_t st) {
-    const BalPlan p = bal_plan(S, L);
-    const int64_t n = S * p.chunks;
+    const int64_t n = bal_runs(S * L, 4).n + S;
     char* w = static_cast<char*>(workspace);
+    uint32_t* done = reinterpret_cast<uint32_t*>(w);
+    w += 256;
     float* part = reinterpret_cast<float*>(w);
     w += align256(sizeof(float) * n * E);
     int32_t* cnt = reinterpret_cast<int32_t*>(w);
     w += align256(sizeof(int32_t) * n * (E + 1));
-    double* seq_loss = reinterpret_cast<double*>(w);
+    float* seq_loss = reinterpret_cast<float*>(w);
     const int e32 = static_cast<int>(E);
-    cudaError_t e = with_ne(E, [&](auto ne) {
-        return launch_pdl(balance_partial_kernel<decltype(ne)::value>, dim3(static_cast<unsigned>(n)), dim3(kBalThreads),
-                          sizeof(float) * kBalWarps * E + sizeof(int32_t) * (E + 1), st, logits, lt, idx, mask, L,
-                          p.chunks, p.chunk_tokens, e32, k, part, cnt);
+    BalRuns runs{};
+    cudaError_t e = with_row(E, [&](auto row) {
+        runs = bal_runs(S * L, bal_ctas_forward(decltype(row)::kN));
+        return launch_pdl(balance_partial_kernel<decltype(row)>, dim3(static_cast<unsigned>(runs.n)), dim3(kBalThreads),
+                          sizeof(float) * kBalWarps * E + sizeof(int32_t) * (E + 1), st, logits, lt, idx, mask,
+                          static_cast<int>(L), runs, e32, k, part, cnt, done);
     });
-    if (e == cudaSuccess)
-        e = launch_pdl(balance_sequence_kernel, dim3(static_cast<unsigned>(S)), dim3(kBalThreads), 0, st,
-                       static_cast<const float*>(part), static_cast<const int32_t*>(cnt), p.chunks, e32, k, counts, prob,
-                       tokens, seq_loss);
-    if (e == cudaSuccess)
-        e = launch_pdl(balance_loss_kernel, dim3(1), dim3(kBalThreads), 0, st, static_cast<const double*>(seq_loss),
-                       static_cast<const int32_t*>(tokens), S, loss);
-    return e;
+    if (e != cudaSuccess) return e;
+    return launch_pdl(balance_sequence_kernel, dim3(static_cast<unsigned>(S * expert_blocks(E))), dim3(kBalThreads), 0, st,
+                      static_cast<const float*>(part), static_cast<const int32_t*>(cnt), static_cast<int>(S),
+                      static_cast<int>(L), runs, e32, k, counts, prob,
+                      tokens, seq_loss, done, loss);
 }
 
 cudaError_t launch_balance_backward(const void* logits, int lt, const int32_t* counts, const int32_t* tokens,
                                     const uint8_t* mask, const float* grad_loss, int64_t S, int64_t L, int64_t E, int k,
-                                    void* grad, int num_sms, cudaStream_t st) {
-    const BalPlan p = bal_plan(S, L);
-    const int64_t n = std::min<int64_t>(S * p.chunks, 4ll * num_sms);
-    return with_ne(E, [&](auto ne) {
-        return launch_pdl(balance_backward_kernel<decltype(ne)::value>, dim3(static_cast<unsigned>(n)),
-                          dim3(kBalThreads), sizeof(float) * E, st, logits, lt, counts, tokens, mask, grad_loss, S, L,
-                          p.chunks, p.chunk_tokens, static_cast<int>(E), k, grad);
+                                    void* grad, cudaStream_t st) {
+    return with_row(E, [&](auto row) {
+        const BalRuns runs = bal_runs(S * L, bal_ctas_backward(decltype(row)::kN));
+        return launch_pdl(balance_backward_kernel<decltype(row)>, dim3(static_cast<unsigned>(runs.n)), dim3(kBalThreads), 0,
+                          st, logits, lt, counts, tokens, mask, grad_loss, static_cast<int>(S), static_cast<int>(L), runs,
+                          static_cast<int>(E), k, grad);
     });
 }
 

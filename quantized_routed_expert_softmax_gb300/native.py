@@ -120,8 +120,10 @@ def _ptr(t) -> int | None:
 
 def _stream(stream=None) -> int:
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle alone: building a torch.cuda.Stream around it takes longer than a small kernel
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def q8_0_bytes(rows: int, cols: int) -> int:
