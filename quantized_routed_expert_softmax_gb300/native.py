@@ -192,6 +192,11 @@ def mxfp4_bytes(rows: int, cols: int) -> int:
     return int(lib().moe_mxfp4_bytes(rows, cols))
 
 
+def _mxfp4_size(rows: int, cols: int) -> int:
+    """mxfp4_bytes for the operand checks (the C call takes longer than the sum; it refuses bad sizes)."""
+    return (rows * cols // 2 + 4 * rows * ((cols + 127) // 128) + 15) // 16 * 16
+
+
 def _operand(name: str, t, dtype, numel: int | None = None) -> int | None:
     """The pointer of an operand, checked: contiguous device memory of the type and size that the
     entry point reads or writes (the C side sees only a pointer)."""
@@ -213,19 +218,20 @@ def quantize_mxfp4(x, rows=None, out=None, stream=None):
     outside x gives a row of zeros)."""
     import torch
     xt = _x_dtype(x)
-    x_rows, cols = x.shape[-2], x.shape[-1]
-    n_rows = x_rows if rows is None else rows.numel()
-    n = x.numel() // max(1, x_rows * cols)
-    if rows is not None and x.dim() != 2:
-        raise ValueError("rows needs one matrix x [rows, cols]")
+    x_rows, cols = x.shape[-2:]
+    n, n_rows = 1, x_rows
     if rows is not None:
-        n = 1
-    per = mxfp4_bytes(max(1, n_rows), cols)
+        if x.dim() != 2:
+            raise ValueError("rows needs one matrix x [rows, cols]")
+        n_rows = rows.numel()
+    elif x.dim() != 2:
+        n = x.numel() // max(1, x_rows * cols)
+    per = _mxfp4_size(n_rows, cols)
     if out is None:
-        out = torch.empty((n, per if n_rows else 0), dtype=torch.uint8, device=x.device)
+        out = torch.empty((n, per), dtype=torch.uint8, device=x.device)
     _check("moe_quantize_mxfp4", lib().moe_quantize_mxfp4(
         _operand("x", x, x.dtype), xt, x_rows, _operand("rows", rows, torch.int32), n, n_rows, cols,
-        _operand("out", out, torch.uint8, n * per if n_rows else 0), _stream(stream)))
+        _operand("out", out, torch.uint8, n * per), _stream(stream)))
     return out
 
 
@@ -234,11 +240,11 @@ def dequantize_mxfp4(q, rows: int, cols: int, dtype=None, out=None, stream=None)
     dtype float32 (the default) or bfloat16."""
     import torch
     n = q.shape[0] if q.dim() == 2 else 1
-    shape = (n, rows, cols) if q.dim() == 2 else (rows, cols)
     if out is None:
+        shape = (n, rows, cols) if q.dim() == 2 else (rows, cols)
         out = torch.empty(shape, dtype=dtype or torch.float32, device=q.device)
     _check("moe_dequantize_mxfp4", lib().moe_dequantize_mxfp4(
-        _operand("q", q, torch.uint8, n * mxfp4_bytes(rows, cols)), n, rows, cols,
+        _operand("q", q, torch.uint8, n * _mxfp4_size(rows, cols)), n, rows, cols,
         _operand("out", out, out.dtype, n * rows * cols), _x_dtype(out), _stream(stream)))
     return out
 
@@ -262,8 +268,8 @@ def mxfp4_matmul(xq, wq, offsets, rows: int, n: int, cols: int, act: str = "none
     if workspace is None:
         workspace = mxfp4_workspace(xq.device)
     _check("moe_mxfp4_matmul", lib().moe_mxfp4_matmul(
-        _operand("xq", xq, torch.uint8, mxfp4_bytes(rows, cols)), rows,
-        _operand("wq", wq, torch.uint8, E * mxfp4_bytes(n, cols)), E, n, cols,
+        _operand("xq", xq, torch.uint8, _mxfp4_size(rows, cols)), rows,
+        _operand("wq", wq, torch.uint8, E * _mxfp4_size(n, cols)), E, n, cols,
         _operand("offsets", offsets, torch.int32, E + 1), MATMUL_ACT[act],
         _operand("out", out, out.dtype, rows * width), _x_dtype(out),
         _operand("workspace", workspace, torch.uint8), workspace.numel(), _stream(stream)))
