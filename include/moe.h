@@ -61,7 +61,11 @@ typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_RELU2 = 1, MOE_ACT_NONE = 2 } moe_act
 /* Expert weight formats.  INT8PC: per-channel int8 (the Inferentia page, "Squeezing a 26B MoE
  * onto the cheapest Inferentia instance", section "Wall 1: the memory math": experts in int8
  * with one scale per output channel): per row s = amax/127 (fp32), q = round-half-away(x / s). */
-typedef enum { MOE_W_Q8_0 = 0, MOE_W_NVFP4 = 1, MOE_W_INT8PC = 2 } moe_wfmt;
+/* MXFP4: E2M1 codes with an E8M0 scale per 32 (see moe_mxfp4_bytes), both operands of the experts'
+ * products: such a layer codes its experts' inputs too (x for gate.up, h for down, by
+ * moe_quantize_mxfp4), runs moe_mxfp4_matmul's kernels at every T, and needs path AUTO, act_quant
+ * NONE and weights in device memory (else MOE_ERR_UNSUPPORTED).  (3 is no format.) */
+typedef enum { MOE_W_Q8_0 = 0, MOE_W_NVFP4 = 1, MOE_W_INT8PC = 2, MOE_W_MXFP4 = 4 } moe_wfmt;
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
 
 /*
@@ -309,7 +313,8 @@ typedef struct {
     const float* router_w;        /* fp32 [d][E] */
     const void* w_gate_up;        /* E matrices [rows_gu][d], MOE_LAYOUT_DEVICE, back to back;
                                      SwiGLU: rows 0..f-1 gate, f..2f-1 up */
-    const void* w_down;           /* E matrices [d][f]: Q8_0 / INT8PC MOE_LAYOUT_DEVICE, NVFP4 MOE_LAYOUT_NEURON */
+    const void* w_down;           /* E matrices [d][f]: Q8_0 / INT8PC MOE_LAYOUT_DEVICE, NVFP4 MOE_LAYOUT_NEURON
+                                     (MXFP4: both stacks as moe_quantize_mxfp4 writes them) */
     const float* gate_up_tscale;  /* NVFP4: fp32 [E] tensor scales of the gate/up matrices */
     const float* down_tscale;     /* NVFP4: fp32 [E] tensor scales of the down matrices */
     const void* l2_prefetch;      /* optional, may be NULL: device bytes to pull into L2 while this
@@ -350,7 +355,7 @@ typedef struct {
     int32_t* perm;     /* [T*k]: pair id (t*k+j) at each sorted row */
     int32_t* pos;      /* [T*k]: sorted row of each pair */
     float* h;          /* [T*k][f] activations in sorted-row order (MOE_ACTQ_Q8_0: the coded values
-                          the down projection read) */
+                          the down projection read; MXFP4: before the coding) */
     void* stage_events[5];
 } moe_trace;
 
@@ -378,7 +383,7 @@ size_t moe_layer_workspace_bytes(const moe_layer_desc* desc, int64_t T_max);
  *            words zero again after every call).
  * trace      optional copies of intermediates, or NULL.
  * T = 0 returns MOE_OK, launches nothing and touches no buffer (they may be NULL).
- * Errors: INVALID_ARG, SHAPE (d a multiple of 256 up to 65536; f a multiple of 32 (Q8_0) or
+ * Errors: INVALID_ARG, SHAPE (d a multiple of 256 up to 65536; f a multiple of 32 (Q8_0, MXFP4) or
  * 64 (NVFP4) up to 32768; E a multiple of 4 up to 1024), ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA.
  */
 moe_status moe_layer_forward(const moe_layer_desc* desc, const void* x, moe_dtype xt, int64_t T,

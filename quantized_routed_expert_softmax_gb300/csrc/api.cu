@@ -69,6 +69,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 int64_t matrix_bytes(int wfmt, int64_t rows, int64_t cols) {
     if (wfmt == MOE_W_Q8_0) return static_cast<int64_t>(moe_q8_0_bytes(rows, cols));
     if (wfmt == MOE_W_NVFP4) return static_cast<int64_t>(moe_nvfp4_bytes(rows, cols));
+    if (wfmt == MOE_W_MXFP4) return mx_bytes(rows, cols);
     return static_cast<int64_t>(moe_int8pc_bytes(rows, cols));
 }
 
@@ -131,6 +132,7 @@ struct Plan {
     int nv_split;       // NVFP4 down with fused combine: group splits per (row tile, slot)
     bool nv_mma;        // NVFP4 down on the tensor cores (tt_dn tokens per pass)
     bool decode1;       // one token, Q8_0 SwiGLU: the shape fits the one-kernel decode layer
+    bool mx;            // MXFP4 experts: coded inputs and the 4-bit tensor-core product
 };
 
 // Router experts per routing CTA of the one-kernel decode layer (0: E too large for `ctas`).
@@ -236,6 +238,7 @@ bool decode_split_fits(const moe_layer_desc* d, const DecodeSplit& sp, int xt) {
 // The GEMM path tiles rows by 128 (SwiGLU gate.up: 64 neurons' gate and up rows) and K by 64.
 bool gemm_shape_ok(const moe_layer_desc* d) {
     if (d->wfmt == MOE_W_INT8PC) return false;   // per-channel int8 runs on the GEMV kernels
+    if (d->wfmt == MOE_W_MXFP4) return false;    // has a product of its own
     if (d->flags & MOE_FLAG_HOST_WEIGHTS) return false;   // TMA loads device memory only
     if (d->f % 64 != 0 || d->d % 64 != 0) return false;
     if (d->act == MOE_ACT_RELU2 && d->f % 128 != 0) return false;
@@ -269,7 +272,8 @@ Plan make_plan(const moe_layer_desc* d, int64_t T, int xt = MOE_BF16) {
     p.small_route = (T <= kSmallT && p.P <= kSmallPairs && T * d->E <= kFusedRouteLogits) &&
                     route_decode_fits(T, d->d, d->E);
     const int64_t rows_per_tile = (d->wfmt == MOE_W_NVFP4) ? 256 : 32;
-    p.fuse_combine = T * rows_per_tile <= 256;
+    p.mx = d->wfmt == MOE_W_MXFP4;
+    p.fuse_combine = T * rows_per_tile <= 256 && !p.mx;
     const int64_t dn_bytes = matrix_bytes(d->wfmt, d->d, d->f);
     p.prefetch_down = static_cast<int64_t>(p.slot_cap) * dn_bytes <= kPrefetchBudget &&
                       !(d->flags & MOE_FLAG_HOST_DOWN);   // no bulk L2 prefetch of host memory
@@ -298,7 +302,7 @@ Plan make_plan(const moe_layer_desc* d, int64_t T, int xt = MOE_BF16) {
 
 struct Layout {
     size_t err, route_ctr, n_active, wait_limit, row_ctr, logits, rpart, idx, w, offsets, perm, pos, act_e, slot_info, chunk_cnt,
-        local_rank, gmask, h, y, xs_hi, xs_lo, h_hi, h_lo, dec_bar, dec_sel, dec_grec, dec_drec, xnext, xq, total;
+        local_rank, gmask, h, y, xs_hi, xs_lo, h_hi, h_lo, dec_bar, dec_sel, dec_grec, dec_drec, xnext, xq, mx_x, mx_h, total;
 };
 
 // The control region at the start of every workspace: a 256-byte header (the error word,
@@ -361,6 +365,8 @@ Layout layout_for(const moe_layer_desc* d, int64_t T) {
     L.dec_drec = take(dec ? sizeof(float) * sp.rec_d * sp.items_d * sp.cov_d : 0);
     L.xnext = take(T == 1 ? sizeof(uint16_t) * d->d : 0);   // a stack's next input (one token)
     L.xq = take(d->act_quant ? sizeof(float) * T * d->d : 0);   // the coded expert input (MOE_ACTQ_Q8_0)
+    L.mx_x = take(p.mx ? static_cast<size_t>(mx_bytes(p.P, d->d)) : 0);   // the MXFP4 experts' coded inputs
+    L.mx_h = take(p.mx ? static_cast<size_t>(mx_bytes(p.P, d->f)) : 0);
     L.total = off;
     return L;
 }
@@ -402,7 +408,8 @@ Workspace bind(void* base, const Layout& L) {
 moe_status validate_desc(const moe_layer_desc* d) {
     if (!d) return MOE_ERR_INVALID_ARG;
     if (d->act != MOE_ACT_SWIGLU && d->act != MOE_ACT_RELU2) return MOE_ERR_INVALID_ARG;
-    if (d->wfmt != MOE_W_Q8_0 && d->wfmt != MOE_W_NVFP4 && d->wfmt != MOE_W_INT8PC) return MOE_ERR_INVALID_ARG;
+    if (d->wfmt != MOE_W_Q8_0 && d->wfmt != MOE_W_NVFP4 && d->wfmt != MOE_W_INT8PC && d->wfmt != MOE_W_MXFP4)
+        return MOE_ERR_INVALID_ARG;
     if (d->path != MOE_PATH_AUTO && d->path != MOE_PATH_GEMV && d->path != MOE_PATH_GEMM) return MOE_ERR_INVALID_ARG;
     if (d->E < 1 || d->E > kMaxE || d->E % 4 != 0) return MOE_ERR_SHAPE;
     if (d->k < 1 || d->k > kMaxK || d->k > d->E) return MOE_ERR_INVALID_ARG;
@@ -418,6 +425,7 @@ moe_status validate_desc(const moe_layer_desc* d) {
     if (d->act_quant == MOE_ACTQ_Q8_0 && d->wfmt != MOE_W_Q8_0) return MOE_ERR_UNSUPPORTED;
     if (d->flags & ~MOE_FLAG_HOST_WEIGHTS) return MOE_ERR_INVALID_ARG;   // unknown bits
     if ((d->flags & MOE_FLAG_HOST_WEIGHTS) && d->path == MOE_PATH_GEMM) return MOE_ERR_UNSUPPORTED;
+    if (d->wfmt == MOE_W_MXFP4 && (d->path != MOE_PATH_AUTO || (d->flags & MOE_FLAG_HOST_WEIGHTS))) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
@@ -801,6 +809,28 @@ moe_status moe_layer_forward(const moe_layer_desc* desc, const void* x, moe_dtyp
     }
     if (e != cudaSuccess) return MOE_ERR_CUDA;
 
+    // MXFP4 experts: the rows of every expert coded side by side, gate.up with the activation, h coded,
+    // down, combine
+    if (p.mx) {
+        char* base = static_cast<char*>(workspace);
+        void *mx_x = base + L.mx_x, *mx_h = base + L.mx_h;
+        const int64_t rows_gu = desc->act == MOE_ACT_SWIGLU ? 2 * desc->f : desc->f;
+        mark(1);
+        if (e == cudaSuccess) e = launch_mxfp4_quantize(x, xt, T, ws.perm, k, 1, p.P, desc->d, mx_x, num_sms, s);
+        if (e == cudaSuccess)
+            e = launch_mxfp4_matmul(mx_x, p.P, desc->w_gate_up, desc->E, rows_gu, desc->d, ws.offsets, desc->act, ws.h,
+                                    MOE_F32, ws.err, num_sms, s);
+        mark(2);
+        if (e == cudaSuccess) e = launch_mxfp4_quantize(ws.h, MOE_F32, p.P, nullptr, 1, 1, p.P, desc->f, mx_h, num_sms, s);
+        if (e == cudaSuccess)
+            e = launch_mxfp4_matmul(mx_h, p.P, desc->w_down, desc->E, desc->d, desc->f, ws.offsets, MOE_ACT_NONE, ws.y,
+                                    MOE_F32, ws.err, num_sms, s);
+        mark(3);
+        if (e == cudaSuccess) e = launch_combine(ws.w, ws.pos, ws.y, T, k, desc->d, out, s);
+        mark(4);
+        return e == cudaSuccess ? copy_trace() : MOE_ERR_CUDA;
+    }
+
     // 3. gate.up + activation + group mask, 4. sparse down (+ combine), 5. combine
     ExpertArgs a{};
     a.x = x;
@@ -891,6 +921,7 @@ int32_t moe_layer_forward_launches(const moe_layer_desc* desc, int64_t T, int32_
     else n += (routing_supplied ? 0 : 2) + 3;               // router, top-k; rank, scan, scatter
     n += 2;                                                 // gate.up, down
     if (p.gemm) n += 1;                                     // sorted f16 copy of x
+    if (p.mx) n += 2;                                       // the coded x and h
     if (!p.fuse_combine) n += 1;                            // combine
     if (desc->act_quant) n += 2;                            // the coded x and h
     return n;

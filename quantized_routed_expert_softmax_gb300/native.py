@@ -18,7 +18,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_SHAPE", 3: "M
                 4: "MOE_ERR_WORKSPACE", 5: "MOE_ERR_UNSUPPORTED", 6: "MOE_ERR_CUDA", 7: "MOE_ERR_DEVICE_CHECK"}
 ACT = {"swiglu": 0, "relu2": 1}
 MATMUL_ACT = {**ACT, "none": 2}
-WFMT = {"q8_0": 0, "nvfp4": 1, "int8pc": 2}
+WFMT = {"q8_0": 0, "nvfp4": 1, "int8pc": 2, "mxfp4": 4}
 DTYPE_F32, DTYPE_BF16 = 0, 1
 LAYOUT = {"canonical": 0, "device": 1, "neuron": 2}
 PATH = {"auto": 0, "gemv": 1, "gemm": 2}
@@ -371,6 +371,7 @@ class MoELayer:
 
     gate_up: uint8 [E, bytes] in the device layout (SwiGLU: rows 0..f-1 gate, f..2f-1 up)
     down:    uint8 [E, bytes] (Q8_0 device layout / NVFP4 neuron layout)
+             (MXFP4: both as quantize_mxfp4 packs them)
     router_w: fp32 [d, E]; tscales: fp32 [E] each (NVFP4).
     """
 

@@ -97,3 +97,21 @@ def test_reference_codec_on_the_format_s_own_values():
     assert c[0, :8].tolist() == list(range(8)) and c[0, 16:24].tolist() == [0, 2, 2, 4, 4, 6, 6, 7]
     assert c[0, 8] == 0                          # a zero magnitude is +0
     np.testing.assert_array_equal(ref.values(c, s)[:, :16], x[:, :16].astype(np.float64))
+
+
+def test_layer_descriptor_with_mxfp4(L):
+    import ctypes
+
+    def desc(**kw):
+        base = dict(d=256, f=96, E=8, k=2, act=0, wfmt=4, path=0, router_w=FAKE, w_gate_up=FAKE, w_down=FAKE)
+        base.update(kw)
+        return native.LayerDesc(**base)
+    need = L.moe_layer_workspace_bytes(ctypes.byref(desc()), 16)
+    assert need > 0
+    F = lambda d, nb=need: L.moe_layer_forward(ctypes.byref(d), FAKE, 0, 16, None, None, FAKE, FAKE, nb, None, None)  # noqa: E731
+    assert F(desc(f=80)) == 2 and F(desc(wfmt=3)) == 1 and F(desc(act=2)) == 1
+    assert F(desc(path=1)) == 5 and F(desc(path=2)) == 5 and F(desc(act_quant=1)) == 5 and F(desc(flags=2)) == 5
+    assert L.moe_layer_forward(ctypes.byref(desc()), FAKE, 0, 16, None, None, FAKE, FAKE, 1024, None, None) == 4
+    # router, top-k, three of the permutation (or one kernel); coded x, gate.up, coded h, down, combine
+    assert L.moe_layer_forward_launches(ctypes.byref(desc()), 4096, 0) == 10
+    assert L.moe_layer_forward_launches(ctypes.byref(desc()), 4096, 1) == 8
