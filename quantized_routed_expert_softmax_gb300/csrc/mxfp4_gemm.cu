@@ -58,12 +58,14 @@ template <int NT>
 struct MxCfg {
     static constexpr int kStage = kMxABytes + NT * 128;
     static constexpr int kStages = NT > 128 ? 4 : 6;
+    static constexpr int kPair = NT > 128 ? 1 : 2;   // stages that one commit gives back (a commit takes 190 cycles to issue)
     static constexpr int kXWords = (NT + 31) / 32;   // columns of a panel's scales of x
     static constexpr int kXCols = NT > 128 ? 8 : 4;
     static constexpr uint32_t kSfCol = 2 * NT, kSfStage = 8 + 2 * kXCols;
     static constexpr int kBoxes = NT > 128 ? 5 : 4;
     static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage;
     static_assert(kSmem + 30 * 1024 <= 227 * 1024, "ring fits beside the item table");
+    static_assert(kStages % kPair == 0, "whole pairs");
     static_assert(kSfCol + kSfStage * kStages <= kMxTmemCols, "scale columns of every stage");
 };
 // Rows of box i of x: 16, 32, 64, 128, 192.
@@ -104,9 +106,9 @@ struct MxWalk {
     int stride_t, stride_m;   // stride / mtiles, stride % mtiles
     int tile, mtile;          // of the item that `at` describes
     int slot;
-    __device__ MxWalk(const int* prefix_, const int2* rows_, const uint16_t* height_, const uint16_t* expert_, int n_slots_,
-                      int mtiles_, int lane_, int item, int stride)
-        : prefix(prefix_), rows(rows_), height(height_), expert(expert_), n_slots(n_slots_), mtiles(mtiles_), lane(lane_),
+    __device__ MxWalk(const int* prefix_, const int2* rows_, const uint16_t* height_, const uint16_t* expert_, int mtiles_,
+                      int lane_, int item, int stride)
+        : prefix(prefix_), rows(rows_), height(height_), expert(expert_), n_slots(0), mtiles(mtiles_), lane(lane_),
           stride_t(stride / mtiles_), stride_m(stride % mtiles_), tile(item / mtiles_), mtile(item % mtiles_), slot(0) {}
     __device__ void next() {
         tile += stride_t;
@@ -165,15 +167,15 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     extern __shared__ __align__(16) unsigned char dsm_raw[];
     unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) &
                                                            ~static_cast<uintptr_t>(1023));
-    __shared__ uint64_t full[Cfg::kStages], empty[Cfg::kStages];
+    __shared__ uint64_t full[Cfg::kStages], empty[Cfg::kStages / Cfg::kPair];
     __shared__ uint64_t acc_full[2], acc_empty[2];
-    __shared__ uint32_t issued, committed;   // steps whose loads / MMAs this CTA has issued
+    __shared__ uint32_t issued, committed;   // steps whose loads, commits to `empty` that this CTA has issued
     __shared__ uint32_t tmem_base;
     __shared__ int prefix[kMaxE];
     __shared__ int2 rows[kMaxE];
     __shared__ uint16_t height[kMaxE], expert[kMaxE];
-    __shared__ long long warp_tiles[kMxWarps];
-    __shared__ int warp_live[kMxWarps], n_slots, n_items;
+    __shared__ int2 warp_sums[kMxWarps];
+    __shared__ int n_slots, n_items;
     __shared__ uint4 trans[8][kMxTransChunks];
     __shared__ volatile int s_fail;
     // the warp number through a shuffle, so that the compiler takes the roles' branches as uniform and
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     if (tid == 0) {
         for (int s = 0; s < Cfg::kStages; ++s) {
             tc::mbar_init(&full[s], 5);   // the TMA's arrival and bytes, four scale warps
-            tc::mbar_init(&empty[s], 1);
+            if (s % Cfg::kPair == 0) tc::mbar_init(&empty[s / Cfg::kPair], 1);
         }
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&acc_full[s], 1);
@@ -203,15 +205,14 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         s_fail = 0;
         issued = committed = 0;
     }
+    const int mtiles = (g.N + kMxTileM - 1) / kMxTileM;
+    MxWalk<NT> walk(prefix, rows, height, expert, mtiles, lane, blockIdx.x, gridDim.x);
     pdl_wait();
     pdl_trigger();
-    const int mtiles = (g.N + kMxTileM - 1) / kMxTileM;
-    {   // the slots and an exclusive prefix over them of the row tiles.  Offsets that overlap could count
-        // past 32 bits: counts are cut at kMxMaxItems, which increasing offsets stay far below
+    {   // the slots and an exclusive prefix over them of the row tiles (2^18 and a few an expert at most, so
+        // 32 bits hold their sum even where a caller's offsets overlap)
         constexpr int kPer = (kMaxE + kMxThreads - 1) / kMxThreads;
-        int first[kPer], last[kPer];
-        long long tiles = 0;
-        int live = 0;
+        int first[kPer], last[kPer], tiles = 0, live = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             first[i] = last[i] = 0;
@@ -219,41 +220,34 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             tiles += (last[i] - first[i] + NT - 1) / NT;
             live += last[i] > first[i];
         }
-        long long t_incl = tiles;
-        int l_incl = live;
+        int t_incl = tiles, l_incl = live;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, t_incl, o);
-            const int l = __shfl_up_sync(0xffffffffu, l_incl, o);
+            const int t = __shfl_up_sync(0xffffffffu, t_incl, o), l = __shfl_up_sync(0xffffffffu, l_incl, o);
             if (lane >= o) t_incl += t, l_incl += l;
         }
-        if (lane == 31) warp_tiles[warp] = t_incl, warp_live[warp] = l_incl;
+        if (lane == 31) warp_sums[warp] = make_int2(t_incl, l_incl);
         __syncthreads();
-        long long t_before = lane < warp ? warp_tiles[lane] : 0;
-        int l_before = lane < warp ? warp_live[lane] : 0;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            t_before += __shfl_xor_sync(0xffffffffu, t_before, o);
-            l_before += __shfl_xor_sync(0xffffffffu, l_before, o);
-        }
-        long long run = t_before + t_incl - tiles;
-        int slot = l_before + l_incl - live;
+        const int2 before = lane < warp ? warp_sums[lane] : make_int2(0, 0);
+        int run = __reduce_add_sync(0xffffffffu, before.x) + t_incl - tiles;
+        int slot = __reduce_add_sync(0xffffffffu, before.y) + l_incl - live;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             if (last[i] > first[i]) {
-                prefix[slot] = static_cast<int>(min(run, kMxMaxItems));
                 // an expert's row tiles are equally high, up to the 16 that the MMA's N is a multiple of
                 const int n = last[i] - first[i], n_tiles = (n + NT - 1) / NT;
-                height[slot] = static_cast<uint16_t>(((n + n_tiles - 1) / n_tiles + 15) & ~15);
+                prefix[slot] = run;
+                height[slot] = static_cast<uint16_t>(n_tiles == 1 ? (n + 15) & ~15 : ((n + n_tiles - 1) / n_tiles + 15) & ~15);
                 rows[slot] = make_int2(first[i], last[i]);
                 expert[slot] = static_cast<uint16_t>(tid * kPer + i);
                 ++slot;
-                run += (last[i] - first[i] + NT - 1) / NT;
+                run += n_tiles;
             }
         }
         if (tid == kMxThreads - 1) {
             n_slots = slot;
-            n_items = static_cast<int>(min(run * mtiles, kMxMaxItems));
+            // (increasing offsets stay far below the cut)
+            n_items = static_cast<int>(min(static_cast<long long>(run) * mtiles, kMxMaxItems));
         }
     }
     tc::fence_before();
@@ -263,7 +257,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     const int total = n_items;
     const int ksteps = (g.K + kMxStepK - 1) / kMxStepK;
     constexpr uint32_t stages = Cfg::kStages;
-    MxWalk<NT> walk(prefix, rows, height, expert, n_slots, mtiles, lane, blockIdx.x, gridDim.x);
+    walk.n_slots = n_slots;
 
     if (warp == 0) {
         // -------------------------------------------------------------------- TMA producer
@@ -277,7 +271,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             while (bi + 1 < Cfg::kBoxes && mx_box(bi) < it.nt) ++bi;   // smallest box covering the rows
             const uint32_t bytes = static_cast<uint32_t>(kMxABytes + mx_box(bi) * 128);
             for (int ks = 0; ks < ksteps; ++ks) {
-                if (use > 0 && !tc::mbar_wait_warp(&empty[st], use - 1, &s_fail)) {
+                if (use > 0 && !tc::mbar_wait_warp(&empty[st / Cfg::kPair], use - 1, &s_fail)) {
                     ok = false;
                     break;
                 }
@@ -330,7 +324,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                     for (int kk = 0; kk < 4; ++kk)   // 32 bytes of codes; blocks 2 (kk % 2), + 1 of panel kk / 2
                         tc::umma_mxf4(dt, da + 2 * kk, db + 2 * kk, idesc | tc::idesc_sf((kk & 1) * 2),
                                       ta + 4 * (kk >> 1), tb + Cfg::kXCols * (kk >> 1), ks > 0 || kk > 0);
-                    tc::commit(&empty[st]);
+                    if (st % Cfg::kPair == Cfg::kPair - 1) tc::commit(&empty[st / Cfg::kPair]);
                     if (ks + 1 == ksteps) tc::commit(&acc_full[buf]);
                 }
                 st = st1;
@@ -338,8 +332,14 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             }
         }
         if (leader) {
-            committed = use * stages + st;
-            if (!ok) mx_fail(g, &s_fail);
+            committed = (use * stages + st) / Cfg::kPair;
+            if (!ok) {
+                if (st % Cfg::kPair != 0) {   // a pair's first step is on its way
+                    tc::commit(&empty[st / Cfg::kPair]);
+                    ++committed;
+                }
+                mx_fail(g, &s_fail);
+            }
         }
     } else if (warp >= kMxSf0) {
         // -------------------------------------------------------------------- scales
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
 #pragma unroll
             for (int i = 0; i < kMxAhead; ++i) {
                 if (g0 + i >= steps || !ok) break;
-                if (use > 0 && !tc::mbar_wait_warp(&empty[st], use - 1, &s_fail)) {
+                if (use > 0 && !tc::mbar_wait_warp(&empty[st / Cfg::kPair], use - 1, &s_fail)) {
                     ok = false;
                     break;
                 }
@@ -486,7 +486,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float other = __shfl_xor_sync(0xffffffffu, up ? y[j] : y[j + 8], 16);
-                        y[j] = up ? mx_silu(other) * y[j + 8] : mx_silu(y[j]) * other;
+                        const float gate = up ? other : y[j], value = up ? y[j + 8] : other;   // (no branch)
+                        y[j] = mx_silu(gate) * value;
                     }
                 } else if (ACT == MOE_ACT_RELU2) {
 #pragma unroll
@@ -536,8 +537,9 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     if (s_fail) {
         if (tid == 0) {
             for (uint32_t n = issued > stages ? issued - stages : 0; n < issued; ++n) tc::mbar_wait(&full[n % stages], n / stages);
-            for (uint32_t n = committed > stages ? committed - stages : 0; n < committed; ++n)
-                tc::mbar_wait(&empty[n % stages], n / stages);
+            constexpr uint32_t kPairs = stages / Cfg::kPair;
+            for (uint32_t n = committed > kPairs ? committed - kPairs : 0; n < committed; ++n)
+                tc::mbar_wait(&empty[n % kPairs], n / kPairs);
         }
         __syncthreads();
     }
