@@ -5,6 +5,10 @@
 // rounded to nearest even and saturated at 6 (2 is E2M1's largest exponent, so amax lands in
 // [4, 8)).  Every step is exact up to the one rounding into the code: the exponent is read off the
 // fp32 bits and 2^-X is a power of two in fp32's normal range (-X is in [-125, 127]).
+//
+// Measured (GB300): quantising 45056 x 2816 fp32 85.8 us, 6.7 TB/s read and written, the rate of a copy; 4096
+// gathered rows x 2816 bf16 from L2 8.7 us, bound by instructions.  The decode of the former to fp32 105 us, 5.5
+// TB/s, seven eighths of it stores.
 #include <algorithm>
 
 #include "mxfp4.cuh"

@@ -5,27 +5,38 @@
 //
 // The MMA takes the codes as they lie in memory and both scales per block, so nothing is dequantised:
 // the kernel moves bytes and issues instructions.  Weight rows fill the MMA's M = 128 and an expert's
-// rows its N = 16 .. 128, so a decode batch pads its few rows to 16 and not to 128.
+// rows its N = 16 .. 192, so a decode batch pads its few rows to 16 and not to 128.
 //
 // A persistent grid (one CTA per SM) walks the (expert, row tile of x, tile of weight rows) items that
 // every CTA derives from the offsets.  Warps have fixed roles, linked by mbarriers:
-//   warp 0     TMA: per K step of 256, 128 weight rows and up to NT rows of x, 128 bytes each, into
-//              128-byte-swizzled tiles;
-//   warp 1     one thread issues the step's four K = 64 MMAs, operands in shared memory, scales in
-//              tensor memory;
-//   warps 4-11 epilogue: accumulators to registers, activation, stores.  Two accumulators alternate;
-//   warps 12-19 the scales, every other step by each group of four: a panel's 4-byte words (128 columns) of the weight rows and of the rows of x,
-//              read some steps ahead into registers and written straight into the form that the MMA
-//              takes them from tensor memory in: row r's word in lane r % 32 of every quadrant of 32
-//              lanes, column r / 32 (a warp writes the quadrant warp % 4).  Rows of x start anywhere and
-//              SwiGLU interleaves gate and up rows, so no bulk copy makes that form; asynchronous copies
-//              into shared memory for tcgen05.cp took 0.8 us a step, as the proxy fence that publishes
-//              one step's words also waits for the later steps' copies (512-expert up, 32 tokens: 179 us).
+//   warp 0      TMA: per K step of 256, 128 weight rows and up to NT rows of x, 128 bytes each, into
+//               128-byte-swizzled tiles;
+//   warp 1      one thread issues the step's four K = 64 MMAs, operands in shared memory, scales in
+//               tensor memory;
+//   warps 4-11  epilogue: accumulators to registers, activation, stores; each quadrant of 32 lanes has two
+//               warps that take 16 rows of x in turn.  Two accumulators alternate;
+//   warps 12-19 the scales, every other step by each group of four: a panel's 4-byte words (128 columns) of
+//               the weight rows and of the rows of x, read some steps ahead into registers and written
+//               straight into the form that the MMA takes them from tensor memory in: row r's word in lane
+//               r % 32 of every quadrant, column r / 32 (a warp writes the quadrant warp % 4).  Rows of x
+//               start anywhere and SwiGLU interleaves gate and up rows, so no bulk copy makes that form.
 // SwiGLU tiles hold 16 gate rows and the same neurons' 16 up rows in every 32 lanes, so one shuffle
 // pairs them.
 //
 // Codes past a matrix or past K arrive as zero; rows of the tile that are no rows of the item are computed
 // and not stored, and the last panel's blocks past K hold 2^0.
+//
+// Decode and short prefills are bound by the weights' bytes: up of 512 latent experts (1024 -> 2688, ReLU^2)
+// for 32 tokens 76.6 us, 7.4 TB/s of the bytes it cannot do without; gate.up (2816 -> 2 x 704) of 128 experts for
+// 512 tokens 48.2 us, 5.8 TB/s.  Long prefills are bound by storing the output while tiles come from L2: down
+// (704 -> 2816) for 8191 tokens 114 us, 4.6 TB/s; 83 us without its stores and 71 us without its epilogue.  One
+// token (16.9 MB from L2 or HBM over 88 CTAs) takes 6.8 us, most of it the chain offsets -> items -> first
+// tiles -> 11 steps -> epilogue.
+// What it took to get there, 512-expert up for 32 tokens / down for 8191 tokens, us: scales by asynchronous copies
+// and tcgen05.cp 176 / 240; scales through registers 157 / 260; role branches on a uniform warp number, which
+// keeps the operands of MMAs and TMA in uniform registers, 109 / 208; one barrier a step, slots found 32 at a
+// time 78 / 148; epilogue compiled per activation 78 / 127; 192-row tiles 78 / 115; eight epilogue warps 78 / 114
+// (and gate.up of 256 rows an expert 134 -> 108).
 #include <cuda.h>   // CUtensorMap and its enums; the encoder is looked up in the driver at run time
 #include <cudaTypedefs.h>
 
@@ -39,7 +50,7 @@
 namespace moe {
 
 constexpr int kMxThreads = 640, kMxWarps = kMxThreads / 32;
-constexpr int kMxEpi0 = 4, kMxSf0 = 12;   // first epilogue and first scale warp (the MMA warps' neighbours idle)
+constexpr int kMxEpi0 = 4, kMxSf0 = 12;   // first epilogue and first scale warp (a warp's quadrant is its number mod 4; 2 and 3 idle)
 constexpr int kMxTileM = 128;            // weight rows of an item (SwiGLU: 64 gate and 64 up rows)
 constexpr int kMxStepK = 256;            // one 128-byte swizzle row of 4-bit codes
 constexpr int kMxABytes = kMxTileM * 128;
