@@ -123,7 +123,7 @@ def _stream(stream=None) -> int:
     if stream is not None:
         return stream.cuda_stream
     # the handle alone: building a torch.cuda.Stream around it takes longer than a small kernel
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def q8_0_bytes(rows: int, cols: int) -> int:
@@ -202,13 +202,13 @@ def _operand(name: str, t, dtype, numel: int | None = None) -> int | None:
     entry point reads or writes (the C side sees only a pointer)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (numel is None or t.numel() == numel):
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor on the GPU")
-    if numel is not None and t.numel() != numel:
-        raise ValueError(f"{name} must hold {numel} values, not {t.numel()}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must hold {numel} values, not {t.numel()}")
 
 
 def quantize_mxfp4(x, rows=None, out=None, stream=None):

@@ -78,6 +78,26 @@ def test_codec_of_a_stack_and_of_gathered_rows():
     assert native.quantize_mxfp4(torch.empty(0, 96, device="cuda")).numel() == 0
 
 
+def test_codec_on_16_byte_aligned_operands():
+    # rows and results that start 16 bytes into their buffers (the 32-byte accesses do not apply)
+    rows, cols = 37, 288
+    for dtype in (torch.float32, torch.bfloat16):
+        x = _codec_rows(rows, cols, 5, dtype)
+        shift = 16 // x.element_size()
+        buf = torch.zeros(rows * cols + shift, dtype=dtype, device="cuda")
+        xs = buf[shift:].view(rows, cols)
+        xs.copy_(x)
+        assert xs.data_ptr() % 32 == 16
+        q = native.quantize_mxfp4(xs)
+        end = ref.pack(*ref.quantize(_host(x)))[1]
+        assert torch.equal(q[:, :end], native.quantize_mxfp4(x)[:, :end])
+        o = torch.full((rows * cols + 2 * shift,), 3.0, dtype=dtype, device="cuda")
+        native.dequantize_mxfp4(q[0], rows, cols, out=o[shift : shift + rows * cols].view(rows, cols))
+        v = ref.values(*ref.quantize(_host(x))).astype(np.float32)
+        assert np.array_equal(_host(o[shift : shift + rows * cols]).reshape(rows, cols), v, equal_nan=True)
+        assert (o[:shift] == 3).all() and (o[shift + rows * cols :] == 3).all()
+
+
 def test_codec_past_32_bit_offsets():
     rows, cols = 1_050_000, 2112        # 2.2e9 values
     x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
@@ -188,6 +208,33 @@ def test_product_many_experts():
     g = np.random.default_rng(5)
     _case(g.integers(0, 4, 512).tolist(), 64, 64, "relu2", torch.bfloat16)
     _case((g.random(1024) < 0.1).astype(int).tolist(), 32, 128, "none", torch.float32)
+
+
+@pytest.mark.parametrize("P,N,K", [(2, 8, 65536), (3, 131072, 32), (20, 64, 8192 + 96)])
+def test_product_largest_dimensions(P, N, K):
+    xq, xv = _coded(P, K, P)
+    wq, wv = _coded(N, K, 9, K ** -0.5)
+    out = native.mxfp4_matmul(xq, wq, None, P, N, K)
+    want, err = _want(xv, wv[None], [0, P], "none")
+    _check(out, want, err)
+
+
+def test_product_from_two_streams_at_once():
+    # overlapping calls with one error word, their outputs offset by 16 bytes in their buffers
+    groups, K, N = [40, 0, 300, 7], 704, 256
+    cases = [_case(groups, K, N, "none", torch.bfloat16, seed=s) for s in (1, 2)]
+    ws = native.mxfp4_workspace()
+    streams = [torch.cuda.Stream() for _ in cases]
+    P = cases[0][3]
+    outs = [[torch.zeros(P * N + 8, dtype=torch.bfloat16, device="cuda")[8:].view(P, N) for _ in range(6)] for _ in cases]
+    torch.cuda.synchronize()
+    for k in range(6):
+        for c, s, o in zip(cases, streams, outs):
+            native.mxfp4_matmul(c[0], c[1], c[2], P, N, K, out=o[k], workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for c, o in zip(cases, outs):
+        assert all(torch.equal(x, c[4]) for x in o)
+    assert native.device_status(ws) == 0
 
 
 def test_product_one_matrix_without_offsets():
