@@ -8,7 +8,10 @@ import of the functions below fails loudly.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmoe.so")
@@ -119,7 +122,6 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream=None) -> int:
-    import torch
     if stream is not None:
         return stream.cuda_stream
     # the handle alone: building a torch.cuda.Stream around it takes longer than a small kernel
@@ -136,7 +138,6 @@ def nvfp4_bytes(rows: int, cols: int) -> int:
 
 def quantize_q8_0(src, layout: str = "device", out=None, stream=None):
     """moe_quantize_q8_0 on a device fp32 tensor [..., rows, cols] -> uint8 [n_mat, bytes]."""
-    import torch
     rows, cols = src.shape[-2], src.shape[-1]
     n = src.numel() // (rows * cols)
     per = q8_0_bytes(rows, cols)
@@ -149,7 +150,6 @@ def quantize_q8_0(src, layout: str = "device", out=None, stream=None):
 
 def pack_nvfp4(src, layout: str = "device", out=None, tscale=None, stream=None):
     """moe_pack_nvfp4 on a device fp32 tensor [..., rows, cols] -> (uint8 [n_mat, bytes], fp32 [n_mat])."""
-    import torch
     rows, cols = src.shape[-2], src.shape[-1]
     n = src.numel() // (rows * cols)
     per = nvfp4_bytes(rows, cols)
@@ -168,7 +168,6 @@ def int8pc_bytes(rows: int, cols: int) -> int:
 
 def quantize_int8pc(src, layout: str = "device", out=None, stream=None):
     """moe_quantize_int8pc: src fp32 [n, rows, cols] (or [rows, cols]) -> uint8 [n, bytes]."""
-    import torch
     s3 = src if src.dim() == 3 else src.unsqueeze(0)
     n, rows, cols = s3.shape
     if out is None:
@@ -180,7 +179,6 @@ def quantize_int8pc(src, layout: str = "device", out=None, stream=None):
 
 def quantize_act_q8_0(x, out=None, stream=None):
     """moe_quantize_act_q8_0: x [rows, cols] fp32 or bf16 -> the Q8_0-coded values, fp32."""
-    import torch
     if out is None:
         out = torch.empty(x.shape, dtype=torch.float32, device=x.device)
     _check("moe_quantize_act_q8_0", lib().moe_quantize_act_q8_0(_ptr(x), _x_dtype(x), x.shape[0], x.shape[1],
@@ -190,6 +188,18 @@ def quantize_act_q8_0(x, out=None, stream=None):
 
 def mxfp4_bytes(rows: int, cols: int) -> int:
     return int(lib().moe_mxfp4_bytes(rows, cols))
+
+
+def _on_stream(fn):
+    """With stream= a call runs as if that stream were the current one: what it allocates (results, a
+    workspace that it drops at its end) belongs to the stream that its kernels run on."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
 def _mxfp4_size(rows: int, cols: int) -> int:
@@ -211,57 +221,63 @@ def _operand(name: str, t, dtype, numel: int | None = None) -> int | None:
     raise ValueError(f"{name} must hold {numel} values, not {t.numel()}")
 
 
-def quantize_mxfp4(x, rows=None, out=None, stream=None):
+@_on_stream
+def quantize_mxfp4(x, rows=None, out=None):
     """moe_quantize_mxfp4: x [..., rows, cols] fp32 or bf16 -> uint8 [n_mat, bytes].
 
     rows: int32 [n] row indices; the result is then one matrix of x's rows in that order (an index
     outside x gives a row of zeros)."""
-    import torch
-    xt = _x_dtype(x)
-    x_rows, cols = x.shape[-2:]
+    xt, shape = _x_dtype(x), x.shape
+    x_rows, cols = shape[-2], shape[-1]
     n, n_rows = 1, x_rows
     if rows is not None:
-        if x.dim() != 2:
+        if len(shape) != 2:
             raise ValueError("rows needs one matrix x [rows, cols]")
         n_rows = rows.numel()
-    elif x.dim() != 2:
+    elif len(shape) != 2:
         n = x.numel() // max(1, x_rows * cols)
     per = _mxfp4_size(n_rows, cols)
+    src = _operand("x", x, x.dtype)
     if out is None:
         out = torch.empty((n, per), dtype=torch.uint8, device=x.device)
+        dst = out.data_ptr()
+    else:
+        dst = _operand("out", out, torch.uint8, n * per)
     _check("moe_quantize_mxfp4", lib().moe_quantize_mxfp4(
-        _operand("x", x, x.dtype), xt, x_rows, _operand("rows", rows, torch.int32), n, n_rows, cols,
-        _operand("out", out, torch.uint8, n * per), _stream(stream)))
+        src, xt, x_rows, _operand("rows", rows, torch.int32), n, n_rows, cols, dst, _stream()))
     return out
 
 
-def dequantize_mxfp4(q, rows: int, cols: int, dtype=None, out=None, stream=None):
+@_on_stream
+def dequantize_mxfp4(q, rows: int, cols: int, dtype=None, out=None):
     """moe_dequantize_mxfp4: uint8 [bytes] -> [rows, cols], or uint8 [n_mat, bytes] -> [n_mat, rows, cols];
     dtype float32 (the default) or bfloat16."""
-    import torch
-    n = q.shape[0] if q.dim() == 2 else 1
+    shape = q.shape
+    n = shape[0] if len(shape) == 2 else 1
+    src = _operand("q", q, torch.uint8, n * _mxfp4_size(rows, cols))
     if out is None:
-        shape = (n, rows, cols) if q.dim() == 2 else (rows, cols)
-        out = torch.empty(shape, dtype=dtype or torch.float32, device=q.device)
-    _check("moe_dequantize_mxfp4", lib().moe_dequantize_mxfp4(
-        _operand("q", q, torch.uint8, n * _mxfp4_size(rows, cols)), n, rows, cols,
-        _operand("out", out, out.dtype, n * rows * cols), _x_dtype(out), _stream(stream)))
+        out = torch.empty((n, rows, cols) if len(shape) == 2 else (rows, cols), dtype=dtype or torch.float32,
+                          device=q.device)
+        dst = out.data_ptr()
+    else:
+        dst = _operand("out", out, out.dtype, n * rows * cols)
+    _check("moe_dequantize_mxfp4", lib().moe_dequantize_mxfp4(src, n, rows, cols, dst, _x_dtype(out), _stream()))
     return out
 
 
 def mxfp4_workspace(device="cuda"):
     """A zero-filled workspace of moe_mxfp4_matmul (device_status reads its error word)."""
-    import torch
     return torch.zeros(int(lib().moe_mxfp4_matmul_workspace_bytes()), dtype=torch.uint8, device=device)
 
 
+@_on_stream
 def mxfp4_matmul(xq, wq, offsets, rows: int, n: int, cols: int, act: str = "none", dtype=None, out=None,
-                 workspace=None, stream=None):
+                 workspace=None):
     """moe_mxfp4_matmul: xq one MXFP4 matrix [rows, cols] sorted by expert, wq uint8 [E, bytes] of MXFP4
     matrices [n, cols], offsets int32 [E + 1] (None with one matrix) -> [rows, n], or [rows, n / 2] for
     act "swiglu"; dtype float32 (the default) or bfloat16.  Without a workspace the call makes one."""
-    import torch
-    E = wq.shape[0] if wq.dim() == 2 else 1
+    shape = wq.shape
+    E = shape[0] if len(shape) == 2 else 1
     width = n // 2 if act == "swiglu" else n
     if out is None:
         out = torch.empty((rows, width), dtype=dtype or torch.float32, device=xq.device)
@@ -272,71 +288,81 @@ def mxfp4_matmul(xq, wq, offsets, rows: int, n: int, cols: int, act: str = "none
         _operand("wq", wq, torch.uint8, E * _mxfp4_size(n, cols)), E, n, cols,
         _operand("offsets", offsets, torch.int32, E + 1), MATMUL_ACT[act],
         _operand("out", out, out.dtype, rows * width), _x_dtype(out),
-        _operand("workspace", workspace, torch.uint8), workspace.numel(), _stream(stream)))
+        _operand("workspace", workspace, torch.uint8), workspace.numel(), _stream()))
     return out
 
 
 def _mask_operand(mask, T: int):
-    import torch
     if mask is None:
         return None
     return _operand("mask", mask, torch.bool if mask.dtype is torch.bool else torch.uint8, T)
 
 
-def balance_loss(logits, idx, mask=None, n_seq: int = 1, workspace=None, stream=None):
+@functools.lru_cache(maxsize=64)
+def _balance_bytes(n_seq: int, seq_len: int, E: int) -> int:
+    return int(lib().moe_balance_workspace_bytes(n_seq, seq_len, E))
+
+
+@_on_stream
+def balance_loss(logits, idx, mask=None, n_seq: int = 1, workspace=None):
     """moe_balance_loss: logits [T, E] fp32 or bf16, idx int32 [T, k], mask bool or uint8 [T], T = n_seq
     sequences of one (padded) length -> (loss fp32 [1], counts int32 [n_seq, E], prob fp32 [n_seq, E],
     tokens int32 [n_seq])."""
-    import torch
     (T, E), k = logits.shape, idx.shape[-1]
     if n_seq < 1 or T % n_seq:
         raise ValueError(f"{T} tokens are not {n_seq} sequences of one length")
-    dev = logits.device
-    # zeros where the library launches nothing
-    new = torch.empty if T else torch.zeros
-    loss = new(1, dtype=torch.float32, device=dev)
-    counts = new((n_seq, E), dtype=torch.int32, device=dev)
-    prob = new((n_seq, E), dtype=torch.float32, device=dev)
-    tokens = new(n_seq, dtype=torch.int32, device=dev)
+    lt, lp, ip = _x_dtype(logits), _operand("logits", logits, logits.dtype), _operand("idx", idx, torch.int32, T * k)
+    mp, dev, f32, i32 = _mask_operand(mask, T), logits.device, torch.float32, torch.int32
+    new = torch.empty if T else torch.zeros    # zeros where the library launches nothing
+    loss = new(1, dtype=f32, device=dev)
+    counts = new((n_seq, E), dtype=i32, device=dev)
+    prob = new((n_seq, E), dtype=f32, device=dev)
+    tokens = new(n_seq, dtype=i32, device=dev)
     if workspace is None:
-        workspace = torch.empty(int(lib().moe_balance_workspace_bytes(n_seq, T // n_seq, E)), dtype=torch.uint8,
-                                device=dev)
+        nbytes = _balance_bytes(n_seq, T // n_seq, E)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        wp = workspace.data_ptr()
+    else:
+        wp, nbytes = _operand("workspace", workspace, torch.uint8), workspace.numel()
     _check("moe_balance_loss", lib().moe_balance_loss(
-        _operand("logits", logits, logits.dtype), _x_dtype(logits), _operand("idx", idx, torch.int32, T * k),
-        _mask_operand(mask, T), n_seq, T // n_seq, E, k, _ptr(loss), _ptr(counts), _ptr(prob), _ptr(tokens),
-        _operand("workspace", workspace, torch.uint8), workspace.numel(), _stream(stream)))
+        lp, lt, ip, mp, n_seq, T // n_seq, E, k, loss.data_ptr(), counts.data_ptr(), prob.data_ptr(),
+        tokens.data_ptr(), wp, nbytes, _stream()))
     return loss, counts, prob, tokens
 
 
-def balance_loss_backward(logits, counts, tokens, grad_loss, k: int, mask=None, out=None, stream=None):
+@_on_stream
+def balance_loss_backward(logits, counts, tokens, grad_loss, k: int, mask=None, out=None):
     """moe_balance_loss_backward: the logits' gradient [T, E] from balance_loss's counts and tokens and
     the loss's gradient (fp32 [1])."""
-    import torch
     T, E = logits.shape
     n_seq = tokens.numel()
     if n_seq < 1 or T % n_seq:
         raise ValueError(f"{T} tokens are not {n_seq} sequences of one length")
+    lt, lp = _x_dtype(logits), _operand("logits", logits, logits.dtype)
     if out is None:
-        out = torch.empty_like(logits)
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        op = out.data_ptr()
+    else:
+        op = _operand("out", out, logits.dtype, T * E)
     _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
-        _operand("logits", logits, logits.dtype), _x_dtype(logits), _operand("counts", counts, torch.int32, n_seq * E),
-        _operand("tokens", tokens, torch.int32), _mask_operand(mask, T), _operand("grad_loss", grad_loss, torch.float32, 1),
-        n_seq, T // n_seq, E, k, _operand("out", out, logits.dtype, T * E), _stream(stream)))
+        lp, lt, _operand("counts", counts, torch.int32, n_seq * E), _operand("tokens", tokens, torch.int32),
+        _mask_operand(mask, T), _operand("grad_loss", grad_loss, torch.float32, 1), n_seq, T // n_seq, E, k, op,
+        _stream()))
     return out
 
 
+_X_DTYPE = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
 def _x_dtype(x) -> int:
-    import torch
-    if x.dtype == torch.float32:
-        return DTYPE_F32
-    if x.dtype == torch.bfloat16:
-        return DTYPE_BF16
-    raise TypeError("x must be float32 or bfloat16")
+    t = _X_DTYPE.get(x.dtype)
+    if t is None:
+        raise TypeError("x must be float32 or bfloat16")
+    return t
 
 
 def router_topk(x, W, k: int, return_logits: bool = False, stream=None):
     """moe_router_topk: (idx int32 [T,k], w fp32 [T,k][, logits fp32 [T,E]])."""
-    import torch
     T, d = x.shape
     E = W.shape[1]
     idx = torch.empty((T, k), dtype=torch.int32, device=x.device)
@@ -348,7 +374,6 @@ def router_topk(x, W, k: int, return_logits: bool = False, stream=None):
 
 
 def rmsnorm_bf16(x, eps: float = 1e-6, out=None, stream=None):
-    import torch
     T, d = x.shape
     if out is None:
         out = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
@@ -408,7 +433,6 @@ class MoELayer:
     def workspace(self, T: int):
         """A zero-filled workspace for up to T tokens with the current descriptor (kept, and
         replaced by a larger one when T or the descriptor needs more)."""
-        import torch
         need = self.workspace_bytes(T)
         if self._ws is None or self._ws.numel() < need:
             self._ws = torch.zeros(need, dtype=torch.uint8, device=self.router_w.device)
@@ -424,7 +448,6 @@ class MoELayer:
         """moe_layer_forward.  trace: a dict filled with device copies of the intermediates.
         stage_events: up to 5 torch.cuda.Event (timing enabled, already recorded once so
         that the handle exists) recorded at the stage boundaries."""
-        import torch
         T = x.shape[0]
         if out is None:
             out = torch.empty((T, self.d), dtype=torch.float32, device=x.device)
@@ -462,7 +485,6 @@ class MoELayer:
     def forward_noalloc(self, x, idx_in=None, w_in=None, out=None, stream=None):
         """moe_layer_forward_noalloc: the same forward with the library's fixed scratch
         instead of a workspace (for callers that cannot allocate device memory)."""
-        import torch
         T = x.shape[0]
         if out is None:
             out = torch.empty((T, self.d), dtype=torch.float32, device=x.device)
@@ -502,7 +524,6 @@ class MoEStack:
         self.descs = (LayerDesc * len(self.layers))(*[l.desc for l in self.layers])
 
     def workspace(self):
-        import torch
         if self._ws is None:
             self._ws = torch.zeros(self.layers[0].workspace_bytes(1), dtype=torch.uint8,
                                    device=self.layers[0].router_w.device)
@@ -515,7 +536,6 @@ class MoEStack:
         """x: [1, d] fp32 or bf16 on the device.  Returns outs fp32 [n_layers, d]; x_next
         (bf16 [n_layers, d]) and routing (dict with idx int32 / w fp32 [n_layers, k]) are
         filled when given."""
-        import torch
         n, l0 = len(self.layers), self.layers[0]
         if outs is None:
             outs = torch.empty((n, l0.d), dtype=torch.float32, device=x.device)

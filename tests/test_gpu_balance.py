@@ -187,6 +187,13 @@ def test_captured_and_on_another_stream():
     for _ in range(2):
         g.replay()
     assert all(torch.equal(u, v) for u, v in zip(a, b)) and torch.equal(ga, gb)
+    # stream= with everything made by the call: results and workspace belong to that stream
+    torch.cuda.synchronize()
+    d = native.balance_loss(logits, idx, mask=mask, n_seq=3, stream=s)
+    gd = native.balance_loss_backward(logits, d[1], d[3], one, 8, mask=mask, stream=s)
+    noise = [torch.full((4 << 20,), 7.0, device="cuda") for _ in range(4)]      # on the current stream meanwhile
+    s.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(a, d)) and torch.equal(ga, gd) and float(noise[0][0]) == 7
     logits.copy_(logits.flip(0))
     idx.copy_(idx.flip(0))
     g.replay()
