@@ -164,7 +164,6 @@ __global__ void __launch_bounds__(kBalThreads, bal_ctas_forward(Row::kN)) balanc
     int L, BalRuns runs, int E, int k, float* __restrict__ part, int32_t* __restrict__ cnt,
     uint32_t* __restrict__ done, BalOut out) {
     pdl_wait();
-    pdl_trigger();
     constexpr int N = Row::kN;
     extern __shared__ float red[];                                     // [kBalWarps][E]
     int32_t* hist = reinterpret_cast<int32_t*>(red + kBalWarps * E);   // [E + 1]
@@ -261,7 +260,6 @@ __global__ void __launch_bounds__(kBalThreads) balance_sequence_kernel(
     int32_t* __restrict__ counts, float* __restrict__ prob, int32_t* tokens, float* seq_loss, uint32_t* done,
     float* __restrict__ loss) {
     pdl_wait();
-    pdl_trigger();
     __shared__ float sp[kBalWarps][32], rd[kBalWarps];
     __shared__ int sc[kBalWarps][33], ri[kBalWarps];
     __shared__ bool last;
@@ -326,7 +324,6 @@ __global__ void __launch_bounds__(kBalThreads, bal_ctas_backward(Row::kN)) balan
     const uint8_t* __restrict__ mask, const float* __restrict__ grad_loss, int S, int L, BalRuns runs, int E,
     int k, void* __restrict__ grad) {
     pdl_wait();
-    pdl_trigger();
     constexpr int N = Row::kN;
     __shared__ int ri[kBalWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % Row::kLanes, grp = lane / Row::kLanes;

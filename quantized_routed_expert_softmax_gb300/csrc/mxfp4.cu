@@ -78,7 +78,6 @@ __global__ void __launch_bounds__(256, kMxCtas) mxfp4_quantize_kernel(const char
                                                                        MxRuns runs, int64_t n_mat, int64_t rows, int cols,
                                                                        bool wide, uint8_t* __restrict__ dst) {
     pdl_wait();
-    pdl_trigger();
     constexpr int kElem = F32 ? 4 : 2;
     const int lane16 = threadIdx.x & 15;
     for (int64_t m = blockIdx.y; m < n_mat; m += gridDim.y) {
@@ -151,7 +150,6 @@ __global__ void __launch_bounds__(256, mx_decode_ctas(F32)) mxfp4_dequantize_ker
                                                                          int64_t n_mat, int64_t rows, int cols, bool wide,
                                                                          char* __restrict__ out) {
     pdl_wait();
-    pdl_trigger();
     constexpr int kElem = F32 ? 4 : 2;
     const int lane16 = threadIdx.x & 15;
     const int64_t r0 = blockIdx.z * n.slab_rows;

@@ -3,6 +3,10 @@
 
 #include "common.cuh"
 
+// The kernels of the MXFP4 operators and of the balance loss wait for the kernel before them (pdl_wait), and
+// let the next one start as their CTAs end: allowed in earlier, its CTAs fill what room the SMs have left,
+// unevenly, and a grid of one wave with equal shares then runs at the pace of the fullest SM (45056 x 2816 fp32,
+// quantise and decode in turn: 205 us, 190 without).
 namespace moe {
 
 // A matrix [rows, cols]: codes row-major (cols / 2 bytes a row), then panels of 128 columns, each

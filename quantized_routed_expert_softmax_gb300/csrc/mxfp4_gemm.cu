@@ -219,7 +219,6 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     const int mtiles = (g.N + kMxTileM - 1) / kMxTileM;
     MxWalk<NT> walk(prefix, rows, height, expert, mtiles, lane, blockIdx.x, gridDim.x);
     pdl_wait();
-    pdl_trigger();
     {   // the slots and an exclusive prefix over them of the row tiles (2^18 and a few an expert at most, so
         // 32 bits hold their sum even where a caller's offsets overlap)
         constexpr int kPer = (kMaxE + kMxThreads - 1) / kMxThreads;
