@@ -256,8 +256,9 @@ moe_status moe_mxfp4_matmul(const void* xq, int64_t P, const void* wq, int64_t E
  *            or NULL.
  * loss       device fp32 [1];  counts  int32 [n_seq][E];  prob  fp32 [n_seq][E];  tokens  int32
  *            [n_seq] (all written).
- * workspace  device, moe_balance_workspace_bytes(n_seq, seq_len, E) bytes, 256-byte aligned; needs no
- *            clearing.  Calls that may overlap need workspaces of their own.
+ * workspace  device, moe_balance_workspace_bytes(n_seq, seq_len, E) bytes, 256-byte aligned (may be NULL
+ *            when that is 0, as for small batches); needs no clearing.  Calls that may overlap need
+ *            workspaces of their own.
  * T = 0 returns MOE_OK, launches nothing and touches no buffer.
  * Errors: INVALID_ARG (NULL, bad dtype, k outside 1 .. min(E, 32)), SHAPE (E from 1 to 1024, T up to
  * 2^20), ALIGNMENT, WORKSPACE, CUDA.

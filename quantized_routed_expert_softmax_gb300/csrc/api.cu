@@ -662,8 +662,10 @@ moe_status moe_balance_loss(const void* logits, moe_dtype lt, const int32_t* idx
     if (!aligned16(logits) || !aligned16(idx) || !aligned16(counts) || !aligned16(prob) || !aligned16(tokens) ||
         (reinterpret_cast<uintptr_t>(loss) & 3u))
         return MOE_ERR_ALIGNMENT;
-    if (!workspace || ws_bytes < balance_workspace_bytes(n_seq, seq_len, E)) return MOE_ERR_WORKSPACE;
-    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MOE_ERR_ALIGNMENT;
+    if (const size_t need = balance_workspace_bytes(n_seq, seq_len, E)) {
+        if (!workspace || ws_bytes < need) return MOE_ERR_WORKSPACE;
+        if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MOE_ERR_ALIGNMENT;
+    }
     return cuda_status(launch_balance_loss(logits, lt, idx, mask, n_seq, seq_len, E, k, loss, counts, prob, tokens,
                                            workspace, reinterpret_cast<cudaStream_t>(stream)));
 }

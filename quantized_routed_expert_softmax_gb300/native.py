@@ -319,9 +319,10 @@ def balance_loss(logits, idx, mask=None, n_seq: int = 1, workspace=None):
     prob = new((n_seq, E), dtype=f32, device=dev)
     tokens = new(n_seq, dtype=i32, device=dev)
     if workspace is None:
-        nbytes = _balance_bytes(n_seq, T // n_seq, E)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        wp = workspace.data_ptr()
+        wp, nbytes = None, _balance_bytes(n_seq, T // n_seq, E)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            wp = workspace.data_ptr()
     else:
         wp, nbytes = _operand("workspace", workspace, torch.uint8), workspace.numel()
     _check("moe_balance_loss", lib().moe_balance_loss(

@@ -30,6 +30,7 @@ def test_sizes(L):
         assert L.moe_mxfp4_bytes(rows, cols) == 0
     assert L.moe_mxfp4_matmul_workspace_bytes() == 256
     assert L.moe_balance_workspace_bytes(4, 100, 128) > 0
+    assert L.moe_balance_workspace_bytes(1, 16, 8) == 0          # one CTA's work: no workspace
     assert L.moe_balance_workspace_bytes(4, 0, 128) == 0 and L.moe_balance_workspace_bytes(1, 1, 1025) == 0
 
 
@@ -58,7 +59,7 @@ def test_matmul_refusals(L):
 
 
 def test_balance_refusals(L):
-    def B(lg=FAKE, lt=0, ix=FAKE, S=2, T=8, E=8, k=2, loss=FAKE, c=FAKE, p=FAKE, n=FAKE, ws=FAKE, nb=1 << 30):
+    def B(lg=FAKE, lt=0, ix=FAKE, S=2, T=4000, E=8, k=2, loss=FAKE, c=FAKE, p=FAKE, n=FAKE, ws=FAKE, nb=1 << 30):
         return L.moe_balance_loss(lg, lt, ix, None, S, T, E, k, loss, c, p, n, ws, nb, None)
     for kw in (dict(lg=None), dict(ix=None), dict(loss=None), dict(c=None), dict(p=None), dict(n=None), dict(lt=2),
                dict(k=0), dict(k=9), dict(E=64, k=33)):
@@ -66,7 +67,7 @@ def test_balance_refusals(L):
     for kw in (dict(E=1025), dict(S=-1), dict(T=-1), dict(S=1 << 11, T=1 << 10), dict(T=1 << 40), dict(S=1 << 62, T=4)):
         assert B(**kw) == 2, kw
     assert B(lg=FAKE + 4) == 3 and B(ws=FAKE + 16) == 3
-    assert B(ws=None) == 4 and B(nb=L.moe_balance_workspace_bytes(2, 8, 8) - 1) == 4
+    assert B(ws=None) == 4 and B(nb=L.moe_balance_workspace_bytes(2, 4000, 8) - 1) == 4
     assert B(S=0) == 0 and B(T=0, lg=None) == 0
 
     def G(lg=FAKE, lt=0, c=FAKE, n=FAKE, g=FAKE, S=2, T=8, E=8, k=2, out=FAKE):
