@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     __shared__ uint64_t acc_full[2], acc_empty[2];
     __shared__ uint32_t issued, committed;   // steps whose loads, commits to `empty` that this CTA has issued
     __shared__ uint32_t tmem_base;
+    __shared__ int stage_nt[Cfg::kStages];   // rows of x of the stage's item, written before the TMA's arrival
     __shared__ int prefix[kMaxE];
     __shared__ int2 rows[kMaxE];
     __shared__ uint16_t height[kMaxE], expert[kMaxE];
@@ -286,6 +287,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                     break;
                 }
                 if (leader) {
+                    stage_nt[st] = it.nt;
                     tc::mbar_arrive_expect_tx(&full[st], bytes);
                     const uint32_t dst = ring0 + st * Cfg::kStage;
                     if (kSwiglu) tc::tma_5d(dst, &g.tw, ks * 128, 0, 0, it.mtile * 4, it.e, &full[st]);
@@ -304,23 +306,24 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         const bool leader = tc::elect_one();
         const uint64_t da0 = tc::sdesc_k128(tc::s_addr(ring));
         const uint64_t db0 = tc::sdesc_k128(tc::s_addr(ring + kMxABytes));
-        uint32_t st = 0, use = 0, n_item = 0;
+        const int items = total > static_cast<int>(blockIdx.x) ? (total - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+        uint32_t st = 0, use = 0;
         bool ok = true;
         bool ready = false;   // the step's stage was already full when the step before was issued
-        for (int item = blockIdx.x; item < total && ok; item += gridDim.x, ++n_item, walk.next()) {
-            const MxItem it = walk.at();
-            const uint32_t idesc = tc::idesc_mxf4((it.nt + 15) & ~15);
+        for (int n_item = 0; n_item < items && ok; ++n_item) {
             const uint32_t buf = n_item & 1, ub = n_item >> 1;
             if (ub > 0 && !tc::mbar_wait_warp(&acc_empty[buf], ub - 1, &s_fail)) {
                 ok = false;
                 break;
             }
             const uint32_t dt = tmem + buf * NT;
+            uint32_t idesc = 0;
             for (int ks = 0; ks < ksteps; ++ks) {
                 if (!__all_sync(0xffffffffu, ready) && !tc::mbar_wait_warp(&full[st], use, &s_fail)) {
                     ok = false;
                     break;
                 }
+                if (ks == 0) idesc = tc::idesc_mxf4((stage_nt[st] + 15) & ~15);
                 const uint32_t st1 = st + 1 == stages ? 0 : st + 1, use1 = use + (st1 == 0);
                 ready = tc::mbar_test_wait(&full[st1], use1 & 1u);
                 tc::fence_after();
