@@ -30,7 +30,7 @@
 // for 32 tokens 76.6 us, 7.4 TB/s of the bytes it cannot do without; gate.up (2816 -> 2 x 704) of 128 experts for
 // 512 tokens 48.2 us, 5.8 TB/s.  Long prefills are bound by storing the output while tiles come from L2: down
 // (704 -> 2816) for 8191 tokens 114 us, 4.6 TB/s; 83 us without its stores and 71 us without its epilogue.  One
-// token (16.9 MB from L2 or HBM over 88 CTAs) takes 6.8 us, most of it the chain offsets -> items -> first
+// token (16.9 MB from L2 or HBM over 88 CTAs) takes 6.2 us, most of it the chain offsets -> items -> first
 // tiles -> 11 steps -> epilogue.
 // What it took to get there, 512-expert up for 32 tokens / down for 8191 tokens, us: scales by asynchronous copies
 // and tcgen05.cp 176 / 240; scales through registers 157 / 260; role branches on a uniform warp number, which
@@ -68,12 +68,12 @@ __device__ const uint32_t kMxOne = 0x7f7f7f7fu;   // scales of 2^0
 template <int NT>
 struct MxCfg {
     static constexpr int kStage = kMxABytes + NT * 128;
-    static constexpr int kStages = NT > 128 ? 4 : 6;
-    static constexpr int kPair = NT > 128 ? 1 : 2;   // stages that one commit gives back (a commit takes 190 cycles to issue)
+    static constexpr int kStages = NT > 128 ? 4 : (NT > 32 ? 6 : 9);
+    static constexpr int kPair = NT > 128 ? 1 : (NT > 32 ? 2 : 3);   // stages that one commit gives back (a commit takes 190 cycles to issue)
     static constexpr int kXWords = (NT + 31) / 32;   // columns of a panel's scales of x
     static constexpr int kXCols = NT > 128 ? 8 : 4;
     static constexpr uint32_t kSfCol = 2 * NT, kSfStage = 8 + 2 * kXCols;
-    static constexpr int kBoxes = NT > 128 ? 5 : 4;
+    static constexpr int kBoxes = NT > 128 ? 5 : (NT > 32 ? 4 : 2);
     static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage;
     static_assert(kSmem + 30 * 1024 <= 227 * 1024, "ring fits beside the item table");
     static_assert(kStages % kPair == 0, "whole pairs");
@@ -605,6 +605,7 @@ MxKernel mx_kernel(int act, int out, size_t* smem) {
     return mx_kernel<NT, MOE_ACT_NONE>(out);
 }
 MxKernel mx_kernel(int nt, int act, int out, size_t* smem) {
+    if (nt == 32) return mx_kernel<32>(act, out, smem);
     return nt == 128 ? mx_kernel<128>(act, out, smem) : mx_kernel<192>(act, out, smem);
 }
 
@@ -612,7 +613,7 @@ MxKernel mx_kernel(int nt, int act, int out, size_t* smem) {
 
 cudaError_t configure_mxfp4_kernels() {
     cudaError_t e = mx_encoder();
-    for (int nt : {128, 192})
+    for (int nt : {32, 128, 192})
         for (int act : {MOE_ACT_SWIGLU, MOE_ACT_RELU2, MOE_ACT_NONE})
             for (int out : {kOutF32, kOutWide, kOutBf16}) {
                 size_t smem = 0;
@@ -655,10 +656,12 @@ cudaError_t launch_mxfp4_matmul(const void* xq, int64_t P, const void* wq, int64
     }
     if (e != cudaSuccess) return e;
     const int64_t avg = P / std::min(E, P);
-    // Row tiles of 128, or of 192 from 160 rows an expert on, where the loads of weights and x from L2 bound
-    // the kernel: down (704 -> 2816) of 128 experts, us: 64 rows an expert 33.5 (192: 35.2), 128: 44.1
-    // (43.6), 256: 72.0 (66.7).  Tiles of 16, 32 and 64 rows are no faster at any number of rows.
-    const int nt = avg <= 160 ? 128 : 192;
+    // Row tiles of 128; of 192 from 160 rows an expert on, where the loads of weights and x from L2 bound the
+    // kernel; of 32 for calls of few rows, whose deeper ring has a whole item's loads on their way at once.  us:
+    //   down (704 -> 2816) of 128 experts, 64 rows an expert: 33.5 (192: 35.2); 128: 44.1 (43.6); 256: 72.0 (66.7)
+    //   gate.up (2816 -> 2 x 704), 8 rows in all: 7.2 (32: 6.6); 64: 21.1 (20.6); 512: 42.0 (41.5)
+    //   up of 512 experts (1024 -> 2688), 176 rows in all: 35.2 (35.5); 1408: 98.2 (99.1)
+    const int nt = P <= 512 && avg <= 16 ? 32 : (avg <= 160 ? 128 : 192);
     // boxes of x: the powers of two from 16 up to the tile, so that a short group does not load a tile
     const cuuint64_t xd[2] = {kb, static_cast<cuuint64_t>(P)}, xst[1] = {kb};
     for (int i = 0; i < kMxMaxBoxes && mx_box(i) <= nt; ++i) {

@@ -180,7 +180,7 @@ def _case(counts, K, N, act, dtype, seed=0, first=0, behind=0):
 SHAPES = [  # K, N
     (32, 64), (64, 128), (96, 192), (160, 64), (256, 320), (288, 128), (512, 256), (704, 2816), (2816, 1408),
 ]
-GROUPS = [[1], [0, 1, 0], [3, 0, 0, 17, 1], [16, 33, 64, 0, 7], [128, 129], [200, 0, 5, 300], [193, 0, 400], [577]]
+GROUPS = [[1], [0, 1, 0], [3, 0, 0, 17, 1], [16, 33, 64, 0, 7], [128, 129], [200, 0, 5, 300], [193, 0, 400], [577], [33, 64, 1, 0, 31, 32, 2, 0, 0, 70, 16, 15, 17, 4, 4, 4] + [2] * 20]
 
 
 @pytest.mark.parametrize("act", ["none", "swiglu", "relu2"])
