@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         const int items = total > static_cast<int>(blockIdx.x) ? (total - 1 - blockIdx.x) / gridDim.x + 1 : 0;
         uint32_t st = 0, use = 0;
         bool ok = true;
-        bool ready = false;   // the step's stage was already full when the step before was issued
+        bool ready = false;   // (the leader's) the step's stage was already full when the step before was issued
         for (int n_item = 0; n_item < items && ok; ++n_item) {
             const uint32_t buf = n_item & 1, ub = n_item >> 1;
             if (ub > 0 && !tc::mbar_wait_warp(&acc_empty[buf], ub - 1, &s_fail)) {
@@ -319,13 +319,16 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             const uint32_t dt = tmem + buf * NT;
             uint32_t idesc = 0;
             for (int ks = 0; ks < ksteps; ++ks) {
-                if (!__all_sync(0xffffffffu, ready) && !tc::mbar_wait_warp(&full[st], use, &s_fail)) {
+                if (!__any_sync(0xffffffffu, ready) && !tc::mbar_wait_warp(&full[st], use, &s_fail)) {
                     ok = false;
                     break;
                 }
-                if (ks == 0) idesc = tc::idesc_mxf4((stage_nt[st] + 15) & ~15);
+                if (ks == 0) {
+                    __syncwarp();   // (the leader alone may have seen the stage full)
+                    idesc = tc::idesc_mxf4((stage_nt[st] + 15) & ~15);
+                }
                 const uint32_t st1 = st + 1 == stages ? 0 : st + 1, use1 = use + (st1 == 0);
-                ready = tc::mbar_test_wait(&full[st1], use1 & 1u);
+                ready = false;
                 tc::fence_after();
                 if (leader) {
                     // (the descriptors' start address, bytes / 16, is linear in the address)
@@ -337,6 +340,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                     for (int kk = 0; kk < 4; ++kk)   // 32 bytes of codes; blocks 2 (kk % 2), + 1 of panel kk / 2
                         tc::umma_mxf4(dt, da + 2 * kk, db + 2 * kk, idesc | tc::idesc_sf((kk & 1) * 2),
                                       ta + 4 * (kk >> 1), tb + Cfg::kXCols * (kk >> 1), ks > 0 || kk > 0);
+                    ready = tc::mbar_test_wait(&full[st1], use1 & 1u);   // beside the MMAs
                     if (st % Cfg::kPair == Cfg::kPair - 1) tc::commit(&empty[st / Cfg::kPair]);
                     if (ks + 1 == ksteps) tc::commit(&acc_full[buf]);
                 }
