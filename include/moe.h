@@ -321,7 +321,8 @@ typedef struct {
     const void* l2_prefetch;      /* optional, may be NULL: device bytes to pull into L2 while this
                                      layer's expert weights stream -- in a stack, the next layer's
                                      router weights, so its routing does not wait on HBM.  A hint:
-                                     never read by the layer's arithmetic; 16-byte aligned */
+                                     never read by the layer's arithmetic; 16-byte aligned (MXFP4
+                                     experts: checked, not used) */
     int64_t l2_prefetch_bytes;    /* bytes at l2_prefetch (rounded down to a multiple of 16) */
     int32_t act_quant;            /* moe_act_quant (MOE_ACTQ_Q8_0 needs Q8_0 weights) */
     int32_t flags;                /* MOE_FLAG_* bits, 0 for the default */

@@ -275,7 +275,8 @@ def mxfp4_matmul(xq, wq, offsets, rows: int, n: int, cols: int, act: str = "none
                  workspace=None):
     """moe_mxfp4_matmul: xq one MXFP4 matrix [rows, cols] sorted by expert, wq uint8 [E, bytes] of MXFP4
     matrices [n, cols], offsets int32 [E + 1] (None with one matrix) -> [rows, n], or [rows, n / 2] for
-    act "swiglu"; dtype float32 (the default) or bfloat16.  Without a workspace the call makes one."""
+    act "swiglu"; dtype float32 (the default) or bfloat16.  Without a workspace the call makes one, which
+    takes its error word with it: pass one to be able to ask device_status."""
     shape = wq.shape
     E = shape[0] if len(shape) == 2 else 1
     width = n // 2 if act == "swiglu" else n
