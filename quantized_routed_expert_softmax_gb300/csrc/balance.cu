@@ -31,7 +31,7 @@ namespace moe {
 constexpr int kBalThreads = 256, kBalWarps = kBalThreads / 32;
 
 // The runs: CTA b of n has tokens [start(b), start(b + 1)), multiples of 8 up to the end.  Run b's part of
-// sequence s is record b + s: both grow along the tokens, one at a time.  (T is at most 2^20 and n 608:
+// sequence s is record b + s: both grow along the tokens, one at a time.  (T is at most 2^20 and n below 4096:
 // 32 bits hold the products.)
 struct BalRuns {
     int T, n;
@@ -129,6 +129,19 @@ struct BalRow {
     }
 };
 
+// A running sum with the part that its additions rounded off beside it (two-sum: the rounding error of an
+// addition, exact), so that it holds about 48 bits however many terms come.  (Not fp64: GB300 adds that at a
+// small fraction of fp32's rate.)
+struct BalSum {
+    float hi = 0.0f, lo = 0.0f;
+    __device__ __forceinline__ void add(float v) {
+        const float s = __fadd_rn(hi, v), b = __fsub_rn(s, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(v, b)));
+        hi = s;
+    }
+    __device__ __forceinline__ float value() const { return hi + lo; }
+};
+
 // Sum over threads of one CTA, the same on every thread; `red` holds kBalWarps values.
 template <typename T>
 __device__ __forceinline__ T block_sum(T v, T* red) {
@@ -155,6 +168,18 @@ struct BalOut {
     int32_t* tokens;
 };
 
+// 1 / n for a mean over n terms, 0 over none: formed before the sums that it meets are there.
+__device__ __forceinline__ float bal_inverse(int n) { return n > 0 ? 1.0f / static_cast<float>(n) : 0.0f; }
+// Pairwise sum of the warps' parts.
+template <typename T>
+__device__ __forceinline__ T warp_parts(T a[kBalWarps]) {
+#pragma unroll
+    for (int h = kBalWarps / 2; h >= 1; h >>= 1)
+#pragma unroll
+        for (int w = 0; w < h; ++w) a[w] += a[w + h];
+    return a[0];
+}
+
 // One CTA per run.  A record is part[E], the sums of p, and cnt[E + 1], the experts' counts and, last, the
 // counted tokens.  A single run has every sequence in one record, and its CTA writes the results itself (16
 // tokens of 8 experts: one launch and no workspace, 2.3 us in place of 5.2).
@@ -170,7 +195,7 @@ __global__ void __launch_bounds__(kBalThreads, bal_ctas_forward(Row::kN)) balanc
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % Row::kLanes, grp = lane / Row::kLanes;
     __shared__ float rd[kBalWarps];
     if (runs.n > 1 && blockIdx.x == 0 && threadIdx.x == 0) *done = 0;   // the next kernel's counter
-    float loss = 0.0f;
+    BalSum loss;
     int live_seq = 0;
     constexpr int kStep = kBalWarps * Row::kGroups;
     const int end = runs.start(blockIdx.x + 1);
@@ -224,33 +249,35 @@ __global__ void __launch_bounds__(kBalThreads, bal_ctas_forward(Row::kN)) balanc
         __syncthreads();
         const int64_t rec = static_cast<int64_t>(blockIdx.x) + s;
         const bool only = runs.n == 1;
-        const float rn = hist[E] > 0 ? 1.0f / static_cast<float>(hist[E]) : 0.0f;
+        const int tokens = hist[E];
+        const float rn = bal_inverse(tokens), factor = rn * (static_cast<float>(E) / static_cast<float>(k));
         float dot = 0.0f;
         for (int e = threadIdx.x; e < E; e += kBalThreads) {
-            float a = 0.0f;
+            float a[kBalWarps];
 #pragma unroll
-            for (int w = 0; w < kBalWarps; ++w) a += red[w * E + e];
+            for (int w = 0; w < kBalWarps; ++w) a[w] = red[w * E + e];
+            const float total = warp_parts(a);
             if (only) {
-                a *= rn;
-                out.prob[rec * E + e] = a;
+                const float mean = total * rn;
+                out.prob[rec * E + e] = mean;
                 out.counts[rec * E + e] = hist[e];
-                dot += a * (static_cast<float>(hist[e]) * rn);
+                dot += mean * static_cast<float>(hist[e]);
             } else {
-                part[rec * E + e] = a;
+                part[rec * E + e] = total;
             }
         }
         if (only) {
             dot = block_sum(dot, rd);
-            if (threadIdx.x == 0) out.tokens[s] = hist[E];
-            loss += dot * (static_cast<float>(E) / static_cast<float>(k));
-            live_seq += hist[E] > 0;
+            if (threadIdx.x == 0) out.tokens[s] = tokens;
+            loss.add(dot * factor);
+            live_seq += tokens > 0;
         } else {
             for (int e = threadIdx.x; e <= E; e += kBalThreads) cnt[rec * (E + 1) + e] = hist[e];
         }
         __syncthreads();
         t0 = t1;
     }
-    if (runs.n == 1 && threadIdx.x == 0) *out.loss = live_seq > 0 ? loss / static_cast<float>(live_seq) : 0.0f;
+    if (runs.n == 1 && threadIdx.x == 0) *out.loss = live_seq > 0 ? loss.value() / static_cast<float>(live_seq) : 0.0f;
 }
 
 // One CTA per (sequence, 32 experts): warp w adds the sequence's records w, w + 8, ..; counts, tokens, prob and the
@@ -270,27 +297,29 @@ __global__ void __launch_bounds__(kBalThreads) balance_sequence_kernel(
     const int chunks = runs.run_of(static_cast<int>(s + 1) * L - 1) - b0 + 1;
     const float* ps = part + (b0 + s) * E + e;
     const int32_t* cs = cnt + (b0 + s) * (E + 1);
-    float p = 0.0f;
+    BalSum sum;
     int count = 0, n = 0;
 #pragma unroll 4
     for (int c = warp; c < chunks; c += kBalWarps) {
         if (e < E) {
-            p += __ldcg(ps + static_cast<int64_t>(c) * E);
+            sum.add(__ldcg(ps + static_cast<int64_t>(c) * E));
             count += __ldcg(cs + static_cast<int64_t>(c) * (E + 1) + e);
         }
         n += lane == 0 ? __ldcg(cs + static_cast<int64_t>(c) * (E + 1) + E) : 0;
     }
-    sp[warp][lane] = p;
+    sp[warp][lane] = sum.value();
     sc[warp][lane] = count;
     if (lane == 0) sc[warp][32] = n;
     __syncthreads();
     if (warp == 0) {
-        p = 0.0f, count = n = 0;
+        int ns[kBalWarps], cs8[kBalWarps];
+        float ps8[kBalWarps];
 #pragma unroll
-        for (int w = 0; w < kBalWarps; ++w) p += sp[w][lane], count += sc[w][lane], n += sc[w][32];
-        const float rn = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
-        p *= rn;
-        float dot = e < E ? p * (static_cast<float>(count) * rn) : 0.0f;
+        for (int w = 0; w < kBalWarps; ++w) ns[w] = sc[w][32], cs8[w] = sc[w][lane], ps8[w] = sp[w][lane];
+        n = warp_parts(ns);
+        count = warp_parts(cs8);
+        const float rn = bal_inverse(n), p = warp_parts(ps8) * rn;
+        float dot = e < E ? p * static_cast<float>(count) : 0.0f;
         if (e < E) {
             counts[s * E + e] = count;
             prob[s * E + e] = p;
@@ -299,7 +328,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_sequence_kernel(
         for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
         if (lane == 0) {
             if (e < 32) tokens[s] = n;
-            seq_loss[blockIdx.x] = dot * (static_cast<float>(E) / static_cast<float>(k));
+            seq_loss[blockIdx.x] = dot * (rn * (static_cast<float>(E) / static_cast<float>(k)));
             __threadfence();
             last = atomicAdd(done, 1u) == gridDim.x - 1;
         }
@@ -307,13 +336,13 @@ __global__ void __launch_bounds__(kBalThreads) balance_sequence_kernel(
     __syncthreads();
     if (!last) return;
     __threadfence();
-    float v = 0.0f;
+    BalSum v;   // (a thread adds 2^17 blocks at most)
     int live = 0;
-    for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += kBalThreads) v += __ldcg(seq_loss + i);   // 0 where n_s = 0
+    for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += kBalThreads) v.add(__ldcg(seq_loss + i));   // 0 where n_s = 0
     for (int i = threadIdx.x; i < S; i += kBalThreads) live += __ldcg(tokens + i) > 0;
-    v = block_sum(v, rd);
+    const float total = block_sum(v.value(), rd);
     live = block_sum(live, ri);
-    if (threadIdx.x == 0) *loss = live > 0 ? v / static_cast<float>(live) : 0.0f;
+    if (threadIdx.x == 0) *loss = live > 0 ? total / static_cast<float>(live) : 0.0f;
 }
 
 // One CTA per run: per sequence f_e - 1/E times E / (S' n_s) times the incoming gradient in registers, then
@@ -345,11 +374,11 @@ __global__ void __launch_bounds__(kBalThreads, bal_ctas_backward(Row::kN)) balan
             for (int i = threadIdx.x; i < S; i += kBalThreads) c += __ldg(tokens + i) > 0;
             live_seq = block_sum(c, ri);
         }
-        // (E counts - k n) / (E k n) * g E / (S' n), the difference in integers
+        // (E counts - k n) / (E k n) * g E / (S' n), the difference and the divisor (2^45 at most) in integers: four
+        // fp32 roundings in all
         const int n = __ldg(tokens + s);
         const int64_t kn = static_cast<int64_t>(k) * n;
-        const float scale =
-            n > 0 ? g / (static_cast<float>(kn) * (static_cast<float>(live_seq) * static_cast<float>(n))) : 0.0f;
+        const float scale = n > 0 ? g / static_cast<float>(kn * (static_cast<int64_t>(live_seq) * n)) : 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int e = Row::expert(l, i);
@@ -416,11 +445,17 @@ int64_t expert_blocks(int64_t E) { return (E + 31) / 32; }
 
 }  // namespace
 
-// The forward pass's runs.
+// The forward pass's runs.  A lane adds its rows of a run in turn, and a sequential fp32 sum of n like terms may be off
+// by n / 2 units of 2^-24: a run has at most 64 passes, which takes more than one wave of them from 77824 tokens (E
+// above 512; 233472 above 256) on.
+constexpr int64_t kBalMaxPasses = 64;
 static BalRuns bal_runs_forward(int64_t T, int64_t E) {
     BalRuns runs{};
     (void)with_row(E, [&](auto row) {
-        runs = bal_runs(T, bal_ctas_forward(decltype(row)::kN), decltype(row)::kGroups, 4);
+        using Row = decltype(row);
+        runs = bal_runs(T, bal_ctas_forward(Row::kN), Row::kGroups, 4);
+        const int64_t wave = kBalSms * bal_ctas_forward(Row::kN) * kBalMaxPasses * kBalWarps * Row::kGroups;
+        if (T > wave) runs.n *= static_cast<int>((T + wave - 1) / wave);
         return cudaSuccess;
     });
     return runs;
@@ -428,7 +463,7 @@ static BalRuns bal_runs_forward(int64_t T, int64_t E) {
 
 size_t balance_workspace_bytes(int64_t S, int64_t L, int64_t E) {
     if (bal_runs_forward(S * L, E).n == 1) return 0;   // no records
-    const int64_t n = bal_runs(S * L, 4, 1, 1).n + S;   // records, at most
+    const int64_t n = bal_runs_forward(S * L, E).n + S;   // records, at most
     return 256 + align256(sizeof(float) * n * E) + align256(sizeof(int32_t) * n * (E + 1)) +
            align256(sizeof(float) * S * expert_blocks(E));
 }
@@ -436,7 +471,8 @@ size_t balance_workspace_bytes(int64_t S, int64_t L, int64_t E) {
 cudaError_t launch_balance_loss(const void* logits, int lt, const int32_t* idx, const uint8_t* mask, int64_t S,
                                 int64_t L, int64_t E, int k, float* loss, int32_t* counts, float* prob, int32_t* tokens,
                                 void* workspace, cudaStream_t st) {
-    const int64_t n = bal_runs(S * L, 4, 1, 1).n + S;
+    const BalRuns runs = bal_runs_forward(S * L, E);
+    const int64_t n = runs.n + S;
     char* w = static_cast<char*>(workspace);
     uint32_t* done = reinterpret_cast<uint32_t*>(w);
     w += 256;
@@ -446,7 +482,6 @@ cudaError_t launch_balance_loss(const void* logits, int lt, const int32_t* idx, 
     w += align256(sizeof(int32_t) * n * (E + 1));
     float* seq_loss = reinterpret_cast<float*>(w);
     const int e32 = static_cast<int>(E);
-    const BalRuns runs = bal_runs_forward(S * L, E);
     cudaError_t e = with_row(E, [&](auto row) {
         return launch_pdl(balance_partial_kernel<decltype(row)>, dim3(static_cast<unsigned>(runs.n)), dim3(kBalThreads),
                           sizeof(float) * kBalWarps * E + sizeof(int32_t) * (E + 1), st, logits, lt, idx, mask,
