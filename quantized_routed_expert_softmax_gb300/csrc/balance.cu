@@ -47,6 +47,29 @@ struct BalRuns {
     }
 };
 
+// a, b -> exp(a - m), exp(b - m), m at least both.  With d = a - m and t = d log2 e rounded, exp(d) = 2^t exp(d - t ln 2),
+// and q = d - t ln 2, exact up to 2^-24 of itself through ln 2 in two parts, is so small that exp(q) = 1 + q to 2^-33:
+// the result is as good as the hardware's 2^t (2^-22 of it) at any distance, where 2^t alone is off by
+// up to |d| 2^-24 more (at -80 by 20 times as much).  Below 2^-126 it is 0.  Pairs go in packed instructions:
+// 16 x 4096 x 512 fp32 forward 35.1 us, with expf 38.1, with 2^t alone 33.9.
+__device__ __forceinline__ void bal_exp(float& a, float& b, float m) {
+    constexpr float kLog2e = 1.44269504f, kLn2Hi = 0.693145752f, kLn2Lo = 1.42860677e-6f;   // (hi has 16 bits)
+    const uint64_t d = add_f32x2(pack_f32x2(a, b), pack_f32x2(-m, -m));
+    uint64_t t, q = d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(d), "l"(pack_f32x2(kLog2e, kLog2e)));
+    fma_f32x2(q, t, pack_f32x2(-kLn2Hi, -kLn2Hi));
+    fma_f32x2(q, t, pack_f32x2(-kLn2Lo, -kLn2Lo));
+    const float2 tf = unpack_f32x2(t), qf = unpack_f32x2(q);
+    float ea, eb;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ea) : "f"(tf.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(eb) : "f"(tf.y));
+    // (where t is -inf e is 0 and q +inf or, for d = -inf, NaN; a NaN logit is NaN in e)
+    uint64_t e = pack_f32x2(ea, eb);
+    fma_f32x2(e, pack_f32x2(ea, eb), pack_f32x2(fminf(qf.x, 1.0f), fminf(qf.y, 1.0f)));
+    const float2 r = unpack_f32x2(e);
+    a = r.x, b = r.y;
+}
+
 // How a warp holds rows of E logits.  Vector form (E a multiple of 4): element i of lane l of a group of
 // LANES is expert 4 (l + LANES (i / 4)) + i % 4.  Scalar form: expert l + 32 i.
 template <int LANES, int N, bool VEC>
@@ -105,11 +128,9 @@ struct BalRow {
         for (int o = LANES / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     }
-    // Logits -> probabilities, exp(x - m) by the hardware's 2^x (2 units in the last place; the largest
-    // logit's is exactly 1).  A row of -inf has no probability at all (p = 0); a NaN or +inf logit makes the
-    // row NaN.
+    // Logits -> probabilities.  A row of -inf has no probability at all (p = 0); a NaN or +inf logit makes the row
+    // NaN.
     static __device__ __forceinline__ void softmax(float v[N]) {
-        constexpr float kLog2e = 1.44269504f;
         float m = v[0];
 #pragma unroll
         for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
@@ -118,9 +139,10 @@ struct BalRow {
         if (m == -INFINITY) m = 0.0f;
         float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"((v[i] - m) * kLog2e));
+        for (int i = 0; i < N; i += 2) {
+            bal_exp(v[i], v[i + 1], m);
             s += v[i];
+            s += v[i + 1];
         }
         s = sum(s);
         const float inv = s == 0.0f ? 0.0f : 1.0f / s;
