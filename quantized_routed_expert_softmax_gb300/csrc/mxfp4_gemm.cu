@@ -147,10 +147,15 @@ struct MxWalk {
 // Output forms: fp32; bf16 where 16 bytes of a row are aligned; other bf16.
 enum { kOutF32 = 0, kOutWide = 1, kOutBf16 = 2 };
 
-// SiLU by the fast exponential and division (2 units in the last place each; a divisor past fp32 gives 0,
-// as -88 and below should).  With the correctly rounded ones the SwiGLU epilogue of 128 x 128 results took
-// 10,000 cycles.
-__device__ __forceinline__ float mx_silu(float g) { return g * __fdividef(1.0f, 1.0f + __expf(-g)); }
+// SiLU to a few units in the last place at any gate: exp(-|g|) is at most 1, so that the divisor of the fast division
+// lies in [1, 2], where it is good to 2 units (past 2^126 it would give 0, and a fast exponential is off by |g| units).
+// Below -87 silu is still a normal fp32, down to -3e-37, and then a subnormal one.  With a correctly
+// rounded division the SwiGLU epilogue of 128 x 128 results took 10,000 cycles; with the fast exponential
+// 4096 tokens' gate.up (256 rows an expert) takes 78.1 us in place of 81.2, 512 tokens' 47.8 in place of 48.0.
+__device__ __forceinline__ float mx_silu(float g) {
+    const float e = expf(-fabsf(g));
+    return __fdividef(g < 0.0f ? g * e : g, 1.0f + e);
+}
 
 // The epilogue's transposition: column f's 16 values (32 bytes) start at this 16-byte chunk.  Both the
 // writes and the gathered reads of 8 lanes then meet 8 different chunks mod 8.
