@@ -857,12 +857,12 @@ __global__ void __launch_bounds__(256, NT <= 2 ? 2 : 1) down_nv_mma_kernel(Exper
 // ------------------------------------------------------------------------------ combine
 // out[t] = sum_{j<k} w[t][j] * y[pos(t,j)], in slot order.
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ w, const int32_t* __restrict__ pos,
-                                                       const float* __restrict__ y, int k, int d,
-                                                       float* __restrict__ out) {
+                                                       const float* __restrict__ y, int T, int k,
+                                                       int d, float* __restrict__ out) {
     pdl_wait();
-    const int t = blockIdx.y;
+    const int t = token_block();
     const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
-    if (c >= d) return;
+    if (c >= d || t >= T) return;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int j = 0; j < k; ++j) {
         const int r = pos[t * k + j];
@@ -1041,8 +1041,8 @@ cudaError_t launch_down_gemv(const ExpertArgs& a, int wfmt, int slot_cap, cudaSt
 cudaError_t launch_combine(const float* w, const int32_t* pos, const float* y, int64_t T, int k, int64_t d,
                            float* out, cudaStream_t s) {
     const int64_t cols4 = d / 4;
-    const dim3 grid(static_cast<unsigned>((cols4 + 255) / 256), static_cast<unsigned>(T));
-    return launch_pdl(combine_kernel, grid, dim3(256), 0, s, w, pos, y, k, static_cast<int>(d), out);
+    return launch_pdl(combine_kernel, token_grid((cols4 + 255) / 256, T), dim3(256), 0, s, w, pos, y, static_cast<int>(T), k,
+                      static_cast<int>(d), out);
 }
 
 cudaError_t launch_rmsnorm_bf16(const float* x, int64_t T, int64_t d, float eps, uint16_t* xo, cudaStream_t s) {
