@@ -19,6 +19,7 @@
 // Dequantisation is exact (int8 or e2m1 codes times the block scale); accumulation is
 // fp32; the tokens of one expert sit in shared memory as fp32.
 #include "gemv_core.cuh"
+#include "grid.cuh"
 
 namespace moe {
 
