@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "grid.cuh"
 
 namespace moe {
 
@@ -25,7 +26,8 @@ __global__ void __launch_bounds__(256) router_logits_kernel(const void* __restri
     pdl_wait();
     const int l = threadIdx.x;
     const int e0 = blockIdx.x * 4;
-    const int t0 = blockIdx.y * TT;
+    const int t0 = token_block() * TT;
+    if (t0 >= T) return;   // (the whole block)
     const int nt = min(TT, T - t0);
     float acc[TT][4];
 #pragma unroll
@@ -104,7 +106,8 @@ __global__ void __launch_bounds__(256, 2) router_logits_warp_kernel(const void* 
     pdl_wait();
     const int l = threadIdx.x, warp = l >> 5, lane = l & 31;
     const int e0 = blockIdx.x * kRtE;
-    const int t0 = blockIdx.y * kRtT;
+    const int t0 = token_block() * kRtT;
+    if (t0 >= T) return;   // (the whole block)
     const int nt = min(kRtT, T - t0);
     const int M = d / kRouterPartials;
     unsigned char* ring = sm + warp * kStages * kStage;
@@ -243,11 +246,11 @@ cudaError_t launch_router_logits(const void* x, int xt, const float* W, int64_t 
     if (T <= 2) return launch_pdl(router_logits_kernel<2>, dim3(E / 4, 1), block, 0, s, x, xt, W, Ti, di, Ei, logits);
     if (T <= 4) return launch_pdl(router_logits_kernel<4>, dim3(E / 4, 1), block, 0, s, x, xt, W, Ti, di, Ei, logits);
     if (E % 8 == 0) {
-        const dim3 grid(static_cast<unsigned>(E / 8), static_cast<unsigned>((T + 7) / 8));
+        const dim3 grid = token_grid(E / 8, (T + 7) / 8);
         if (xt == MOE_F32) return launch_pdl(router_logits_warp_kernel<true>, grid, block, 0, s, x, W, Ti, di, Ei, logits);
         return launch_pdl(router_logits_warp_kernel<false>, grid, block, 0, s, x, W, Ti, di, Ei, logits);
     }
-    return launch_pdl(router_logits_kernel<8>, dim3(E / 4, (unsigned)((T + 7) / 8)), block, 0, s, x, xt, W, Ti, di, Ei,
+    return launch_pdl(router_logits_kernel<8>, token_grid(E / 4, (T + 7) / 8), block, 0, s, x, xt, W, Ti, di, Ei,
                       logits);
 }
 

@@ -36,3 +36,22 @@ def _check(w, L, T, step):
 def test_layer_past_65535_tokens(wfmt, T):
     w, L = _layer(wfmt)
     _check(w, L, T, 32769)
+
+
+@pytest.mark.parametrize("x_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E", [8, 12])      # eight experts a block, and four
+def test_router_past_524280_tokens(E, x_dtype):
+    T, d, k, step = 524288 + 9, 256, 2, 262149
+    g = torch.Generator("cuda").manual_seed(E)
+    x = torch.randn(T, d, device="cuda", generator=g).to(x_dtype)
+    W = torch.randn(d, E, device="cuda", generator=g)
+    idx, w, logits = native.router_topk(x, W, k, return_logits=True)
+    for a in range(0, T, step):
+        a = min(a, T - step)
+        part = native.router_topk(x[a : a + step].contiguous(), W, k, return_logits=True)
+        assert all(torch.equal(whole[a : a + step], p) for whole, p in zip((idx, w, logits), part)), a
+
+
+def test_layer_of_the_largest_batch():
+    w, L = _layer("mxfp4")
+    _check(w, L, 1 << 20, 1 << 19)
