@@ -231,7 +231,8 @@ moe_status moe_dequantize_mxfp4(const void* src, int64_t n_mat, int64_t rows, in
  * out      device, [P][N] or [P][N/2], fp32 or bf16 (ot; rounded once).
  * workspace  device, moe_mxfp4_matmul_workspace_bytes() bytes, zero-filled before its first use: an
  *          error word that moe_get_device_status() reads and clears (2: a wait ran past its
- *          limit, out is not valid).  Calls that may overlap can share it.
+ *          limit, a second unless the int64 at byte 32 is not 0; out is not valid).  Calls that may
+ *          overlap can share it.
  * The same inputs give the same bits.  P = 0 returns MOE_OK, launches nothing and touches no buffer.
  * Errors: INVALID_ARG (NULL, bad enum, offsets NULL with E > 1), SHAPE (K a positive multiple of 32 up
  * to 65536; P up to 2^25; N from 1 to 131072, for SWIGLU a multiple of 64; E up to 1024), ALIGNMENT,

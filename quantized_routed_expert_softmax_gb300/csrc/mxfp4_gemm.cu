@@ -59,6 +59,10 @@ constexpr uint32_t kMxTmemCols = 512;
 constexpr int kMxTransChunks = 3 * 31 + 2 * 3 + 2;   // 16-byte chunks of an epilogue warp's transposition
 constexpr int kMxMaxBoxes = 5;
 constexpr long long kMxMaxItems = 1ll << 30;
+// The waits' limit in ns (int64) sits at this 32-bit word of the workspace, as in a layer's: 0 means a second; tests set
+// another (-1: a wait gives up at its first look past the hardware's own suspension).
+constexpr int kMxLimitWord = 8;
+static_assert((kMxThreads - 1) * 2 >= kMaxE, "the last thread has no offsets");
 
 __device__ const uint32_t kMxOne = 0x7f7f7f7fu;   // scales of 2^0
 
@@ -94,8 +98,8 @@ struct MxArgs {
     int32_t* err;
 };
 
-__device__ __forceinline__ void mx_fail(const MxArgs& g, volatile int* s_fail) {
-    *s_fail = 1;
+__device__ __forceinline__ void mx_fail(const MxArgs& g, volatile tc::Waits* waits) {
+    waits->fail = 1;
     set_error(g.err, tc::kErrTimeout);
 }
 
@@ -184,8 +188,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) &
                                                            ~static_cast<uintptr_t>(1023));
     __shared__ uint64_t full[Cfg::kStages], empty[Cfg::kStages / Cfg::kPair];
-    __shared__ uint64_t acc_full[2], acc_empty[2];
-    __shared__ uint32_t issued, committed;   // steps whose loads, commits to `empty` that this CTA has issued
+    __shared__ uint64_t acc_full[2], acc_empty[2], drained;
+    __shared__ uint32_t issued;   // steps whose loads this CTA has issued
     __shared__ uint32_t tmem_base;
     __shared__ int stage_nt[Cfg::kStages];   // rows of x of the stage's item, written before the TMA's arrival
     __shared__ int prefix[kMaxE];
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     __shared__ int2 warp_sums[kMxWarps];
     __shared__ int n_slots, n_items;
     __shared__ uint4 trans[8][kMxTransChunks];
-    __shared__ volatile int s_fail;
+    __shared__ volatile tc::Waits waits;
     // the warp number through a shuffle, so that the compiler takes the roles' branches as uniform and
     // keeps descriptors and coordinates in uniform registers, where the tensor core and the copy engine
     // take them from (read out of divergent code, a step's four MMAs took 800 cycles to issue)
@@ -218,13 +222,18 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             tc::mbar_init(&acc_full[s], 1);
             tc::mbar_init(&acc_empty[s], 8);
         }
+        tc::mbar_init(&drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        s_fail = 0;
-        issued = committed = 0;
+        waits.fail = 0;
+        issued = 0;
     }
     const int mtiles = (g.N + kMxTileM - 1) / kMxTileM;
     MxWalk<NT> walk(prefix, rows, height, expert, mtiles, lane, blockIdx.x, gridDim.x);
     pdl_wait();
+    if (tid == kMxThreads - 1) {   // (a thread without offsets to read)
+        const long long limit = *reinterpret_cast<const volatile long long*>(g.err + kMxLimitWord);
+        waits.limit_ns = limit != 0 ? limit : tc::kWaitLimitNs;
+    }
     {   // the slots and an exclusive prefix over them of the row tiles (2^18 and a few an expert at most, so
         // 32 bits hold their sum even where a caller's offsets overlap)
         constexpr int kPer = (kMaxE + kMxThreads - 1) / kMxThreads;
@@ -274,6 +283,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
     const int ksteps = (g.K + kMxStepK - 1) / kMxStepK;
     constexpr uint32_t stages = Cfg::kStages;
     walk.n_slots = n_slots;
+    uint32_t sf_steps = 0;   // own K steps that a scale warp has arrived for
 
     if (warp == 0) {
         // -------------------------------------------------------------------- TMA producer
@@ -287,7 +297,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             while (bi + 1 < Cfg::kBoxes && mx_box(bi) < it.nt) ++bi;   // smallest box covering the rows
             const uint32_t bytes = static_cast<uint32_t>(kMxABytes + mx_box(bi) * 128);
             for (int ks = 0; ks < ksteps; ++ks) {
-                if (use > 0 && !tc::mbar_wait_warp(&empty[st / Cfg::kPair], use - 1, &s_fail)) {
+                if (use > 0 && !tc::mbar_wait_warp(&empty[st / Cfg::kPair], use - 1, &waits)) {
                     ok = false;
                     break;
                 }
@@ -304,7 +314,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         }
         if (leader) {
             issued = use * stages + st;
-            if (!ok) mx_fail(g, &s_fail);
+            if (!ok) mx_fail(g, &waits);
         }
     } else if (warp == 1) {
         // -------------------------------------------------------------------- MMA issuer
@@ -317,14 +327,14 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         bool ready = false;   // (the leader's) the step's stage was already full when the step before was issued
         for (int n_item = 0; n_item < items && ok; ++n_item) {
             const uint32_t buf = n_item & 1, ub = n_item >> 1;
-            if (ub > 0 && !tc::mbar_wait_warp(&acc_empty[buf], ub - 1, &s_fail)) {
+            if (ub > 0 && !tc::mbar_wait_warp(&acc_empty[buf], ub - 1, &waits)) {
                 ok = false;
                 break;
             }
             const uint32_t dt = tmem + buf * NT;
             uint32_t idesc = 0;
             for (int ks = 0; ks < ksteps; ++ks) {
-                if (!__any_sync(0xffffffffu, ready) && !tc::mbar_wait_warp(&full[st], use, &s_fail)) {
+                if (!__any_sync(0xffffffffu, ready) && !tc::mbar_wait_warp(&full[st], use, &waits)) {
                     ok = false;
                     break;
                 }
@@ -353,16 +363,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                 use = use1;
             }
         }
-        if (leader) {
-            committed = (use * stages + st) / Cfg::kPair;
-            if (!ok) {
-                if (st % Cfg::kPair != 0) {   // a pair's first step is on its way
-                    tc::commit(&empty[st / Cfg::kPair]);
-                    ++committed;
-                }
-                mx_fail(g, &s_fail);
-            }
-        }
+        if (leader && !ok) mx_fail(g, &waits);
     } else if (warp >= kMxSf0) {
         // -------------------------------------------------------------------- scales
         // Group grp takes the steps whose number has parity grp, so that one group's waits overlap the
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
 #pragma unroll
             for (int i = 0; i < kMxAhead; ++i) {
                 if (g0 + i >= steps || !ok) break;
-                if (use > 0 && !tc::mbar_wait_warp(&empty[st / Cfg::kPair], use - 1, &s_fail)) {
+                if (use > 0 && !tc::mbar_wait_warp(&empty[st / Cfg::kPair], use - 1, &waits)) {
                     ok = false;
                     break;
                 }
@@ -455,11 +456,12 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&full[st]);
+                ++sf_steps;
                 st += 2;
                 if (st >= stages) st -= stages, ++use;
             }
         }
-        if (!ok && lane == 0) mx_fail(g, &s_fail);
+        if (!ok && lane == 0) mx_fail(g, &waits);
     } else if (warp >= kMxEpi0) {
         // -------------------------------------------------------------------- epilogue
         // (activation and output form are template parameters: the loop over 16 rows of x has to stay
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
         for (int item = blockIdx.x; item < total; item += gridDim.x, ++n_item, walk.next()) {
             const MxItem it = walk.at();
             const uint32_t buf = n_item & 1;
-            if (!tc::mbar_wait_warp(&acc_full[buf], n_item >> 1, &s_fail)) {
+            if (!tc::mbar_wait_warp(&acc_full[buf], n_item >> 1, &waits)) {
                 ok = false;
                 break;
             }
@@ -549,19 +551,25 @@ __global__ void __launch_bounds__(kMxThreads, 1) mxfp4_gemm_kernel(const __grid_
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
         }
-        if (!ok && lane == 0) mx_fail(g, &s_fail);
+        if (!ok && lane == 0) mx_fail(g, &waits);
     }
 
     // Every copy and MMA this CTA issued has landed before its memories are given back: the MMAs waited
-    // for every copy and the epilogue for every MMA, unless a wait ran out.
+    // for every copy and the epilogue for every MMA.  Where a wait ran out that has to be made up for.  A stage
+    // is full with its copies' bytes and four scale warps: those that gave up arrive for what else was issued (at
+    // most one use of each stage, as the copies wait for the MMAs), so that only the bytes are waited for, and
+    // one more commit tracks all MMAs.  The first of these waits that runs out ends them: then copies or MMAs
+    // have not moved for a second, and no wait would bring them to an end.
     tc::fence_before();
     __syncthreads();
-    if (s_fail) {
+    if (waits.fail) {
+        if (warp >= kMxSf0 && lane == 0)
+            for (uint32_t n = 2 * sf_steps + ((warp - kMxSf0) >> 2); n < issued; n += 2) tc::mbar_arrive(&full[n % stages]);
+        if (warp == 1 && tc::elect_one()) tc::commit(&drained);   // (the lane that issued them)
+        __syncthreads();
         if (tid == 0) {
-            for (uint32_t n = issued > stages ? issued - stages : 0; n < issued; ++n) tc::mbar_wait(&full[n % stages], n / stages);
-            constexpr uint32_t kPairs = stages / Cfg::kPair;
-            for (uint32_t n = committed > kPairs ? committed - kPairs : 0; n < committed; ++n)
-                tc::mbar_wait(&empty[n % kPairs], n / kPairs);
+            bool ok = tc::mbar_wait(&drained, 0);
+            for (uint32_t n = issued > stages ? issued - stages : 0; n < issued && ok; ++n) ok = tc::mbar_wait(&full[n % stages], n / stages);
         }
         __syncthreads();
     }

@@ -67,14 +67,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t n) {
     }
 }
 
-// The same by a whole warp, all lanes with one answer; also gives up once *fail is set.
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t n, const volatile int* fail) {
+// The same by a whole warp, all lanes with one answer, for at most w->limit_ns; also gives up once w->fail is set.
+// (The first try suspends the warp for some microseconds, so that few waits come to the loop.)
+struct Waits {
+    int fail;
+    long long limit_ns;
+};
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t n, const volatile Waits* w) {
     const uint32_t parity = n & 1u;
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     const long long t0 = global_ns();
-    for (uint32_t i = 1;; ++i) {
+    for (uint32_t i = 0;; ++i) {
+        if ((i & 63u) == 0 && __any_sync(0xffffffffu, w->fail || global_ns() - t0 > w->limit_ns)) return false;
         if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        if ((i & 63u) == 0 && __any_sync(0xffffffffu, *fail || global_ns() - t0 > kWaitLimitNs)) return false;
     }
 }
 
