@@ -207,18 +207,32 @@ def _mxfp4_size(rows: int, cols: int) -> int:
     return (rows * cols // 2 + 4 * rows * ((cols + 127) // 128) + 15) // 16 * 16
 
 
-def _operand(name: str, t, dtype, numel: int | None = None) -> int | None:
-    """The pointer of an operand, checked: contiguous device memory of the type and size that the
-    entry point reads or writes (the C side sees only a pointer)."""
+def _operand(name: str, t, dtype, dev: int, numel: int | None = None) -> int | None:
+    """The pointer of an operand, checked: contiguous memory of device `dev` (the first operand's), of the
+    type and size that the entry point reads or writes (the C side sees only a pointer)."""
     if t is None:
         return None
-    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (numel is None or t.numel() == numel):
+    if t.dtype is dtype and t.get_device() == dev >= 0 and t.is_contiguous() and (numel is None or t.numel() == numel):
         return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor on the GPU")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on device {t.get_device()}, the first operand on device {dev}")
     raise ValueError(f"{name} must hold {numel} values, not {t.numel()}")
+
+
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _stream_on(dev: int) -> int:
+    """The current stream, for operands on device `dev`: a kernel runs on the current device."""
+    cur = _current_device()
+    if cur != dev:
+        raise ValueError(f"the operands are on device {dev}, and the current device is {cur}")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 @_on_stream
@@ -237,14 +251,15 @@ def quantize_mxfp4(x, rows=None, out=None):
     elif len(shape) != 2:
         n = x.numel() // max(1, x_rows * cols)
     per = _mxfp4_size(n_rows, cols)
-    src = _operand("x", x, x.dtype)
+    dev = x.get_device()
+    src = _operand("x", x, x.dtype, dev)
     if out is None:
         out = torch.empty((n, per), dtype=torch.uint8, device=x.device)
         dst = out.data_ptr()
     else:
-        dst = _operand("out", out, torch.uint8, n * per)
+        dst = _operand("out", out, torch.uint8, dev, n * per)
     _check("moe_quantize_mxfp4", lib().moe_quantize_mxfp4(
-        src, xt, x_rows, _operand("rows", rows, torch.int32), n, n_rows, cols, dst, _stream()))
+        src, xt, x_rows, _operand("rows", rows, torch.int32, dev), n, n_rows, cols, dst, _stream_on(dev)))
     return out
 
 
@@ -254,14 +269,15 @@ def dequantize_mxfp4(q, rows: int, cols: int, dtype=None, out=None):
     dtype float32 (the default) or bfloat16."""
     shape = q.shape
     n = shape[0] if len(shape) == 2 else 1
-    src = _operand("q", q, torch.uint8, n * _mxfp4_size(rows, cols))
+    dev = q.get_device()
+    src = _operand("q", q, torch.uint8, dev, n * _mxfp4_size(rows, cols))
     if out is None:
         out = torch.empty((n, rows, cols) if len(shape) == 2 else (rows, cols), dtype=dtype or torch.float32,
                           device=q.device)
         dst = out.data_ptr()
     else:
-        dst = _operand("out", out, out.dtype, n * rows * cols)
-    _check("moe_dequantize_mxfp4", lib().moe_dequantize_mxfp4(src, n, rows, cols, dst, _x_dtype(out), _stream()))
+        dst = _operand("out", out, out.dtype, dev, n * rows * cols)
+    _check("moe_dequantize_mxfp4", lib().moe_dequantize_mxfp4(src, n, rows, cols, dst, _x_dtype(out), _stream_on(dev)))
     return out
 
 
@@ -279,24 +295,24 @@ def mxfp4_matmul(xq, wq, offsets, rows: int, n: int, cols: int, act: str = "none
     takes its error word with it: pass one to be able to ask device_status."""
     shape = wq.shape
     E = shape[0] if len(shape) == 2 else 1
-    width = n // 2 if act == "swiglu" else n
+    width, dev = n // 2 if act == "swiglu" else n, xq.get_device()
     if out is None:
         out = torch.empty((rows, width), dtype=dtype or torch.float32, device=xq.device)
     if workspace is None:
         workspace = mxfp4_workspace(xq.device)
     _check("moe_mxfp4_matmul", lib().moe_mxfp4_matmul(
-        _operand("xq", xq, torch.uint8, _mxfp4_size(rows, cols)), rows,
-        _operand("wq", wq, torch.uint8, E * _mxfp4_size(n, cols)), E, n, cols,
-        _operand("offsets", offsets, torch.int32, E + 1), MATMUL_ACT[act],
-        _operand("out", out, out.dtype, rows * width), _x_dtype(out),
-        _operand("workspace", workspace, torch.uint8), workspace.numel(), _stream()))
+        _operand("xq", xq, torch.uint8, dev, _mxfp4_size(rows, cols)), rows,
+        _operand("wq", wq, torch.uint8, dev, E * _mxfp4_size(n, cols)), E, n, cols,
+        _operand("offsets", offsets, torch.int32, dev, E + 1), MATMUL_ACT[act],
+        _operand("out", out, out.dtype, dev, rows * width), _x_dtype(out),
+        _operand("workspace", workspace, torch.uint8, dev), workspace.numel(), _stream_on(dev)))
     return out
 
 
-def _mask_operand(mask, T: int):
+def _mask_operand(mask, dev: int, T: int):
     if mask is None:
         return None
-    return _operand("mask", mask, torch.bool if mask.dtype is torch.bool else torch.uint8, T)
+    return _operand("mask", mask, torch.bool if mask.dtype is torch.bool else torch.uint8, dev, T)
 
 
 @functools.lru_cache(maxsize=64)
@@ -312,23 +328,24 @@ def balance_loss(logits, idx, mask=None, n_seq: int = 1, workspace=None):
     (T, E), k = logits.shape, idx.shape[-1]
     if n_seq < 1 or T % n_seq:
         raise ValueError(f"{T} tokens are not {n_seq} sequences of one length")
-    lt, lp, ip = _x_dtype(logits), _operand("logits", logits, logits.dtype), _operand("idx", idx, torch.int32, T * k)
-    mp, dev, f32, i32 = _mask_operand(mask, T), logits.device, torch.float32, torch.int32
+    lt, dev = _x_dtype(logits), logits.get_device()
+    lp, ip = _operand("logits", logits, logits.dtype, dev), _operand("idx", idx, torch.int32, dev, T * k)
+    mp, where, f32, i32 = _mask_operand(mask, dev, T), logits.device, torch.float32, torch.int32
     new = torch.empty if T else torch.zeros    # zeros where the library launches nothing
-    loss = new(1, dtype=f32, device=dev)
-    counts = new((n_seq, E), dtype=i32, device=dev)
-    prob = new((n_seq, E), dtype=f32, device=dev)
-    tokens = new(n_seq, dtype=i32, device=dev)
+    loss = new(1, dtype=f32, device=where)
+    counts = new((n_seq, E), dtype=i32, device=where)
+    prob = new((n_seq, E), dtype=f32, device=where)
+    tokens = new(n_seq, dtype=i32, device=where)
     if workspace is None:
         wp, nbytes = None, _balance_bytes(n_seq, T // n_seq, E)
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=where)
             wp = workspace.data_ptr()
     else:
-        wp, nbytes = _operand("workspace", workspace, torch.uint8), workspace.numel()
+        wp, nbytes = _operand("workspace", workspace, torch.uint8, dev), workspace.numel()
     _check("moe_balance_loss", lib().moe_balance_loss(
         lp, lt, ip, mp, n_seq, T // n_seq, E, k, loss.data_ptr(), counts.data_ptr(), prob.data_ptr(),
-        tokens.data_ptr(), wp, nbytes, _stream()))
+        tokens.data_ptr(), wp, nbytes, _stream_on(dev)))
     return loss, counts, prob, tokens
 
 
@@ -340,16 +357,17 @@ def balance_loss_backward(logits, counts, tokens, grad_loss, k: int, mask=None, 
     n_seq = tokens.numel()
     if n_seq < 1 or T % n_seq:
         raise ValueError(f"{T} tokens are not {n_seq} sequences of one length")
-    lt, lp = _x_dtype(logits), _operand("logits", logits, logits.dtype)
+    lt, dev = _x_dtype(logits), logits.get_device()
+    lp = _operand("logits", logits, logits.dtype, dev)
     if out is None:
         out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
         op = out.data_ptr()
     else:
-        op = _operand("out", out, logits.dtype, T * E)
+        op = _operand("out", out, logits.dtype, dev, T * E)
     _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
-        lp, lt, _operand("counts", counts, torch.int32, n_seq * E), _operand("tokens", tokens, torch.int32),
-        _mask_operand(mask, T), _operand("grad_loss", grad_loss, torch.float32, 1), n_seq, T // n_seq, E, k, op,
-        _stream()))
+        lp, lt, _operand("counts", counts, torch.int32, dev, n_seq * E), _operand("tokens", tokens, torch.int32, dev),
+        _mask_operand(mask, dev, T), _operand("grad_loss", grad_loss, torch.float32, dev, 1), n_seq, T // n_seq, E, k, op,
+        _stream_on(dev)))
     return out
 
 
