@@ -10,8 +10,9 @@
 // numbers.  As sum p = 1 a constant may be taken off f first: with f_e - 1/E, which is formed from
 // the integer counts, (E counts_e - k n_s) / (E k n_s), nothing cancels.
 //
-// One wave of CTAs, each with an equal run of the batch's tokens, whatever the sequences' length (chunks of
-// one sequence left up to a third of the SMs idle in the last wave: 16 x 4096 x 512 fp32 forward 43 us).
+// One wave of CTAs (of the largest batches' forward pass several), each with an equal run of the batch's tokens,
+// whatever the sequences' length (chunks of one sequence left up to a third of the SMs idle in the last wave: 16 x
+// 4096 x 512 fp32 forward 43 us).
 // No floating-point atomics: every part of a run that lies in one sequence writes a record of partial sums,
 // and the records of a sequence are added in order.
 //
@@ -20,8 +21,9 @@
 // a lane and a warp takes up to 16 rows of a small router at once.  The next row's logits and expert
 // indices are read before this row's softmax, and the mask of the row after it, so that no read waits for
 // another.
-// Measured (GB300), 16 sequences of 4096 tokens, 512 experts, top-22, fp32: forward 34.5 us (134 MB read), backward
-// 46 us (134 MB read and 134 MB written, 5.8 TB/s); 7 x 1021 tokens, 128 experts, bf16: 12 and 6 us, latency.
+// Measured (GB300), 16 sequences of 4096 tokens, 512 experts, top-22, fp32: forward 35.0 us (134 MB read), backward
+// 46.7 us (134 MB read and 134 MB written, 5.7 TB/s); 7 x 1021 tokens, 128 experts, bf16: 12.1 and 6.4 us, latency;
+// 65536 x 128 bf16 17.4 and 16.5, 32768 x 256 fp32 17.4 and 15.9 us, the forward's share of its reduction kernel.
 #include <algorithm>
 
 #include "common.cuh"
@@ -441,7 +443,8 @@ BalRuns bal_runs(int64_t T, int ctas_per_sm, int groups, int passes) {
 }
 
 // Two rows a warp up to 256 experts: half the shuffles a row and two chains at once (65536 x 128 bf16, us: forward
-// 23.6 -> 19.7, backward 16.6 -> 13.8; 32768 x 256 fp32: forward 20.1 -> 16.5).
+// 23.6 -> 19.7, backward 16.6 -> 13.8; 32768 x 256 fp32: forward 20.1 -> 16.5).  Ten values a lane in place of 16 up to
+// 320 experts: 32768 x 257 fp32 forward 26.4 -> 23.4, backward 20.0 -> 18.1; 65536 x 319 32.8 -> 27.6, 36.8 -> 35.3.
 template <typename F>
 cudaError_t with_row(int64_t E, F f) {
     if (E % 4 == 0) {

@@ -7,8 +7,8 @@
 // fp32 bits and 2^-X is a power of two in fp32's normal range (-X is in [-125, 127]).
 //
 // Measured (GB300): quantising 45056 x 2816 fp32 85.8 us, 6.7 TB/s read and written, the rate of a copy; 4096
-// gathered rows x 2816 bf16 from L2 8.7 us, bound by instructions.  The decode of the former to fp32 105 us, 5.5
-// TB/s, seven eighths of it stores.
+// rows x 2816 bf16 from L2 8.2 us (gathered 8.7), bound by instructions; 45056 x 2816 bf16 64.0 us, 5.0 TB/s.  The
+// decode of the same to fp32 92 us, 6.2 TB/s, seven eighths of it stores, to bf16 58.8 us, 5.5 TB/s.
 #include <algorithm>
 
 #include "mxfp4.cuh"
@@ -141,7 +141,7 @@ struct MxItems {
     int64_t slab_rows;
 };
 
-// CTAs per SM.  fp32: with 4 (up to 64 registers) 45056 x 2816 takes 95 us, with 6 (40) 102; bf16: 4096 x 2816 from
+// CTAs per SM.  fp32: with 4 (up to 64 registers) 45056 x 2816 took 95 us, with 6 (40) 102; bf16: 4096 x 2816 from
 // L2 8.7 and 7.3.
 constexpr int mx_decode_ctas(bool f32) { return f32 ? 4 : 6; }
 

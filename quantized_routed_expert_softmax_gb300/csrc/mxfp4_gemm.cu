@@ -27,10 +27,10 @@
 // and not stored, and the last panel's blocks past K hold 2^0.
 //
 // Decode and short prefills are bound by the weights' bytes: up of 512 latent experts (1024 -> 2688, ReLU^2)
-// for 32 tokens 76.6 us, 7.4 TB/s of the bytes it cannot do without; gate.up (2816 -> 2 x 704) of 128 experts for
-// 512 tokens 48.2 us, 5.8 TB/s.  Long prefills are bound by storing the output while tiles come from L2: down
-// (704 -> 2816) for 8191 tokens 114 us, 4.6 TB/s; 83 us without its stores and 71 us without its epilogue.  One
-// token (16.9 MB from L2 or HBM over 88 CTAs) takes 6.2 us, most of it the chain offsets -> items -> first
+// for 32 tokens 77.2 us, 6.5 TB/s (499 MB of the experts that have rows, every byte read once); gate.up (2816 -> 2 x
+// 704) of 128 experts for 512 tokens 48.0 us, 5.9 TB/s.  Long prefills are bound by storing the output while tiles come
+// from L2: down (704 -> 2816) for 8191 tokens 114 us, 4.6 TB/s (into fp32 157); 83 us without its stores and 71 us
+// without its epilogue.  One token (16.9 MB from L2 or HBM over 88 CTAs) takes 6.1 us, most of it the chain offsets -> items -> first
 // tiles -> 11 steps -> epilogue.
 // What it took to get there, 512-expert up for 32 tokens / down for 8191 tokens, us: scales by asynchronous copies
 // and tcgen05.cp 176 / 240; scales through registers 157 / 260; role branches on a uniform warp number, which
