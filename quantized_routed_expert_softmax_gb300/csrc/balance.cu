@@ -23,7 +23,7 @@
 // another.
 // Measured (GB300), 16 sequences of 4096 tokens, 512 experts, top-22, fp32: forward 35.0 us (134 MB read), backward
 // 46.7 us (134 MB read and 134 MB written, 5.7 TB/s); 7 x 1021 tokens, 128 experts, bf16: 12.1 and 6.4 us, latency;
-// 65536 x 128 bf16 17.4 and 16.5, 32768 x 256 fp32 17.4 and 15.9 us, the forward's share of its reduction kernel.
+// 65536 x 128 bf16 17.4 and 16.5, 32768 x 256 fp32 17.4 and 15.9 us, much of the forward's in its reduction kernel.
 #include <algorithm>
 
 #include "common.cuh"
