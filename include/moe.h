@@ -56,7 +56,7 @@ typedef enum {
     MOE_ERR_DEVICE_CHECK = 7   /* a kernel recorded an error in the workspace (see below) */
 } moe_status;
 
-/* NONE: moe_mxfp4_matmul only (a layer has an activation). */
+/* NONE: moe_mxfp4_matmul and moe_int8_matmul only (a layer has an activation). */
 typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_RELU2 = 1, MOE_ACT_NONE = 2 } moe_act;
 /* Expert weight formats.  INT8PC: per-channel int8 (the Inferentia page, "Squeezing a 26B MoE
  * onto the cheapest Inferentia instance", section "Wall 1: the memory math": experts in int8
@@ -117,7 +117,11 @@ typedef enum { MOE_PATH_AUTO = 0, MOE_PATH_GEMV = 1, MOE_PATH_GEMM = 2 } moe_pat
  * Q8_0 codec (see moe_quantize_act_q8_0), and every weight row meets the coded values: per
  * block, the 32 code products summed exactly, times both fp16 scales, the blocks summed in
  * fp32.  Routing still reads the unquantised x.  Q8_0 weights only. */
-typedef enum { MOE_ACTQ_NONE = 0, MOE_ACTQ_Q8_0 = 1 } moe_act_quant;
+/* INT8: per-channel int8 experts (MOE_W_INT8PC, else MOE_ERR_UNSUPPORTED) over rows that are coded in int8
+ * too, one scale a row: x for gate.up, h for down, by moe_quantize_int8; runs moe_int8_matmul's kernels at
+ * every T, with path AUTO and weights in device memory (else MOE_ERR_UNSUPPORTED).  Routing still reads the
+ * unquantised x.  (2 is no quantiser.) */
+typedef enum { MOE_ACTQ_NONE = 0, MOE_ACTQ_Q8_0 = 1, MOE_ACTQ_INT8 = 3 } moe_act_quant;
 
 /* Bytes of one quantised matrix: rows*cols/32*34 (Q8_0), rows*cols/2 + rows*cols/16
  * (NVFP4).  Returns 0 for non-positive or non-multiple sizes. */
@@ -242,6 +246,97 @@ size_t moe_mxfp4_matmul_workspace_bytes(void);
 moe_status moe_mxfp4_matmul(const void* xq, int64_t P, const void* wq, int64_t E, int64_t N, int64_t K,
                             const int32_t* offsets, moe_act act, void* out, moe_dtype ot, void* workspace,
                             size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * int8 matrices with one scale a row, for weights and expert inputs alike.  [rows, cols], cols a multiple of
+ * 32, any number of rows: the fp32 scale of every row (4 * rows bytes, rounded up to a multiple of 16; the
+ * bytes in between are not read, not written), then panel b = columns 32b .. 32b+31: the 32 int8 codes of
+ * every row.  With a multiple of 4 rows that is INT8PC in MOE_LAYOUT_DEVICE, byte for byte, so weights that
+ * moe_quantize_int8pc packed are such matrices.  A stack of matrices is the matrices back to back,
+ * moe_int8_bytes(rows, cols) apart.  moe_int8_bytes returns 0 for sizes that are not positive, not a
+ * multiple or too large.
+ */
+size_t moe_int8_bytes(int64_t rows, int64_t cols);
+
+/*
+ * moe_quantize_int8 -- rows (tokens, or a weight matrix's channels) to int8.  Per row:
+ *   s = amax/127 (fp32 IEEE divide); q = round-half-away(x / s) (fp32 IEEE divide), 0 when s = 0.
+ * A row that holds a NaN or an infinity gets a NaN scale and zero codes: all its values stand for NaN.
+ * x         device, fp32 or bf16 (xt): [n_mat][rows][cols], or [x_rows][cols] when src_rows is given.
+ * src_rows  device int32 [rows], or NULL: row r of the result is row src_rows[r] of x (n_mat 1).  An index
+ *           outside [0, x_rows) gives a row of zeros.  x_rows is not read without src_rows.
+ * dst       device, n_mat * moe_int8_bytes(rows, cols) bytes.
+ * rows = 0 or n_mat = 0 returns MOE_OK, launches nothing and touches no buffer (they may be NULL).
+ * Errors: INVALID_ARG (NULL, bad dtype, src_rows with n_mat > 1), SHAPE (cols a positive multiple of 32 up
+ * to 65536, rows up to 2^25, n_mat up to 65535), ALIGNMENT, CUDA.
+ */
+moe_status moe_quantize_int8(const void* x, moe_dtype xt, int64_t x_rows, const int32_t* src_rows, int64_t n_mat,
+                             int64_t rows, int64_t cols, void* dst, moe_stream_t stream);
+
+/*
+ * moe_dequantize_int8 -- the values q * s that the codes of n_mat int8 matrices stand for, [n_mat][rows][cols]
+ * in fp32 or bf16 (ot), rounded once.  Errors: as moe_quantize_int8.
+ */
+moe_status moe_dequantize_int8(const void* src, int64_t n_mat, int64_t rows, int64_t cols, void* out, moe_dtype ot,
+                               moe_stream_t stream);
+
+/*
+ * moe_int8_matmul -- the expert-indexed product of int8 rows with per-channel int8 weights, the activation
+ * fused:
+ *   z[r][n] = sx[r] * sw[e(r)][n] * sum_i xq[r][i] * wq[e(r)][n][i]
+ * (the code products of up to 1024 columns summed exactly, those sums in fp32), then NONE, SWIGLU or RELU2
+ * as in moe_mxfp4_matmul.
+ * xq       device, one int8 matrix [P][K]: the rows sorted by expert.
+ * wq       device, E int8 matrices [N][K] back to back (SWIGLU: rows 0..N/2-1 gate, the rest up).
+ * offsets  device int32 [E+1]: expert e owns rows offsets[e] .. offsets[e+1]-1, or NULL with E = 1: every
+ *          row.  Values are clamped to [0, P], and a reversed range is empty; with increasing offsets no row
+ *          has two experts.  Rows outside [offsets[0], offsets[E]) are left as they were.
+ * out      device, [P][N] or [P][N/2], fp32 or bf16 (ot; rounded once).
+ * workspace  device, moe_int8_matmul_workspace_bytes() bytes, zero-filled before its first use: an error word
+ *          that moe_get_device_status() reads and clears (2: a wait ran past its limit, a second unless the
+ *          int64 at byte 32 is not 0; out is not valid).  Calls that may overlap can share it.
+ * The same inputs give the same bits.  P = 0 returns MOE_OK, launches nothing and touches no buffer.
+ * Errors: INVALID_ARG (NULL, bad enum, offsets NULL with E > 1), SHAPE (K a positive multiple of 32 up to
+ * 65536; P up to 2^25; N from 1 to 131072, for SWIGLU a multiple of 64; E up to 1024), ALIGNMENT, WORKSPACE,
+ * CUDA.
+ */
+size_t moe_int8_matmul_workspace_bytes(void);
+moe_status moe_int8_matmul(const void* xq, int64_t P, const void* wq, int64_t E, int64_t N, int64_t K,
+                           const int32_t* offsets, moe_act act, void* out, moe_dtype ot, void* workspace,
+                           size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_ffn_forward, moe_ffn_backward -- the gated feed-forward block over bf16 weights, for trained experts and
+ * (E = 1) for a dense block or a shared expert, with its gradients.  Row r has expert e(r):
+ *   z = Wgu[e] x;  h = silu(z_gate) * z_up  (SWIGLU; gate rows 0..f-1 first)  or  max(z, 0)^2  (RELU2);
+ *   y = Wd[e] h.
+ * Backward, from dy:  dh = Wd^T dy;  dz = dh * dh/dz;  dx = Wgu^T dz;
+ *   dWgu[e] = sum over the expert's rows of dz x^T;  dWd[e] = sum of dy h^T  (0 for an expert without rows).
+ * Sums are fp32; z, h, y, dz, dx are rounded to bf16 once each, and the activation reads z before its rounding
+ * (forward), its gradient the stored z.  No atomics: the same inputs give the same bits.
+ * x, y, dy, dx   device bf16 [P][d], rows sorted by expert.   w_gate_up  device bf16 [E][2f][d] (RELU2:
+ *           [E][f][d]).   w_down  device bf16 [E][d][f].
+ * z, h      device bf16 [P][2f] (RELU2: [P][f]) and [P][f]: kept by the forward pass for the backward one.
+ *           Forward: z may be NULL (not written), h may be NULL (then in the workspace).
+ * offsets   device int32 [E+1], or NULL with E = 1, as in moe_int8_matmul.  Rows outside [offsets[0],
+ *           offsets[E]) are left as they were in y, z, h and dx, and have no part in the weights' gradients.
+ * dx, dw_gate_up, dw_down   written; each may be NULL (not computed).   dw_*  in the layout of the weights, bf16
+ *           or fp32 (gt).
+ * workspace device, moe_ffn_workspace_bytes(P, f, act, backward) bytes (forward with h given: 256), 256-byte
+ *           aligned, zero-filled before its first use; holds an error word as moe_int8_matmul's does, and
+ *           scratch.  Calls that may overlap need workspaces of their own.
+ * P = 0: MOE_OK; the forward pass launches nothing, the backward pass clears dw_gate_up and dw_down.
+ * Errors: INVALID_ARG (NULL, bad enum, offsets NULL with E > 1), SHAPE (d and f positive multiples of 16 up to
+ * 65536 and 32768; P up to 2^25; E from 1 to 1024), ALIGNMENT, WORKSPACE, CUDA.
+ */
+size_t moe_ffn_workspace_bytes(int64_t P, int64_t f, moe_act act, int32_t backward);
+moe_status moe_ffn_forward(const uint16_t* x, int64_t P, const uint16_t* w_gate_up, const uint16_t* w_down, int64_t E,
+                           int64_t d, int64_t f, const int32_t* offsets, moe_act act, uint16_t* y, uint16_t* z,
+                           uint16_t* h, void* workspace, size_t ws_bytes, moe_stream_t stream);
+moe_status moe_ffn_backward(const uint16_t* dy, const uint16_t* x, int64_t P, const uint16_t* w_gate_up,
+                            const uint16_t* w_down, int64_t E, int64_t d, int64_t f, const int32_t* offsets, moe_act act,
+                            const uint16_t* z, const uint16_t* h, uint16_t* dx, void* dw_gate_up, void* dw_down,
+                            moe_dtype gt, void* workspace, size_t ws_bytes, moe_stream_t stream);
 
 /*
  * moe_balance_loss -- how evenly the router loads its experts, over n_seq sequences of seq_len tokens

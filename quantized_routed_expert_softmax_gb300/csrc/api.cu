@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "int8.cuh"
 #include "mxfp4.cuh"
 
 namespace moe {
@@ -50,6 +51,17 @@ cudaError_t launch_balance_loss(const void*, int, const int32_t*, const uint8_t*
                                 int32_t*, float*, int32_t*, void*, cudaStream_t);
 cudaError_t launch_balance_backward(const void*, int, const int32_t*, const int32_t*, const uint8_t*, const float*,
                                     int64_t, int64_t, int64_t, int, void*, cudaStream_t);
+// (int8.cu, int8_gemm.cu, ffn.cu)
+cudaError_t launch_int8_quantize(const void*, int, int64_t, const int32_t*, int, int64_t, int64_t, int64_t, void*, int,
+                                 cudaStream_t);
+cudaError_t launch_int8_dequantize(const void*, int64_t, int64_t, int64_t, void*, int, int, cudaStream_t);
+cudaError_t launch_int8_matmul(const void*, int64_t, const void*, int64_t, int64_t, int64_t, const int32_t*, int, void*,
+                               int, int32_t*, int, cudaStream_t);
+cudaError_t launch_ffn_forward(const uint16_t*, int64_t, const uint16_t*, const uint16_t*, int64_t, int64_t, int64_t,
+                               const int32_t*, int, uint16_t*, uint16_t*, uint16_t*, int32_t*, int, cudaStream_t);
+cudaError_t launch_ffn_backward(const uint16_t*, const uint16_t*, int64_t, const uint16_t*, const uint16_t*, int64_t,
+                                int64_t, int64_t, const int32_t*, int, const uint16_t*, const uint16_t*, uint16_t*,
+                                uint16_t*, void*, void*, int, int32_t*, int, cudaStream_t);
 
 namespace {
 
@@ -104,12 +116,26 @@ cudaError_t ensure_configured(int* num_sms) {
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 constexpr size_t kMxWorkspaceBytes = 256;   // the MXFP4 product's error word
+constexpr size_t kErrWorkspaceBytes = 256;  // the error word of the int8 product and of the feed-forward block
 
 bool dtype_ok(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16; }
 
 bool mx_shape_ok(int64_t rows, int64_t cols) {
     return rows >= 0 && rows <= kMaxTokens * kMaxK && cols > 0 && cols % 32 == 0 && cols <= kMaxDim;
 }
+
+// Columns of the feed-forward block's pre-activations z.
+int64_t ffn_z_cols(int64_t f, int act) { return act == MOE_ACT_SWIGLU ? 2 * f : f; }
+
+moe_status ffn_shape(int64_t P, int64_t E, int64_t d, int64_t f, int act) {
+    if (act != MOE_ACT_SWIGLU && act != MOE_ACT_RELU2) return MOE_ERR_INVALID_ARG;
+    if (P < 0 || P > kMaxTokens * kMaxK || E < 1 || E > kMaxE) return MOE_ERR_SHAPE;
+    if (d < 16 || d > kMaxDim || d % 16 != 0 || f < 16 || f > kMaxF || f % 16 != 0) return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+// The block's workspace: the error word, then scratch of P rows of `cols` bf16 values.
+size_t ffn_scratch(int64_t P, int64_t cols) { return kErrWorkspaceBytes + round_up(2 * static_cast<size_t>(P) * cols, 256); }
 
 // n_seq sequences of seq_len tokens over E experts (each factor bounded before the product is taken).
 moe_status balance_shape(int64_t n_seq, int64_t seq_len, int64_t E) {
@@ -644,6 +670,110 @@ moe_status moe_mxfp4_matmul(const void* xq, int64_t P, const void* wq, int64_t E
     if (ensure_configured(&num_sms) != cudaSuccess) return MOE_ERR_CUDA;
     return cuda_status(launch_mxfp4_matmul(xq, P, wq, E, N, K, offsets, act, out, ot, static_cast<int32_t*>(workspace),
                                            num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_int8_bytes(int64_t rows, int64_t cols) {
+    return mx_shape_ok(rows, cols) && rows > 0 ? static_cast<size_t>(i8_bytes(rows, cols)) : 0;
+}
+
+moe_status moe_quantize_int8(const void* x, moe_dtype xt, int64_t x_rows, const int32_t* src_rows, int64_t n_mat,
+                             int64_t rows, int64_t cols, void* dst, moe_stream_t stream) {
+    if (n_mat < 0 || !dtype_ok(xt)) return MOE_ERR_INVALID_ARG;
+    if (src_rows && (n_mat > 1 || x_rows < 0)) return MOE_ERR_INVALID_ARG;
+    if (!mx_shape_ok(rows, cols) || n_mat > 65535) return MOE_ERR_SHAPE;
+    if (n_mat == 0 || rows == 0) return MOE_OK;
+    if (!x || !dst) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(dst) || (reinterpret_cast<uintptr_t>(src_rows) & 3u)) return MOE_ERR_ALIGNMENT;
+    int num_sms = 0;
+    if (ensure_configured(&num_sms) != cudaSuccess) return MOE_ERR_CUDA;
+    return cuda_status(launch_int8_quantize(x, xt, x_rows, src_rows, 1, n_mat, rows, cols, dst, num_sms,
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_dequantize_int8(const void* src, int64_t n_mat, int64_t rows, int64_t cols, void* out, moe_dtype ot,
+                               moe_stream_t stream) {
+    if (n_mat < 0 || !dtype_ok(ot)) return MOE_ERR_INVALID_ARG;
+    if (!mx_shape_ok(rows, cols) || n_mat > 65535) return MOE_ERR_SHAPE;
+    if (n_mat == 0 || rows == 0) return MOE_OK;
+    if (!src || !out) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(src) || !aligned16(out)) return MOE_ERR_ALIGNMENT;
+    int num_sms = 0;
+    if (ensure_configured(&num_sms) != cudaSuccess) return MOE_ERR_CUDA;
+    return cuda_status(launch_int8_dequantize(src, n_mat, rows, cols, out, ot, num_sms,
+                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_int8_matmul_workspace_bytes(void) { return kErrWorkspaceBytes; }
+
+moe_status moe_int8_matmul(const void* xq, int64_t P, const void* wq, int64_t E, int64_t N, int64_t K,
+                           const int32_t* offsets, moe_act act, void* out, moe_dtype ot, void* workspace,
+                           size_t ws_bytes, moe_stream_t stream) {
+    if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU && act != MOE_ACT_RELU2) return MOE_ERR_INVALID_ARG;
+    if (!dtype_ok(ot) || E < 1) return MOE_ERR_INVALID_ARG;
+    if (!mx_shape_ok(P, K) || E > kMaxE || N < 1 || N > 2 * kMaxDim) return MOE_ERR_SHAPE;
+    if (act == MOE_ACT_SWIGLU && N % 64 != 0) return MOE_ERR_SHAPE;
+    if (P == 0) return MOE_OK;
+    if (!xq || !wq || !out || (!offsets && E != 1)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(xq) || !aligned16(wq) || !aligned16(out) || (reinterpret_cast<uintptr_t>(offsets) & 3u))
+        return MOE_ERR_ALIGNMENT;
+    if (!workspace || ws_bytes < kErrWorkspaceBytes) return MOE_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MOE_ERR_ALIGNMENT;
+    int num_sms = 0;
+    if (ensure_configured(&num_sms) != cudaSuccess) return MOE_ERR_CUDA;
+    return cuda_status(launch_int8_matmul(xq, P, wq, E, N, K, offsets, act, out, ot, static_cast<int32_t*>(workspace),
+                                          num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_ffn_workspace_bytes(int64_t P, int64_t f, moe_act act, int32_t backward) {
+    if (ffn_shape(P, 1, 16, f, act) != MOE_OK) return 0;
+    return ffn_scratch(P, backward ? ffn_z_cols(f, act) : f);
+}
+
+moe_status moe_ffn_forward(const uint16_t* x, int64_t P, const uint16_t* w_gate_up, const uint16_t* w_down, int64_t E,
+                           int64_t d, int64_t f, const int32_t* offsets, moe_act act, uint16_t* y, uint16_t* z,
+                           uint16_t* h, void* workspace, size_t ws_bytes, moe_stream_t stream) {
+    const moe_status st = ffn_shape(P, E, d, f, act);
+    if (st != MOE_OK) return st;
+    if (P == 0) return MOE_OK;
+    if (!x || !w_gate_up || !w_down || !y || (!offsets && E != 1)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(w_gate_up) || !aligned16(w_down) || !aligned16(y) || !aligned16(z) || !aligned16(h) ||
+        (reinterpret_cast<uintptr_t>(offsets) & 3u))
+        return MOE_ERR_ALIGNMENT;
+    if (!workspace || ws_bytes < ffn_scratch(P, h ? 0 : f)) return MOE_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MOE_ERR_ALIGNMENT;
+    int num_sms = 0;
+    if (ensure_configured(&num_sms) != cudaSuccess) return MOE_ERR_CUDA;
+    if (!h) h = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + kErrWorkspaceBytes);
+    return cuda_status(launch_ffn_forward(x, P, w_gate_up, w_down, E, d, f, offsets, act, y, z, h,
+                                          static_cast<int32_t*>(workspace), num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_ffn_backward(const uint16_t* dy, const uint16_t* x, int64_t P, const uint16_t* w_gate_up,
+                            const uint16_t* w_down, int64_t E, int64_t d, int64_t f, const int32_t* offsets, moe_act act,
+                            const uint16_t* z, const uint16_t* h, uint16_t* dx, void* dw_gate_up, void* dw_down,
+                            moe_dtype gt, void* workspace, size_t ws_bytes, moe_stream_t stream) {
+    const moe_status st = ffn_shape(P, E, d, f, act);
+    if (st != MOE_OK) return st;
+    if (!dtype_ok(gt)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(dw_gate_up) || !aligned16(dw_down)) return MOE_ERR_ALIGNMENT;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (P == 0) {   // no rows: the weights' gradients are zero
+        const size_t b = (gt == MOE_F32 ? 4 : 2) * static_cast<size_t>(E * d);
+        cudaError_t e = dw_gate_up ? cudaMemsetAsync(dw_gate_up, 0, b * ffn_z_cols(f, act), s) : cudaSuccess;
+        if (e == cudaSuccess && dw_down) e = cudaMemsetAsync(dw_down, 0, b * f, s);
+        return cuda_status(e);
+    }
+    if (!dy || !x || !w_gate_up || !w_down || !z || !h || (!offsets && E != 1)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(x) || !aligned16(w_gate_up) || !aligned16(w_down) || !aligned16(z) || !aligned16(h) ||
+        !aligned16(dx) || (reinterpret_cast<uintptr_t>(offsets) & 3u))
+        return MOE_ERR_ALIGNMENT;
+    if (!workspace || ws_bytes < ffn_scratch(P, ffn_z_cols(f, act))) return MOE_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MOE_ERR_ALIGNMENT;
+    int num_sms = 0;
+    if (ensure_configured(&num_sms) != cudaSuccess) return MOE_ERR_CUDA;
+    uint16_t* dz = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + kErrWorkspaceBytes);
+    return cuda_status(launch_ffn_backward(dy, x, P, w_gate_up, w_down, E, d, f, offsets, act, z, h, dz, dx, dw_gate_up,
+                                           dw_down, gt, static_cast<int32_t*>(workspace), num_sms, s));
 }
 
 size_t moe_balance_workspace_bytes(int64_t n_seq, int64_t seq_len, int64_t E) {

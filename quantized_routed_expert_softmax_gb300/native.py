@@ -25,7 +25,7 @@ WFMT = {"q8_0": 0, "nvfp4": 1, "int8pc": 2, "mxfp4": 4}
 DTYPE_F32, DTYPE_BF16 = 0, 1
 LAYOUT = {"canonical": 0, "device": 1, "neuron": 2}
 PATH = {"auto": 0, "gemv": 1, "gemm": 2}
-ACT_QUANT = {"none": 0, "q8_0": 1}
+ACT_QUANT = {"none": 0, "q8_0": 1, "int8": 3}
 FLAG_HOST_GATE_UP, FLAG_HOST_DOWN = 1, 2
 
 # Every symbol include/moe.h declares.
@@ -37,7 +37,9 @@ EXPORTS = ["moe_q8_0_bytes", "moe_nvfp4_bytes", "moe_int8pc_bytes", "moe_quantiz
            "moe_layer_forward_noalloc", "moe_layer_forward_noalloc_status", "moe_stack_forward",
            "moe_stack_forward_launches",
            "moe_mxfp4_bytes", "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_mxfp4_matmul_workspace_bytes",
-           "moe_mxfp4_matmul", "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward"]
+           "moe_mxfp4_matmul", "moe_int8_bytes", "moe_quantize_int8", "moe_dequantize_int8",
+           "moe_int8_matmul_workspace_bytes", "moe_int8_matmul", "moe_ffn_workspace_bytes", "moe_ffn_forward",
+           "moe_ffn_backward", "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward"]
 
 
 class MoeError(RuntimeError):
@@ -100,6 +102,14 @@ def lib() -> ctypes.CDLL:
             "moe_dequantize_mxfp4": (I32, [P, I64, I64, I64, P, I32, P]),
             "moe_mxfp4_matmul_workspace_bytes": (SZ, []),
             "moe_mxfp4_matmul": (I32, [P, I64, P, I64, I64, I64, P, I32, P, I32, P, SZ, P]),
+            "moe_int8_bytes": (SZ, [I64, I64]),
+            "moe_quantize_int8": (I32, [P, I32, I64, P, I64, I64, I64, P, P]),
+            "moe_dequantize_int8": (I32, [P, I64, I64, I64, P, I32, P]),
+            "moe_int8_matmul_workspace_bytes": (SZ, []),
+            "moe_int8_matmul": (I32, [P, I64, P, I64, I64, I64, P, I32, P, I32, P, SZ, P]),
+            "moe_ffn_workspace_bytes": (SZ, [I64, I64, I32, I32]),
+            "moe_ffn_forward": (I32, [P, I64, P, P, I64, I64, I64, P, I32, P, P, P, P, SZ, P]),
+            "moe_ffn_backward": (I32, [P, P, I64, P, P, I64, I64, I64, P, I32, P, P, P, P, P, I32, P, SZ, P]),
             "moe_balance_workspace_bytes": (SZ, [I64, I64, I64]),
             "moe_balance_loss": (I32, [P, I32, P, P, I64, I64, I64, I32, P, P, P, P, P, SZ, P]),
             "moe_balance_loss_backward": (I32, [P, I32, P, P, P, P, I64, I64, I64, I32, P, P]),
@@ -307,6 +317,163 @@ def mxfp4_matmul(xq, wq, offsets, rows: int, n: int, cols: int, act: str = "none
         _operand("out", out, out.dtype, dev, rows * width), _x_dtype(out),
         _operand("workspace", workspace, torch.uint8, dev), workspace.numel(), _stream_on(dev)))
     return out
+
+
+def int8_bytes(rows: int, cols: int) -> int:
+    return int(lib().moe_int8_bytes(rows, cols))
+
+
+def _int8_size(rows: int, cols: int) -> int:
+    """int8_bytes for the operand checks."""
+    return (4 * rows + 15) // 16 * 16 + rows * cols
+
+
+@_on_stream
+def quantize_int8(x, rows=None, out=None):
+    """moe_quantize_int8: x [..., rows, cols] fp32 or bf16 -> uint8 [n_mat, bytes].
+
+    rows: int32 [n] row indices; the result is then one matrix of x's rows in that order (an index
+    outside x gives a row of zeros)."""
+    xt, shape = _x_dtype(x), x.shape
+    x_rows, cols = shape[-2], shape[-1]
+    n, n_rows = 1, x_rows
+    if rows is not None:
+        if len(shape) != 2:
+            raise ValueError("rows needs one matrix x [rows, cols]")
+        n_rows = rows.numel()
+    elif len(shape) != 2:
+        n = x.numel() // max(1, x_rows * cols)
+    per = _int8_size(n_rows, cols)
+    dev = x.get_device()
+    src = _operand("x", x, x.dtype, dev)
+    if out is None:
+        out = torch.empty((n, per), dtype=torch.uint8, device=x.device)
+        dst = out.data_ptr()
+    else:
+        dst = _operand("out", out, torch.uint8, dev, n * per)
+    _check("moe_quantize_int8", lib().moe_quantize_int8(
+        src, xt, x_rows, _operand("rows", rows, torch.int32, dev), n, n_rows, cols, dst, _stream_on(dev)))
+    return out
+
+
+@_on_stream
+def dequantize_int8(q, rows: int, cols: int, dtype=None, out=None):
+    """moe_dequantize_int8: uint8 [bytes] -> [rows, cols], or uint8 [n_mat, bytes] -> [n_mat, rows, cols];
+    dtype float32 (the default) or bfloat16."""
+    shape = q.shape
+    n = shape[0] if len(shape) == 2 else 1
+    dev = q.get_device()
+    src = _operand("q", q, torch.uint8, dev, n * _int8_size(rows, cols))
+    if out is None:
+        out = torch.empty((n, rows, cols) if len(shape) == 2 else (rows, cols), dtype=dtype or torch.float32,
+                          device=q.device)
+        dst = out.data_ptr()
+    else:
+        dst = _operand("out", out, out.dtype, dev, n * rows * cols)
+    _check("moe_dequantize_int8", lib().moe_dequantize_int8(src, n, rows, cols, dst, _x_dtype(out), _stream_on(dev)))
+    return out
+
+
+def int8_workspace(device="cuda"):
+    """A zero-filled workspace of moe_int8_matmul (device_status reads its error word)."""
+    return torch.zeros(int(lib().moe_int8_matmul_workspace_bytes()), dtype=torch.uint8, device=device)
+
+
+@_on_stream
+def int8_matmul(xq, wq, offsets, rows: int, n: int, cols: int, act: str = "none", dtype=None, out=None,
+                workspace=None):
+    """moe_int8_matmul: xq one int8 matrix [rows, cols] sorted by expert, wq uint8 [E, bytes] of int8 matrices
+    [n, cols] (quantize_int8, or quantize_int8pc in the device layout), offsets int32 [E + 1] (None with one
+    matrix) -> [rows, n], or [rows, n / 2] for act "swiglu"; dtype float32 (the default) or bfloat16.  Without
+    a workspace the call makes one, which takes its error word with it: pass one to be able to ask
+    device_status."""
+    shape = wq.shape
+    E = shape[0] if len(shape) == 2 else 1
+    width, dev = n // 2 if act == "swiglu" else n, xq.get_device()
+    if out is None:
+        out = torch.empty((rows, width), dtype=dtype or torch.float32, device=xq.device)
+    if workspace is None:
+        workspace = int8_workspace(xq.device)
+    _check("moe_int8_matmul", lib().moe_int8_matmul(
+        _operand("xq", xq, torch.uint8, dev, _int8_size(rows, cols)), rows,
+        _operand("wq", wq, torch.uint8, dev, E * _int8_size(n, cols)), E, n, cols,
+        _operand("offsets", offsets, torch.int32, dev, E + 1), MATMUL_ACT[act],
+        _operand("out", out, out.dtype, dev, rows * width), _x_dtype(out),
+        _operand("workspace", workspace, torch.uint8, dev), workspace.numel(), _stream_on(dev)))
+    return out
+
+
+def ffn_workspace(rows: int, f: int, act: str = "swiglu", backward: bool = False, device="cuda"):
+    """A zero-filled workspace of ffn_forward (and, with backward, of ffn_backward) for up to `rows` rows
+    (device_status reads its error word)."""
+    n = int(lib().moe_ffn_workspace_bytes(rows, f, ACT[act], int(backward)))
+    if n == 0:
+        raise MoeError("moe_ffn_workspace_bytes", 2)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _ffn_shape(x, w_gate_up, w_down, act: str):
+    """(P, E, d, f, columns of z) of the block's operands."""
+    P, d = x.shape
+    if w_gate_up.dim() not in (2, 3) or w_down.dim() != w_gate_up.dim():
+        raise ValueError("the weights must be [E, rows, cols] each, or one matrix each")
+    E, f = (w_down.shape[0] if w_down.dim() == 3 else 1), w_down.shape[-1]
+    nz = 2 * f if act == "swiglu" else f
+    if tuple(w_down.shape[-2:]) != (d, f) or tuple(w_gate_up.shape[-2:]) != (nz, d):
+        raise ValueError(f"rows of {d} values and act {act!r} need w_gate_up [{nz}, {d}] and w_down [{d}, {f}] matrices, "
+                         f"not {tuple(w_gate_up.shape)} and {tuple(w_down.shape)}")
+    return P, E, d, f, nz
+
+
+@_on_stream
+def ffn_forward(x, w_gate_up, w_down, offsets=None, act: str = "swiglu", save: bool = False, out=None, workspace=None):
+    """moe_ffn_forward: x bf16 [P, d] sorted by expert, w_gate_up bf16 [E, 2f, d] (act "relu2": [E, f, d]),
+    w_down bf16 [E, d, f], offsets int32 [E + 1] (None with one expert) -> y bf16 [P, d]; with save
+    (y, saved), saved = (z, h) for ffn_backward.  Rows that no expert owns are left as they are (in `out`;
+    a result that the call makes is not initialised there)."""
+    P, E, d, f, nz = _ffn_shape(x, w_gate_up, w_down, act)
+    bf, dev, where = torch.bfloat16, x.get_device(), x.device
+    xp = _operand("x", x, bf, dev)
+    gp, dp = _operand("w_gate_up", w_gate_up, bf, dev, E * nz * d), _operand("w_down", w_down, bf, dev, E * d * f)
+    op = _operand("offsets", offsets, torch.int32, dev, E + 1)
+    if out is None:
+        out = torch.empty((P, d), dtype=bf, device=where)
+    z = h = None
+    if save:
+        z, h = torch.empty((P, nz), dtype=bf, device=where), torch.empty((P, f), dtype=bf, device=where)
+    if workspace is None:
+        workspace = ffn_workspace(0 if save else P, f, act, device=where)
+    _check("moe_ffn_forward", lib().moe_ffn_forward(
+        xp, P, gp, dp, E, d, f, op, ACT[act], _operand("out", out, bf, dev, P * d), _ptr(z), _ptr(h),
+        _operand("workspace", workspace, torch.uint8, dev), workspace.numel(), _stream_on(dev)))
+    return (out, (z, h)) if save else out
+
+
+@_on_stream
+def ffn_backward(grad, x, w_gate_up, w_down, saved, offsets=None, act: str = "swiglu", dtype=None,
+                 need=(True, True, True), workspace=None):
+    """moe_ffn_backward: grad bf16 [P, d], the operands of ffn_forward and its saved (z, h) -> (dx bf16 [P, d],
+    dw_gate_up, dw_down), the weights' gradients in dtype bfloat16 (the default) or float32.  need: which of the
+    three are computed (None in the place of the others)."""
+    P, E, d, f, nz = _ffn_shape(x, w_gate_up, w_down, act)
+    bf, dev, where = torch.bfloat16, x.get_device(), x.device
+    z, h = saved
+    wt = dtype or bf
+    dx = torch.empty((P, d), dtype=bf, device=where) if need[0] else None
+    dgu = torch.empty(w_gate_up.shape, dtype=wt, device=where) if need[1] else None
+    dd = torch.empty(w_down.shape, dtype=wt, device=where) if need[2] else None
+    if workspace is None:
+        workspace = ffn_workspace(P, f, act, backward=True, device=where)
+    t = _X_DTYPE.get(wt)
+    if t is None:
+        raise TypeError("dtype must be float32 or bfloat16")
+    _check("moe_ffn_backward", lib().moe_ffn_backward(
+        _operand("grad", grad, bf, dev, P * d), _operand("x", x, bf, dev), P,
+        _operand("w_gate_up", w_gate_up, bf, dev, E * nz * d), _operand("w_down", w_down, bf, dev, E * d * f), E, d, f,
+        _operand("offsets", offsets, torch.int32, dev, E + 1), ACT[act], _operand("z", z, bf, dev, P * nz),
+        _operand("h", h, bf, dev, P * f), _ptr(dx), _ptr(dgu), _ptr(dd), t,
+        _operand("workspace", workspace, torch.uint8, dev), workspace.numel(), _stream_on(dev)))
+    return dx, dgu, dd
 
 
 def _mask_operand(mask, dev: int, T: int):
