@@ -1,132 +1,607 @@
-// ffn.cu -- the gated feed-forward block over bf16 weights, rows sorted by expert, forward and backward.
-#include <algorithm>
+// ffn.cu -- the gated feed-forward block over bf16 weights, rows sorted by expert, forward and backward, on the
+// 5th-generation tensor cores: bf16 MMAs by CTA pairs (tcgen05 cta_group::2), accumulators in tensor memory.
+//
+// All six products are out[n][m] = sum_k A(m, k) B(n, k), m the contiguous column of the result:
+//                                     A (M = 256 a pair)   B (N <= 256)           k
+//   z = x Wgu^T, h = act(z)           Wgu[e]   K-major     x        K-major       columns of x
+//   y = h Wd^T                        Wd[e]    K-major     h        K-major       neurons
+//   dh = dy Wd, dz = dh * dh/dz       Wd[e]    M-major     dy       K-major       columns of y
+//   dx = dz Wgu                       Wgu[e]   M-major     dz       K-major       columns of z
+//   dWgu[e] = dz^T x                  x        M-major     dz       N-major       the expert's rows
+//   dWd[e] = dy^T h                   h        M-major     dy       N-major       the expert's rows
+// TMA lays every tile down as the tensor core reads it in either order, so nothing is transposed in memory.  Tokens are
+// the MMA's N, which goes down to 32, so an expert with few rows does not pay for 256, and an expert's row tiles are
+// equally high.
+//
+// A persistent grid, a CTA pair per two SMs; warps have fixed roles, linked by mbarriers:
+//   warp 0      TMA: per K step of 64, the CTA's 128 rows of A and half of the tile's rows of B;
+//   warp 1      of CTA 0: one thread issues the step's four MMAs for both CTAs;
+//   warp 2      tells CTA 0 that the CTA's tiles have landed; for the weights' gradients it first clears the rows of
+//               the last step that belong to the next expert (in both operands: 0 times infinity is no 0);
+//   warps 4-11  epilogue, two groups of four warps (a warp reaches 32 lanes of tensor memory) that take 32 columns (rows
+//               of the result) in turn.  Fragments of the accumulators go through stmatrix, transposed, into rows of the
+//               result in shared memory, and from there to memory in 16-byte pieces of whole rows.
+// Two accumulators alternate, so that the epilogue runs beside the next tile's MMAs.
+#include <cuda.h>   // CUtensorMap and its enums; the encoder is looked up in the driver at run time
+#include <cudaTypedefs.h>
 
-#include "int8.cuh"
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "pair.cuh"
 
 namespace moe {
 
-// One kernel for the block's six products: out[e][n][m] = sum_k A(m, k) B(n, k), a thread a result.
-//   rows:  n is a row of the expert, k a column; A a weight of expert e.
-//   grad:  k runs over the expert's rows, m and n are columns.
-struct FfnProduct {
-    const uint16_t *a, *b;
-    int64_t a_mat, a_m, a_k;   // strides of A: expert, m, k
-    int64_t b_n, b_k;
-    int M, N, K;
-    bool grad;
-};
+constexpr int kFfThreads = 384;
+constexpr int kFfEpi0 = 4;              // first epilogue warp
+constexpr int kFfNT = 256;              // rows of B of a tile
+constexpr int kFfStepK = 64;            // 128 bytes of bf16
+constexpr int kFfABytes = 128 * 128, kFfStage = 2 * kFfABytes, kFfStages = 5;
+constexpr int kFfEpiBytes = 16 * 1024;  // staging of an epilogue group
+constexpr uint32_t kFfTmemCols = 512;
+constexpr int kFfLimitWord = 8;         // the waits' limit in ns (int64) in the workspace: 0 means a second
+constexpr size_t kFfSmem = 1024 + kFfStages * kFfStage + 2 * kFfEpiBytes;
+static_assert(kFfSmem + sizeof(RowTiles) + 512 <= 227 * 1024, "ring and staging fit beside the table");
+static_assert((kFfThreads - 1) * 3 >= kMaxE, "the last thread has no offsets");
 
-enum { kFfnPlain = 0, kFfnAct = 1, kFfnActGrad = 2 };
+// What is done with a tile's sums.
+enum FfEpi { kEpiBf16, kEpiF32, kEpiSwiglu, kEpiRelu2, kEpiSwigluGrad, kEpiRelu2Grad };
+// Which operands are K-major.
+enum FfOrder { kOrderKK, kOrderMK, kOrderGrad };
 
-struct FfnSimple {
-    FfnProduct p;
+struct FfArgs {
+    CUtensorMap ta;       // KK {k, m, expert}, SwiGLU {k, 16, half, block, expert}; MK {m, k, expert}; Grad {m, row}
+    CUtensorMap tb[4];    // KK, MK {k, row}, boxes of 16 << i rows; Grad tb[0] {n, row}
     const int32_t* offsets;
-    int P, E, f, act, epi;
+    int E, P, M, N, K;    // N: Grad only.  Grad has the expert's rows for K.
+    int f;                // neurons
+    void* out;            // y, dx or the weights' gradient: rows of M values
     const uint16_t* z_in;
-    uint16_t *z_out, *h_out;
-    void* out;
-    int ot;
+    uint16_t* z_out;      // z (may be null) or dz
+    uint16_t* h_out;
+    int32_t* err;
 };
 
-__device__ __forceinline__ uint16_t ffn_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
-
-__global__ void __launch_bounds__(256) ffn_simple_kernel(FfnSimple g) {
-    pdl_wait();
-    const FfnProduct& p = g.p;
-    const int m = blockIdx.x * 32 + (threadIdx.x & 31);
-    for (int e = blockIdx.y; e < g.E; e += gridDim.y) {
-        int first, last;
-        expert_rows(g.offsets, e, g.P, &first, &last);
-        const int n0 = p.grad ? 0 : first, n1 = p.grad ? p.N : last;
-        const int k0 = p.grad ? first : 0, k1 = p.grad ? last : p.K;
-        if (m >= p.M) continue;
-        const uint16_t* a = p.a + e * p.a_mat + m * p.a_m;
-        for (int n = n0 + (threadIdx.x >> 5) + 8 * blockIdx.z; n < n1; n += 8 * gridDim.z) {
-            const uint16_t* b = p.b + n * p.b_n;
-            float s = 0.0f, s2 = 0.0f;
-            for (int64_t k = k0; k < k1; ++k) {
-                const float bv = bf16_bits_to_f32(b[k * p.b_k]);
-                s = fmaf(bf16_bits_to_f32(a[k * p.a_k]), bv, s);
-                if (g.epi == kFfnAct && g.act == MOE_ACT_SWIGLU) s2 = fmaf(bf16_bits_to_f32(a[g.f * p.a_m + k * p.a_k]), bv, s2);
-            }
-            const int64_t row = static_cast<int64_t>(n);
-            if (g.epi == kFfnPlain) {
-                const int64_t o = (p.grad ? (static_cast<int64_t>(e) * p.N + n) : row) * p.M + m;
-                if (g.ot == MOE_F32) static_cast<float*>(g.out)[o] = s;
-                else static_cast<uint16_t*>(g.out)[o] = ffn_bf16(s);
-            } else if (g.epi == kFfnAct) {
-                const bool gated = g.act == MOE_ACT_SWIGLU;
-                const int64_t zo = row * (gated ? 2 * g.f : g.f) + m;
-                if (g.z_out) {
-                    g.z_out[zo] = ffn_bf16(s);
-                    if (gated) g.z_out[zo + g.f] = ffn_bf16(s2);
-                }
-                g.h_out[row * g.f + m] = ffn_bf16(gated ? silu(s) * s2 : (s > 0.0f ? s * s : (s <= 0.0f ? 0.0f : s)));
-            } else {
-                const bool gated = g.act == MOE_ACT_SWIGLU;
-                const int64_t zo = row * (gated ? 2 * g.f : g.f) + m;
-                const float zg = bf16_bits_to_f32(g.z_in[zo]);
-                if (gated) {
-                    const float zu = bf16_bits_to_f32(g.z_in[zo + g.f]), sg = 1.0f / (1.0f + expf(-zg));
-                    g.z_out[zo] = ffn_bf16(s * zu * (sg * (1.0f + zg * (1.0f - sg))));
-                    g.z_out[zo + g.f] = ffn_bf16(s * (zg * sg));
-                } else {
-                    g.z_out[zo] = ffn_bf16(s * (2.0f * (zg > 0.0f ? zg : (zg <= 0.0f ? 0.0f : zg))));
-                }
-            }
-        }
-    }
+__device__ __forceinline__ void ff_fail(const FfArgs& g, volatile tc::Waits* waits, uint32_t rank) {
+    waits->fail = 1;
+    tc::st_cluster(tc::peer_addr(tc::s_addr(const_cast<const int*>(&waits->fail)), rank ^ 1u), 1u);
+    set_error(g.err, tc::kErrTimeout);
 }
 
-static cudaError_t ffn_simple(const FfnSimple& g, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>((g.p.M + 31) / 32), static_cast<unsigned>(g.E), g.p.grad ? 8u : (g.E == 1 ? 64u : 4u));
-    return launch_pdl(ffn_simple_kernel, grid, dim3(256), 0, s, g);
+__device__ __forceinline__ uint32_t ff_pack(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float ff_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float ff_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// The sigmoid s and 1 - s.  exp(-|g|) is at most 1, so that the fast division's divisor lies in [1, 2], and neither s nor
+// 1 - s comes of a difference.  The hardware's 2^x is off by a few 2^-23 per unit of |g|, far below a bf16's step.
+__device__ __forceinline__ float2 ff_sigmoid(float g) {
+    const float e = __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + e), t = e * r;
+    return g < 0.0f ? make_float2(t, r) : make_float2(r, t);
+}
+__device__ __forceinline__ float ff_relu(float z) { return z > 0.0f ? z : (z <= 0.0f ? 0.0f : z); }
+
+// The items of one role: ROWS (row tile, tile of M), GRAD (expert, tile of N, tile of M); M tiles fastest.
+template <bool GRAD>
+struct FfWalk {
+    TileWalk w;
+    int ntiles, e, n0, n, k0, steps;   // n0, n: first row of B's tile and rows; k0, steps: GRAD, the expert's rows
+    const FfArgs& g;
+    __device__ FfWalk(const RowTiles& t, const FfArgs& g_, int first, int stride)
+        : w(t, (g_.M + 255) / 256, first, stride), ntiles((g_.N + kFfNT - 1) / kFfNT), g(g_) {}
+    __device__ bool more() const { return GRAD ? w.tile < g.E * ntiles : w.more(); }
+    __device__ void next() { w.next(); }
+    __device__ int m0() const { return w.mtile * 256; }
+    int rows = 0;   // GRAD: rows of the expert
+    __device__ void at() {
+        if constexpr (GRAD) {
+            e = w.tile / ntiles;
+            n0 = (w.tile - e * ntiles) * kFfNT;
+            n = min(kFfNT, g.N - n0);
+            int last;
+            expert_rows(g.offsets, e, g.P, &k0, &last);
+            rows = last - k0;
+            steps = (rows + kFfStepK - 1) / kFfStepK;
+        } else {
+            w.at(&e, &n0, &n);
+            steps = (g.K + kFfStepK - 1) / kFfStepK;
+        }
+    }
+    __device__ int mma_n() const { return (n + 31) & ~31; }
+};
+
+template <int EPI, int ORDER>
+__global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constant__ FfArgs g) {
+    constexpr bool kGrad = ORDER == kOrderGrad;
+    constexpr bool kGated = EPI == kEpiSwiglu;   // gate and up rows interleaved in A
+    extern __shared__ __align__(16) unsigned char dsm_raw[];
+    unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char* staging = ring + kFfStages * kFfStage;
+    __shared__ uint64_t full[kFfStages], ready[kFfStages], empty[kFfStages];
+    __shared__ uint64_t acc_full[2], acc_empty[2], drained;
+    __shared__ uint32_t issued, tmem_base;
+    __shared__ volatile tc::Waits waits;
+    __shared__ RowTiles tiles;
+    // (the warp number through a shuffle, so that the roles' branches are uniform)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const uint32_t rank = tc::cluster_rank();
+
+    if (warp == 0 && lane == 0) {
+        tc::prefetch_map(&g.ta);
+        tc::prefetch_map(&g.tb[0]);
+    }
+    if (warp == 3) tc::pair_alloc(&tmem_base, kFfTmemCols);
+    if (tid == 0) {
+        for (int s = 0; s < kFfStages; ++s) {
+            tc::mbar_init(&full[s], 1);
+            tc::mbar_init(&ready[s], 2);
+            tc::mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(&acc_full[s], 1);
+            tc::mbar_init(&acc_empty[s], 16);
+        }
+        tc::mbar_init(&drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        waits.fail = 0;
+        issued = 0;
+    }
+    pdl_wait();
+    if (tid == kFfThreads - 1) {
+        const long long limit = *reinterpret_cast<const volatile long long*>(g.err + kFfLimitWord);
+        waits.limit_ns = limit != 0 ? limit : tc::kWaitLimitNs;
+    }
+    if constexpr (!kGrad) build_row_tiles<kFfThreads>(tiles, g.offsets, g.E, g.P, kFfNT);
+    tc::fence_before();
+    tc::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = tmem_base;
+    FfWalk<kGrad> walk(tiles, g, blockIdx.x >> 1, gridDim.x >> 1);
+
+    if (warp == 0) {
+        // -------------------------------------------------------------------- TMA producer
+        const bool leader = tc::elect_one();
+        const uint32_t ring0 = tc::s_addr(ring);
+        uint32_t st = 0, use = 0;
+        bool ok = true;
+        for (; walk.more() && ok; walk.next()) {
+            walk.at();
+            const int half = walk.mma_n() >> 1, b0 = walk.n0 + static_cast<int>(rank) * half;
+            const int am = walk.m0() + static_cast<int>(rank) * 128;
+            int bi = 0;
+            while ((16 << bi) < half) ++bi;   // the smallest box of rows of B
+            const uint32_t bytes = kFfABytes + (kGrad ? (half > 64 ? 2 : 1) * 8192 : (16 << bi) * 128);
+            for (int ks = 0; ks < walk.steps; ++ks) {
+                if (use > 0 && !tc::mbar_wait_warp_cluster(&empty[st], use - 1, &waits)) {
+                    ok = false;
+                    break;
+                }
+                if (leader) {
+                    const uint32_t a = ring0 + st * kFfStage, b = a + kFfABytes;
+                    tc::mbar_arrive_expect_tx(&full[st], bytes);
+                    if constexpr (kGrad) {
+                        const int k = walk.k0 + ks * kFfStepK;
+                        tc::tma_2d(a, &g.ta, am, k, &full[st]);
+                        tc::tma_2d(a + 8192, &g.ta, am + 64, k, &full[st]);
+                        tc::tma_2d(b, &g.tb[0], b0, k, &full[st]);
+                        if (half > 64) tc::tma_2d(b + 8192, &g.tb[0], b0 + 64, k, &full[st]);
+                    } else {
+                        const int k = ks * kFfStepK;
+                        if constexpr (kGated) {
+                            tc::tma_5d(a, &g.ta, k, 0, 0, am >> 5, walk.e, &full[st]);
+                        } else if constexpr (ORDER == kOrderKK) {
+                            tc::tma_3d(a, &g.ta, k, am, walk.e, &full[st]);
+                        } else {
+                            tc::tma_3d(a, &g.ta, am, k, walk.e, &full[st]);
+                            tc::tma_3d(a + 8192, &g.ta, am + 64, k, walk.e, &full[st]);
+                        }
+                        tc::tma_2d(b, &g.tb[bi], k, b0, &full[st]);
+                    }
+                }
+                if (++st == kFfStages) st = 0, ++use;
+            }
+        }
+        const uint32_t n_issued = use * kFfStages + st;
+        // the MMAs' last arrivals on this CTA's barriers, which have to land before it ends
+        for (uint32_t i = 0; i < kFfStages && ok; ++i) {
+            if (use > 0) ok = tc::mbar_wait_warp_cluster(&empty[st], use - 1, &waits);
+            if (++st == kFfStages) st = 0, ++use;
+        }
+        if (leader) {
+            issued = n_issued;
+            if (!ok) ff_fail(g, &waits, rank);
+        }
+    } else if (warp == 1 && rank == 0) {
+        // -------------------------------------------------------------------- MMA issuer
+        const bool leader = tc::elect_one();
+        const uint32_t ring0 = tc::s_addr(ring);
+        constexpr bool kAmn = ORDER != kOrderKK, kBmn = kGrad;
+        constexpr uint32_t kAstep = kAmn ? 128 : 2, kBstep = kBmn ? 128 : 2;   // 16 values of K, in 16 bytes
+        const uint64_t da0 = kAmn ? tc::sdesc_mn128(ring0, 8192) : tc::sdesc_k128(ring0);
+        const uint64_t db0 = kBmn ? tc::sdesc_mn128(ring0 + kFfABytes, 8192) : tc::sdesc_k128(ring0 + kFfABytes);
+        uint32_t st = 0, use = 0, n_acc = 0;
+        bool ok = true;
+        for (; walk.more() && ok; walk.next()) {
+            walk.at();
+            if (walk.steps == 0) continue;
+            const uint32_t buf = n_acc & 1, ub = n_acc >> 1;
+            ++n_acc;
+            if (ub > 0 && !tc::mbar_wait_warp_cluster(&acc_empty[buf], ub - 1, &waits)) {
+                ok = false;
+                break;
+            }
+            const uint32_t dt = tmem + buf * kFfNT, idesc = tc::pair_idesc(walk.mma_n(), 1, kAmn, kBmn);
+            for (int ks = 0; ks < walk.steps; ++ks) {
+                if (!tc::mbar_wait_warp_cluster(&ready[st], use, &waits)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                if (leader) {
+                    const uint64_t da = da0 + st * (kFfStage >> 4), db = db0 + st * (kFfStage >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc::pair_mma(dt, da + kk * kAstep, db + kk * kBstep, idesc, ks > 0 || kk > 0);
+                    tc::pair_commit(&empty[st]);
+                    if (ks + 1 == walk.steps) tc::pair_commit(&acc_full[buf]);
+                }
+                if (++st == kFfStages) st = 0, ++use;
+            }
+        }
+        if (leader && !ok) ff_fail(g, &waits, rank);
+    } else if (warp == 2) {
+        // -------------------------------------------------------------------- landed tiles
+        uint32_t st = 0, use = 0;
+        bool ok = true;
+        const uint32_t ready0 = tc::peer_addr(tc::s_addr(&ready[0]), 0);
+        for (; walk.more() && ok; walk.next()) {
+            walk.at();
+            for (int ks = 0; ks < walk.steps; ++ks) {
+                if (!tc::mbar_wait_warp(&full[st], use, &waits)) {
+                    ok = false;
+                    break;
+                }
+                if constexpr (kGrad) {
+                    const int valid = walk.rows - ks * kFfStepK;
+                    if (valid < kFfStepK) {   // rows valid .. 63 of every box
+                        unsigned char* p = ring + st * kFfStage;
+                        const int boxes = 2 + (walk.mma_n() > 128 ? 2 : 1);
+                        for (int b = 0; b < boxes; ++b)
+                            for (int i = valid * 8 + lane; i < kFfStepK * 8; i += 32)
+                                *reinterpret_cast<uint4*>(p + b * 8192 + i * 16) = make_uint4(0, 0, 0, 0);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                }
+                if (lane == 0) tc::mbar_arrive_cluster(ready0 + st * 8);
+                if (++st == kFfStages) st = 0, ++use;
+            }
+        }
+        if (!ok && lane == 0) ff_fail(g, &waits, rank);
+    } else if (warp >= kFfEpi0) {
+        // -------------------------------------------------------------------- epilogue
+        const int q = warp & 3, grp = (warp - kFfEpi0) >> 2, t128 = tid & 127;
+        const uint32_t sb = tc::s_addr(staging + grp * kFfEpiBytes);
+        const uint32_t acc0 = tc::peer_addr(tc::s_addr(&acc_empty[0]), 0);
+        const int mrow = lane >> 2, ncol = 2 * (lane & 3);        // this lane's place in a fragment
+        // stmatrix / ldmatrix: this lane's row (of 8 tokens) and 16-byte piece, rows of 256 bytes (32 neurons of the warp)
+        // and of 128 bytes (16).  A piece's place is xored with its row, so that 8 rows of a piece meet all banks.
+        const int r8 = lane & 7, p4 = q * 4 + (lane >> 3);
+        const uint32_t at256 = sb + r8 * 256 + ((p4 ^ r8) << 4);
+        const uint32_t at128 = sb + r8 * 128 + (((q * 2 + ((lane >> 3) & 1)) ^ r8) << 4);
+        uint32_t n_acc = 0;
+        bool ok = true;
+        for (; walk.more(); walk.next()) {
+            walk.at();
+            // (an expert without rows: zeros; after a wait that ran out too, as the group's warps meet at barriers and
+            // all have to come there)
+            bool none = !ok || (kGrad && walk.steps == 0);
+            const uint32_t buf = n_acc & 1;
+            if (!none) {
+                ok = tc::mbar_wait_warp_cluster(&acc_full[buf], n_acc >> 1, &waits);
+                none = !ok;
+                ++n_acc;
+                tc::fence_after();
+            }
+            const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * kFfNT;
+            const int am = walk.m0() + static_cast<int>(rank) * 128;
+#pragma unroll 1
+            for (int c0 = 32 * grp; c0 < walk.n; c0 += 64) {
+                float lo[16], hi[16];
+                const int left = walk.n - c0;   // rows of the result from c0 on
+                const int64_t row0 = (kGrad ? static_cast<int64_t>(walk.e) * g.N : 0) + walk.n0 + c0;
+                if (none) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) lo[i] = hi[i] = 0.0f;
+                } else {
+                    tc::tmem_ld_frag(tb + c0, lo);
+                    tc::tmem_ld_frag(tb + (16u << 16) + c0, hi);
+                }
+                if constexpr (EPI == kEpiSwigluGrad || EPI == kEpiRelu2Grad) {
+                    // z of these rows and neurons into shared memory
+                    constexpr int kHalves = EPI == kEpiSwigluGrad ? 2 : 1;
+#pragma unroll
+                    for (int j = 0; j < 4 * kHalves; ++j) {
+                        const int i = j * 128 + t128, half = i >> 9, r = (i >> 4) & 31, p = i & 15;
+                        const int m = am + 8 * p;
+                        const bool in = r < left && m < g.M;
+                        const uint16_t* src = g.z_in + (row0 + (in ? r : 0)) * (kHalves * g.f) + half * g.f + (in ? m : 0);
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sb + half * 8192 + r * 256 + ((p ^ (r & 7)) << 4)),
+                                     "l"(src), "r"(in ? 16 : 0)
+                                     : "memory");
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    tc::named_sync(1 + grp, 128);
+                }
+                if (!none) tc::tmem_wait32(lo, hi);
+                if constexpr (EPI == kEpiBf16) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tc::stsm4_t(at256 + i * 2048, ff_pack(lo[4 * i], lo[4 * i + 1]), ff_pack(lo[4 * i + 2], lo[4 * i + 3]),
+                                    ff_pack(hi[4 * i], hi[4 * i + 1]), ff_pack(hi[4 * i + 2], hi[4 * i + 3]));
+                } else if constexpr (EPI == kEpiF32) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {   // (column ^ 8 * row / 2: the lanes of a store meet all banks)
+                        const float v = j < 16 ? lo[j] : hi[j - 16];
+                        const int i = (j & 15) >> 2, r = 8 * i + ncol + (j & 1), c = q * 32 + (j >> 4) * 16 + ((j >> 1) & 1) * 8 + mrow;
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + r * 512 + ((c ^ (8 * (lane & 3))) << 2)), "f"(v) : "memory");
+                    }
+                } else if constexpr (EPI == kEpiSwiglu) {
+                    if (g.z_out) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)   // gate, gate + 8, up, up + 8
+                            tc::stsm4_t(at128 + 4096 + (lane >> 4) * 4096 + i * 1024, ff_pack(lo[4 * i], lo[4 * i + 1]),
+                                        ff_pack(lo[4 * i + 2], lo[4 * i + 3]), ff_pack(hi[4 * i], hi[4 * i + 1]),
+                                        ff_pack(hi[4 * i + 2], hi[4 * i + 3]));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) lo[j] = lo[j] * ff_sigmoid(lo[j]).x * hi[j];
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2)
+                        tc::stsm4_t(at128 + (i + (lane >> 4)) * 1024, ff_pack(lo[4 * i], lo[4 * i + 1]), ff_pack(lo[4 * i + 2], lo[4 * i + 3]),
+                                    ff_pack(lo[4 * i + 4], lo[4 * i + 5]), ff_pack(lo[4 * i + 6], lo[4 * i + 7]));
+                } else if constexpr (EPI == kEpiRelu2) {
+                    if (g.z_out) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            tc::stsm4_t(at256 + 8192 + i * 2048, ff_pack(lo[4 * i], lo[4 * i + 1]), ff_pack(lo[4 * i + 2], lo[4 * i + 3]),
+                                        ff_pack(hi[4 * i], hi[4 * i + 1]), ff_pack(hi[4 * i + 2], hi[4 * i + 3]));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        lo[j] = ff_relu(lo[j]) * ff_relu(lo[j]);
+                        hi[j] = ff_relu(hi[j]) * ff_relu(hi[j]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tc::stsm4_t(at256 + i * 2048, ff_pack(lo[4 * i], lo[4 * i + 1]), ff_pack(lo[4 * i + 2], lo[4 * i + 3]),
+                                    ff_pack(hi[4 * i], hi[4 * i + 1]), ff_pack(hi[4 * i + 2], hi[4 * i + 3]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t zg[4], zu[4];   // rows lane / 4, + 8, + 16, + 24 of the warp's neurons, a pair of tokens each
+                        tc::ldsm4_t(at256 + i * 2048, zg);
+                        if constexpr (EPI == kEpiSwigluGrad) tc::ldsm4_t(at256 + 8192 + i * 2048, zu);
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            float* d = (m < 2 ? lo : hi) + 4 * i + 2 * (m & 1);   // dh of the pair
+                            float a[2], b[2];
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const float z = u ? ff_hi(zg[m]) : ff_lo(zg[m]);
+                                if constexpr (EPI == kEpiSwigluGrad) {
+                                    const float2 s = ff_sigmoid(z);
+                                    const float silu = z * s.x;
+                                    a[u] = d[u] * (u ? ff_hi(zu[m]) : ff_lo(zu[m])) * (s.x + silu * s.y);
+                                    b[u] = d[u] * silu;
+                                } else {
+                                    a[u] = d[u] * (2.0f * ff_relu(z));
+                                }
+                            }
+                            zg[m] = ff_pack(a[0], a[1]);
+                            if constexpr (EPI == kEpiSwigluGrad) zu[m] = ff_pack(b[0], b[1]);
+                        }
+                        __syncwarp();   // (every lane's z of these rows is read)
+                        tc::stsm4_t(at256 + i * 2048, zg[0], zg[1], zg[2], zg[3]);
+                        if constexpr (EPI == kEpiSwigluGrad) tc::stsm4_t(at256 + 8192 + i * 2048, zu[0], zu[1], zu[2], zu[3]);
+                    }
+                }
+                tc::named_sync(1 + grp, 128);
+                // whole rows from shared memory to memory, 16 bytes a lane
+                auto copy = [&](uint32_t from, void* to, int64_t ld, int col, int cols, int row_bytes, int elem) {
+                    const int per = row_bytes / 16, each = 16 / elem;
+#pragma unroll
+                    for (int j = 0; j < 32 * row_bytes / 16 / 128; ++j) {
+                        const int i = j * 128 + t128, r = i / per, p = i % per;
+                        const int place = elem == 4 ? p ^ (2 * ((r >> 1) & 3)) : p ^ (r & 7);
+                        if (r >= left || p * each >= cols) continue;
+                        uint4 v;
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from + r * row_bytes + (place << 4)));
+                        *reinterpret_cast<uint4*>(static_cast<char*>(to) + ((row0 + r) * ld + col + p * each) * elem) = v;
+                    }
+                };
+                if constexpr (EPI == kEpiBf16) {
+                    copy(sb, g.out, g.M, am, g.M - am, 256, 2);
+                } else if constexpr (EPI == kEpiF32) {
+                    copy(sb, g.out, g.M, am, g.M - am, 512, 4);
+                } else if constexpr (EPI == kEpiSwiglu) {
+                    const int j0 = am >> 1;   // the CTA's first neuron
+                    copy(sb, g.h_out, g.f, j0, g.f - j0, 128, 2);
+                    if (g.z_out) {
+                        copy(sb + 4096, g.z_out, 2 * g.f, j0, g.f - j0, 128, 2);
+                        copy(sb + 8192, g.z_out, 2 * g.f, g.f + j0, g.f - j0, 128, 2);
+                    }
+                } else if constexpr (EPI == kEpiRelu2) {
+                    copy(sb, g.h_out, g.f, am, g.f - am, 256, 2);
+                    if (g.z_out) copy(sb + 8192, g.z_out, g.f, am, g.f - am, 256, 2);
+                } else {
+                    constexpr int kHalves = EPI == kEpiSwigluGrad ? 2 : 1;
+                    copy(sb, g.z_out, kHalves * g.f, am, g.f - am, 256, 2);
+                    if (kHalves == 2) copy(sb + 8192, g.z_out, 2 * g.f, g.f + am, g.f - am, 256, 2);
+                }
+                tc::named_sync(1 + grp, 128);   // the staging is free again
+            }
+            if (!none) {
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(acc0 + buf * 8);
+            }
+        }
+        if (!ok && lane == 0) ff_fail(g, &waits, rank);
+    }
+
+    // Every copy and MMA of the pair has landed before its memories are given back: the producers waited for the MMAs, the
+    // epilogues for every accumulator.  Where a wait ran out (both CTAs know it then) the copies that were issued are
+    // waited for, and one more commit tracks all MMAs; the first of these waits that runs out ends them.
+    __syncwarp();   // (roles end with one lane at work)
+    tc::fence_before();
+    tc::cluster_sync();
+    if (waits.fail) {
+        if (warp == 1 && rank == 0 && tc::elect_one()) tc::pair_commit(&drained);   // (the lane that issued them)
+        __syncthreads();
+        if (tid == 0) {
+            bool ok = tc::mbar_wait(&drained, 0);
+            for (uint32_t n = issued > kFfStages ? issued - kFfStages : 0; n < issued && ok; ++n)
+                ok = tc::mbar_wait(&full[n % kFfStages], n / kFfStages);
+        }
+        __syncwarp();
+        tc::cluster_sync();
+    }
+    tc::fence_after();
+    if (warp == 3) tc::pair_dealloc(tmem, kFfTmemCols);
+}
+
+// ------------------------------------------------------------------------------- host side
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 g_ff_encode = nullptr;
+
+cudaError_t ff_encoder() {
+    static std::once_flag once;
+    static cudaError_t status = cudaSuccess;
+    std::call_once(once, [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        status = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+        if (status == cudaSuccess && (q != cudaDriverEntryPointSuccess || fn == nullptr)) status = cudaErrorNotSupported;
+        if (status == cudaSuccess) g_ff_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    });
+    return status;
+}
+
+// bf16 values in 128-byte-swizzled boxes; what lies outside the tensor reads as zero.  strides in values.
+cudaError_t ff_map(CUtensorMap* m, int rank, const void* base, std::initializer_list<int64_t> dims, std::initializer_list<int64_t> strides,
+                   std::initializer_list<int> box) {
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5];
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    std::copy(dims.begin(), dims.end(), d);
+    std::transform(strides.begin(), strides.end(), st, [](int64_t v) { return static_cast<cuuint64_t>(2 * v); });
+    std::copy(box.begin(), box.end(), b);
+    const CUresult r = g_ff_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, b, es,
+                                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Rows of B, K-major: boxes of 16, 32, 64, 128 rows.
+cudaError_t ff_map_rows(FfArgs& g, const uint16_t* rows, int64_t P, int64_t cols) {
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < 4 && e == cudaSuccess; ++i) e = ff_map(&g.tb[i], 2, rows, {cols, P}, {cols}, {kFfStepK, 16 << i});
+    return e;
+}
+
+template <int EPI, int ORDER>
+cudaError_t ff_launch(const FfArgs& g, int num_sms, cudaStream_t s) {
+    const int64_t mt = (g.M + 255) / 256;
+    const int64_t rows = ORDER == kOrderGrad ? static_cast<int64_t>(g.E) * ((g.N + kFfNT - 1) / kFfNT)
+                                             : std::min(g.E, g.P) + g.P / kFfNT;
+    const int pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms / 2, mt * rows)));
+    return launch_pairs(ffn_kernel<EPI, ORDER>, pairs, kFfThreads, kFfSmem, s, g);
+}
+
+template <int EPI, int ORDER>
+cudaError_t ff_configure() {
+    const void* fn = reinterpret_cast<const void*>(&ffn_kernel<EPI, ORDER>);
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFfSmem));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t configure_ffn_kernels() {
+    cudaError_t e = ff_encoder();
+    if (e == cudaSuccess) e = ff_configure<kEpiSwiglu, kOrderKK>();
+    if (e == cudaSuccess) e = ff_configure<kEpiRelu2, kOrderKK>();
+    if (e == cudaSuccess) e = ff_configure<kEpiBf16, kOrderKK>();
+    if (e == cudaSuccess) e = ff_configure<kEpiSwigluGrad, kOrderMK>();
+    if (e == cudaSuccess) e = ff_configure<kEpiRelu2Grad, kOrderMK>();
+    if (e == cudaSuccess) e = ff_configure<kEpiBf16, kOrderMK>();
+    if (e == cudaSuccess) e = ff_configure<kEpiBf16, kOrderGrad>();
+    if (e == cudaSuccess) e = ff_configure<kEpiF32, kOrderGrad>();
+    return e;
 }
 
 cudaError_t launch_ffn_forward(const uint16_t* x, int64_t P, const uint16_t* wgu, const uint16_t* wd, int64_t E, int64_t d, int64_t f,
-                               const int32_t* offsets, int act, uint16_t* y, uint16_t* z, uint16_t* h, int32_t*, int, cudaStream_t s) {
-    const int64_t nz = act == MOE_ACT_SWIGLU ? 2 * f : f;
-    FfnSimple g{};
-    g.offsets = offsets, g.P = static_cast<int>(P), g.E = static_cast<int>(E), g.f = static_cast<int>(f), g.act = act;
-    g.p = {wgu, x, nz * d, d, 1, d, 1, static_cast<int>(f), 0, static_cast<int>(d), false};
-    g.epi = kFfnAct, g.z_out = z, g.h_out = h;
-    cudaError_t e = ffn_simple(g, s);
-    if (e != cudaSuccess) return e;
-    g.p = {wd, h, d * f, f, 1, f, 1, static_cast<int>(d), 0, static_cast<int>(f), false};
-    g.epi = kFfnPlain, g.out = y, g.ot = MOE_BF16;
-    return ffn_simple(g, s);
+                               const int32_t* offsets, int act, uint16_t* y, uint16_t* z, uint16_t* h, int32_t* err, int num_sms,
+                               cudaStream_t s) {
+    FfArgs g;
+    std::memset(&g, 0, sizeof(g));
+    g.offsets = offsets, g.E = static_cast<int>(E), g.P = static_cast<int>(P), g.f = static_cast<int>(f), g.err = err;
+    g.z_out = z, g.h_out = h;
+    g.K = static_cast<int>(d);
+    cudaError_t e = ff_map_rows(g, x, P, d);
+    if (e == cudaSuccess) {
+        if (act == MOE_ACT_SWIGLU) {   // 16 gate rows, the same neurons' 16 up rows, four times
+            g.M = static_cast<int>(2 * f);
+            e = ff_map(&g.ta, 5, wgu, {d, 16, 2, f / 16, E}, {d, f * d, 16 * d, 2 * f * d}, {kFfStepK, 16, 2, 4, 1});
+            if (e == cudaSuccess) e = ff_launch<kEpiSwiglu, kOrderKK>(g, num_sms, s);
+        } else {
+            g.M = static_cast<int>(f);
+            e = ff_map(&g.ta, 3, wgu, {d, f, E}, {d, f * d}, {kFfStepK, 128, 1});
+            if (e == cudaSuccess) e = ff_launch<kEpiRelu2, kOrderKK>(g, num_sms, s);
+        }
+    }
+    if (e == cudaSuccess) e = ff_map_rows(g, h, P, f);
+    if (e == cudaSuccess) e = ff_map(&g.ta, 3, wd, {f, d, E}, {f, d * f}, {kFfStepK, 128, 1});
+    g.M = static_cast<int>(d), g.K = static_cast<int>(f), g.out = y;
+    if (e == cudaSuccess) e = ff_launch<kEpiBf16, kOrderKK>(g, num_sms, s);
+    return e;
 }
 
 cudaError_t launch_ffn_backward(const uint16_t* dy, const uint16_t* x, int64_t P, const uint16_t* wgu, const uint16_t* wd, int64_t E,
                                 int64_t d, int64_t f, const int32_t* offsets, int act, const uint16_t* z, const uint16_t* h,
-                                uint16_t* dz, uint16_t* dx, void* dwgu, void* dwd, int gt, int32_t*, int, cudaStream_t s) {
+                                uint16_t* dz, uint16_t* dx, void* dwgu, void* dwd, int gt, int32_t* err, int num_sms, cudaStream_t s) {
     const int64_t nz = act == MOE_ACT_SWIGLU ? 2 * f : f;
-    const int id = static_cast<int>(d), jf = static_cast<int>(f), jz = static_cast<int>(nz);
-    FfnSimple g{};
-    g.offsets = offsets, g.P = static_cast<int>(P), g.E = static_cast<int>(E), g.f = jf, g.act = act;
+    FfArgs g;
+    std::memset(&g, 0, sizeof(g));
+    g.offsets = offsets, g.E = static_cast<int>(E), g.P = static_cast<int>(P), g.f = static_cast<int>(f), g.err = err;
     cudaError_t e = cudaSuccess;
     if (dx || dwgu) {
-        g.p = {wd, dy, d * f, 1, f, d, 1, jf, 0, id, false};
-        g.epi = kFfnActGrad, g.z_in = z, g.z_out = dz;
-        e = ffn_simple(g, s);
+        g.M = static_cast<int>(f), g.K = static_cast<int>(d), g.z_in = z, g.z_out = dz;
+        e = ff_map_rows(g, dy, P, d);
+        if (e == cudaSuccess) e = ff_map(&g.ta, 3, wd, {f, d, E}, {f, d * f}, {64, kFfStepK, 1});
+        if (e == cudaSuccess)
+            e = act == MOE_ACT_SWIGLU ? ff_launch<kEpiSwigluGrad, kOrderMK>(g, num_sms, s) : ff_launch<kEpiRelu2Grad, kOrderMK>(g, num_sms, s);
     }
-    g.epi = kFfnPlain;
     if (dx && e == cudaSuccess) {
-        g.p = {wgu, dz, nz * d, 1, d, nz, 1, id, 0, jz, false};
-        g.out = dx, g.ot = MOE_BF16;
-        e = ffn_simple(g, s);
+        g.M = static_cast<int>(d), g.K = static_cast<int>(nz), g.out = dx;
+        e = ff_map_rows(g, dz, P, nz);
+        if (e == cudaSuccess) e = ff_map(&g.ta, 3, wgu, {d, nz, E}, {d, nz * d}, {64, kFfStepK, 1});
+        if (e == cudaSuccess) e = ff_launch<kEpiBf16, kOrderMK>(g, num_sms, s);
     }
-    g.ot = gt;
-    if (dwgu && e == cudaSuccess) {
-        g.p = {x, dz, 0, 1, d, 1, nz, id, jz, 0, true};
-        g.out = dwgu;
-        e = ffn_simple(g, s);
-    }
-    if (dwd && e == cudaSuccess) {
-        g.p = {h, dy, 0, 1, f, 1, d, jf, id, 0, true};
-        g.out = dwd;
-        e = ffn_simple(g, s);
-    }
+    auto grad = [&](const uint16_t* a, int64_t m, const uint16_t* b, int64_t n, void* out) {
+        g.M = static_cast<int>(m), g.N = static_cast<int>(n), g.out = out;
+        cudaError_t r = ff_map(&g.ta, 2, a, {m, P}, {m}, {64, kFfStepK});
+        if (r == cudaSuccess) r = ff_map(&g.tb[0], 2, b, {n, P}, {n}, {64, kFfStepK});
+        if (r == cudaSuccess) r = gt == MOE_F32 ? ff_launch<kEpiF32, kOrderGrad>(g, num_sms, s) : ff_launch<kEpiBf16, kOrderGrad>(g, num_sms, s);
+        return r;
+    };
+    if (dwgu && e == cudaSuccess) e = grad(x, d, dz, nz, dwgu);
+    if (dwd && e == cudaSuccess) e = grad(h, f, dy, d, dwd);
     return e;
 }
 

@@ -1,0 +1,223 @@
+// pair.cuh -- two CTAs on one tile (tcgen05 cta_group::2): cluster barriers, tensor-memory and MMA instructions, and the
+// table of row tiles that the persistent expert products walk (sm_103a).
+//
+// A pair's MMA has M = 256: each CTA holds 128 rows of A, half of B's rows, and in its own tensor memory the
+// accumulators of its 128 rows for all of B's.  CTA 0 issues the MMAs for both.
+#pragma once
+
+#include "int8.cuh"
+#include "tc.cuh"
+
+namespace moe {
+namespace tc {
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// All threads of both CTAs.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of CTA `rank`'s copy of a shared variable.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t cluster_addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+// mbar_wait_warp for barriers that the other CTA arrives on.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, "
+        "p;\n\t}"
+        : "=r"(ok)
+        : "r"(s_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_warp_cluster(uint64_t* bar, uint32_t n, const volatile Waits* w) {
+    const uint32_t parity = n & 1u;
+    if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
+    const long long t0 = global_ns();
+    for (uint32_t i = 0;; ++i) {
+        if ((i & 63u) == 0 && __any_sync(0xffffffffu, w->fail || global_ns() - t0 > w->limit_ns)) return false;
+        if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
+    }
+}
+
+__device__ __forceinline__ void pair_alloc(uint32_t* base, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s_addr(base)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void pair_dealloc(uint32_t base, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
+}
+// Arrives on the barrier at this address in both CTAs once every MMA that this thread has issued is complete.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(s_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+// Instruction descriptor of a 16-bit MMA with fp32 accumulators; `format` 0 f16, 1 bf16 (both operands); M = 256.
+__device__ __forceinline__ uint32_t pair_idesc(int n, uint32_t format, bool a_mn, bool b_mn) {
+    return (1u << 4) | (format << 7) | (format << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(n >> 3) << 17) | ((256u >> 4) << 24);
+}
+__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+// Shared-memory descriptor of an M/N-major tile in 128-byte swizzle: per K row 64 values of M (N) in 128 bytes, 8 K rows
+// 1024 bytes apart (stride byte offset), the next 64 values of M (N) `group` bytes on (leading byte offset).
+__device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr, uint32_t group) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(group >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
+// 16 lanes by 32 columns of tensor memory as MMA fragments: v[4 i + 0, 1] row lane / 4, columns 8 i + 2 (lane % 4) and
+// the next, v[4 i + 2, 3] the same of row lane / 4 + 8.  Valid after tmem_wait32.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait32(float* a, float* b) {   // (the registers pass through: no use moves in front)
+    tmem_ld_wait(a);
+    tmem_ld_wait(b);
+}
+
+// Four 8 x 8 matrices of 16-bit values between registers (fragments as above, column pairs packed) and shared memory,
+// transposed: lane l has the address of row l % 8 of matrix l / 8 as it lies in shared memory.
+__device__ __forceinline__ void stsm4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* w) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+}  // namespace tc
+
+// The row tiles of the experts that have rows, in shared memory.  An expert's tiles are equally high, a multiple of 32
+// (a pair's MMA takes N in steps of 32) and at most `nt`.
+struct RowTiles {
+    int prefix[kMaxE];   // first tile of a slot
+    int2 rows[kMaxE];    // first row, last row + 1
+    uint16_t height[kMaxE], expert[kMaxE];
+    int2 warp_sums[32];
+    int n_slots, n_tiles;
+};
+
+// By all THREADS threads of the CTA; ends with a __syncthreads().
+template <int THREADS>
+__device__ __forceinline__ void build_row_tiles(RowTiles& t, const int32_t* offsets, int E, int P, int nt) {
+    constexpr int kPer = (kMaxE + THREADS - 1) / THREADS;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int first[kPer], last[kPer], tiles = 0, live = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        first[i] = last[i] = 0;
+        if (tid * kPer + i < E) expert_rows(offsets, tid * kPer + i, P, &first[i], &last[i]);
+        tiles += (last[i] - first[i] + nt - 1) / nt;
+        live += last[i] > first[i];
+    }
+    int t_incl = tiles, l_incl = live;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, t_incl, o), b = __shfl_up_sync(0xffffffffu, l_incl, o);
+        if (lane >= o) t_incl += a, l_incl += b;
+    }
+    if (lane == 31) t.warp_sums[warp] = make_int2(t_incl, l_incl);
+    __syncthreads();
+    const int2 before = lane < warp ? t.warp_sums[lane] : make_int2(0, 0);
+    int run = __reduce_add_sync(0xffffffffu, before.x) + t_incl - tiles;
+    int slot = __reduce_add_sync(0xffffffffu, before.y) + l_incl - live;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (last[i] > first[i]) {
+            const int n = last[i] - first[i], n_tiles = (n + nt - 1) / nt;
+            t.prefix[slot] = run;
+            t.height[slot] = static_cast<uint16_t>(((n + n_tiles - 1) / n_tiles + 31) & ~31);
+            t.rows[slot] = make_int2(first[i], last[i]);
+            t.expert[slot] = static_cast<uint16_t>(tid * kPer + i);
+            ++slot;
+            run += n_tiles;
+        }
+    }
+    if (tid == THREADS - 1) {
+        t.n_slots = slot;
+        t.n_tiles = run;   // (2^17 and a few an expert at most: 32 bits hold even the sum of overlapping ranges)
+    }
+    __syncthreads();
+}
+
+// One role's walk over the items (row tile, weight tile), weight tiles fastest, from item `first` in steps of `stride`.
+struct TileWalk {
+    const RowTiles& t;
+    int mtiles, lane, stride_t, stride_m, tile, mtile, slot = 0;
+    __device__ TileWalk(const RowTiles& table, int mtiles_, int first, int stride)
+        : t(table), mtiles(mtiles_), lane(threadIdx.x & 31), stride_t(stride / mtiles_), stride_m(stride % mtiles_),
+          tile(first / mtiles_), mtile(first % mtiles_) {}
+    __device__ bool more() const { return tile < t.n_tiles; }
+    __device__ void next() {
+        tile += stride_t;
+        mtile += stride_m;
+        if (mtile >= mtiles) mtile -= mtiles, ++tile;
+    }
+    // The item's expert, first row and rows (the whole warp; tiles are asked for in increasing order).
+    __device__ void at(int* e, int* r_first, int* n) {
+        for (;;) {
+            const int i = slot + 1 + lane;
+            const int k = __popc(__ballot_sync(0xffffffffu, i < t.n_slots && t.prefix[i] <= tile));
+            slot += k;
+            if (k < 32) break;
+        }
+        const int2 r = t.rows[slot];
+        const int h = t.height[slot];
+        *e = t.expert[slot];
+        *r_first = r.x + (tile - t.prefix[slot]) * h;
+        *n = min(h, r.y - *r_first);
+    }
+};
+
+// Launch of CTA pairs, with the overlap that launch_pdl allows.
+template <typename... Exp, typename... Act>
+inline cudaError_t launch_pairs(void (*kernel)(Exp...), int pairs, int threads, size_t smem, cudaStream_t s, Act&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Act>(args)...);
+}
+
+}  // namespace moe
