@@ -102,10 +102,14 @@ struct FfWalk {
             n = min(kFfNT, g.N - n0);
             int last;
             expert_rows(g.offsets, e, g.P, &k0, &last);
-            rows = last - k0;
+            k0 = __shfl_sync(0xffffffffu, k0, 0);
+            rows = __shfl_sync(0xffffffffu, last - k0, 0);
             steps = (rows + kFfStepK - 1) / kFfStepK;
         } else {
             w.at(&e, &n0, &n);
+            e = __shfl_sync(0xffffffffu, e, 0);
+            n0 = __shfl_sync(0xffffffffu, n0, 0);
+            n = __shfl_sync(0xffffffffu, n, 0);
             steps = (g.K + kFfStepK - 1) / kFfStepK;
         }
     }
@@ -116,6 +120,8 @@ template <int EPI, int ORDER>
 __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constant__ FfArgs g) {
     constexpr bool kGrad = ORDER == kOrderGrad;
     constexpr bool kGated = EPI == kEpiSwiglu;   // gate and up rows interleaved in A
+    constexpr bool kActGrad = EPI == kEpiSwigluGrad || EPI == kEpiRelu2Grad;
+    constexpr int kZ = EPI == kEpiSwigluGrad ? 8 : 4;   // 16-byte pieces of z a lane (32 rows, 128 neurons, gate and up)
     extern __shared__ __align__(16) unsigned char dsm_raw[];
     unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char* staging = ring + kFfStages * kFfStage;
@@ -124,9 +130,10 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
     __shared__ uint32_t issued, tmem_base;
     __shared__ volatile tc::Waits waits;
     __shared__ RowTiles tiles;
-    // (the warp number through a shuffle, so that the roles' branches are uniform)
+    // (through shuffles, so that the compiler takes the roles' branches as uniform and keeps descriptors and coordinates
+    // in uniform registers, where the tensor core and the copy engine take them from)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const uint32_t rank = tc::cluster_rank();
+    const uint32_t rank = __shfl_sync(0xffffffffu, tc::cluster_rank(), 0);
 
     if (warp == 0 && lane == 0) {
         tc::prefetch_map(&g.ta);
@@ -174,7 +181,7 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
             while ((16 << bi) < half) ++bi;   // the smallest box of rows of B
             const uint32_t bytes = kFfABytes + (kGrad ? (half > 64 ? 2 : 1) * 8192 : (16 << bi) * 128);
             for (int ks = 0; ks < walk.steps; ++ks) {
-                if (use > 0 && !tc::mbar_wait_warp_cluster(&empty[st], use - 1, &waits)) {
+                if (use > 0 && !tc::mbar_wait_warp(&empty[st], use - 1, &waits)) {
                     ok = false;
                     break;
                 }
@@ -206,7 +213,7 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
         const uint32_t n_issued = use * kFfStages + st;
         // the MMAs' last arrivals on this CTA's barriers, which have to land before it ends
         for (uint32_t i = 0; i < kFfStages && ok; ++i) {
-            if (use > 0) ok = tc::mbar_wait_warp_cluster(&empty[st], use - 1, &waits);
+            if (use > 0) ok = tc::mbar_wait_warp(&empty[st], use - 1, &waits);
             if (++st == kFfStages) st = 0, ++use;
         }
         if (leader) {
@@ -228,13 +235,13 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
             if (walk.steps == 0) continue;
             const uint32_t buf = n_acc & 1, ub = n_acc >> 1;
             ++n_acc;
-            if (ub > 0 && !tc::mbar_wait_warp_cluster(&acc_empty[buf], ub - 1, &waits)) {
+            if (ub > 0 && !tc::mbar_wait_warp(&acc_empty[buf], ub - 1, &waits)) {
                 ok = false;
                 break;
             }
             const uint32_t dt = tmem + buf * kFfNT, idesc = tc::pair_idesc(walk.mma_n(), 1, kAmn, kBmn);
             for (int ks = 0; ks < walk.steps; ++ks) {
-                if (!tc::mbar_wait_warp_cluster(&ready[st], use, &waits)) {
+                if (!tc::mbar_wait_warp(&ready[st], use, &waits)) {
                     ok = false;
                     break;
                 }
@@ -298,9 +305,21 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
             // (an expert without rows: zeros; after a wait that ran out too, as the group's warps meet at barriers and
             // all have to come there)
             bool none = !ok || (kGrad && walk.steps == 0);
+            [[maybe_unused]] uint4 zr[kZ];
+            [[maybe_unused]] auto read_z = [&](int c) {   // rows c .. c + 31 of the tile, 16 bytes of a row a lane
+#pragma unroll
+                for (int j = 0; j < kZ; ++j) {
+                    const int i = j * 128 + t128, half = i >> 9, r = c + ((i >> 4) & 31);
+                    const int m = walk.m0() + static_cast<int>(rank) * 128 + 8 * (i & 15);
+                    zr[j] = make_uint4(0, 0, 0, 0);
+                    if (r < walk.n && m < g.M)
+                        zr[j] = __ldg(reinterpret_cast<const uint4*>(g.z_in + static_cast<int64_t>(walk.n0 + r) * (kZ / 4 * g.f) + half * g.f + m));
+                }
+            };
+            if constexpr (kActGrad) read_z(32 * grp);
             const uint32_t buf = n_acc & 1;
             if (!none) {
-                ok = tc::mbar_wait_warp_cluster(&acc_full[buf], n_acc >> 1, &waits);
+                ok = tc::mbar_wait_warp(&acc_full[buf], n_acc >> 1, &waits);
                 none = !ok;
                 ++n_acc;
                 tc::fence_after();
@@ -319,20 +338,16 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                     tc::tmem_ld_frag(tb + c0, lo);
                     tc::tmem_ld_frag(tb + (16u << 16) + c0, hi);
                 }
-                if constexpr (EPI == kEpiSwigluGrad || EPI == kEpiRelu2Grad) {
-                    // z of these rows and neurons into shared memory
-                    constexpr int kHalves = EPI == kEpiSwigluGrad ? 2 : 1;
+                if constexpr (kActGrad) {
+                    // z of these rows and neurons into shared memory, the next rows' on their way to registers
 #pragma unroll
-                    for (int j = 0; j < 4 * kHalves; ++j) {
+                    for (int j = 0; j < kZ; ++j) {
                         const int i = j * 128 + t128, half = i >> 9, r = (i >> 4) & 31, p = i & 15;
-                        const int m = am + 8 * p;
-                        const bool in = r < left && m < g.M;
-                        const uint16_t* src = g.z_in + (row0 + (in ? r : 0)) * (kHalves * g.f) + half * g.f + (in ? m : 0);
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sb + half * 8192 + r * 256 + ((p ^ (r & 7)) << 4)),
-                                     "l"(src), "r"(in ? 16 : 0)
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sb + half * 8192 + r * 256 + ((p ^ (r & 7)) << 4)),
+                                     "r"(zr[j].x), "r"(zr[j].y), "r"(zr[j].z), "r"(zr[j].w)
                                      : "memory");
                     }
-                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    if (left > 64) read_z(c0 + 64);
                     tc::named_sync(1 + grp, 128);
                 }
                 if (!none) tc::tmem_wait32(lo, hi);

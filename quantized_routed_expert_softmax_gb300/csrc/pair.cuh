@@ -26,33 +26,16 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
     return a;
 }
+// Arrivals and waits between the pair's CTAs hand over tiles that the async proxy wrote (or that a fence.proxy.async in the
+// writer's CTA has made visible to it) and tensor memory, to MMAs that read each CTA's memories from that CTA's own side.
+// They go without release and acquire over the cluster, which costs some 900 cycles each: with them a K step took 1950
+// cycles, without them 500.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void st_cluster(uint32_t cluster_addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
-// mbar_wait_warp for barriers that the other CTA arrives on.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, "
-        "p;\n\t}"
-        : "=r"(ok)
-        : "r"(s_addr(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_warp_cluster(uint64_t* bar, uint32_t n, const volatile Waits* w) {
-    const uint32_t parity = n & 1u;
-    if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
-    const long long t0 = global_ns();
-    for (uint32_t i = 0;; ++i) {
-        if ((i & 63u) == 0 && __any_sync(0xffffffffu, w->fail || global_ns() - t0 > w->limit_ns)) return false;
-        if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
-    }
-}
-
 __device__ __forceinline__ void pair_alloc(uint32_t* base, uint32_t cols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s_addr(base)), "r"(cols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
