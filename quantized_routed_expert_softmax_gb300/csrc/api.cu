@@ -33,6 +33,7 @@ cudaError_t configure_gemm_kernels();
 cudaError_t configure_route_kernels();
 cudaError_t configure_mxfp4_kernels();
 cudaError_t configure_ffn_kernels();
+cudaError_t configure_int8_kernels();
 cudaError_t launch_expert_gemm(const ExpertArgs&, int, int, int, int, int, int, cudaStream_t);
 cudaError_t launch_gather_x_f16(const ExpertArgs&, int, cudaStream_t);
 cudaError_t configure_decode_kernel(int, int);
@@ -106,6 +107,7 @@ cudaError_t ensure_configured(int* num_sms) {
         if (e == cudaSuccess) e = configure_route_kernels();
         if (e == cudaSuccess) e = configure_mxfp4_kernels();
         if (e == cudaSuccess) e = configure_ffn_kernels();
+        if (e == cudaSuccess) e = configure_int8_kernels();
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&g_num_sms[dev], cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess) e = configure_decode_kernel(dev, g_num_sms[dev]);
         if (e != cudaSuccess) return e;

@@ -1,54 +1,512 @@
 // int8_gemm.cu -- the expert-indexed product of int8 rows with per-channel int8 weights:
 //   z[r][n] = sx[r] sw[n] * sum_i qx[r][i] qw[n][i]
-// with the sum of code products in integers, exact.
+//
+// GB300's tensor cores take 8-bit integers at a small fraction of their f16 rate, so the codes, which f16 holds exactly, go
+// through f16 MMAs (tcgen05 cta_group::2) with fp32 accumulators.  A product of two codes is at most 127^2, so the sum of
+// 1024 columns is below 2^24 and exact; longer sums are cut into segments of 1024 whose exact sums are added in fp32, in
+// tensor memory.
+//
+// Weights are the MMA's M (256 a pair of CTAs), an expert's rows its N (32 .. 128), so that an expert with few rows does not
+// pay for a full tile.  A persistent grid of CTA pairs; warps have fixed roles, linked by mbarriers:
+//   warp 0       bulk copies of the codes: per K step of 64, 128 weight rows and half of the tile's rows.  A panel of 32
+//                columns holds the codes of consecutive rows side by side, so a tile is one run of bytes wherever it starts;
+//   warps 4-11   weight codes -> f16, straight into tensor memory as the MMA's A (row i in lane i), every other step by each
+//                four;
+//   warps 12-15  codes of the rows -> f16 into 128-byte-swizzled shared memory, as B;
+//   warp 1       of CTA 0: one thread issues the step's four MMAs for both CTAs;
+//   warps 16-23  epilogue: two groups of four warps that take 32 rows in turn.  Scales, activation, and through shared
+//                memory in 16-byte pieces of whole rows to memory.
+// Two accumulators alternate.
+//
+// A code c is converted by arithmetic on bits: 0x64 in front of the byte c + 128 is the f16 value 1152 + c, and subtracting
+// 1152 is exact; two values an instruction.
 #include <algorithm>
 
-#include "int8.cuh"
+#include "pair.cuh"
 
 namespace moe {
 
-// A thread has one result (SwiGLU: a gate and an up sum); a block 32 columns of 8 rows of one expert.
-__global__ void __launch_bounds__(256) int8_product_kernel(const uint8_t* __restrict__ xq, int P, const uint8_t* __restrict__ wq,
-                                                           int E, int N, int K, const int32_t* __restrict__ offsets, int act,
-                                                           void* __restrict__ out, int ot) {
+constexpr int kI8Threads = 768;
+constexpr int kI8ConvA0 = 4, kI8ConvB0 = 12, kI8Epi0 = 16;   // first warps of the roles
+constexpr int kI8NT = 128, kI8StepK = 64;
+constexpr int kI8SegSteps = 1024 / kI8StepK;
+constexpr int kI8RawA = 128 * kI8StepK, kI8Raw = kI8RawA + kI8NT / 2 * kI8StepK, kI8RawStages = 10;
+constexpr int kI8ConvB = kI8NT / 2 * 128, kI8ConvStages = 4;
+constexpr int kI8EpiBytes = 16 * 1024;
+constexpr uint32_t kI8TotCol = 2 * kI8NT, kI8ACol = 3 * kI8NT, kI8TmemCols = 512;
+constexpr int kI8LimitWord = 8;   // the waits' limit in ns (int64) in the workspace: 0 means a second
+constexpr size_t kI8Smem = 1024 + kI8ConvStages * kI8ConvB + kI8RawStages * kI8Raw + 2 * kI8EpiBytes;
+static_assert(kI8ACol + 32 * kI8ConvStages <= kI8TmemCols, "tensor memory");
+static_assert(kI8Smem + sizeof(RowTiles) + 512 <= 227 * 1024, "rings and staging fit beside the table");
+static_assert((kI8Threads - 1) * 2 >= kMaxE, "the last thread has no offsets");
+
+struct I8Args {
+    const uint8_t *xq, *wq;
+    int64_t w_mat;   // bytes between weight matrices
+    const int32_t* offsets;
+    int E, P, N, K;
+    void* out;
+    int32_t* err;
+};
+
+// Four codes -> two pairs of f16.
+__device__ __forceinline__ void i8_f16(uint32_t w, uint32_t* h) {
+    const uint32_t u = w ^ 0x80808080u, k1152 = 0x64806480u;
+    asm("{\n\t.reg .b32 a, b;\n\tprmt.b32 a, %2, %4, 0x4140;\n\tprmt.b32 b, %2, %4, 0x4342;\n\t"
+        "sub.rn.f16x2 %0, a, %3;\n\tsub.rn.f16x2 %1, b, %3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1])
+        : "r"(u), "r"(k1152), "r"(0x64646464u));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint32_t* v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(tc::s_addr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
+        "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]),
+        "r"(v[31])
+        : "memory");
+}
+// The inverse of tc::tmem_ld_frag.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const float* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+        "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void i8_mma(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+__device__ __forceinline__ void i8_fail(const I8Args& g, volatile tc::Waits* waits, uint32_t rank) {
+    waits->fail = 1;
+    tc::st_cluster(tc::peer_addr(tc::s_addr(const_cast<const int*>(&waits->fail)), rank ^ 1u), 1u);
+    set_error(g.err, tc::kErrTimeout);
+}
+
+// SiLU to a few units in the last place at any gate: exp(-|g|) is at most 1, so that the divisor of the fast division lies
+// in [1, 2], where it is good to 2 units.
+__device__ __forceinline__ float i8_silu(float g) {
+    const float e = expf(-fabsf(g));
+    return __fdividef(g < 0.0f ? g * e : g, 1.0f + e);
+}
+__device__ __forceinline__ uint32_t i8_pack(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int ACT, bool F32>
+__global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_constant__ I8Args g) {
+    constexpr bool kGated = ACT == MOE_ACT_SWIGLU;
+    extern __shared__ __align__(16) unsigned char dsm_raw[];
+    unsigned char* convb = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char* raw = convb + kI8ConvStages * kI8ConvB;
+    unsigned char* staging = raw + kI8RawStages * kI8Raw;
+    __shared__ uint64_t raw_full[kI8RawStages], raw_empty[kI8RawStages], ready[kI8ConvStages], empty[kI8ConvStages];
+    __shared__ uint64_t acc_full[2], acc_empty[2], drained;
+    __shared__ uint32_t issued, tmem_base;
+    __shared__ volatile tc::Waits waits;
+    __shared__ RowTiles tiles;
+    // (through shuffles, so that the compiler takes the roles' branches as uniform)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const uint32_t rank = __shfl_sync(0xffffffffu, tc::cluster_rank(), 0);
+
+    if (warp == 3) tc::pair_alloc(&tmem_base, kI8TmemCols);
+    if (tid == 0) {
+        for (int s = 0; s < kI8RawStages; ++s) {
+            tc::mbar_init(&raw_full[s], 1);
+            tc::mbar_init(&raw_empty[s], 8);   // four warps for A, four for B
+        }
+        for (int s = 0; s < kI8ConvStages; ++s) {
+            tc::mbar_init(&ready[s], 16);      // the same of both CTAs
+            tc::mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(&acc_full[s], 1);
+            tc::mbar_init(&acc_empty[s], 16);
+        }
+        tc::mbar_init(&drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        waits.fail = 0;
+        issued = 0;
+    }
     pdl_wait();
-    const int width = act == MOE_ACT_SWIGLU ? N / 2 : N;
-    const float* sx = reinterpret_cast<const float*>(xq);
-    for (int e = blockIdx.y; e < E; e += gridDim.y) {
-        int first, last;
-        expert_rows(offsets, e, P, &first, &last);
-        const uint8_t* w = wq + e * i8_bytes(N, K);
-        const float* sw = reinterpret_cast<const float*>(w);
-        for (int n0 = blockIdx.x * 32; n0 < width; n0 += gridDim.x * 32) {
-            const int n = n0 + (threadIdx.x & 31);
-            if (n >= width) continue;
-            for (int r = first + (threadIdx.x >> 5); r < last; r += 8) {
-                int a = 0, b = 0;
-                for (int p = 0; p < K / 32; ++p) {
-                    const int* xp = reinterpret_cast<const int*>(xq + i8_scale_bytes(P) + (static_cast<int64_t>(p) * P + r) * 32);
-                    const uint8_t* wp = w + i8_scale_bytes(N) + (static_cast<int64_t>(p) * N + n) * 32;
-                    for (int i = 0; i < 8; ++i) {
-                        a = __dp4a(xp[i], reinterpret_cast<const int*>(wp)[i], a);
-                        if (act == MOE_ACT_SWIGLU) b = __dp4a(xp[i], reinterpret_cast<const int*>(wp + 32ll * width)[i], b);
+    if (tid == kI8Threads - 1) {
+        const long long limit = *reinterpret_cast<const volatile long long*>(g.err + kI8LimitWord);
+        waits.limit_ns = limit != 0 ? limit : tc::kWaitLimitNs;
+    }
+    build_row_tiles<kI8Threads>(tiles, g.offsets, g.E, g.P, kI8NT);
+    tc::fence_before();
+    tc::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = tmem_base;
+    TileWalk walk(tiles, (g.N + 255) / 256, blockIdx.x >> 1, gridDim.x >> 1);
+    const int ksteps = (g.K + kI8StepK - 1) / kI8StepK, panels = g.K / 32;
+    const int width = kGated ? g.N / 2 : g.N;
+    int e = 0, n0 = 0, n = 0;
+    auto item = [&] {
+        walk.at(&e, &n0, &n);
+        e = __shfl_sync(0xffffffffu, e, 0);
+        n0 = __shfl_sync(0xffffffffu, n0, 0);
+        n = __shfl_sync(0xffffffffu, n, 0);
+    };
+    auto mma_n = [&] { return (n + 31) & ~31; };
+
+    if (warp == 0) {
+        // -------------------------------------------------------------------- copies
+        const bool leader = tc::elect_one();
+        const uint32_t raw0 = tc::s_addr(raw);
+        uint32_t st = 0, use = 0;
+        bool ok = true;
+        for (; walk.more() && ok; walk.next()) {
+            item();
+            const int half = mma_n() >> 1, before = static_cast<int>(rank) * half;
+            const int col = walk.mtile * (kGated ? 128 : 256) + static_cast<int>(rank) * (kGated ? 64 : 128);   // of the result
+            const uint32_t a_bytes = 32u * static_cast<uint32_t>(max(0, min(kGated ? 64 : 128, width - col)));
+            const uint32_t b_bytes = 32u * static_cast<uint32_t>(max(0, min(half, n - before)));
+            const uint8_t* a = g.wq + e * g.w_mat + i8_scale_bytes(g.N) + 32ll * col;
+            const uint8_t* b = g.xq + i8_scale_bytes(g.P) + 32ll * (n0 + before);
+            for (int ks = 0; ks < ksteps; ++ks) {
+                if (use > 0 && !tc::mbar_wait_warp(&raw_empty[st], use - 1, &waits)) {
+                    ok = false;
+                    break;
+                }
+                if (leader) {
+                    const int np = min(2, panels - 2 * ks);
+                    const uint32_t dst = raw0 + st * kI8Raw;
+                    tc::mbar_arrive_expect_tx(&raw_full[st], np * ((kGated ? 2 : 1) * a_bytes + b_bytes));
+                    for (int p = 0; p < np; ++p) {
+                        if (a_bytes) {
+                            bulk_copy(dst + p * 4096, a, a_bytes, &raw_full[st]);
+                            if (kGated) bulk_copy(dst + p * 4096 + 2048, a + 32ll * width, a_bytes, &raw_full[st]);
+                        }
+                        if (b_bytes) bulk_copy(dst + kI8RawA + p * 2048, b, b_bytes, &raw_full[st]);
+                        a += 32ll * g.N;
+                        b += 32ll * g.P;
                     }
                 }
-                float y = static_cast<float>(a) * (sx[r] * sw[n]);
-                if (act == MOE_ACT_SWIGLU) y = silu(y) * (static_cast<float>(b) * (sx[r] * sw[width + n]));
-                else if (act == MOE_ACT_RELU2) y = y > 0.0f ? y * y : (y <= 0.0f ? 0.0f : y);
-                const int64_t o = static_cast<int64_t>(r) * width + n;
-                if (ot == MOE_F32) static_cast<float*>(out)[o] = y;
-                else static_cast<__nv_bfloat16*>(out)[o] = __float2bfloat16_rn(y);
+                if (++st == kI8RawStages) st = 0, ++use;
             }
         }
+        if (leader) {
+            issued = use * kI8RawStages + st;
+            if (!ok) i8_fail(g, &waits, rank);
+        }
+    } else if (warp == 1 && rank == 0) {
+        // -------------------------------------------------------------------- MMA issuer
+        const bool leader = tc::elect_one();
+        const uint64_t db0 = tc::sdesc_k128(tc::s_addr(convb));
+        uint32_t st = 0, use = 0, n_acc = 0;
+        bool ok = true;
+        for (; walk.more() && ok; walk.next()) {
+            item();
+            const uint32_t idesc = tc::pair_idesc(mma_n(), 0, false, false);
+            for (int ks = 0; ks < ksteps; ++ks) {
+                const int in_seg = ks % kI8SegSteps;
+                const uint32_t buf = n_acc & 1, ub = n_acc >> 1;
+                if (in_seg == 0 && ub > 0 && !tc::mbar_wait_warp(&acc_empty[buf], ub - 1, &waits)) {
+                    ok = false;
+                    break;
+                }
+                if (!tc::mbar_wait_warp(&ready[st], use, &waits)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                const bool last = in_seg + 1 == kI8SegSteps || ks + 1 == ksteps;
+                if (leader) {
+                    const uint64_t db = db0 + st * (kI8ConvB >> 4);
+                    const uint32_t ta = tmem + kI8ACol + 32 * st;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) i8_mma(tmem + buf * kI8NT, ta + 8 * kk, db + 2 * kk, idesc, in_seg > 0 || kk > 0);
+                    tc::pair_commit(&empty[st]);
+                    if (last) tc::pair_commit(&acc_full[buf]);
+                }
+                if (last) ++n_acc;
+                if (++st == kI8ConvStages) st = 0, ++use;
+            }
+        }
+        if (leader && !ok) i8_fail(g, &waits, rank);
+    } else if (warp >= kI8ConvA0 && warp < kI8Epi0) {
+        // -------------------------------------------------------------------- codes to f16
+        const bool is_a = warp < kI8ConvB0;
+        const int q = warp & 3, t128 = tid & 127;
+        const uint32_t by = is_a ? 2 : 1, first = is_a ? (warp - kI8ConvA0) >> 2 : 0;
+        const uint32_t raw0 = tc::s_addr(raw), conv0 = tc::s_addr(convb), ready0 = tc::peer_addr(tc::s_addr(&ready[0]), 0);
+        // A: this lane's row in a panel of the raw tile (SwiGLU: 64 gate rows, then 64 up rows)
+        const int arow = kGated ? (lane >> 4) * 64 + 16 * q + (lane & 15) : 32 * q + lane;
+        // B: this lane's row, panel and its first 16 codes of it; lanes 4-7 of 8 begin with the second half, so that 8 lanes
+        // meet all banks both in the raw tile and in the swizzled one
+        const int brow = t128 & 63, bpanel = t128 >> 6;
+        uint32_t rs = first, cs = first, ruse = 0, cuse = 0;
+        int ks = static_cast<int>(first);   // of the step in its item
+        bool ok = true;
+        for (; walk.more() && ok; walk.next()) {
+            item();
+            const int half = mma_n() >> 1;
+            for (; ks < ksteps; ks += by) {
+                if (!tc::mbar_wait_warp(&raw_full[rs], ruse, &waits) || (cuse > 0 && !tc::mbar_wait_warp(&empty[cs], cuse - 1, &waits))) {
+                    ok = false;
+                    break;
+                }
+                const bool two = 2 * ks + 1 < panels;
+                const uint32_t src = raw0 + rs * kI8Raw;
+                if (is_a) {
+                    tc::fence_after();
+                    uint32_t h[32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {   // 16 codes
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (i < 2 || two) v = lds128(src + (i >> 1) * 4096 + arow * 32 + (i & 1) * 16);
+                        i8_f16(v.x, h + 8 * i), i8_f16(v.y, h + 8 * i + 2), i8_f16(v.z, h + 8 * i + 4), i8_f16(v.w, h + 8 * i + 6);
+                    }
+                    tmem_st32(tmem + (static_cast<uint32_t>(q * 32) << 16) + kI8ACol + 32 * cs, h);
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    tc::fence_before();
+                } else {
+                    if (brow < half) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int hf = ((brow >> 2) & 1) ^ j;
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (bpanel == 0 || two) v = lds128(src + kI8RawA + bpanel * 2048 + brow * 32 + hf * 16);
+                            uint32_t h[8];
+                            i8_f16(v.x, h), i8_f16(v.y, h + 2), i8_f16(v.z, h + 4), i8_f16(v.w, h + 6);
+                            const uint32_t row = conv0 + cs * kI8ConvB + brow * 128;
+                            const int c = bpanel * 4 + hf * 2;
+                            sts128(row + ((c ^ (brow & 7)) << 4), h);
+                            sts128(row + (((c + 1) ^ (brow & 7)) << 4), h + 4);
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    tc::mbar_arrive(&raw_empty[rs]);
+                    tc::mbar_arrive_cluster(ready0 + cs * 8);
+                }
+                rs += by, cs += by;
+                if (rs >= kI8RawStages) rs -= kI8RawStages, ++ruse;
+                if (cs >= kI8ConvStages) cs -= kI8ConvStages, ++cuse;
+            }
+            ks -= ksteps;
+        }
+        // the MMAs' last arrivals on this CTA's barriers, which have to land before it ends (the warps for B see every stage)
+        for (int i = 0; i < kI8ConvStages && ok && !is_a; ++i) {
+            if (cuse > 0) ok = tc::mbar_wait_warp(&empty[cs], cuse - 1, &waits);
+            if (++cs == kI8ConvStages) cs = 0, ++cuse;
+        }
+        if (!ok && lane == 0) i8_fail(g, &waits, rank);
+    } else if (warp >= kI8Epi0) {
+        // -------------------------------------------------------------------- epilogue
+        constexpr int kRow = (kGated ? 64 : 128) * (F32 ? 4 : 2);   // bytes of a staged row
+        const int q = warp & 3, grp = (warp - kI8Epi0) >> 2, t128 = tid & 127;
+        const uint32_t sb = tc::s_addr(staging + grp * kI8EpiBytes);
+        const uint32_t acc0 = tc::peer_addr(tc::s_addr(&acc_empty[0]), 0);
+        const int mrow = lane >> 2, ncol = 2 * (lane & 3);   // this lane's place in a fragment
+        const int r8 = lane & 7;
+        const int piece = kGated ? q * 2 + ((lane >> 3) & 1) : q * 4 + (lane >> 3);   // stmatrix (bf16): this lane's 16 bytes
+        const uint32_t at = sb + r8 * kRow + ((piece ^ r8) << 4) + (kGated ? (lane >> 4) * 8 * kRow : 0);
+        const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        const float* sx = reinterpret_cast<const float*>(g.xq);
+        const bool wide = width % (F32 ? 4 : 8) == 0;
+        const int segs = (ksteps + kI8SegSteps - 1) / kI8SegSteps;
+        uint32_t n_acc = 0;
+        bool ok = true;
+        for (; walk.more(); walk.next()) {
+            item();
+            const int col0 = walk.mtile * (kGated ? 128 : 256) + static_cast<int>(rank) * (kGated ? 64 : 128);
+            float sw[4];   // rows mrow, + 8, + 16, + 24 of the warp's (SwiGLU: gate, gate + 8, up, up + 8)
+            {
+                const float* ws = reinterpret_cast<const float*>(g.wq + e * g.w_mat);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = col0 + (kGated ? 16 * q + 8 * (i & 1) : 32 * q + 8 * i) + mrow;
+                    sw[i] = __ldg(ws + (kGated && i >= 2 ? width : 0) + min(c, width - 1));
+                }
+            }
+            for (int seg = 0; seg < segs; ++seg) {
+                // (after a wait that ran out the group's warps go on, as they meet at barriers: zeros, not valid)
+                const uint32_t buf = n_acc & 1;
+                if (ok) ok = tc::mbar_wait_warp(&acc_full[buf], n_acc >> 1, &waits);
+                ++n_acc;
+                tc::fence_after();
+                const bool last = seg + 1 == segs;
+#pragma unroll 1
+                for (int c0 = 32 * grp; c0 < n; c0 += 64) {
+                    float lo[16], hi[16], s[8];
+                    if (last) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) s[j] = __ldg(sx + n0 + min(c0 + 8 * (j >> 1) + ncol + (j & 1), n - 1));
+                    }
+                    if (ok) {
+                        tc::tmem_ld_frag(tq + buf * kI8NT + c0, lo);
+                        tc::tmem_ld_frag(tq + (16u << 16) + buf * kI8NT + c0, hi);
+                        tc::tmem_wait32(lo, hi);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) lo[j] = hi[j] = 0.0f;
+                    }
+                    if (seg > 0 && ok) {   // the segments so far
+                        float t[16];
+                        tc::tmem_ld_frag(tq + kI8TotCol + c0, t);
+                        tc::tmem_ld_wait(t);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) lo[j] += t[j];
+                        tc::tmem_ld_frag(tq + (16u << 16) + kI8TotCol + c0, t);
+                        tc::tmem_ld_wait(t);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) hi[j] += t[j];
+                    }
+                    if (!last) {
+                        if (ok) {
+                            tmem_st_frag(tq + kI8TotCol + c0, lo);
+                            tmem_st_frag(tq + (16u << 16) + kI8TotCol + c0, hi);
+                            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                        }
+                        continue;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float t = s[2 * (j >> 2) + (j & 1)];
+                        lo[j] *= t * sw[(j >> 1) & 1];
+                        hi[j] *= t * sw[2 + ((j >> 1) & 1)];
+                        if (kGated) lo[j] = i8_silu(lo[j]) * hi[j];
+                        if (ACT == MOE_ACT_RELU2) {
+                            lo[j] = lo[j] > 0.0f ? lo[j] * lo[j] : (lo[j] <= 0.0f ? 0.0f : lo[j]);
+                            hi[j] = hi[j] > 0.0f ? hi[j] * hi[j] : (hi[j] <= 0.0f ? 0.0f : hi[j]);
+                        }
+                    }
+                    if constexpr (F32) {
+#pragma unroll
+                        for (int j = 0; j < (kGated ? 16 : 32); ++j) {   // (column ^ 8 * row / 2: the lanes of a store meet all banks)
+                            const float v = j < 16 ? lo[j] : hi[j - 16];
+                            const int r = 8 * ((j & 15) >> 2) + ncol + (j & 1);
+                            const int c = q * (kGated ? 16 : 32) + (j >> 4) * 16 + ((j >> 1) & 1) * 8 + mrow;
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + r * kRow + ((c ^ (8 * (lane & 3))) << 2)), "f"(v) : "memory");
+                        }
+                    } else if constexpr (kGated) {
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2)
+                            tc::stsm4_t(at + i * 8 * kRow, i8_pack(lo[4 * i], lo[4 * i + 1]), i8_pack(lo[4 * i + 2], lo[4 * i + 3]),
+                                        i8_pack(lo[4 * i + 4], lo[4 * i + 5]), i8_pack(lo[4 * i + 6], lo[4 * i + 7]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            tc::stsm4_t(at + i * 8 * kRow, i8_pack(lo[4 * i], lo[4 * i + 1]), i8_pack(lo[4 * i + 2], lo[4 * i + 3]),
+                                        i8_pack(hi[4 * i], hi[4 * i + 1]), i8_pack(hi[4 * i + 2], hi[4 * i + 3]));
+                    }
+                    tc::named_sync(1 + grp, 128);
+                    const int left = n - c0, cols = width - col0;
+                    const int64_t o0 = static_cast<int64_t>(n0 + c0) * width + col0;
+                    constexpr int kElem = F32 ? 4 : 2, kPer = kRow / 16, kEach = 16 / kElem;
+                    if (wide) {   // whole rows, 16 bytes a lane
+#pragma unroll
+                        for (int j = 0; j < kRow * 32 / 16 / 128; ++j) {
+                            const int i = j * 128 + t128, r = i / kPer, p = i % kPer;
+                            const int place = F32 ? p ^ (2 * ((r >> 1) & 3)) : p ^ (r & 7);
+                            if (r >= left || p * kEach >= cols) continue;
+                            *reinterpret_cast<uint4*>(static_cast<char*>(g.out) + (o0 + static_cast<int64_t>(r) * width + p * kEach) * kElem) =
+                                lds128(sb + r * kRow + (place << 4));
+                        }
+                    } else {   // rows that start anywhere: a value a lane
+                        for (int i = t128; i < 32 * kPer * kEach; i += 128) {
+                            const int r = i / (kPer * kEach), c = i % (kPer * kEach);
+                            if (r >= left || c >= cols) continue;
+                            const int place = F32 ? (c / kEach) ^ (2 * ((r >> 1) & 3)) : (c / kEach) ^ (r & 7);
+                            const unsigned char* p = staging + grp * kI8EpiBytes + r * kRow + (place << 4) + (c % kEach) * kElem;
+                            const int64_t o = o0 + static_cast<int64_t>(r) * width + c;
+                            if (F32) static_cast<float*>(g.out)[o] = *reinterpret_cast<const float*>(p);
+                            else static_cast<uint16_t*>(g.out)[o] = *reinterpret_cast<const uint16_t*>(p);
+                        }
+                    }
+                    tc::named_sync(1 + grp, 128);   // the staging is free again
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0 && ok) tc::mbar_arrive_cluster(acc0 + buf * 8);
+            }
+        }
+        if (!ok && lane == 0) i8_fail(g, &waits, rank);
     }
+
+    // Every copy and MMA of the pair has landed before its memories are given back: the converters waited for every copy
+    // and, at the end, for the MMAs, the epilogues for every accumulator.  Where a wait ran out (both CTAs know it then)
+    // the copies that were issued are waited for, and one more commit tracks all MMAs; the first of these waits that runs
+    // out ends them.
+    __syncwarp();   // (roles end with one lane at work)
+    tc::fence_before();
+    tc::cluster_sync();
+    if (waits.fail) {
+        if (warp == 1 && rank == 0 && tc::elect_one()) tc::pair_commit(&drained);   // (the lane that issued them)
+        __syncthreads();
+        if (tid == 0) {
+            bool ok = tc::mbar_wait(&drained, 0);
+            for (uint32_t i = issued > kI8RawStages ? issued - kI8RawStages : 0; i < issued && ok; ++i)
+                ok = tc::mbar_wait(&raw_full[i % kI8RawStages], i / kI8RawStages);
+        }
+        __syncwarp();
+        tc::cluster_sync();
+    }
+    tc::fence_after();
+    if (warp == 3) tc::pair_dealloc(tmem, kI8TmemCols);
+}
+
+// ------------------------------------------------------------------------------- host side
+namespace {
+
+using I8Kernel = void (*)(I8Args);
+
+I8Kernel i8_kernel(int act, bool f32) {
+    if (act == MOE_ACT_SWIGLU) return f32 ? int8_gemm_kernel<MOE_ACT_SWIGLU, true> : int8_gemm_kernel<MOE_ACT_SWIGLU, false>;
+    if (act == MOE_ACT_RELU2) return f32 ? int8_gemm_kernel<MOE_ACT_RELU2, true> : int8_gemm_kernel<MOE_ACT_RELU2, false>;
+    return f32 ? int8_gemm_kernel<MOE_ACT_NONE, true> : int8_gemm_kernel<MOE_ACT_NONE, false>;
+}
+
+}  // namespace
+
+cudaError_t configure_int8_kernels() {
+    cudaError_t e = cudaSuccess;
+    for (int act : {MOE_ACT_SWIGLU, MOE_ACT_RELU2, MOE_ACT_NONE})
+        for (bool f32 : {false, true}) {
+            const void* fn = reinterpret_cast<const void*>(i8_kernel(act, f32));
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kI8Smem));
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        }
+    return e;
 }
 
 cudaError_t launch_int8_matmul(const void* xq, int64_t P, const void* wq, int64_t E, int64_t N, int64_t K, const int32_t* offsets,
-                               int act, void* out, int ot, int32_t*, int, cudaStream_t s) {
-    const int64_t width = act == MOE_ACT_SWIGLU ? N / 2 : N;
-    return launch_pdl(int8_product_kernel, dim3(static_cast<unsigned>((width + 31) / 32), static_cast<unsigned>(E)), dim3(256), 0, s,
-                      static_cast<const uint8_t*>(xq), static_cast<int>(P), static_cast<const uint8_t*>(wq), static_cast<int>(E),
-                      static_cast<int>(N), static_cast<int>(K), offsets, act, out, ot);
+                               int act, void* out, int ot, int32_t* err, int num_sms, cudaStream_t s) {
+    I8Args g{};
+    g.xq = static_cast<const uint8_t*>(xq);
+    g.wq = static_cast<const uint8_t*>(wq);
+    g.w_mat = i8_bytes(N, K);
+    g.offsets = offsets;
+    g.E = static_cast<int>(E), g.P = static_cast<int>(P), g.N = static_cast<int>(N), g.K = static_cast<int>(K);
+    g.out = out;
+    g.err = err;
+    const int64_t bound = (N + 255) / 256 * (std::min(E, P) + P / kI8NT);
+    const int pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms / 2, bound)));
+    return launch_pairs(i8_kernel(act, ot == MOE_F32), pairs, kI8Threads, kI8Smem, s, g);
 }
 
 }  // namespace moe

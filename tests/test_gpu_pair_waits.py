@@ -65,3 +65,14 @@ def test_weight_gradients_give_up_and_recover(dtype):
     ws = native.ffn_workspace(P, f, backward=True)
     _, saved = native.ffn_forward(x, wgu, wd, save=True, workspace=ws)
     _gives_up_and_recovers(lambda: native.ffn_backward(dy, x, wgu, wd, saved, workspace=ws, dtype=dtype, need=(False, False, True))[2:], ws)
+
+
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("P,N", [(300, 512), (600, 4096)])
+def test_int8_product_gives_up_and_recovers(P, N, act):
+    K = 65536
+    g = torch.Generator("cuda").manual_seed(P)
+    xq = native.quantize_int8(torch.randn(P, K, device="cuda", generator=g))[0]
+    wq = native.quantize_int8(torch.randn(N, K, device="cuda", generator=g))[0]
+    ws = native.int8_workspace()
+    _gives_up_and_recovers(lambda: (native.int8_matmul(xq, wq, None, P, N, K, act=act, workspace=ws),), ws)
