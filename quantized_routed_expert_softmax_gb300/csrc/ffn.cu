@@ -22,12 +22,8 @@
 //               of the result) in turn.  Fragments of the accumulators go through stmatrix, transposed, into rows of the
 //               result in shared memory, and from there to memory in 16-byte pieces of whole rows.
 // Two accumulators alternate, so that the epilogue runs beside the next tile's MMAs.
-#include <cuda.h>   // CUtensorMap and its enums; the encoder is looked up in the driver at run time
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cstring>
-#include <mutex>
 
 #include "pair.cuh"
 
@@ -491,34 +487,12 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
 // ------------------------------------------------------------------------------- host side
 namespace {
 
-PFN_cuTensorMapEncodeTiled_v12000 g_ff_encode = nullptr;
-
-cudaError_t ff_encoder() {
-    static std::once_flag once;
-    static cudaError_t status = cudaSuccess;
-    std::call_once(once, [] {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        status = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
-        if (status == cudaSuccess && (q != cudaDriverEntryPointSuccess || fn == nullptr)) status = cudaErrorNotSupported;
-        if (status == cudaSuccess) g_ff_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    });
-    return status;
-}
-
-// bf16 values in 128-byte-swizzled boxes; what lies outside the tensor reads as zero.  strides in values.
+// bf16 values in 128-byte-swizzled boxes; strides in values.
 cudaError_t ff_map(CUtensorMap* m, int rank, const void* base, std::initializer_list<int64_t> dims, std::initializer_list<int64_t> strides,
-                   std::initializer_list<int> box) {
-    cuuint64_t d[5], st[4];
-    cuuint32_t b[5];
-    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
-    std::copy(dims.begin(), dims.end(), d);
-    std::transform(strides.begin(), strides.end(), st, [](int64_t v) { return static_cast<cuuint64_t>(2 * v); });
-    std::copy(box.begin(), box.end(), b);
-    const CUresult r = g_ff_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, b, es,
-                                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+                   std::initializer_list<int64_t> box) {
+    int64_t st[4];
+    std::transform(strides.begin(), strides.end(), st, [](int64_t v) { return 2 * v; });
+    return tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, rank, base, dims.begin(), st, box.begin());
 }
 
 // Rows of B, K-major: boxes of 16, 32, 64, 128 rows.
@@ -548,8 +522,7 @@ cudaError_t ff_configure() {
 }  // namespace
 
 cudaError_t configure_ffn_kernels() {
-    cudaError_t e = ff_encoder();
-    if (e == cudaSuccess) e = ff_configure<kEpiSwiglu, kOrderKK>();
+    cudaError_t e = ff_configure<kEpiSwiglu, kOrderKK>();
     if (e == cudaSuccess) e = ff_configure<kEpiRelu2, kOrderKK>();
     if (e == cudaSuccess) e = ff_configure<kEpiBf16, kOrderKK>();
     if (e == cudaSuccess) e = ff_configure<kEpiSwigluGrad, kOrderMK>();

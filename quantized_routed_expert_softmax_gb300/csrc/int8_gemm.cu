@@ -21,6 +21,7 @@
 // A code c is converted by arithmetic on bits: 0x64 in front of the byte c + 128 is the f16 value 1152 + c, and subtracting
 // 1152 is exact; two values an instruction.
 #include <algorithm>
+#include <cstring>
 
 #include "pair.cuh"
 
@@ -28,19 +29,26 @@ namespace moe {
 
 constexpr int kI8Threads = 768;
 constexpr int kI8ConvA0 = 4, kI8ConvB0 = 12, kI8Epi0 = 16;   // first warps of the roles
-constexpr int kI8NT = 128, kI8StepK = 64;
+constexpr int kI8NT = 128, kI8StepK = 128;
 constexpr int kI8SegSteps = 1024 / kI8StepK;
-constexpr int kI8RawA = 128 * kI8StepK, kI8Raw = kI8RawA + kI8NT / 2 * kI8StepK, kI8RawStages = 10;
-constexpr int kI8ConvB = kI8NT / 2 * 128, kI8ConvStages = 4;
+constexpr int kI8RawA = 128 * kI8StepK, kI8Raw = kI8RawA + kI8NT / 2 * kI8StepK, kI8RawStages = 4;
+constexpr int kI8ConvB = kI8NT / 2 * 2 * kI8StepK, kI8ConvStages = 4;
 constexpr int kI8EpiBytes = 16 * 1024;
-constexpr uint32_t kI8TotCol = 2 * kI8NT, kI8ACol = 3 * kI8NT, kI8TmemCols = 512;
+constexpr uint32_t kI8ACol = 2 * kI8NT, kI8TmemCols = 512;   // A's stages of 64 columns behind the two accumulators
 constexpr int kI8LimitWord = 8;   // the waits' limit in ns (int64) in the workspace: 0 means a second
 constexpr size_t kI8Smem = 1024 + kI8ConvStages * kI8ConvB + kI8RawStages * kI8Raw + 2 * kI8EpiBytes;
-static_assert(kI8ACol + 32 * kI8ConvStages <= kI8TmemCols, "tensor memory");
+static_assert(kI8ACol + 64 * kI8ConvStages <= kI8TmemCols, "tensor memory");
 static_assert(kI8Smem + sizeof(RowTiles) + 512 <= 227 * 1024, "rings and staging fit beside the table");
+static_assert(kI8ConvStages % 2 == 0 && kI8RawStages % 2 == 0, "the two groups of warps for A have stages of their own");
 static_assert((kI8Threads - 1) * 2 >= kMaxE, "the last thread has no offsets");
+// Sums of more than 1024 columns: the epilogue's warps hold their segments' sums in registers, which the other warps give
+// up (sixteen warps of 48 and eight of 144 are the 24 of 80 that the block starts with).
+constexpr int kI8RegsOther = 48, kI8RegsEpi = 144;
+static_assert(16 * kI8RegsOther + 8 * kI8RegsEpi <= 24 * 80, "registers of the block");
 
 struct I8Args {
+    CUtensorMap tw;      // codes of the weights {8 bytes, panel, matrix}, boxes of 64 rows by 4 panels
+    CUtensorMap tx[3];   // codes of the rows {8 bytes, panel}, boxes of 16 << i rows by 4 panels
     const uint8_t *xq, *wq;
     int64_t w_mat;   // bytes between weight matrices
     const int32_t* offsets;
@@ -65,27 +73,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ void sts128(uint32_t a, const uint32_t* v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-                 "r"(bytes), "r"(tc::s_addr(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
-        "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]),
-        "r"(v[31])
-        : "memory");
-}
-// The inverse of tc::tmem_ld_frag.
-__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const float* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
-        "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
 __device__ __forceinline__ void i8_mma(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accumulate) {
@@ -113,7 +105,7 @@ __device__ __forceinline__ uint32_t i8_pack(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int ACT, bool F32>
+template <int ACT, bool F32, bool MULTI>
 __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_constant__ I8Args g) {
     constexpr bool kGated = ACT == MOE_ACT_SWIGLU;
     extern __shared__ __align__(16) unsigned char dsm_raw[];
@@ -129,6 +121,10 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t rank = __shfl_sync(0xffffffffu, tc::cluster_rank(), 0);
 
+    if (warp == 0 && lane == 0) {
+        tc::prefetch_map(&g.tw);
+        tc::prefetch_map(&g.tx[0]);
+    }
     if (warp == 3) tc::pair_alloc(&tmem_base, kI8TmemCols);
     if (tid == 0) {
         for (int s = 0; s < kI8RawStages; ++s) {
@@ -159,7 +155,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
     tc::fence_after();
     const uint32_t tmem = tmem_base;
     TileWalk walk(tiles, (g.N + 255) / 256, blockIdx.x >> 1, gridDim.x >> 1);
-    const int ksteps = (g.K + kI8StepK - 1) / kI8StepK, panels = g.K / 32;
+    const int ksteps = (g.K + kI8StepK - 1) / kI8StepK;
     const int width = kGated ? g.N / 2 : g.N;
     int e = 0, n0 = 0, n = 0;
     auto item = [&] {
@@ -170,152 +166,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
     };
     auto mma_n = [&] { return (n + 31) & ~31; };
 
-    if (warp == 0) {
-        // -------------------------------------------------------------------- copies
-        const bool leader = tc::elect_one();
-        const uint32_t raw0 = tc::s_addr(raw);
-        uint32_t st = 0, use = 0;
-        bool ok = true;
-        for (; walk.more() && ok; walk.next()) {
-            item();
-            const int half = mma_n() >> 1, before = static_cast<int>(rank) * half;
-            const int col = walk.mtile * (kGated ? 128 : 256) + static_cast<int>(rank) * (kGated ? 64 : 128);   // of the result
-            const uint32_t a_bytes = 32u * static_cast<uint32_t>(max(0, min(kGated ? 64 : 128, width - col)));
-            const uint32_t b_bytes = 32u * static_cast<uint32_t>(max(0, min(half, n - before)));
-            const uint8_t* a = g.wq + e * g.w_mat + i8_scale_bytes(g.N) + 32ll * col;
-            const uint8_t* b = g.xq + i8_scale_bytes(g.P) + 32ll * (n0 + before);
-            for (int ks = 0; ks < ksteps; ++ks) {
-                if (use > 0 && !tc::mbar_wait_warp(&raw_empty[st], use - 1, &waits)) {
-                    ok = false;
-                    break;
-                }
-                if (leader) {
-                    const int np = min(2, panels - 2 * ks);
-                    const uint32_t dst = raw0 + st * kI8Raw;
-                    tc::mbar_arrive_expect_tx(&raw_full[st], np * ((kGated ? 2 : 1) * a_bytes + b_bytes));
-                    for (int p = 0; p < np; ++p) {
-                        if (a_bytes) {
-                            bulk_copy(dst + p * 4096, a, a_bytes, &raw_full[st]);
-                            if (kGated) bulk_copy(dst + p * 4096 + 2048, a + 32ll * width, a_bytes, &raw_full[st]);
-                        }
-                        if (b_bytes) bulk_copy(dst + kI8RawA + p * 2048, b, b_bytes, &raw_full[st]);
-                        a += 32ll * g.N;
-                        b += 32ll * g.P;
-                    }
-                }
-                if (++st == kI8RawStages) st = 0, ++use;
-            }
-        }
-        if (leader) {
-            issued = use * kI8RawStages + st;
-            if (!ok) i8_fail(g, &waits, rank);
-        }
-    } else if (warp == 1 && rank == 0) {
-        // -------------------------------------------------------------------- MMA issuer
-        const bool leader = tc::elect_one();
-        const uint64_t db0 = tc::sdesc_k128(tc::s_addr(convb));
-        uint32_t st = 0, use = 0, n_acc = 0;
-        bool ok = true;
-        for (; walk.more() && ok; walk.next()) {
-            item();
-            const uint32_t idesc = tc::pair_idesc(mma_n(), 0, false, false);
-            for (int ks = 0; ks < ksteps; ++ks) {
-                const int in_seg = ks % kI8SegSteps;
-                const uint32_t buf = n_acc & 1, ub = n_acc >> 1;
-                if (in_seg == 0 && ub > 0 && !tc::mbar_wait_warp(&acc_empty[buf], ub - 1, &waits)) {
-                    ok = false;
-                    break;
-                }
-                if (!tc::mbar_wait_warp(&ready[st], use, &waits)) {
-                    ok = false;
-                    break;
-                }
-                tc::fence_after();
-                const bool last = in_seg + 1 == kI8SegSteps || ks + 1 == ksteps;
-                if (leader) {
-                    const uint64_t db = db0 + st * (kI8ConvB >> 4);
-                    const uint32_t ta = tmem + kI8ACol + 32 * st;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) i8_mma(tmem + buf * kI8NT, ta + 8 * kk, db + 2 * kk, idesc, in_seg > 0 || kk > 0);
-                    tc::pair_commit(&empty[st]);
-                    if (last) tc::pair_commit(&acc_full[buf]);
-                }
-                if (last) ++n_acc;
-                if (++st == kI8ConvStages) st = 0, ++use;
-            }
-        }
-        if (leader && !ok) i8_fail(g, &waits, rank);
-    } else if (warp >= kI8ConvA0 && warp < kI8Epi0) {
-        // -------------------------------------------------------------------- codes to f16
-        const bool is_a = warp < kI8ConvB0;
-        const int q = warp & 3, t128 = tid & 127;
-        const uint32_t by = is_a ? 2 : 1, first = is_a ? (warp - kI8ConvA0) >> 2 : 0;
-        const uint32_t raw0 = tc::s_addr(raw), conv0 = tc::s_addr(convb), ready0 = tc::peer_addr(tc::s_addr(&ready[0]), 0);
-        // A: this lane's row in a panel of the raw tile (SwiGLU: 64 gate rows, then 64 up rows)
-        const int arow = kGated ? (lane >> 4) * 64 + 16 * q + (lane & 15) : 32 * q + lane;
-        // B: this lane's row, panel and its first 16 codes of it; lanes 4-7 of 8 begin with the second half, so that 8 lanes
-        // meet all banks both in the raw tile and in the swizzled one
-        const int brow = t128 & 63, bpanel = t128 >> 6;
-        uint32_t rs = first, cs = first, ruse = 0, cuse = 0;
-        int ks = static_cast<int>(first);   // of the step in its item
-        bool ok = true;
-        for (; walk.more() && ok; walk.next()) {
-            item();
-            const int half = mma_n() >> 1;
-            for (; ks < ksteps; ks += by) {
-                if (!tc::mbar_wait_warp(&raw_full[rs], ruse, &waits) || (cuse > 0 && !tc::mbar_wait_warp(&empty[cs], cuse - 1, &waits))) {
-                    ok = false;
-                    break;
-                }
-                const bool two = 2 * ks + 1 < panels;
-                const uint32_t src = raw0 + rs * kI8Raw;
-                if (is_a) {
-                    tc::fence_after();
-                    uint32_t h[32];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {   // 16 codes
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (i < 2 || two) v = lds128(src + (i >> 1) * 4096 + arow * 32 + (i & 1) * 16);
-                        i8_f16(v.x, h + 8 * i), i8_f16(v.y, h + 8 * i + 2), i8_f16(v.z, h + 8 * i + 4), i8_f16(v.w, h + 8 * i + 6);
-                    }
-                    tmem_st32(tmem + (static_cast<uint32_t>(q * 32) << 16) + kI8ACol + 32 * cs, h);
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    tc::fence_before();
-                } else {
-                    if (brow < half) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int hf = ((brow >> 2) & 1) ^ j;
-                            uint4 v = make_uint4(0, 0, 0, 0);
-                            if (bpanel == 0 || two) v = lds128(src + kI8RawA + bpanel * 2048 + brow * 32 + hf * 16);
-                            uint32_t h[8];
-                            i8_f16(v.x, h), i8_f16(v.y, h + 2), i8_f16(v.z, h + 4), i8_f16(v.w, h + 6);
-                            const uint32_t row = conv0 + cs * kI8ConvB + brow * 128;
-                            const int c = bpanel * 4 + hf * 2;
-                            sts128(row + ((c ^ (brow & 7)) << 4), h);
-                            sts128(row + (((c + 1) ^ (brow & 7)) << 4), h + 4);
-                        }
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    tc::mbar_arrive(&raw_empty[rs]);
-                    tc::mbar_arrive_cluster(ready0 + cs * 8);
-                }
-                rs += by, cs += by;
-                if (rs >= kI8RawStages) rs -= kI8RawStages, ++ruse;
-                if (cs >= kI8ConvStages) cs -= kI8ConvStages, ++cuse;
-            }
-            ks -= ksteps;
-        }
-        // the MMAs' last arrivals on this CTA's barriers, which have to land before it ends (the warps for B see every stage)
-        for (int i = 0; i < kI8ConvStages && ok && !is_a; ++i) {
-            if (cuse > 0) ok = tc::mbar_wait_warp(&empty[cs], cuse - 1, &waits);
-            if (++cs == kI8ConvStages) cs = 0, ++cuse;
-        }
-        if (!ok && lane == 0) i8_fail(g, &waits, rank);
-    } else if (warp >= kI8Epi0) {
+    if (warp >= kI8Epi0) {
+        if constexpr (MULTI) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kI8RegsEpi));
         // -------------------------------------------------------------------- epilogue
         constexpr int kRow = (kGated ? 64 : 128) * (F32 ? 4 : 2);   // bytes of a staged row
         const int q = warp & 3, grp = (warp - kI8Epi0) >> 2, t128 = tid & 127;
@@ -343,47 +195,38 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                     sw[i] = __ldg(ws + (kGated && i >= 2 ? width : 0) + min(c, width - 1));
                 }
             }
+            float sums[MULTI ? 2 : 1][32];   // of 32 rows (two times, SwiGLU: gate and up rows): 16 lanes, the other 16
             for (int seg = 0; seg < segs; ++seg) {
-                // (after a wait that ran out the group's warps go on, as they meet at barriers: zeros, not valid)
+                // (after a wait that ran out the group's warps go on, as they meet at barriers; the sums are not valid then)
                 const uint32_t buf = n_acc & 1;
                 if (ok) ok = tc::mbar_wait_warp(&acc_full[buf], n_acc >> 1, &waits);
                 ++n_acc;
                 tc::fence_after();
                 const bool last = seg + 1 == segs;
-#pragma unroll 1
-                for (int c0 = 32 * grp; c0 < n; c0 += 64) {
-                    float lo[16], hi[16], s[8];
-                    if (last) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) s[j] = __ldg(sx + n0 + min(c0 + 8 * (j >> 1) + ncol + (j & 1), n - 1));
-                    }
-                    if (ok) {
+#pragma unroll (MULTI ? 2 : 1)
+                for (int ch = 0; ch < 2; ++ch) {
+                    const int c0 = 32 * grp + 64 * ch;
+                    if (c0 >= n) continue;
+                    float* lo = sums[MULTI ? ch : 0];
+                    float* hi = lo + 16;
+                    if (!MULTI || seg == 0) {
                         tc::tmem_ld_frag(tq + buf * kI8NT + c0, lo);
                         tc::tmem_ld_frag(tq + (16u << 16) + buf * kI8NT + c0, hi);
                         tc::tmem_wait32(lo, hi);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) lo[j] = hi[j] = 0.0f;
-                    }
-                    if (seg > 0 && ok) {   // the segments so far
-                        float t[16];
-                        tc::tmem_ld_frag(tq + kI8TotCol + c0, t);
-                        tc::tmem_ld_wait(t);
+                        for (int u = 0; u < 2; ++u) {
+                            float v[16];
+                            tc::tmem_ld_frag(tq + (u ? 16u << 16 : 0u) + buf * kI8NT + c0, v);
+                            tc::tmem_ld_wait(v);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) lo[j] += t[j];
-                        tc::tmem_ld_frag(tq + (16u << 16) + kI8TotCol + c0, t);
-                        tc::tmem_ld_wait(t);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) hi[j] += t[j];
-                    }
-                    if (!last) {
-                        if (ok) {
-                            tmem_st_frag(tq + kI8TotCol + c0, lo);
-                            tmem_st_frag(tq + (16u << 16) + kI8TotCol + c0, hi);
-                            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                            for (int j = 0; j < 16; ++j) lo[16 * u + j] += v[j];
                         }
-                        continue;
                     }
+                    if (MULTI && !last) continue;
+                    float s[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[j] = __ldg(sx + n0 + min(c0 + 8 * (j >> 1) + ncol + (j & 1), n - 1));
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const float t = s[2 * (j >> 2) + (j & 1)];
@@ -446,6 +289,165 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
             }
         }
         if (!ok && lane == 0) i8_fail(g, &waits, rank);
+    } else {
+        if constexpr (MULTI) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kI8RegsOther));
+        if (warp == 0) {
+            // -------------------------------------------------------------------- copies
+            const bool leader = tc::elect_one();
+            const uint32_t raw0 = tc::s_addr(raw);
+            uint32_t st = 0, use = 0;
+            bool ok = true;
+            for (; walk.more() && ok; walk.next()) {
+                item();
+                const int half = mma_n() >> 1, before = static_cast<int>(rank) * half;
+                const int col = walk.mtile * (kGated ? 128 : 256) + static_cast<int>(rank) * (kGated ? 64 : 128);   // of the result
+                int bi = 0;
+                while ((16 << bi) < half) ++bi;   // the smallest box of rows
+                for (int ks = 0; ks < ksteps; ++ks) {
+                    if (use > 0 && !tc::mbar_wait_warp(&raw_empty[st], use - 1, &waits)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) {
+                        // (rows and panels past a matrix's end arrive as zeros)
+                        const uint32_t dst = raw0 + st * kI8Raw;
+                        tc::mbar_arrive_expect_tx(&raw_full[st], kI8RawA + (16 << bi) * kI8StepK);
+                        tc::tma_3d(dst, &g.tw, 4 * col, 4 * ks, e, &raw_full[st]);
+                        tc::tma_3d(dst + kI8RawA / 2, &g.tw, 4 * (col + (kGated ? width : 64)), 4 * ks, e, &raw_full[st]);
+                        tc::tma_2d(dst + kI8RawA, &g.tx[bi], 4 * (n0 + before), 4 * ks, &raw_full[st]);
+                    }
+                    if (++st == kI8RawStages) st = 0, ++use;
+                }
+            }
+            if (leader) {
+                issued = use * kI8RawStages + st;
+                if (!ok) i8_fail(g, &waits, rank);
+            }
+        } else if (warp == 1 && rank == 0) {
+            // -------------------------------------------------------------------- MMA issuer
+            const bool leader = tc::elect_one();
+            const uint64_t db0 = tc::sdesc_k128(tc::s_addr(convb));
+            uint32_t st = 0, use = 0, n_acc = 0;
+            bool ok = true;
+            for (; walk.more() && ok; walk.next()) {
+                item();
+                const uint32_t idesc = tc::pair_idesc(mma_n(), 0, false, false);
+                for (int ks = 0; ks < ksteps; ++ks) {
+                    const int in_seg = ks % kI8SegSteps;
+                    const uint32_t buf = n_acc & 1, ub = n_acc >> 1;
+                    if (in_seg == 0 && ub > 0 && !tc::mbar_wait_warp(&acc_empty[buf], ub - 1, &waits)) {
+                        ok = false;
+                        break;
+                    }
+                    if (!tc::mbar_wait_warp(&ready[st], use, &waits)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    const bool last = in_seg + 1 == kI8SegSteps || ks + 1 == ksteps;
+                    if (leader) {
+                        const uint64_t db = db0 + st * (kI8ConvB >> 4);
+                        const uint32_t ta = tmem + kI8ACol + 64 * st;
+    #pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)   // (64 columns of B's rows, then the next 64)
+                            i8_mma(tmem + buf * kI8NT, ta + 8 * kk, db + (kk >> 2) * (kI8ConvB / 2 / 16) + 2 * (kk & 3), idesc, in_seg > 0 || kk > 0);
+                        tc::pair_commit(&empty[st]);
+                        if (last) tc::pair_commit(&acc_full[buf]);
+                    }
+                    if (last) ++n_acc;
+                    if (++st == kI8ConvStages) st = 0, ++use;
+                }
+            }
+            if (leader && !ok) i8_fail(g, &waits, rank);
+        } else if (warp >= kI8ConvA0 && warp < kI8Epi0) {
+            // -------------------------------------------------------------------- codes to f16
+            const bool is_a = warp < kI8ConvB0;
+            const int q = warp & 3, t128 = tid & 127;
+            const uint32_t by = is_a ? 2 : 1, first = is_a ? (warp - kI8ConvA0) >> 2 : 0;
+            const uint32_t raw0 = tc::s_addr(raw), conv0 = tc::s_addr(convb), ready0 = tc::peer_addr(tc::s_addr(&ready[0]), 0);
+            // A: this lane's row in a panel of the raw tile (two boxes of 64 rows; SwiGLU: gate rows, then up rows).  Lanes 4-7 of
+            // 8 read a row's second half first, so that 8 lanes meet all banks.
+            const int arow = kGated ? (lane >> 4) * 64 + 16 * q + (lane & 15) : 32 * q + lane;
+            const uint32_t aoff = (arow >> 6) * (kI8RawA / 2) + (arow & 63) * 32;
+            const bool swap = (lane >> 2) & 1;
+            // B: this lane's row and half of the step's columns, in the same order, which also spreads the swizzled stores
+            const int brow = t128 & 63, bset = t128 >> 6, bhalf = (brow >> 2) & 1;
+            uint32_t rs = first, cs = first, ruse = 0, cuse = 0;
+            int ks = static_cast<int>(first);   // of the step in its item
+            bool ok = true;
+            for (; walk.more() && ok; walk.next()) {
+                item();
+                const int half = mma_n() >> 1;
+                int bi = 0;
+                while ((16 << bi) < half) ++bi;
+                const uint32_t pstride = 32u * (16 << bi);   // of the panels of the rows' box
+                for (; ks < ksteps; ks += by) {
+                    if (!tc::mbar_wait_warp(&raw_full[rs], ruse, &waits)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t src = raw0 + rs * kI8Raw;
+                    if (is_a) {
+                        // (the first panel is read and converted before the wait for the MMAs that use the stage)
+                        uint32_t h[16];
+                        auto read = [&](int p) {
+                            const uint4 v = lds128(src + aoff + p * 2048 + (swap ? 16 : 0)), w = lds128(src + aoff + p * 2048 + (swap ? 0 : 16));
+                            i8_f16(swap ? w.x : v.x, h), i8_f16(swap ? w.y : v.y, h + 2), i8_f16(swap ? w.z : v.z, h + 4), i8_f16(swap ? w.w : v.w, h + 6);
+                            i8_f16(swap ? v.x : w.x, h + 8), i8_f16(swap ? v.y : w.y, h + 10), i8_f16(swap ? v.z : w.z, h + 12), i8_f16(swap ? v.w : w.w, h + 14);
+                        };
+                        read(0);
+                        if (cuse > 0 && !tc::mbar_wait_warp(&empty[cs], cuse - 1, &waits)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after();
+                        const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + kI8ACol + 64 * cs;
+                        tmem_st16(t, h);
+    #pragma unroll
+                        for (int p = 1; p < 4; ++p) {
+                            read(p);
+                            tmem_st16(t + 16 * p, h);
+                        }
+                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                        tc::fence_before();
+                    } else {
+                        if (cuse > 0 && !tc::mbar_wait_warp(&empty[cs], cuse - 1, &waits)) {
+                            ok = false;
+                            break;
+                        }
+                        if (brow < half) {
+                            const uint32_t row = conv0 + cs * kI8ConvB + bset * (kI8ConvB / 2) + brow * 128;
+                            const uint32_t from = src + kI8RawA + bset * 2 * pstride + brow * 32;
+    #pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int hf = bhalf ^ (j & 1), c = (j >> 1) * 4 + hf * 2;
+                                const uint4 v = lds128(from + (j >> 1) * pstride + hf * 16);
+                                uint32_t h[8];
+                                i8_f16(v.x, h), i8_f16(v.y, h + 2), i8_f16(v.z, h + 4), i8_f16(v.w, h + 6);
+                                sts128(row + ((c ^ (brow & 7)) << 4), h);
+                                sts128(row + (((c + 1) ^ (brow & 7)) << 4), h + 4);
+                            }
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::mbar_arrive(&raw_empty[rs]);
+                        tc::mbar_arrive_cluster(ready0 + cs * 8);
+                    }
+                    rs += by, cs += by;
+                    if (rs >= kI8RawStages) rs -= kI8RawStages, ++ruse;
+                    if (cs >= kI8ConvStages) cs -= kI8ConvStages, ++cuse;
+                }
+                ks -= ksteps;
+            }
+            // the MMAs' last arrivals on this CTA's barriers, which have to land before it ends (the warps for B see every stage)
+            for (int i = 0; i < kI8ConvStages && ok && !is_a; ++i) {
+                if (cuse > 0) ok = tc::mbar_wait_warp(&empty[cs], cuse - 1, &waits);
+                if (++cs == kI8ConvStages) cs = 0, ++cuse;
+            }
+            if (!ok && lane == 0) i8_fail(g, &waits, rank);
+        }
     }
 
     // Every copy and MMA of the pair has landed before its memories are given back: the converters waited for every copy
@@ -475,10 +477,11 @@ namespace {
 
 using I8Kernel = void (*)(I8Args);
 
+template <bool MULTI>
 I8Kernel i8_kernel(int act, bool f32) {
-    if (act == MOE_ACT_SWIGLU) return f32 ? int8_gemm_kernel<MOE_ACT_SWIGLU, true> : int8_gemm_kernel<MOE_ACT_SWIGLU, false>;
-    if (act == MOE_ACT_RELU2) return f32 ? int8_gemm_kernel<MOE_ACT_RELU2, true> : int8_gemm_kernel<MOE_ACT_RELU2, false>;
-    return f32 ? int8_gemm_kernel<MOE_ACT_NONE, true> : int8_gemm_kernel<MOE_ACT_NONE, false>;
+    if (act == MOE_ACT_SWIGLU) return f32 ? int8_gemm_kernel<MOE_ACT_SWIGLU, true, MULTI> : int8_gemm_kernel<MOE_ACT_SWIGLU, false, MULTI>;
+    if (act == MOE_ACT_RELU2) return f32 ? int8_gemm_kernel<MOE_ACT_RELU2, true, MULTI> : int8_gemm_kernel<MOE_ACT_RELU2, false, MULTI>;
+    return f32 ? int8_gemm_kernel<MOE_ACT_NONE, true, MULTI> : int8_gemm_kernel<MOE_ACT_NONE, false, MULTI>;
 }
 
 }  // namespace
@@ -486,17 +489,19 @@ I8Kernel i8_kernel(int act, bool f32) {
 cudaError_t configure_int8_kernels() {
     cudaError_t e = cudaSuccess;
     for (int act : {MOE_ACT_SWIGLU, MOE_ACT_RELU2, MOE_ACT_NONE})
-        for (bool f32 : {false, true}) {
-            const void* fn = reinterpret_cast<const void*>(i8_kernel(act, f32));
-            if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kI8Smem));
-            if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-        }
+        for (bool f32 : {false, true})
+            for (bool multi : {false, true}) {
+                const void* fn = reinterpret_cast<const void*>(multi ? i8_kernel<true>(act, f32) : i8_kernel<false>(act, f32));
+                if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kI8Smem));
+                if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+            }
     return e;
 }
 
 cudaError_t launch_int8_matmul(const void* xq, int64_t P, const void* wq, int64_t E, int64_t N, int64_t K, const int32_t* offsets,
                                int act, void* out, int ot, int32_t* err, int num_sms, cudaStream_t s) {
-    I8Args g{};
+    I8Args g;
+    std::memset(&g, 0, sizeof(g));
     g.xq = static_cast<const uint8_t*>(xq);
     g.wq = static_cast<const uint8_t*>(wq);
     g.w_mat = i8_bytes(N, K);
@@ -504,9 +509,17 @@ cudaError_t launch_int8_matmul(const void* xq, int64_t P, const void* wq, int64_
     g.E = static_cast<int>(E), g.P = static_cast<int>(P), g.N = static_cast<int>(N), g.K = static_cast<int>(K);
     g.out = out;
     g.err = err;
+    // codes as 8-byte elements, four a row and panel: a box takes 64 rows of a panel as one run
+    cudaError_t e = tensor_map(&g.tw, CU_TENSOR_MAP_DATA_TYPE_INT64, CU_TENSOR_MAP_SWIZZLE_NONE, 3, g.wq + i8_scale_bytes(N), {4 * N, K / 32, E},
+                               {32 * N, g.w_mat}, {256, 4, 1});
+    for (int i = 0; i < 3 && e == cudaSuccess; ++i)
+        e = tensor_map(&g.tx[i], CU_TENSOR_MAP_DATA_TYPE_INT64, CU_TENSOR_MAP_SWIZZLE_NONE, 2, g.xq + i8_scale_bytes(P), {4 * P, K / 32}, {32 * P},
+                       {64 << i, 4});
+    if (e != cudaSuccess) return e;
     const int64_t bound = (N + 255) / 256 * (std::min(E, P) + P / kI8NT);
     const int pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms / 2, bound)));
-    return launch_pairs(i8_kernel(act, ot == MOE_F32), pairs, kI8Threads, kI8Smem, s, g);
+    return launch_pairs(K > kI8SegSteps * kI8StepK ? i8_kernel<true>(act, ot == MOE_F32) : i8_kernel<false>(act, ot == MOE_F32), pairs, kI8Threads,
+                        kI8Smem, s, g);
 }
 
 }  // namespace moe

@@ -5,6 +5,8 @@
 // accumulators of its 128 rows for all of B's.  CTA 0 issues the MMAs for both.
 #pragma once
 
+#include <initializer_list>
+
 #include "int8.cuh"
 #include "tc.cuh"
 
@@ -183,6 +185,16 @@ struct TileWalk {
         *n = min(h, r.y - *r_first);
     }
 };
+
+// A tiled tensor map (strides in bytes, one fewer than dimensions); what lies outside the tensor reads as zero.  The driver's
+// encoder is looked up at run time (pair.cu).
+cudaError_t tensor_map(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, int rank, const void* base, const int64_t* dims,
+                       const int64_t* strides, const int64_t* box);
+inline cudaError_t tensor_map(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, int rank, const void* base,
+                              std::initializer_list<int64_t> dims, std::initializer_list<int64_t> strides,
+                              std::initializer_list<int64_t> box) {
+    return tensor_map(m, type, swizzle, rank, base, dims.begin(), strides.begin(), box.begin());
+}
 
 // Launch of CTA pairs, with the overlap that launch_pdl allows.
 template <typename... Exp, typename... Act>
