@@ -73,12 +73,17 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ void sts128(uint32_t a, const uint32_t* v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+// 16 lanes by 16 columns of tensor memory: v[0, 1] row lane / 4, columns 2 (lane % 4) and the next, v[2, 3] row + 8,
+// v[4 .. 7] the same of columns 8 on.
+__device__ __forceinline__ void tmem_st_frag16(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 __device__ __forceinline__ void i8_mma(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
@@ -348,7 +353,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                     if (leader) {
                         const uint64_t db = db0 + st * (kI8ConvB >> 4);
                         const uint32_t ta = tmem + kI8ACol + 64 * st;
-    #pragma unroll
+#pragma unroll
                         for (int kk = 0; kk < 8; ++kk)   // (64 columns of B's rows, then the next 64)
                             i8_mma(tmem + buf * kI8NT, ta + 8 * kk, db + (kk >> 2) * (kI8ConvB / 2 / 16) + 2 * (kk & 3), idesc, in_seg > 0 || kk > 0);
                         tc::pair_commit(&empty[st]);
@@ -365,12 +370,14 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
             const int q = warp & 3, t128 = tid & 127;
             const uint32_t by = is_a ? 2 : 1, first = is_a ? (warp - kI8ConvA0) >> 2 : 0;
             const uint32_t raw0 = tc::s_addr(raw), conv0 = tc::s_addr(convb), ready0 = tc::peer_addr(tc::s_addr(&ready[0]), 0);
-            // A: this lane's row in a panel of the raw tile (two boxes of 64 rows; SwiGLU: gate rows, then up rows).  Lanes 4-7 of
-            // 8 read a row's second half first, so that 8 lanes meet all banks.
-            const int arow = kGated ? (lane >> 4) * 64 + 16 * q + (lane & 15) : 32 * q + lane;
-            const uint32_t aoff = (arow >> 6) * (kI8RawA / 2) + (arow & 63) * 32;
-            const bool swap = (lane >> 2) & 1;
-            // B: this lane's row and half of the step's columns, in the same order, which also spreads the swizzled stores
+            // A lane of A takes the codes 8 t .. 8 t + 7 (t = lane % 4) of the rows lane / 4, + 8, + 16, + 24 in a panel's 32, so
+            // that a warp's loads are runs of 256 bytes.  As fragments a panel's columns then come in the order of its 4-code
+            // words 0 2 4 6 1 3 5 7; the rows of B are stored in the same order.
+            // (the raw tile of A is two boxes of 64 rows; SwiGLU: gate rows, then up rows)
+            const uint32_t alo = (kGated ? 16 * q * 32 : (q >> 1) * (kI8RawA / 2) + (q & 1) * 1024) + lane * 8;
+            const uint32_t ahi = alo + (kGated ? kI8RawA / 2 : 512);
+            // B: this lane's row and half of the step's columns; lanes 4-7 of 8 begin with the second 16 bytes of a panel, so
+            // that 8 lanes meet all banks, here and in the swizzled stores.
             const int brow = t128 & 63, bset = t128 >> 6, bhalf = (brow >> 2) & 1;
             uint32_t rs = first, cs = first, ruse = 0, cuse = 0;
             int ks = static_cast<int>(first);   // of the step in its item
@@ -388,26 +395,32 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                     }
                     const uint32_t src = raw0 + rs * kI8Raw;
                     if (is_a) {
-                        // (the first panel is read and converted before the wait for the MMAs that use the stage)
-                        uint32_t h[16];
-                        auto read = [&](int p) {
-                            const uint4 v = lds128(src + aoff + p * 2048 + (swap ? 16 : 0)), w = lds128(src + aoff + p * 2048 + (swap ? 0 : 16));
-                            i8_f16(swap ? w.x : v.x, h), i8_f16(swap ? w.y : v.y, h + 2), i8_f16(swap ? w.z : v.z, h + 4), i8_f16(swap ? w.w : v.w, h + 6);
-                            i8_f16(swap ? v.x : w.x, h + 8), i8_f16(swap ? v.y : w.y, h + 10), i8_f16(swap ? v.z : w.z, h + 12), i8_f16(swap ? v.w : w.w, h + 14);
+                        // (the first panel is read before the wait for the MMAs that use the stage, the others ahead of their use)
+                        uint2 r[2][4];
+                        auto read = [&](int p, uint2* v) {
+                            v[0] = lds64(src + p * 2048 + alo), v[1] = lds64(src + p * 2048 + alo + 256);
+                            v[2] = lds64(src + p * 2048 + ahi), v[3] = lds64(src + p * 2048 + ahi + 256);
                         };
-                        read(0);
+                        read(0, r[0]);
                         if (cuse > 0 && !tc::mbar_wait_warp(&empty[cs], cuse - 1, &waits)) {
                             ok = false;
                             break;
                         }
                         tc::fence_after();
                         const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + kI8ACol + 64 * cs;
-                        tmem_st16(t, h);
-    #pragma unroll
-                        for (int p = 1; p < 4; ++p) {
-                            read(p);
-                            tmem_st16(t + 16 * p, h);
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            if (p < 3) read(p + 1, r[(p + 1) & 1]);
+                            const uint2* v = r[p & 1];
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                uint32_t h[8];
+                                i8_f16(v[2 * u].x, h), i8_f16(v[2 * u + 1].x, h + 2), i8_f16(v[2 * u].y, h + 4), i8_f16(v[2 * u + 1].y, h + 6);
+                                tmem_st_frag16(t + (static_cast<uint32_t>(16 * u) << 16) + 16 * p, h);
+                            }
                         }
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&raw_empty[rs]);
                         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                         tc::fence_before();
                     } else {
@@ -418,21 +431,23 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                         if (brow < half) {
                             const uint32_t row = conv0 + cs * kI8ConvB + bset * (kI8ConvB / 2) + brow * 128;
                             const uint32_t from = src + kI8RawA + bset * 2 * pstride + brow * 32;
-    #pragma unroll
+                            uint4 v[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) v[j] = lds128(from + (j >> 1) * pstride + (bhalf ^ (j & 1)) * 16);
+#pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const int hf = bhalf ^ (j & 1), c = (j >> 1) * 4 + hf * 2;
-                                const uint4 v = lds128(from + (j >> 1) * pstride + hf * 16);
+                                const int c = (j >> 1) * 4 + (bhalf ^ (j & 1));   // (words 0 2 of the half to piece c, 1 3 to piece c + 2)
                                 uint32_t h[8];
-                                i8_f16(v.x, h), i8_f16(v.y, h + 2), i8_f16(v.z, h + 4), i8_f16(v.w, h + 6);
+                                i8_f16(v[j].x, h), i8_f16(v[j].z, h + 2), i8_f16(v[j].y, h + 4), i8_f16(v[j].w, h + 6);
                                 sts128(row + ((c ^ (brow & 7)) << 4), h);
-                                sts128(row + (((c + 1) ^ (brow & 7)) << 4), h + 4);
+                                sts128(row + (((c + 2) ^ (brow & 7)) << 4), h + 4);
                             }
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
                     __syncwarp();
                     if (lane == 0) {
-                        tc::mbar_arrive(&raw_empty[rs]);
+                        if (!is_a) tc::mbar_arrive(&raw_empty[rs]);
                         tc::mbar_arrive_cluster(ready0 + cs * 8);
                     }
                     rs += by, cs += by;
