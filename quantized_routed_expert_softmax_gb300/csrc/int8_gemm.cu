@@ -12,9 +12,9 @@
 //                columns holds the codes of consecutive rows side by side, so a tile is one run of bytes wherever it starts;
 //   warps 4-11   weight codes -> f16, straight into tensor memory as the MMA's A (row i in lane i), every other step by each
 //                four;
-//   warps 12-15  codes of the rows -> f16 into 128-byte-swizzled shared memory, as B;
+//   warps 12-19  codes of the rows -> f16 into 128-byte-swizzled shared memory, as B, every other step by each four;
 //   warp 1       of CTA 0: one thread issues the step's four MMAs for both CTAs;
-//   warps 16-23  epilogue: two groups of four warps that take 32 rows in turn.  Scales, activation, and through shared
+//   warps 20-27  epilogue: two groups of four warps that take 32 rows in turn.  Scales, activation, and through shared
 //                memory in 16-byte pieces of whole rows to memory.
 // Two accumulators alternate.
 //
@@ -27,8 +27,8 @@
 
 namespace moe {
 
-constexpr int kI8Threads = 768;
-constexpr int kI8ConvA0 = 4, kI8ConvB0 = 12, kI8Epi0 = 16;   // first warps of the roles
+constexpr int kI8Threads = 896;
+constexpr int kI8ConvA0 = 4, kI8ConvB0 = 12, kI8Epi0 = 20;   // first warps of the roles
 constexpr int kI8NT = 128, kI8StepK = 128;
 constexpr int kI8SegSteps = 1024 / kI8StepK;
 constexpr int kI8RawA = 128 * kI8StepK, kI8Raw = kI8RawA + kI8NT / 2 * kI8StepK, kI8RawStages = 4;
@@ -39,12 +39,12 @@ constexpr int kI8LimitWord = 8;   // the waits' limit in ns (int64) in the works
 constexpr size_t kI8Smem = 1024 + kI8ConvStages * kI8ConvB + kI8RawStages * kI8Raw + 2 * kI8EpiBytes;
 static_assert(kI8ACol + 64 * kI8ConvStages <= kI8TmemCols, "tensor memory");
 static_assert(kI8Smem + sizeof(RowTiles) + 512 <= 227 * 1024, "rings and staging fit beside the table");
-static_assert(kI8ConvStages % 2 == 0 && kI8RawStages % 2 == 0, "the two groups of warps for A have stages of their own");
+static_assert(kI8ConvStages % 2 == 0, "the two groups of converting warps have stages of their own");
 static_assert((kI8Threads - 1) * 2 >= kMaxE, "the last thread has no offsets");
 // Sums of more than 1024 columns: the epilogue's warps hold their segments' sums in registers, which the other warps give
-// up (sixteen warps of 48 and eight of 144 are the 24 of 80 that the block starts with).
-constexpr int kI8RegsOther = 48, kI8RegsEpi = 144;
-static_assert(16 * kI8RegsOther + 8 * kI8RegsEpi <= 24 * 80, "registers of the block");
+// up (twenty warps of 48 and eight of 128 are less than the 28 of 72 that the block starts with).
+constexpr int kI8RegsOther = 48, kI8RegsEpi = 128;
+static_assert(20 * kI8RegsOther + 8 * kI8RegsEpi <= 28 * 72, "registers of the block");
 
 struct I8Args {
     CUtensorMap tw;      // codes of the weights {8 bytes, panel, matrix}, boxes of 64 rows by 4 panels
@@ -353,9 +353,10 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                     if (leader) {
                         const uint64_t db = db0 + st * (kI8ConvB >> 4);
                         const uint32_t ta = tmem + kI8ACol + 64 * st;
+                        const bool two = g.K - ks * kI8StepK > kI8StepK / 2;
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)   // (64 columns of B's rows, then the next 64)
-                            i8_mma(tmem + buf * kI8NT, ta + 8 * kk, db + (kk >> 2) * (kI8ConvB / 2 / 16) + 2 * (kk & 3), idesc, in_seg > 0 || kk > 0);
+                            if (kk < 4 || two) i8_mma(tmem + buf * kI8NT, ta + 8 * kk, db + (kk >> 2) * (kI8ConvB / 2 / 16) + 2 * (kk & 3), idesc, in_seg > 0 || kk > 0);
                         tc::pair_commit(&empty[st]);
                         if (last) tc::pair_commit(&acc_full[buf]);
                     }
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
             // -------------------------------------------------------------------- codes to f16
             const bool is_a = warp < kI8ConvB0;
             const int q = warp & 3, t128 = tid & 127;
-            const uint32_t by = is_a ? 2 : 1, first = is_a ? (warp - kI8ConvA0) >> 2 : 0;
+            const uint32_t by = 2, first = ((warp - kI8ConvA0) >> 2) & 1;   // two groups of four warps each
             const uint32_t raw0 = tc::s_addr(raw), conv0 = tc::s_addr(convb), ready0 = tc::peer_addr(tc::s_addr(&ready[0]), 0);
             // A lane of A takes the codes 8 t .. 8 t + 7 (t = lane % 4) of the rows lane / 4, + 8, + 16, + 24 in a panel's 32, so
             // that a warp's loads are runs of 256 bytes.  As fragments a panel's columns then come in the order of its 4-code
@@ -394,6 +395,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                         break;
                     }
                     const uint32_t src = raw0 + rs * kI8Raw;
+                    const bool two = g.K - ks * kI8StepK > kI8StepK / 2;   // the step's second 64 columns are not all past K
                     if (is_a) {
                         // (the first panel is read before the wait for the MMAs that use the stage, the others ahead of their use)
                         uint2 r[2][4];
@@ -410,6 +412,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                         const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + kI8ACol + 64 * cs;
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
+                            if (p == 2 && !two) break;
                             if (p < 3) read(p + 1, r[(p + 1) & 1]);
                             const uint2* v = r[p & 1];
 #pragma unroll
@@ -428,7 +431,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                             ok = false;
                             break;
                         }
-                        if (brow < half) {
+                        if (brow < half && (two || bset == 0)) {
                             const uint32_t row = conv0 + cs * kI8ConvB + bset * (kI8ConvB / 2) + brow * 128;
                             const uint32_t from = src + kI8RawA + bset * 2 * pstride + brow * 32;
                             uint4 v[4];
@@ -456,10 +459,11 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                 }
                 ks -= ksteps;
             }
-            // the MMAs' last arrivals on this CTA's barriers, which have to land before it ends (the warps for B see every stage)
-            for (int i = 0; i < kI8ConvStages && ok && !is_a; ++i) {
+            // the MMAs' last arrivals on this CTA's barriers, which have to land before it ends (the warps for B: each group its stages)
+            for (int i = 0; i < kI8ConvStages / 2 && ok && !is_a; ++i) {
                 if (cuse > 0) ok = tc::mbar_wait_warp(&empty[cs], cuse - 1, &waits);
-                if (++cs == kI8ConvStages) cs = 0, ++cuse;
+                cs += by;
+                if (cs >= kI8ConvStages) cs -= kI8ConvStages, ++cuse;
             }
             if (!ok && lane == 0) i8_fail(g, &waits, rank);
         }
