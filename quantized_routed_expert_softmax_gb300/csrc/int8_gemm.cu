@@ -29,14 +29,18 @@ namespace moe {
 
 constexpr int kI8Threads = 896;
 constexpr int kI8ConvA0 = 4, kI8ConvB0 = 12, kI8Epi0 = 20;   // first warps of the roles
-constexpr int kI8NT = 128, kI8StepK = 128;
+constexpr int kI8NT = 128, kI8StepK = 128;   // rows of a tile at most
 constexpr int kI8SegSteps = 1024 / kI8StepK;
-constexpr int kI8RawA = 128 * kI8StepK, kI8Raw = kI8RawA + kI8NT / 2 * kI8StepK, kI8RawStages = 4;
-constexpr int kI8ConvB = kI8NT / 2 * 2 * kI8StepK, kI8ConvStages = 4;
+constexpr int kI8RawA = 128 * kI8StepK, kI8ConvStages = 4, kI8MaxRawStages = 7;
+// Bytes of a stage of codes and of converted rows, for tiles of up to nt rows (half of them in a CTA).
+__host__ __device__ constexpr int i8_raw(int nt) { return kI8RawA + nt / 2 * kI8StepK; }
+__host__ __device__ constexpr int i8_conv_b(int nt) { return nt / 2 * 2 * kI8StepK; }
+__host__ __device__ constexpr int i8_raw_stages(int nt) { return nt > 64 ? 4 : 7; }
 constexpr int kI8EpiBytes = 16 * 1024;
 constexpr uint32_t kI8ACol = 2 * kI8NT, kI8TmemCols = 512;   // A's stages of 64 columns behind the two accumulators
 constexpr int kI8LimitWord = 8;   // the waits' limit in ns (int64) in the workspace: 0 means a second
-constexpr size_t kI8Smem = 1024 + kI8ConvStages * kI8ConvB + kI8RawStages * kI8Raw + 2 * kI8EpiBytes;
+constexpr size_t i8_smem(int nt) { return 1024 + kI8ConvStages * i8_conv_b(nt) + i8_raw_stages(nt) * i8_raw(nt) + 2 * kI8EpiBytes; }
+constexpr size_t kI8Smem = i8_smem(128) > i8_smem(64) ? i8_smem(128) : i8_smem(64);
 static_assert(kI8ACol + 64 * kI8ConvStages <= kI8TmemCols, "tensor memory");
 static_assert(kI8Smem + sizeof(RowTiles) + 512 <= 227 * 1024, "rings and staging fit beside the table");
 static_assert(kI8ConvStages % 2 == 0, "the two groups of converting warps have stages of their own");
@@ -53,6 +57,7 @@ struct I8Args {
     int64_t w_mat;   // bytes between weight matrices
     const int32_t* offsets;
     int E, P, N, K;
+    int nt;   // rows of a tile at most: 64 or 128
     void* out;
     int32_t* err;
 };
@@ -115,9 +120,10 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
     constexpr bool kGated = ACT == MOE_ACT_SWIGLU;
     extern __shared__ __align__(16) unsigned char dsm_raw[];
     unsigned char* convb = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    unsigned char* raw = convb + kI8ConvStages * kI8ConvB;
-    unsigned char* staging = raw + kI8RawStages * kI8Raw;
-    __shared__ uint64_t raw_full[kI8RawStages], raw_empty[kI8RawStages], ready[kI8ConvStages], empty[kI8ConvStages];
+    const uint32_t raw_bytes = i8_raw(g.nt), raw_stages = i8_raw_stages(g.nt), convb_bytes = i8_conv_b(g.nt);
+    unsigned char* raw = convb + kI8ConvStages * convb_bytes;
+    unsigned char* staging = raw + raw_stages * raw_bytes;
+    __shared__ uint64_t raw_full[kI8MaxRawStages], raw_empty[kI8MaxRawStages], ready[kI8ConvStages], empty[kI8ConvStages];
     __shared__ uint64_t acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t issued, tmem_base;
     __shared__ volatile tc::Waits waits;
@@ -132,7 +138,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
     }
     if (warp == 3) tc::pair_alloc(&tmem_base, kI8TmemCols);
     if (tid == 0) {
-        for (int s = 0; s < kI8RawStages; ++s) {
+        for (int s = 0; s < kI8MaxRawStages; ++s) {
             tc::mbar_init(&raw_full[s], 1);
             tc::mbar_init(&raw_empty[s], 8);   // four warps for A, four for B
         }
@@ -154,7 +160,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
         const long long limit = *reinterpret_cast<const volatile long long*>(g.err + kI8LimitWord);
         waits.limit_ns = limit != 0 ? limit : tc::kWaitLimitNs;
     }
-    build_row_tiles<kI8Threads>(tiles, g.offsets, g.E, g.P, kI8NT);
+    build_row_tiles<kI8Threads>(tiles, g.offsets, g.E, g.P, g.nt);
     tc::fence_before();
     tc::cluster_sync();
     tc::fence_after();
@@ -315,17 +321,17 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                     }
                     if (leader) {
                         // (rows and panels past a matrix's end arrive as zeros)
-                        const uint32_t dst = raw0 + st * kI8Raw;
+                        const uint32_t dst = raw0 + st * raw_bytes;
                         tc::mbar_arrive_expect_tx(&raw_full[st], kI8RawA + (16 << bi) * kI8StepK);
                         tc::tma_3d(dst, &g.tw, 4 * col, 4 * ks, e, &raw_full[st]);
                         tc::tma_3d(dst + kI8RawA / 2, &g.tw, 4 * (col + (kGated ? width : 64)), 4 * ks, e, &raw_full[st]);
                         tc::tma_2d(dst + kI8RawA, &g.tx[bi], 4 * (n0 + before), 4 * ks, &raw_full[st]);
                     }
-                    if (++st == kI8RawStages) st = 0, ++use;
+                    if (++st == raw_stages) st = 0, ++use;
                 }
             }
             if (leader) {
-                issued = use * kI8RawStages + st;
+                issued = use * raw_stages + st;
                 if (!ok) i8_fail(g, &waits, rank);
             }
         } else if (warp == 1 && rank == 0) {
@@ -334,6 +340,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
             const uint64_t db0 = tc::sdesc_k128(tc::s_addr(convb));
             uint32_t st = 0, use = 0, n_acc = 0;
             bool ok = true;
+            bool seen = false;   // (the leader's) the step's stage was already ready when the step before was issued
             for (; walk.more() && ok; walk.next()) {
                 item();
                 const uint32_t idesc = tc::pair_idesc(mma_n(), 0, false, false);
@@ -344,24 +351,29 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                         ok = false;
                         break;
                     }
-                    if (!tc::mbar_wait_warp(&ready[st], use, &waits)) {
+                    if (!__any_sync(0xffffffffu, seen) && !tc::mbar_wait_warp(&ready[st], use, &waits)) {
                         ok = false;
                         break;
                     }
-                    tc::fence_after();
+                    const uint32_t st1 = st + 1 == kI8ConvStages ? 0 : st + 1, use1 = use + (st1 == 0);
                     const bool last = in_seg + 1 == kI8SegSteps || ks + 1 == ksteps;
+                    const bool two = g.K - ks * kI8StepK > kI8StepK / 2;
+                    seen = false;
+                    tc::fence_after();
                     if (leader) {
-                        const uint64_t db = db0 + st * (kI8ConvB >> 4);
+                        const uint64_t db = db0 + st * (convb_bytes >> 4);
                         const uint32_t ta = tmem + kI8ACol + 64 * st;
-                        const bool two = g.K - ks * kI8StepK > kI8StepK / 2;
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)   // (64 columns of B's rows, then the next 64)
-                            if (kk < 4 || two) i8_mma(tmem + buf * kI8NT, ta + 8 * kk, db + (kk >> 2) * (kI8ConvB / 2 / 16) + 2 * (kk & 3), idesc, in_seg > 0 || kk > 0);
+                            if (kk < 4 || two)
+                                i8_mma(tmem + buf * kI8NT, ta + 8 * kk, db + (kk >> 2) * (convb_bytes >> 5) + 2 * (kk & 3), idesc, in_seg > 0 || kk > 0);
+                        seen = tc::mbar_test_wait(&ready[st1], use1 & 1u);   // beside the MMAs
                         tc::pair_commit(&empty[st]);
                         if (last) tc::pair_commit(&acc_full[buf]);
                     }
                     if (last) ++n_acc;
-                    if (++st == kI8ConvStages) st = 0, ++use;
+                    st = st1;
+                    use = use1;
                 }
             }
             if (leader && !ok) i8_fail(g, &waits, rank);
@@ -394,7 +406,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                         ok = false;
                         break;
                     }
-                    const uint32_t src = raw0 + rs * kI8Raw;
+                    const uint32_t src = raw0 + rs * raw_bytes;
                     const bool two = g.K - ks * kI8StepK > kI8StepK / 2;   // the step's second 64 columns are not all past K
                     if (is_a) {
                         // (the first panel is read before the wait for the MMAs that use the stage, the others ahead of their use)
@@ -432,7 +444,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                             break;
                         }
                         if (brow < half && (two || bset == 0)) {
-                            const uint32_t row = conv0 + cs * kI8ConvB + bset * (kI8ConvB / 2) + brow * 128;
+                            const uint32_t row = conv0 + cs * convb_bytes + bset * (convb_bytes >> 1) + brow * 128;
                             const uint32_t from = src + kI8RawA + bset * 2 * pstride + brow * 32;
                             uint4 v[4];
 #pragma unroll
@@ -454,7 +466,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                         tc::mbar_arrive_cluster(ready0 + cs * 8);
                     }
                     rs += by, cs += by;
-                    if (rs >= kI8RawStages) rs -= kI8RawStages, ++ruse;
+                    if (rs >= raw_stages) rs -= raw_stages, ++ruse;
                     if (cs >= kI8ConvStages) cs -= kI8ConvStages, ++cuse;
                 }
                 ks -= ksteps;
@@ -481,8 +493,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
         __syncthreads();
         if (tid == 0) {
             bool ok = tc::mbar_wait(&drained, 0);
-            for (uint32_t i = issued > kI8RawStages ? issued - kI8RawStages : 0; i < issued && ok; ++i)
-                ok = tc::mbar_wait(&raw_full[i % kI8RawStages], i / kI8RawStages);
+            for (uint32_t i = issued > raw_stages ? issued - raw_stages : 0; i < issued && ok; ++i)
+                ok = tc::mbar_wait(&raw_full[i % raw_stages], i / raw_stages);
         }
         __syncwarp();
         tc::cluster_sync();
@@ -535,10 +547,13 @@ cudaError_t launch_int8_matmul(const void* xq, int64_t P, const void* wq, int64_
         e = tensor_map(&g.tx[i], CU_TENSOR_MAP_DATA_TYPE_INT64, CU_TENSOR_MAP_SWIZZLE_NONE, 2, g.xq + i8_scale_bytes(P), {4 * P, K / 32}, {32 * P},
                        {64 << i, 4});
     if (e != cudaSuccess) return e;
-    const int64_t bound = (N + 255) / 256 * (std::min(E, P) + P / kI8NT);
+    // Tiles of up to 64 rows where experts have few: smaller stages leave room for more of them, and what is on its way from
+    // memory bounds the kernel then.
+    g.nt = P / std::min(E, P) <= 48 ? 64 : 128;
+    const int64_t bound = (N + 255) / 256 * (std::min(E, P) + P / g.nt);
     const int pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms / 2, bound)));
     return launch_pairs(K > kI8SegSteps * kI8StepK ? i8_kernel<true>(act, ot == MOE_F32) : i8_kernel<false>(act, ot == MOE_F32), pairs, kI8Threads,
-                        kI8Smem, s, g);
+                        i8_smem(g.nt), s, g);
 }
 
 }  // namespace moe
