@@ -533,9 +533,16 @@ cudaError_t configure_ffn_kernels() {
     return e;
 }
 
+cudaError_t launch_stream_bf16(const uint16_t*, int64_t, const uint16_t*, int64_t, int64_t, int64_t, const int32_t*, int, uint16_t*, uint16_t*, int,
+                               cudaStream_t);
+
 cudaError_t launch_ffn_forward(const uint16_t* x, int64_t P, const uint16_t* wgu, const uint16_t* wd, int64_t E, int64_t d, int64_t f,
                                const int32_t* offsets, int act, uint16_t* y, uint16_t* z, uint16_t* h, int32_t* err, int num_sms,
                                cudaStream_t s) {
+    if (stream_rows(P)) {
+        const cudaError_t r = launch_stream_bf16(x, P, wgu, E, act == MOE_ACT_SWIGLU ? 2 * f : f, d, offsets, act, h, z, num_sms, s);
+        return r == cudaSuccess ? launch_stream_bf16(h, P, wd, E, d, f, offsets, MOE_ACT_NONE, y, nullptr, num_sms, s) : r;
+    }
     FfArgs g;
     std::memset(&g, 0, sizeof(g));
     g.offsets = offsets, g.E = static_cast<int>(E), g.P = static_cast<int>(P), g.f = static_cast<int>(f), g.err = err;

@@ -2,77 +2,241 @@
 // any number of rows), and its inverse.
 //
 // Per row: s = amax / 127, q = round-half-away(x / s), both divisions correctly rounded in fp32, as the per-channel
-// weight packer has them.
+// weight packer has them.  A division a value would bound the kernel by instructions, so the quotient is first taken as
+// x * (1 / s), which is off by less than 2^-15 of a code; only where that lies so close to the middle between two codes are
+// the values divided.
 #include <algorithm>
 
 #include "int8.cuh"
 
 namespace moe {
 
+// Eight consecutive values as fp32.  fp32: one 32-byte access where the base is 32-byte aligned.
 template <bool F32>
-__global__ void __launch_bounds__(256) int8_quantize_kernel(const void* __restrict__ x, int64_t x_rows,
+__device__ __forceinline__ void i8_load8(const char* p, bool wide, uint32_t* raw) {
+    if (F32 && wide) {
+        asm("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+            : "=r"(raw[0]), "=r"(raw[1]), "=r"(raw[2]), "=r"(raw[3]), "=r"(raw[4]), "=r"(raw[5]), "=r"(raw[6]), "=r"(raw[7])
+            : "l"(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
+        }
+    }
+}
+template <bool F32>
+__device__ __forceinline__ void i8_values(const uint32_t* raw, float* v) {
+#pragma unroll
+    for (int i = 0; i < (F32 ? 8 : 4); ++i) {
+        if (F32) {
+            v[i] = __uint_as_float(raw[i]);
+        } else {
+            v[2 * i] = __uint_as_float(raw[i] << 16);
+            v[2 * i + 1] = __uint_as_float(raw[i] & 0xffff0000u);
+        }
+    }
+}
+// The largest magnitude's bits of eight values (non-negative floats order like their bit patterns, NaN above Inf).
+template <bool F32>
+__device__ __forceinline__ uint32_t i8_amax(const uint32_t* raw) {
+    float v[8];
+    i8_values<F32>(raw, v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    return m;
+}
+
+// Eight codes of a row with scale s, inv about 1 / s, or 0 where that is no normal number.  Adding 1.5 * 2^23 rounds to an integer and leaves its two's
+// complement in the low byte; what it took off tells how near the middle between two codes the quotient is.
+template <bool F32>
+__device__ __forceinline__ uint2 i8_codes(const uint32_t* raw, float s, float inv) {
+    constexpr float kMagic = 12582912.0f;
+    float v[8];
+    i8_values<F32>(raw, v);
+    uint32_t b[8];
+    float worst = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = v[i] * inv, r = t + kMagic;
+        worst = fmaxf(worst, fabsf(t - (r - kMagic)));
+        b[i] = __float_as_uint(r);
+    }
+    if (worst >= 0.4999f || inv == 0.0f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            b[i] = static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(roundf(__fdiv_rn(v[i], s)), -127.0f), 127.0f)));
+    }
+    return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+}
+
+constexpr int kQRow = 256;   // columns that a warp covers at a time, eight a lane
+
+// `split` warps a row, 8 / split consecutive rows a CTA, so that a panel's codes of a CTA's rows lie side by side.  ITERS: a
+// lane holds its part of the row, eight values each time, between the search for the largest and the coding; 0: it reads
+// the row again.
+template <bool F32, int ITERS>
+__global__ void __launch_bounds__(256) int8_quantize_kernel(const char* __restrict__ x, int64_t x_rows,
                                                             const int32_t* __restrict__ src_rows, int src_div, int64_t n_mat,
-                                                            int64_t rows, int cols, uint8_t* __restrict__ dst) {
+                                                            int64_t rows, int cols, int split, bool wide,
+                                                            uint8_t* __restrict__ dst) {
+    constexpr int kElem = F32 ? 4 : 2, kRaw = F32 ? 8 : 4;
+    __shared__ uint32_t largest[8];
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < n_mat * rows; row += warps) {
-        const int64_t m = row / rows, r = row - m * rows;
-        int64_t sr = row;
-        if (src_rows) {
-            const int32_t i = __ldg(src_rows + r);
-            sr = i < 0 || i / src_div >= x_rows ? -1 : i / src_div;
-        }
-        uint32_t amax = 0;   // as bits: non-negative floats order like their bit patterns, NaN above Inf
-        if (sr >= 0)
-            for (int c = lane; c < cols; c += 32)
-                amax = max(amax, __float_as_uint(load_x(x, F32 ? MOE_F32 : MOE_BF16, sr * cols + c)) & 0x7fffffffu);
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        const bool bad = amax >= 0x7f800000u;
-        const float s = __fdiv_rn(__uint_as_float(amax), 127.0f);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp & (split - 1), lead = warp - sub;
+    const int per = 8 / split, step = split * kQRow, c0 = sub * kQRow + lane * 8;
+    const int64_t groups = (rows + per - 1) / per;
+    for (int64_t m = blockIdx.y; m < n_mat; m += gridDim.y) {
         uint8_t* out = dst + m * i8_bytes(rows, cols);
-        for (int c = lane; c < cols; c += 32) {
-            int q = 0;
-            if (!bad && s > 0.0f) {
-                const float v = load_x(x, F32 ? MOE_F32 : MOE_BF16, sr * cols + c);
-                q = static_cast<int>(fminf(fmaxf(roundf(__fdiv_rn(v, s)), -127.0f), 127.0f));
+        for (int64_t grp = blockIdx.x; grp < groups; grp += gridDim.x) {
+            const int64_t r = grp * per + warp / split;
+            const bool live = r < rows;
+            int64_t sr = m * rows + r;
+            if (src_rows) {
+                int32_t i = live ? __ldg(src_rows + r) : -1;
+                if (src_div != 1) i = i < 0 ? -1 : i / src_div;
+                sr = i >= x_rows ? -1 : i;
             }
-            out[i8_scale_bytes(rows) + (static_cast<int64_t>(c >> 5) * rows + r) * 32 + (c & 31)] = static_cast<uint8_t>(q);
+            const bool has = live && sr >= 0;
+            const char* src = x + (sr * cols + c0) * kElem;
+            uint32_t raw[ITERS > 0 ? ITERS : 1][kRaw];
+            uint32_t amax = 0;
+            if constexpr (ITERS > 0) {
+#pragma unroll
+                for (int u = 0; u < ITERS; ++u) {
+#pragma unroll
+                    for (int i = 0; i < kRaw; ++i) raw[u][i] = 0;
+                    if (has && c0 + u * step < cols) i8_load8<F32>(src + static_cast<int64_t>(u) * step * kElem, wide, raw[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < ITERS; ++u) amax = max(amax, i8_amax<F32>(raw[u]));
+            } else if (has) {
+                for (int c = c0; c < cols; c += step) {
+                    i8_load8<F32>(src + static_cast<int64_t>(c - c0) * kElem, wide, raw[0]);
+                    amax = max(amax, i8_amax<F32>(raw[0]));
+                }
+            }
+            amax = __reduce_max_sync(0xffffffffu, amax);
+            if (split > 1) {
+                if (lane == 0) largest[warp] = amax;
+                __syncthreads();
+                for (int i = 0; i < split; ++i) amax = max(amax, largest[lead + i]);
+                __syncthreads();
+            }
+            if (!live) continue;
+            const bool bad = amax >= 0x7f800000u;
+            const float s = __fdiv_rn(__uint_as_float(amax), 127.0f);
+            const float inv = s >= 1.2e-38f ? __frcp_rn(s) : 0.0f;   // (s is 2.7e36 at most)
+            const bool code = has && !bad && s > 0.0f;
+            uint8_t* o = out + i8_scale_bytes(rows) + (static_cast<int64_t>(c0 >> 5) * rows + r) * 32 + (c0 & 31);
+            const int64_t o_step = static_cast<int64_t>(step >> 5) * rows * 32;
+            if constexpr (ITERS > 0) {
+#pragma unroll
+                for (int u = 0; u < ITERS; ++u)
+                    if (c0 + u * step < cols)
+                        *reinterpret_cast<uint2*>(o + u * o_step) = code ? i8_codes<F32>(raw[u], s, inv) : make_uint2(0, 0);
+            } else {
+                for (int c = c0; c < cols; c += step, o += o_step) {
+                    if (code) i8_load8<F32>(src + static_cast<int64_t>(c - c0) * kElem, wide, raw[0]);
+                    *reinterpret_cast<uint2*>(o) = code ? i8_codes<F32>(raw[0], s, inv) : make_uint2(0, 0);
+                }
+            }
+            if (sub == 0 && lane == 0) reinterpret_cast<float*>(out)[r] = bad ? __uint_as_float(0x7fffffffu) : s;
         }
-        if (lane == 0) reinterpret_cast<float*>(out)[r] = bad ? __uint_as_float(0x7fffffffu) : s;
     }
 }
 
+// A warp a row, eight consecutive rows a CTA; grid.y takes parts of the columns where there are few rows.
 template <bool F32>
 __global__ void __launch_bounds__(256) int8_dequantize_kernel(const uint8_t* __restrict__ src, int64_t n_mat, int64_t rows,
-                                                              int cols, void* __restrict__ out) {
+                                                              int cols, bool wide, char* __restrict__ out) {
+    constexpr int kElem = F32 ? 4 : 2;
     pdl_wait();
-    const int64_t n = n_mat * rows * cols;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t row = i / cols, m = row / rows, r = row - m * rows;
-        const int c = static_cast<int>(i - row * cols);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int step = gridDim.y * kQRow, c0 = blockIdx.y * kQRow + lane * 8;
+    const int64_t groups = (rows + 7) / 8;
+    for (int64_t m = blockIdx.z; m < n_mat; m += gridDim.z) {
         const uint8_t* in = src + m * i8_bytes(rows, cols);
-        const int8_t q = static_cast<int8_t>(in[i8_scale_bytes(rows) + (static_cast<int64_t>(c >> 5) * rows + r) * 32 + (c & 31)]);
-        const float v = static_cast<float>(q) * reinterpret_cast<const float*>(in)[r];
-        if (F32) static_cast<float*>(out)[i] = v;
-        else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+        for (int64_t grp = blockIdx.x; grp < groups; grp += gridDim.x) {
+            const int64_t r = grp * 8 + warp;
+            if (r >= rows) continue;
+            const float s = __ldg(reinterpret_cast<const float*>(in) + r);
+            const uint8_t* p = in + i8_scale_bytes(rows) + (static_cast<int64_t>(c0 >> 5) * rows + r) * 32 + (c0 & 31);
+            const int64_t p_step = static_cast<int64_t>(step >> 5) * rows * 32;
+            char* d = out + ((m * rows + r) * cols + c0) * kElem;
+#pragma unroll 4
+            for (int c = c0; c < cols; c += step, p += p_step, d += static_cast<int64_t>(step) * kElem) {
+                const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {   // 2^23 in front of the byte c + 128: 2^23 + 128 + c
+                    const uint32_t w = (i < 4 ? q.x : q.y) ^ 0x80808080u;
+                    v[i] = (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7650 + (i & 3))) - 8388736.0f) * s;
+                }
+                if (F32 && wide) {
+                    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(d), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+                                 "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                                 : "memory");
+                } else if (F32) {
+                    reinterpret_cast<float4*>(d)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    reinterpret_cast<float4*>(d)[1] = make_float4(v[4], v[5], v[6], v[7]);
+                } else {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
     }
 }
+
+namespace {
+
+using QuantizeKernel = void (*)(const char*, int64_t, const int32_t*, int, int64_t, int64_t, int, int, bool, uint8_t*);
+
+template <bool F32>
+QuantizeKernel quantize_kernel(int iters) {
+    if (iters <= 0) return int8_quantize_kernel<F32, 0>;
+    if (iters <= 3) return int8_quantize_kernel<F32, 3>;
+    if (iters <= 6) return int8_quantize_kernel<F32, 6>;
+    return int8_quantize_kernel<F32, 12>;
+}
+
+}  // namespace
 
 cudaError_t launch_int8_quantize(const void* x, int xt, int64_t x_rows, const int32_t* src_rows, int src_div, int64_t n_mat,
                                  int64_t rows, int64_t cols, void* dst, int num_sms, cudaStream_t s) {
-    const int64_t ctas = std::min<int64_t>((n_mat * rows + 7) / 8, static_cast<int64_t>(num_sms) * 8);
-    return launch_pdl(xt == MOE_F32 ? int8_quantize_kernel<true> : int8_quantize_kernel<false>, dim3(static_cast<unsigned>(ctas)),
-                      dim3(256), 0, s, x, x_rows, src_rows, src_div, n_mat, rows, static_cast<int>(cols),
-                      static_cast<uint8_t*>(dst));
+    // Warps a row: more while a lane would hold more than 12 times eight values, or while half the SMs would have no CTA
+    // and a warp more than 256 columns.
+    int split = 1;
+    auto iters = [&] { return static_cast<int>((cols + split * kQRow - 1) / (split * kQRow)); };
+    while (split < 8 && (iters() > 12 || (iters() > 1 && n_mat * rows * split < 4ll * num_sms))) split *= 2;
+    const int64_t groups = (rows * split + 7) / 8, ctas = 8ll * num_sms;
+    const int64_t gx = std::min<int64_t>(groups, ctas);
+    const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(std::min<int64_t>(n_mat, std::max<int64_t>(1, ctas / gx))));
+    const int n = iters() > 12 ? 0 : iters();
+    return launch_pdl(xt == MOE_F32 ? quantize_kernel<true>(n) : quantize_kernel<false>(n), grid, dim3(256), 0, s,
+                      static_cast<const char*>(x), x_rows, src_rows, src_div, n_mat, rows, static_cast<int>(cols), split,
+                      (reinterpret_cast<uintptr_t>(x) & 31u) == 0, static_cast<uint8_t*>(dst));
 }
 
 cudaError_t launch_int8_dequantize(const void* src, int64_t n_mat, int64_t rows, int64_t cols, void* out, int ot, int num_sms,
                                    cudaStream_t s) {
-    const int64_t ctas = std::min<int64_t>((n_mat * rows * cols + 255) / 256, static_cast<int64_t>(num_sms) * 8);
+    const int64_t groups = (rows + 7) / 8, ctas = 8ll * num_sms;
+    const int64_t gx = std::min<int64_t>(groups, ctas), chunks = (cols + kQRow - 1) / kQRow;
+    const int64_t gz = std::min<int64_t>(n_mat, std::max<int64_t>(1, ctas / gx));
+    const int64_t gy = std::min<int64_t>(chunks, std::max<int64_t>(1, ctas / (gx * gz)));
     return launch_pdl(ot == MOE_F32 ? int8_dequantize_kernel<true> : int8_dequantize_kernel<false>,
-                      dim3(static_cast<unsigned>(ctas)), dim3(256), 0, s, static_cast<const uint8_t*>(src), n_mat, rows,
-                      static_cast<int>(cols), out);
+                      dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy), static_cast<unsigned>(gz)), dim3(256), 0, s,
+                      static_cast<const uint8_t*>(src), n_mat, rows, static_cast<int>(cols), (reinterpret_cast<uintptr_t>(out) & 31u) == 0,
+                      static_cast<char*>(out));
 }
 
 }  // namespace moe

@@ -10,6 +10,28 @@ namespace moe {
 __host__ __device__ inline int64_t i8_scale_bytes(int64_t rows) { return (4 * rows + 15) / 16 * 16; }
 __host__ __device__ inline int64_t i8_bytes(int64_t rows, int64_t cols) { return i8_scale_bytes(rows) + rows * cols; }
 
+// Four codes -> two pairs of f16, exactly: 0x64 in front of the byte c + 128 is the f16 value 1152 + c, and subtracting 1152
+// leaves c; two values an instruction.
+__device__ __forceinline__ void i8_f16(uint32_t w, uint32_t* h) {
+    const uint32_t u = w ^ 0x80808080u, k1152 = 0x64806480u;
+    asm("{\n\t.reg .b32 a, b;\n\tprmt.b32 a, %2, %4, 0x4140;\n\tprmt.b32 b, %2, %4, 0x4342;\n\t"
+        "sub.rn.f16x2 %0, a, %3;\n\tsub.rn.f16x2 %1, b, %3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1])
+        : "r"(u), "r"(k1152), "r"(0x64646464u));
+}
+// SiLU to a few units in the last place at any gate: exp(-|g|) is at most 1, so that the divisor of the fast division lies
+// in [1, 2], where it is good to 2 units.
+__device__ __forceinline__ float silu_fast(float g) {
+    const float e = expf(-fabsf(g));
+    return __fdividef(g < 0.0f ? g * e : g, 1.0f + e);
+}
+
+// Whether a call's rows are few enough to stream the weights through mma.sync (stream.cu).  us, streamed / by CTA pairs:
+// int8 gate.up (2816 -> 2 x 704), 8 rows of 8 experts 11.0 / 14.9, 64 rows of 48 48 / 41, 256 of 101 116 / 74; one matrix
+// (2816 -> 4224) 1 row 6.3 / 14.5, 8 rows 8.3 / 14.4.  bf16 block (2816, 2112) 1 row 8.7 / 19.7, 8 rows 12.9 / 20.1, of 128
+// experts (2816, 704) 8 rows 22.7 / 22.7.
+inline bool stream_rows(int64_t P) { return P <= 8; }
+
 // The sorted rows [first, last) of expert e.  Offsets are the caller's device data: whatever they hold, the range stays
 // inside [0, P] (an expert whose range is reversed has no rows).
 __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int P, int* first, int* last) {

@@ -17,9 +17,6 @@
 //   warps 20-27  epilogue: two groups of four warps that take 32 rows in turn.  Scales, activation, and through shared
 //                memory in 16-byte pieces of whole rows to memory.
 // Two accumulators alternate.
-//
-// A code c is converted by arithmetic on bits: 0x64 in front of the byte c + 128 is the f16 value 1152 + c, and subtracting
-// 1152 is exact; two values an instruction.
 #include <algorithm>
 #include <cstring>
 
@@ -62,14 +59,6 @@ struct I8Args {
     int32_t* err;
 };
 
-// Four codes -> two pairs of f16.
-__device__ __forceinline__ void i8_f16(uint32_t w, uint32_t* h) {
-    const uint32_t u = w ^ 0x80808080u, k1152 = 0x64806480u;
-    asm("{\n\t.reg .b32 a, b;\n\tprmt.b32 a, %2, %4, 0x4140;\n\tprmt.b32 b, %2, %4, 0x4342;\n\t"
-        "sub.rn.f16x2 %0, a, %3;\n\tsub.rn.f16x2 %1, b, %3;\n\t}"
-        : "=r"(h[0]), "=r"(h[1])
-        : "r"(u), "r"(k1152), "r"(0x64646464u));
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -104,12 +93,6 @@ __device__ __forceinline__ void i8_fail(const I8Args& g, volatile tc::Waits* wai
     set_error(g.err, tc::kErrTimeout);
 }
 
-// SiLU to a few units in the last place at any gate: exp(-|g|) is at most 1, so that the divisor of the fast division lies
-// in [1, 2], where it is good to 2 units.
-__device__ __forceinline__ float i8_silu(float g) {
-    const float e = expf(-fabsf(g));
-    return __fdividef(g < 0.0f ? g * e : g, 1.0f + e);
-}
 __device__ __forceinline__ uint32_t i8_pack(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -243,7 +226,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                         const float t = s[2 * (j >> 2) + (j & 1)];
                         lo[j] *= t * sw[(j >> 1) & 1];
                         hi[j] *= t * sw[2 + ((j >> 1) & 1)];
-                        if (kGated) lo[j] = i8_silu(lo[j]) * hi[j];
+                        if (kGated) lo[j] = silu_fast(lo[j]) * hi[j];
                         if (ACT == MOE_ACT_RELU2) {
                             lo[j] = lo[j] > 0.0f ? lo[j] * lo[j] : (lo[j] <= 0.0f ? 0.0f : lo[j]);
                             hi[j] = hi[j] > 0.0f ? hi[j] * hi[j] : (hi[j] <= 0.0f ? 0.0f : hi[j]);
@@ -529,8 +512,11 @@ cudaError_t configure_int8_kernels() {
     return e;
 }
 
+cudaError_t launch_stream_int8(const void*, int64_t, const void*, int64_t, int64_t, int64_t, const int32_t*, int, void*, int, int, cudaStream_t);
+
 cudaError_t launch_int8_matmul(const void* xq, int64_t P, const void* wq, int64_t E, int64_t N, int64_t K, const int32_t* offsets,
                                int act, void* out, int ot, int32_t* err, int num_sms, cudaStream_t s) {
+    if (stream_rows(P)) return launch_stream_int8(xq, P, wq, E, N, K, offsets, act, out, ot, num_sms, s);
     I8Args g;
     std::memset(&g, 0, sizeof(g));
     g.xq = static_cast<const uint8_t*>(xq);
