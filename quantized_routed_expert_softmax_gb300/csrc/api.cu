@@ -163,6 +163,7 @@ struct Plan {
     bool nv_mma;        // NVFP4 down on the tensor cores (tt_dn tokens per pass)
     bool decode1;       // one token, Q8_0 SwiGLU: the shape fits the one-kernel decode layer
     bool mx;            // MXFP4 experts: coded inputs and the 4-bit tensor-core product
+    bool i8;            // MOE_ACTQ_INT8: coded inputs and the int8 product
 };
 
 // Router experts per routing CTA of the one-kernel decode layer (0: E too large for `ctas`).
@@ -303,7 +304,8 @@ Plan make_plan(const moe_layer_desc* d, int64_t T, int xt = MOE_BF16) {
                     route_decode_fits(T, d->d, d->E);
     const int64_t rows_per_tile = (d->wfmt == MOE_W_NVFP4) ? 256 : 32;
     p.mx = d->wfmt == MOE_W_MXFP4;
-    p.fuse_combine = T * rows_per_tile <= 256 && !p.mx;
+    p.i8 = d->act_quant == MOE_ACTQ_INT8;
+    p.fuse_combine = T * rows_per_tile <= 256 && !p.mx && !p.i8;
     const int64_t dn_bytes = matrix_bytes(d->wfmt, d->d, d->f);
     p.prefetch_down = static_cast<int64_t>(p.slot_cap) * dn_bytes <= kPrefetchBudget &&
                       !(d->flags & MOE_FLAG_HOST_DOWN);   // no bulk L2 prefetch of host memory
@@ -332,7 +334,7 @@ Plan make_plan(const moe_layer_desc* d, int64_t T, int xt = MOE_BF16) {
 
 struct Layout {
     size_t err, route_ctr, n_active, wait_limit, row_ctr, logits, rpart, idx, w, offsets, perm, pos, act_e, slot_info, chunk_cnt,
-        local_rank, gmask, h, y, xs_hi, xs_lo, h_hi, h_lo, dec_bar, dec_sel, dec_grec, dec_drec, xnext, xq, mx_x, mx_h, total;
+        local_rank, gmask, h, y, xs_hi, xs_lo, h_hi, h_lo, dec_bar, dec_sel, dec_grec, dec_drec, xnext, xq, coded_x, coded_h, total;
 };
 
 // The control region at the start of every workspace: a 256-byte header (the error word,
@@ -394,9 +396,10 @@ Layout layout_for(const moe_layer_desc* d, int64_t T) {
     L.dec_grec = take(dec ? sizeof(float) * 32 * (sp.U_g / sp.npan_g) * sp.cov_g : 0);
     L.dec_drec = take(dec ? sizeof(float) * sp.rec_d * sp.items_d * sp.cov_d : 0);
     L.xnext = take(T == 1 ? sizeof(uint16_t) * d->d : 0);   // a stack's next input (one token)
-    L.xq = take(d->act_quant ? sizeof(float) * T * d->d : 0);   // the coded expert input (MOE_ACTQ_Q8_0)
-    L.mx_x = take(p.mx ? static_cast<size_t>(mx_bytes(p.P, d->d)) : 0);   // the MXFP4 experts' coded inputs
-    L.mx_h = take(p.mx ? static_cast<size_t>(mx_bytes(p.P, d->f)) : 0);
+    L.xq = take(d->act_quant == MOE_ACTQ_Q8_0 ? sizeof(float) * T * d->d : 0);   // the coded expert input (MOE_ACTQ_Q8_0)
+    // the coded inputs of MXFP4 and of int8 experts
+    L.coded_x = take(p.mx ? static_cast<size_t>(mx_bytes(p.P, d->d)) : (p.i8 ? static_cast<size_t>(i8_bytes(p.P, d->d)) : 0));
+    L.coded_h = take(p.mx ? static_cast<size_t>(mx_bytes(p.P, d->f)) : (p.i8 ? static_cast<size_t>(i8_bytes(p.P, d->f)) : 0));
     L.total = off;
     return L;
 }
@@ -451,7 +454,9 @@ moe_status validate_desc(const moe_layer_desc* d) {
     if (d->wfmt == MOE_W_NVFP4 && (!d->gate_up_tscale || !d->down_tscale)) return MOE_ERR_INVALID_ARG;
     if (!aligned16(d->router_w) || !aligned16(d->w_gate_up) || !aligned16(d->w_down)) return MOE_ERR_ALIGNMENT;
     if (d->l2_prefetch && (d->l2_prefetch_bytes < 0 || !aligned16(d->l2_prefetch))) return MOE_ERR_ALIGNMENT;
-    if (d->act_quant != MOE_ACTQ_NONE && d->act_quant != MOE_ACTQ_Q8_0) return MOE_ERR_INVALID_ARG;
+    if (d->act_quant != MOE_ACTQ_NONE && d->act_quant != MOE_ACTQ_Q8_0 && d->act_quant != MOE_ACTQ_INT8) return MOE_ERR_INVALID_ARG;
+    if (d->act_quant == MOE_ACTQ_INT8 && (d->wfmt != MOE_W_INT8PC || d->path != MOE_PATH_AUTO || (d->flags & MOE_FLAG_HOST_WEIGHTS)))
+        return MOE_ERR_UNSUPPORTED;
     if (d->act_quant == MOE_ACTQ_Q8_0 && d->wfmt != MOE_W_Q8_0) return MOE_ERR_UNSUPPORTED;
     if (d->flags & ~MOE_FLAG_HOST_WEIGHTS) return MOE_ERR_INVALID_ARG;   // unknown bits
     if ((d->flags & MOE_FLAG_HOST_WEIGHTS) && d->path == MOE_PATH_GEMM) return MOE_ERR_UNSUPPORTED;
@@ -945,22 +950,22 @@ moe_status moe_layer_forward(const moe_layer_desc* desc, const void* x, moe_dtyp
     }
     if (e != cudaSuccess) return MOE_ERR_CUDA;
 
-    // MXFP4 experts: the rows of every expert coded side by side, gate.up with the activation, h coded,
-    // down, combine
-    if (p.mx) {
+    // MXFP4 experts, and int8 ones over int8 rows: the rows of every expert coded side by side, gate.up with the
+    // activation, h coded, down, combine
+    if (p.mx || p.i8) {
         char* base = static_cast<char*>(workspace);
-        void *mx_x = base + L.mx_x, *mx_h = base + L.mx_h;
+        void *cx = base + L.coded_x, *ch = base + L.coded_h;
         const int64_t rows_gu = desc->act == MOE_ACT_SWIGLU ? 2 * desc->f : desc->f;
+        const auto quantize = p.i8 ? launch_int8_quantize : launch_mxfp4_quantize;
+        const auto matmul = p.i8 ? launch_int8_matmul : launch_mxfp4_matmul;
         mark(1);
-        if (e == cudaSuccess) e = launch_mxfp4_quantize(x, xt, T, ws.perm, k, 1, p.P, desc->d, mx_x, num_sms, s);
+        if (e == cudaSuccess) e = quantize(x, xt, T, ws.perm, k, 1, p.P, desc->d, cx, num_sms, s);
         if (e == cudaSuccess)
-            e = launch_mxfp4_matmul(mx_x, p.P, desc->w_gate_up, desc->E, rows_gu, desc->d, ws.offsets, desc->act, ws.h,
-                                    MOE_F32, ws.err, num_sms, s);
+            e = matmul(cx, p.P, desc->w_gate_up, desc->E, rows_gu, desc->d, ws.offsets, desc->act, ws.h, MOE_F32, ws.err, num_sms, s);
         mark(2);
-        if (e == cudaSuccess) e = launch_mxfp4_quantize(ws.h, MOE_F32, p.P, nullptr, 1, 1, p.P, desc->f, mx_h, num_sms, s);
+        if (e == cudaSuccess) e = quantize(ws.h, MOE_F32, p.P, nullptr, 1, 1, p.P, desc->f, ch, num_sms, s);
         if (e == cudaSuccess)
-            e = launch_mxfp4_matmul(mx_h, p.P, desc->w_down, desc->E, desc->d, desc->f, ws.offsets, MOE_ACT_NONE, ws.y,
-                                    MOE_F32, ws.err, num_sms, s);
+            e = matmul(ch, p.P, desc->w_down, desc->E, desc->d, desc->f, ws.offsets, MOE_ACT_NONE, ws.y, MOE_F32, ws.err, num_sms, s);
         mark(3);
         if (e == cudaSuccess) e = launch_combine(ws.w, ws.pos, ws.y, T, k, desc->d, out, s);
         mark(4);

@@ -2,9 +2,8 @@
 // any number of rows), and its inverse.
 //
 // Per row: s = amax / 127, q = round-half-away(x / s), both divisions correctly rounded in fp32, as the per-channel
-// weight packer has them.  A division a value would bound the kernel by instructions, so the quotient is first taken as
-// x * (1 / s), which is off by less than 2^-15 of a code; only where that lies so close to the middle between two codes are
-// the values divided.
+// weight packer has them.  A division a value would bound the kernel by instructions, so the quotient is taken as x * (1 / s),
+// and an exact comparison decides where that lies close to the middle between two codes (i8_codes).
 #include <algorithm>
 
 #include "int8.cuh"
@@ -38,19 +37,23 @@ __device__ __forceinline__ void i8_values(const uint32_t* raw, float* v) {
         }
     }
 }
-// The largest magnitude's bits of eight values (non-negative floats order like their bit patterns, NaN above Inf).
+// The larger of m and the magnitudes of eight values, as bits (non-negative floats order like their bit patterns, NaN above
+// Inf); bf16: of both halves of a word at once.
 template <bool F32>
-__device__ __forceinline__ uint32_t i8_amax(const uint32_t* raw) {
-    float v[8];
-    i8_values<F32>(raw, v);
-    uint32_t m = 0;
+__device__ __forceinline__ uint32_t i8_amax(uint32_t m, const uint32_t* raw) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int i = 0; i < (F32 ? 8 : 4); ++i) m = F32 ? max(m, raw[i] & 0x7fffffffu) : __vmaxu2(m, raw[i] & 0x7fff7fffu);
     return m;
 }
+template <bool F32>
+__device__ __forceinline__ uint32_t i8_amax_bits(uint32_t m) { return F32 ? m : max(m << 16, m & 0xffff0000u); }
 
-// Eight codes of a row with scale s, inv about 1 / s, or 0 where that is no normal number.  Adding 1.5 * 2^23 rounds to an integer and leaves its two's
-// complement in the low byte; what it took off tells how near the middle between two codes the quotient is.
+// Eight codes of a row with scale s, inv about 1 / s, or 0 where s is too small for what follows.  Adding 1.5 * 2^23 rounds
+// to an integer and leaves its two's complement in the low byte; what that took off tells how near the quotient is to the
+// middle m between two codes.  There the rounded quotient decides: it is at least m if |v| / s is at least m less half of
+// fp32's step below m, and |v| - m s, a small difference of numbers of 24 and 32 bits, is exact.  (bf16 rows come to such
+// places often, as v / amax is a ratio of two 8-bit numbers.)
+constexpr float kNearTie = 0.49997f;
 template <bool F32>
 __device__ __forceinline__ uint2 i8_codes(const uint32_t* raw, float s, float inv) {
     constexpr float kMagic = 12582912.0f;
@@ -60,11 +63,23 @@ __device__ __forceinline__ uint2 i8_codes(const uint32_t* raw, float s, float in
     float worst = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float t = v[i] * inv, r = t + kMagic;
-        worst = fmaxf(worst, fabsf(t - (r - kMagic)));
+        const float r = fmaf(v[i], inv, kMagic);
+        worst = fmaxf(worst, fabsf(fmaf(v[i], inv, kMagic - r)));
         b[i] = __float_as_uint(r);
     }
-    if (worst >= 0.4999f || inv == 0.0f) {
+    if (worst >= kNearTie) {   // (the roundings of v inv and inv: 2^-23 of 127 at most, 1.6e-5)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float n = __uint_as_float(b[i]) - kMagic, d = fmaf(v[i], inv, -n);
+            if (fabsf(d) >= kNearTie) {
+                const float m = fabsf(n + copysignf(0.5f, d));
+                const float step = m == 0.5f ? 0x1p-26f : __uint_as_float((__float_as_uint(m) & 0x7f800000u) - (24u << 23));
+                const float code = fmaf(-m, s, fabsf(v[i])) >= -step * s ? m + 0.5f : m - 0.5f;
+                b[i] = __float_as_uint(copysignf(code, v[i]) + kMagic);
+            }
+        }
+    }
+    if (inv == 0.0f) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             b[i] = static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(roundf(__fdiv_rn(v[i], s)), -127.0f), 127.0f)));
@@ -79,7 +94,7 @@ constexpr int kQRow = 256;   // columns that a warp covers at a time, eight a la
 // lane holds its part of the row, eight values each time, between the search for the largest and the coding; 0: it reads
 // the row again.
 template <bool F32, int ITERS>
-__global__ void __launch_bounds__(256) int8_quantize_kernel(const char* __restrict__ x, int64_t x_rows,
+__global__ void __launch_bounds__(256, F32 ? 2 : 4) int8_quantize_kernel(const char* __restrict__ x, int64_t x_rows,
                                                             const int32_t* __restrict__ src_rows, int src_div, int64_t n_mat,
                                                             int64_t rows, int cols, int split, bool wide,
                                                             uint8_t* __restrict__ dst) {
@@ -112,14 +127,21 @@ __global__ void __launch_bounds__(256) int8_quantize_kernel(const char* __restri
                     if (has && c0 + u * step < cols) i8_load8<F32>(src + static_cast<int64_t>(u) * step * kElem, wide, raw[u]);
                 }
 #pragma unroll
-                for (int u = 0; u < ITERS; ++u) amax = max(amax, i8_amax<F32>(raw[u]));
+                for (int u = 0; u < ITERS; ++u) amax = i8_amax<F32>(amax, raw[u]);
             } else if (has) {
-                for (int c = c0; c < cols; c += step) {
-                    i8_load8<F32>(src + static_cast<int64_t>(c - c0) * kElem, wide, raw[0]);
-                    amax = max(amax, i8_amax<F32>(raw[0]));
+                for (int c = c0; c < cols; c += 4 * step) {
+                    uint32_t w[4][kRaw];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                        for (int i = 0; i < kRaw; ++i) w[u][i] = 0;
+                        if (c + u * step < cols) i8_load8<F32>(src + static_cast<int64_t>(c - c0 + u * step) * kElem, false, w[u]);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) amax = i8_amax<F32>(amax, w[u]);
                 }
             }
-            amax = __reduce_max_sync(0xffffffffu, amax);
+            amax = __reduce_max_sync(0xffffffffu, i8_amax_bits<F32>(amax));
             if (split > 1) {
                 if (lane == 0) largest[warp] = amax;
                 __syncthreads();
@@ -129,7 +151,7 @@ __global__ void __launch_bounds__(256) int8_quantize_kernel(const char* __restri
             if (!live) continue;
             const bool bad = amax >= 0x7f800000u;
             const float s = __fdiv_rn(__uint_as_float(amax), 127.0f);
-            const float inv = s >= 1.2e-38f ? __frcp_rn(s) : 0.0f;   // (s is 2.7e36 at most)
+            const float inv = s >= 1e-27f ? __frcp_rn(s) : 0.0f;   // (s is 2.7e36 at most)
             const bool code = has && !bad && s > 0.0f;
             uint8_t* o = out + i8_scale_bytes(rows) + (static_cast<int64_t>(c0 >> 5) * rows + r) * 32 + (c0 & 31);
             const int64_t o_step = static_cast<int64_t>(step >> 5) * rows * 32;
@@ -140,7 +162,7 @@ __global__ void __launch_bounds__(256) int8_quantize_kernel(const char* __restri
                         *reinterpret_cast<uint2*>(o + u * o_step) = code ? i8_codes<F32>(raw[u], s, inv) : make_uint2(0, 0);
             } else {
                 for (int c = c0; c < cols; c += step, o += o_step) {
-                    if (code) i8_load8<F32>(src + static_cast<int64_t>(c - c0) * kElem, wide, raw[0]);
+                    if (code) i8_load8<F32>(src + static_cast<int64_t>(c - c0) * kElem, false, raw[0]);
                     *reinterpret_cast<uint2*>(o) = code ? i8_codes<F32>(raw[0], s, inv) : make_uint2(0, 0);
                 }
             }
@@ -201,12 +223,13 @@ namespace {
 
 using QuantizeKernel = void (*)(const char*, int64_t, const int32_t*, int, int64_t, int64_t, int, int, bool, uint8_t*);
 
-template <bool F32>
-QuantizeKernel quantize_kernel(int iters) {
-    if (iters <= 0) return int8_quantize_kernel<F32, 0>;
-    if (iters <= 3) return int8_quantize_kernel<F32, 3>;
-    if (iters <= 6) return int8_quantize_kernel<F32, 6>;
-    return int8_quantize_kernel<F32, 12>;
+// bf16 rows are read again (from L1): held in registers, the unrolled coding is too much code for the instruction caches
+// (32764 gathered rows of 2816 82 us, read again 57; fp32 rows are bound by memory either way).
+QuantizeKernel quantize_kernel(bool f32, int iters) {
+    if (!f32) return int8_quantize_kernel<false, 0>;
+    if (iters <= 3) return int8_quantize_kernel<true, 3>;
+    if (iters <= 6) return int8_quantize_kernel<true, 6>;
+    return iters <= 12 ? int8_quantize_kernel<true, 12> : int8_quantize_kernel<true, 0>;
 }
 
 }  // namespace
@@ -221,8 +244,7 @@ cudaError_t launch_int8_quantize(const void* x, int xt, int64_t x_rows, const in
     const int64_t groups = (rows * split + 7) / 8, ctas = 8ll * num_sms;
     const int64_t gx = std::min<int64_t>(groups, ctas);
     const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(std::min<int64_t>(n_mat, std::max<int64_t>(1, ctas / gx))));
-    const int n = iters() > 12 ? 0 : iters();
-    return launch_pdl(xt == MOE_F32 ? quantize_kernel<true>(n) : quantize_kernel<false>(n), grid, dim3(256), 0, s,
+    return launch_pdl(quantize_kernel(xt == MOE_F32, iters()), grid, dim3(256), 0, s,
                       static_cast<const char*>(x), x_rows, src_rows, src_div, n_mat, rows, static_cast<int>(cols), split,
                       (reinterpret_cast<uintptr_t>(x) & 31u) == 0, static_cast<uint8_t*>(dst));
 }

@@ -123,3 +123,21 @@ def test_the_restated_codec():
     q, s = ref.quantize(x)
     assert q[0, :4].tolist() == [127, 1, -1, 127] and s[0] == 1.0 and s[1] == 0.0 and np.isnan(s[2])
     assert not q[1:].any()
+
+
+def test_layer_descriptor_refusals(L):
+    import ctypes
+
+    def ws(**kw):
+        d = dict(d=512, f=96, E=16, k=3, act=0, wfmt=2, path=0, router_w=FAKE, w_gate_up=FAKE, w_down=FAKE, act_quant=3)
+        d.update(kw)
+        return L.moe_layer_workspace_bytes(ctypes.byref(native.LayerDesc(**d)), 64)
+
+    plain = ws(act_quant=0)
+    assert ws() >= plain + ref.bytes_of(192, 512) + ref.bytes_of(192, 96) - 2 * 256
+    for bad in (dict(wfmt=0), dict(wfmt=4), dict(path=1), dict(path=2), dict(flags=2), dict(act_quant=2), dict(act_quant=4)):
+        assert ws(**bad) == 0, bad
+    F = lambda **kw: L.moe_layer_forward(ctypes.byref(native.LayerDesc(**{**dict(  # noqa: E731
+        d=512, f=96, E=16, k=3, act=0, wfmt=2, path=0, router_w=FAKE, w_gate_up=FAKE, w_down=FAKE, act_quant=3), **kw})), FAKE, 1, 4, None, None, FAKE,
+        FAKE, 1 << 30, None, None)
+    assert F(wfmt=0) == 5 and F(path=1) == 5 and F(flags=2) == 5 and F(act_quant=4) == 1
