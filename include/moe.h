@@ -312,11 +312,11 @@ moe_status moe_int8_matmul(const void* xq, int64_t P, const void* wq, int64_t E,
  *   y = Wd[e] h.
  * Backward, from dy:  dh = Wd^T dy;  dz = dh * dh/dz;  dx = Wgu^T dz;
  *   dWgu[e] = sum over the expert's rows of dz x^T;  dWd[e] = sum of dy h^T  (0 for an expert without rows).
- * Sums are fp32; z, h, y, dz, dx are rounded to bf16 once each, and the activation reads z before its rounding
- * (forward), its gradient the stored z.  No atomics: the same inputs give the same bits.
+ * Sums are fp32, z is kept in fp32; h, y, dz and dx are rounded to bf16 once each (h and dz as the products' operands).
+ * No atomics: the same inputs give the same bits.
  * x, y, dy, dx   device bf16 [P][d], rows sorted by expert.   w_gate_up  device bf16 [E][2f][d] (RELU2:
  *           [E][f][d]).   w_down  device bf16 [E][d][f].
- * z, h      device bf16 [P][2f] (RELU2: [P][f]) and [P][f]: kept by the forward pass for the backward one.
+ * z, h      device fp32 [P][2f] (RELU2: [P][f]) and bf16 [P][f]: kept by the forward pass for the backward one.
  *           Forward: z may be NULL (not written), h may be NULL (then in the workspace).
  * offsets   device int32 [E+1], or NULL with E = 1, as in moe_int8_matmul.  Rows outside [offsets[0],
  *           offsets[E]) are left as they were in y, z, h and dx, and have no part in the weights' gradients.
@@ -331,11 +331,11 @@ moe_status moe_int8_matmul(const void* xq, int64_t P, const void* wq, int64_t E,
  */
 size_t moe_ffn_workspace_bytes(int64_t P, int64_t f, moe_act act, int32_t backward);
 moe_status moe_ffn_forward(const uint16_t* x, int64_t P, const uint16_t* w_gate_up, const uint16_t* w_down, int64_t E,
-                           int64_t d, int64_t f, const int32_t* offsets, moe_act act, uint16_t* y, uint16_t* z,
+                           int64_t d, int64_t f, const int32_t* offsets, moe_act act, uint16_t* y, float* z,
                            uint16_t* h, void* workspace, size_t ws_bytes, moe_stream_t stream);
 moe_status moe_ffn_backward(const uint16_t* dy, const uint16_t* x, int64_t P, const uint16_t* w_gate_up,
                             const uint16_t* w_down, int64_t E, int64_t d, int64_t f, const int32_t* offsets, moe_act act,
-                            const uint16_t* z, const uint16_t* h, uint16_t* dx, void* dw_gate_up, void* dw_down,
+                            const float* z, const uint16_t* h, uint16_t* dx, void* dw_gate_up, void* dw_down,
                             moe_dtype gt, void* workspace, size_t ws_bytes, moe_stream_t stream);
 
 /*

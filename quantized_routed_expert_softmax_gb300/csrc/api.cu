@@ -60,9 +60,9 @@ cudaError_t launch_int8_dequantize(const void*, int64_t, int64_t, int64_t, void*
 cudaError_t launch_int8_matmul(const void*, int64_t, const void*, int64_t, int64_t, int64_t, const int32_t*, int, void*,
                                int, int32_t*, int, cudaStream_t);
 cudaError_t launch_ffn_forward(const uint16_t*, int64_t, const uint16_t*, const uint16_t*, int64_t, int64_t, int64_t,
-                               const int32_t*, int, uint16_t*, uint16_t*, uint16_t*, int32_t*, int, cudaStream_t);
+                               const int32_t*, int, uint16_t*, float*, uint16_t*, int32_t*, int, cudaStream_t);
 cudaError_t launch_ffn_backward(const uint16_t*, const uint16_t*, int64_t, const uint16_t*, const uint16_t*, int64_t,
-                                int64_t, int64_t, const int32_t*, int, const uint16_t*, const uint16_t*, uint16_t*,
+                                int64_t, int64_t, const int32_t*, int, const float*, const uint16_t*, uint16_t*,
                                 uint16_t*, void*, void*, int, int32_t*, int, cudaStream_t);
 
 namespace {
@@ -739,7 +739,7 @@ size_t moe_ffn_workspace_bytes(int64_t P, int64_t f, moe_act act, int32_t backwa
 }
 
 moe_status moe_ffn_forward(const uint16_t* x, int64_t P, const uint16_t* w_gate_up, const uint16_t* w_down, int64_t E,
-                           int64_t d, int64_t f, const int32_t* offsets, moe_act act, uint16_t* y, uint16_t* z,
+                           int64_t d, int64_t f, const int32_t* offsets, moe_act act, uint16_t* y, float* z,
                            uint16_t* h, void* workspace, size_t ws_bytes, moe_stream_t stream) {
     const moe_status st = ffn_shape(P, E, d, f, act);
     if (st != MOE_OK) return st;
@@ -759,7 +759,7 @@ moe_status moe_ffn_forward(const uint16_t* x, int64_t P, const uint16_t* w_gate_
 
 moe_status moe_ffn_backward(const uint16_t* dy, const uint16_t* x, int64_t P, const uint16_t* w_gate_up,
                             const uint16_t* w_down, int64_t E, int64_t d, int64_t f, const int32_t* offsets, moe_act act,
-                            const uint16_t* z, const uint16_t* h, uint16_t* dx, void* dw_gate_up, void* dw_down,
+                            const float* z, const uint16_t* h, uint16_t* dx, void* dw_gate_up, void* dw_down,
                             moe_dtype gt, void* workspace, size_t ws_bytes, moe_stream_t stream) {
     const moe_status st = ffn_shape(P, E, d, f, act);
     if (st != MOE_OK) return st;

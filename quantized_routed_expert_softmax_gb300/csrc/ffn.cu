@@ -34,7 +34,7 @@ constexpr int kFfEpi0 = 4;              // first epilogue warp
 constexpr int kFfNT = 256;              // rows of B of a tile
 constexpr int kFfStepK = 64;            // 128 bytes of bf16
 constexpr int kFfABytes = 128 * 128, kFfStage = 2 * kFfABytes, kFfStages = 5;
-constexpr int kFfEpiBytes = 16 * 1024;  // staging of an epilogue group
+constexpr int kFfEpiBytes = 24 * 1024;  // staging of an epilogue group
 constexpr uint32_t kFfTmemCols = 512;
 constexpr int kFfLimitWord = 8;         // the waits' limit in ns (int64) in the workspace: 0 means a second
 constexpr size_t kFfSmem = 1024 + kFfStages * kFfStage + 2 * kFfEpiBytes;
@@ -53,9 +53,9 @@ struct FfArgs {
     int E, P, M, N, K;    // N: Grad only.  Grad has the expert's rows for K.
     int f;                // neurons
     void* out;            // y, dx or the weights' gradient: rows of M values
-    const uint16_t* z_in;
-    uint16_t* z_out;      // z (may be null) or dz
-    uint16_t* h_out;
+    const float* z_in;
+    float* z_out;         // may be null
+    uint16_t *h_out, *dz_out;
     int32_t* err;
 };
 
@@ -69,8 +69,11 @@ __device__ __forceinline__ uint32_t ff_pack(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float ff_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float ff_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
 // The sigmoid s and 1 - s.  exp(-|g|) is at most 1, so that the fast division's divisor lies in [1, 2], and neither s nor
 // 1 - s comes of a difference.  The hardware's 2^x is off by a few 2^-23 per unit of |g|, far below a bf16's step.
 __device__ __forceinline__ float2 ff_sigmoid(float g) {
@@ -117,7 +120,7 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
     constexpr bool kGrad = ORDER == kOrderGrad;
     constexpr bool kGated = EPI == kEpiSwiglu;   // gate and up rows interleaved in A
     constexpr bool kActGrad = EPI == kEpiSwigluGrad || EPI == kEpiRelu2Grad;
-    constexpr int kZ = EPI == kEpiSwigluGrad ? 8 : 4;   // 16-byte pieces of z a lane (32 rows, 128 neurons, gate and up)
+    constexpr int kHalves = EPI == kEpiSwiglu || EPI == kEpiSwigluGrad ? 2 : 1;   // z has gate and up columns
     extern __shared__ __align__(16) unsigned char dsm_raw[];
     unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char* staging = ring + kFfStages * kFfStage;
@@ -301,18 +304,18 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
             // (an expert without rows: zeros; after a wait that ran out too, as the group's warps meet at barriers and
             // all have to come there)
             bool none = !ok || (kGrad && walk.steps == 0);
-            [[maybe_unused]] uint4 zr[kZ];
-            [[maybe_unused]] auto read_z = [&](int c) {   // rows c .. c + 31 of the tile, 16 bytes of a row a lane
+            [[maybe_unused]] uint4 zr[4 * kHalves];
+            [[maybe_unused]] auto read_z = [&](int c) {   // z of rows c .. c + 15 of the tile, 16 bytes of a row a lane
 #pragma unroll
-                for (int j = 0; j < kZ; ++j) {
-                    const int i = j * 128 + t128, half = i >> 9, r = c + ((i >> 4) & 31);
-                    const int m = walk.m0() + static_cast<int>(rank) * 128 + 8 * (i & 15);
+                for (int j = 0; j < 4 * kHalves; ++j) {
+                    const int i = j * 128 + t128, half = i >> 9, r = c + ((i >> 5) & 15);
+                    const int m = walk.m0() + static_cast<int>(rank) * 128 + 4 * (i & 31);
                     zr[j] = make_uint4(0, 0, 0, 0);
                     if (r < walk.n && m < g.M)
-                        zr[j] = __ldg(reinterpret_cast<const uint4*>(g.z_in + static_cast<int64_t>(walk.n0 + r) * (kZ / 4 * g.f) + half * g.f + m));
+                        zr[j] = __ldg(reinterpret_cast<const uint4*>(g.z_in + static_cast<int64_t>(walk.n0 + r) * (kHalves * g.f) + half * g.f + m));
                 }
             };
-            if constexpr (kActGrad) read_z(32 * grp);
+            if constexpr (kActGrad) read_z(16 * grp);
             const uint32_t buf = n_acc & 1;
             if (!none) {
                 ok = tc::mbar_wait_warp(&acc_full[buf], n_acc >> 1, &waits);
@@ -322,6 +325,75 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
             }
             const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * kFfNT;
             const int am = walk.m0() + static_cast<int>(rank) * 128;
+            // whole rows from shared memory to memory, 16 bytes a lane
+            auto copy = [&](uint32_t from, int n_rows, void* to, int64_t first, int left, int64_t ld, int col, int cols, int row_bytes, int elem) {
+                const int per = row_bytes / 16, each = 16 / elem;
+#pragma unroll
+                for (int j = 0; j < n_rows * per / 128; ++j) {
+                    const int i = j * 128 + t128, r = i / per, p = i % per;
+                    const int place = elem == 4 ? p ^ (2 * ((r >> 1) & 3)) : p ^ (r & 7);
+                    if (r >= left || p * each >= cols) continue;
+                    uint4 v;
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from + r * row_bytes + (place << 4)));
+                    *reinterpret_cast<uint4*>(static_cast<char*>(to) + ((first + r) * ld + col + p * each) * elem) = v;
+                }
+            };
+            if constexpr (kActGrad) {
+#pragma unroll 1
+                for (int c0 = 16 * grp; c0 < walk.n; c0 += 32) {   // 16 rows of dh
+                    float v[16];   // 16 lanes' neurons, the other 16's
+                    const int left = walk.n - c0;
+                    if (none) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                    } else {
+                        tc::tmem_ld_frag16(tb + c0, v);
+                        tc::tmem_ld_frag16(tb + (16u << 16) + c0, v + 8);
+                    }
+                    // z of these rows and neurons into shared memory, the next rows' on their way to registers
+#pragma unroll
+                    for (int j = 0; j < 4 * kHalves; ++j) {
+                        const int i = j * 128 + t128, half = i >> 9, r = (i >> 5) & 15, p = i & 31;
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sb + half * 8192 + r * 512 + ((p ^ (2 * ((r >> 1) & 3))) << 4)),
+                                     "r"(zr[j].x), "r"(zr[j].y), "r"(zr[j].z), "r"(zr[j].w)
+                                     : "memory");
+                    }
+                    if (left > 32) read_z(c0 + 32);
+                    tc::named_sync(1 + grp, 128);
+                    if (!none) tc::tmem_ld_wait(v);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t a[4], b[4];   // rows lane / 4, + 8, + 16, + 24 of the warp's neurons, a pair of rows of dz each
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const float* d = v + 8 * (m >> 1) + 4 * i + 2 * (m & 1);   // dh of the pair
+                            float ga[2], gb[2];
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int r = 8 * i + ncol + u, c = q * 32 + 8 * m + mrow;
+                                const uint32_t at = sb + r * 512 + ((c ^ (8 * (lane & 3))) << 2);
+                                const float z = lds_f32(at);
+                                if constexpr (EPI == kEpiSwigluGrad) {
+                                    const float2 s = ff_sigmoid(z);
+                                    const float silu = z * s.x;
+                                    ga[u] = d[u] * lds_f32(at + 8192) * (s.x + silu * s.y);
+                                    gb[u] = d[u] * silu;
+                                } else {
+                                    ga[u] = d[u] * (2.0f * ff_relu(z));
+                                }
+                            }
+                            a[m] = ff_pack(ga[0], ga[1]);
+                            if constexpr (EPI == kEpiSwigluGrad) b[m] = ff_pack(gb[0], gb[1]);
+                        }
+                        tc::stsm4_t(at256 + 16384 + i * 2048, a[0], a[1], a[2], a[3]);
+                        if constexpr (EPI == kEpiSwigluGrad) tc::stsm4_t(at256 + 20480 + i * 2048, b[0], b[1], b[2], b[3]);
+                    }
+                    tc::named_sync(1 + grp, 128);   // (the next rows' z goes where z has been read, their dz behind a barrier)
+                    const int64_t row0 = walk.n0 + c0;
+                    copy(sb + 16384, 16, g.dz_out, row0, left, kHalves * g.f, am, g.f - am, 256, 2);
+                    if (kHalves == 2) copy(sb + 20480, 16, g.dz_out, row0, left, 2 * g.f, g.f + am, g.f - am, 256, 2);
+                }
+            } else {
 #pragma unroll 1
             for (int c0 = 32 * grp; c0 < walk.n; c0 += 64) {
                 float lo[16], hi[16];
@@ -333,18 +405,6 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                 } else {
                     tc::tmem_ld_frag(tb + c0, lo);
                     tc::tmem_ld_frag(tb + (16u << 16) + c0, hi);
-                }
-                if constexpr (kActGrad) {
-                    // z of these rows and neurons into shared memory, the next rows' on their way to registers
-#pragma unroll
-                    for (int j = 0; j < kZ; ++j) {
-                        const int i = j * 128 + t128, half = i >> 9, r = (i >> 4) & 31, p = i & 15;
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sb + half * 8192 + r * 256 + ((p ^ (r & 7)) << 4)),
-                                     "r"(zr[j].x), "r"(zr[j].y), "r"(zr[j].z), "r"(zr[j].w)
-                                     : "memory");
-                    }
-                    if (left > 64) read_z(c0 + 64);
-                    tc::named_sync(1 + grp, 128);
                 }
                 if (!none) tc::tmem_wait32(lo, hi);
                 if constexpr (EPI == kEpiBf16) {
@@ -362,10 +422,12 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                 } else if constexpr (EPI == kEpiSwiglu) {
                     if (g.z_out) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)   // gate, gate + 8, up, up + 8
-                            tc::stsm4_t(at128 + 4096 + (lane >> 4) * 4096 + i * 1024, ff_pack(lo[4 * i], lo[4 * i + 1]),
-                                        ff_pack(lo[4 * i + 2], lo[4 * i + 3]), ff_pack(hi[4 * i], hi[4 * i + 1]),
-                                        ff_pack(hi[4 * i + 2], hi[4 * i + 3]));
+                        for (int j = 0; j < 32; ++j) {   // gate, up
+                            const float v = j < 16 ? lo[j] : hi[j - 16];
+                            const int r = 8 * ((j & 15) >> 2) + ncol + (j & 1), c = q * 16 + ((j >> 1) & 1) * 8 + mrow;
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + 4096 + (j >> 4) * 8192 + r * 256 + ((c ^ (8 * (lane & 3))) << 2)), "f"(v)
+                                         : "memory");
+                        }
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j) lo[j] = lo[j] * ff_sigmoid(lo[j]).x * hi[j];
@@ -376,9 +438,11 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                 } else if constexpr (EPI == kEpiRelu2) {
                     if (g.z_out) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tc::stsm4_t(at256 + 8192 + i * 2048, ff_pack(lo[4 * i], lo[4 * i + 1]), ff_pack(lo[4 * i + 2], lo[4 * i + 3]),
-                                        ff_pack(hi[4 * i], hi[4 * i + 1]), ff_pack(hi[4 * i + 2], hi[4 * i + 3]));
+                        for (int j = 0; j < 32; ++j) {
+                            const float v = j < 16 ? lo[j] : hi[j - 16];
+                            const int r = 8 * ((j & 15) >> 2) + ncol + (j & 1), c = q * 32 + (j >> 4) * 16 + ((j >> 1) & 1) * 8 + mrow;
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + 8192 + r * 512 + ((c ^ (8 * (lane & 3))) << 2)), "f"(v) : "memory");
+                        }
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -389,70 +453,25 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                     for (int i = 0; i < 4; ++i)
                         tc::stsm4_t(at256 + i * 2048, ff_pack(lo[4 * i], lo[4 * i + 1]), ff_pack(lo[4 * i + 2], lo[4 * i + 3]),
                                     ff_pack(hi[4 * i], hi[4 * i + 1]), ff_pack(hi[4 * i + 2], hi[4 * i + 3]));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t zg[4], zu[4];   // rows lane / 4, + 8, + 16, + 24 of the warp's neurons, a pair of tokens each
-                        tc::ldsm4_t(at256 + i * 2048, zg);
-                        if constexpr (EPI == kEpiSwigluGrad) tc::ldsm4_t(at256 + 8192 + i * 2048, zu);
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            float* d = (m < 2 ? lo : hi) + 4 * i + 2 * (m & 1);   // dh of the pair
-                            float a[2], b[2];
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const float z = u ? ff_hi(zg[m]) : ff_lo(zg[m]);
-                                if constexpr (EPI == kEpiSwigluGrad) {
-                                    const float2 s = ff_sigmoid(z);
-                                    const float silu = z * s.x;
-                                    a[u] = d[u] * (u ? ff_hi(zu[m]) : ff_lo(zu[m])) * (s.x + silu * s.y);
-                                    b[u] = d[u] * silu;
-                                } else {
-                                    a[u] = d[u] * (2.0f * ff_relu(z));
-                                }
-                            }
-                            zg[m] = ff_pack(a[0], a[1]);
-                            if constexpr (EPI == kEpiSwigluGrad) zu[m] = ff_pack(b[0], b[1]);
-                        }
-                        __syncwarp();   // (every lane's z of these rows is read)
-                        tc::stsm4_t(at256 + i * 2048, zg[0], zg[1], zg[2], zg[3]);
-                        if constexpr (EPI == kEpiSwigluGrad) tc::stsm4_t(at256 + 8192 + i * 2048, zu[0], zu[1], zu[2], zu[3]);
-                    }
                 }
                 tc::named_sync(1 + grp, 128);
-                // whole rows from shared memory to memory, 16 bytes a lane
-                auto copy = [&](uint32_t from, void* to, int64_t ld, int col, int cols, int row_bytes, int elem) {
-                    const int per = row_bytes / 16, each = 16 / elem;
-#pragma unroll
-                    for (int j = 0; j < 32 * row_bytes / 16 / 128; ++j) {
-                        const int i = j * 128 + t128, r = i / per, p = i % per;
-                        const int place = elem == 4 ? p ^ (2 * ((r >> 1) & 3)) : p ^ (r & 7);
-                        if (r >= left || p * each >= cols) continue;
-                        uint4 v;
-                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from + r * row_bytes + (place << 4)));
-                        *reinterpret_cast<uint4*>(static_cast<char*>(to) + ((row0 + r) * ld + col + p * each) * elem) = v;
-                    }
-                };
                 if constexpr (EPI == kEpiBf16) {
-                    copy(sb, g.out, g.M, am, g.M - am, 256, 2);
+                    copy(sb, 32, g.out, row0, left, g.M, am, g.M - am, 256, 2);
                 } else if constexpr (EPI == kEpiF32) {
-                    copy(sb, g.out, g.M, am, g.M - am, 512, 4);
+                    copy(sb, 32, g.out, row0, left, g.M, am, g.M - am, 512, 4);
                 } else if constexpr (EPI == kEpiSwiglu) {
                     const int j0 = am >> 1;   // the CTA's first neuron
-                    copy(sb, g.h_out, g.f, j0, g.f - j0, 128, 2);
+                    copy(sb, 32, g.h_out, row0, left, g.f, j0, g.f - j0, 128, 2);
                     if (g.z_out) {
-                        copy(sb + 4096, g.z_out, 2 * g.f, j0, g.f - j0, 128, 2);
-                        copy(sb + 8192, g.z_out, 2 * g.f, g.f + j0, g.f - j0, 128, 2);
+                        copy(sb + 4096, 32, g.z_out, row0, left, 2 * g.f, j0, g.f - j0, 256, 4);
+                        copy(sb + 12288, 32, g.z_out, row0, left, 2 * g.f, g.f + j0, g.f - j0, 256, 4);
                     }
-                } else if constexpr (EPI == kEpiRelu2) {
-                    copy(sb, g.h_out, g.f, am, g.f - am, 256, 2);
-                    if (g.z_out) copy(sb + 8192, g.z_out, g.f, am, g.f - am, 256, 2);
                 } else {
-                    constexpr int kHalves = EPI == kEpiSwigluGrad ? 2 : 1;
-                    copy(sb, g.z_out, kHalves * g.f, am, g.f - am, 256, 2);
-                    if (kHalves == 2) copy(sb + 8192, g.z_out, 2 * g.f, g.f + am, g.f - am, 256, 2);
+                    copy(sb, 32, g.h_out, row0, left, g.f, am, g.f - am, 256, 2);
+                    if (g.z_out) copy(sb + 8192, 32, g.z_out, row0, left, g.f, am, g.f - am, 512, 4);
                 }
                 tc::named_sync(1 + grp, 128);   // the staging is free again
+            }
             }
             if (!none) {
                 tc::fence_before();
@@ -533,11 +552,11 @@ cudaError_t configure_ffn_kernels() {
     return e;
 }
 
-cudaError_t launch_stream_bf16(const uint16_t*, int64_t, const uint16_t*, int64_t, int64_t, int64_t, const int32_t*, int, uint16_t*, uint16_t*, int,
+cudaError_t launch_stream_bf16(const uint16_t*, int64_t, const uint16_t*, int64_t, int64_t, int64_t, const int32_t*, int, uint16_t*, float*, int,
                                cudaStream_t);
 
 cudaError_t launch_ffn_forward(const uint16_t* x, int64_t P, const uint16_t* wgu, const uint16_t* wd, int64_t E, int64_t d, int64_t f,
-                               const int32_t* offsets, int act, uint16_t* y, uint16_t* z, uint16_t* h, int32_t* err, int num_sms,
+                               const int32_t* offsets, int act, uint16_t* y, float* z, uint16_t* h, int32_t* err, int num_sms,
                                cudaStream_t s) {
     if (stream_rows(P)) {
         const cudaError_t r = launch_stream_bf16(x, P, wgu, E, act == MOE_ACT_SWIGLU ? 2 * f : f, d, offsets, act, h, z, num_sms, s);
@@ -568,7 +587,7 @@ cudaError_t launch_ffn_forward(const uint16_t* x, int64_t P, const uint16_t* wgu
 }
 
 cudaError_t launch_ffn_backward(const uint16_t* dy, const uint16_t* x, int64_t P, const uint16_t* wgu, const uint16_t* wd, int64_t E,
-                                int64_t d, int64_t f, const int32_t* offsets, int act, const uint16_t* z, const uint16_t* h,
+                                int64_t d, int64_t f, const int32_t* offsets, int act, const float* z, const uint16_t* h,
                                 uint16_t* dz, uint16_t* dx, void* dwgu, void* dwd, int gt, int32_t* err, int num_sms, cudaStream_t s) {
     const int64_t nz = act == MOE_ACT_SWIGLU ? 2 * f : f;
     FfArgs g;
@@ -576,7 +595,7 @@ cudaError_t launch_ffn_backward(const uint16_t* dy, const uint16_t* x, int64_t P
     g.offsets = offsets, g.E = static_cast<int>(E), g.P = static_cast<int>(P), g.f = static_cast<int>(f), g.err = err;
     cudaError_t e = cudaSuccess;
     if (dx || dwgu) {
-        g.M = static_cast<int>(f), g.K = static_cast<int>(d), g.z_in = z, g.z_out = dz;
+        g.M = static_cast<int>(f), g.K = static_cast<int>(d), g.z_in = z, g.dz_out = dz;
         e = ff_map_rows(g, dy, P, d);
         if (e == cudaSuccess) e = ff_map(&g.ta, 3, wd, {f, d, E}, {f, d * f}, {64, kFfStepK, 1});
         if (e == cudaSuccess)

@@ -81,21 +81,21 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float* v) {
         : "r"(taddr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, float* v) {   // of 16 columns
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_wait32(float* a, float* b) {   // (the registers pass through: no use moves in front)
     tmem_ld_wait(a);
     tmem_ld_wait(b);
 }
 
-// Four 8 x 8 matrices of 16-bit values between registers (fragments as above, column pairs packed) and shared memory,
-// transposed: lane l has the address of row l % 8 of matrix l / 8 as it lies in shared memory.
+// Four 8 x 8 matrices of 16-bit values from registers (fragments as above, column pairs packed) to shared memory, transposed:
+// lane l has the address of row l % 8 of matrix l / 8 as it lies in shared memory.
 __device__ __forceinline__ void stsm4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* w) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(addr)
                  : "memory");
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {

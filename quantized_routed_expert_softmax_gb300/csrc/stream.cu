@@ -25,7 +25,7 @@ struct StreamArgs {
     int E, P, N, K;
     int split;                  // warps that share an item's K
     void* out;                  // [P][N], SwiGLU [P][N / 2]
-    uint16_t* z_out;            // bf16: z [P][N], or null
+    float* z_out;               // bf16: z [P][N], or null
     int f32;                    // out is fp32
 };
 
@@ -183,7 +183,7 @@ __global__ void __maxnreg__(80) stream_kernel(const StreamArgs g) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
                     if (c[kGated ? 0 : u] < width)
-                        g.z_out[row * g.N + (kGated ? u * width + c[0] : c[u])] = __bfloat16_as_ushort(__float2bfloat16_rn(v[u]));
+                        g.z_out[row * g.N + (kGated ? u * width + c[0] : c[u])] = v[u];
             }
             if (kGated) v[0] = silu_fast(v[0]) * v[1];
 #pragma unroll
@@ -240,7 +240,7 @@ cudaError_t launch_stream_int8(const void* xq, int64_t P, const void* wq, int64_
 }
 
 cudaError_t launch_stream_bf16(const uint16_t* x, int64_t P, const uint16_t* w, int64_t E, int64_t N, int64_t K, const int32_t* offsets,
-                               int act, uint16_t* out, uint16_t* z, int num_sms, cudaStream_t s) {
+                               int act, uint16_t* out, float* z, int num_sms, cudaStream_t s) {
     StreamArgs g{};
     g.x = reinterpret_cast<const uint8_t*>(x);
     g.w = reinterpret_cast<const uint8_t*>(w);

@@ -429,7 +429,7 @@ def _ffn_shape(x, w_gate_up, w_down, act: str):
 def ffn_forward(x, w_gate_up, w_down, offsets=None, act: str = "swiglu", save: bool = False, out=None, workspace=None):
     """moe_ffn_forward: x bf16 [P, d] sorted by expert, w_gate_up bf16 [E, 2f, d] (act "relu2": [E, f, d]),
     w_down bf16 [E, d, f], offsets int32 [E + 1] (None with one expert) -> y bf16 [P, d]; with save
-    (y, saved), saved = (z, h) for ffn_backward.  Rows that no expert owns are left as they are (in `out`;
+    (y, saved), saved = (z fp32, h bf16) for ffn_backward.  Rows that no expert owns are left as they are (in `out`;
     a result that the call makes is not initialised there)."""
     P, E, d, f, nz = _ffn_shape(x, w_gate_up, w_down, act)
     bf, dev, where = torch.bfloat16, x.get_device(), x.device
@@ -440,7 +440,7 @@ def ffn_forward(x, w_gate_up, w_down, offsets=None, act: str = "swiglu", save: b
         out = torch.empty((P, d), dtype=bf, device=where)
     z = h = None
     if save:
-        z, h = torch.empty((P, nz), dtype=bf, device=where), torch.empty((P, f), dtype=bf, device=where)
+        z, h = torch.empty((P, nz), dtype=torch.float32, device=where), torch.empty((P, f), dtype=bf, device=where)
     if workspace is None:
         workspace = ffn_workspace(0 if save else P, f, act, device=where)
     _check("moe_ffn_forward", lib().moe_ffn_forward(
@@ -470,7 +470,7 @@ def ffn_backward(grad, x, w_gate_up, w_down, saved, offsets=None, act: str = "sw
     _check("moe_ffn_backward", lib().moe_ffn_backward(
         _operand("grad", grad, bf, dev, P * d), _operand("x", x, bf, dev), P,
         _operand("w_gate_up", w_gate_up, bf, dev, E * nz * d), _operand("w_down", w_down, bf, dev, E * d * f), E, d, f,
-        _operand("offsets", offsets, torch.int32, dev, E + 1), ACT[act], _operand("z", z, bf, dev, P * nz),
+        _operand("offsets", offsets, torch.int32, dev, E + 1), ACT[act], _operand("z", z, torch.float32, dev, P * nz),
         _operand("h", h, bf, dev, P * f), _ptr(dx), _ptr(dgu), _ptr(dd), t,
         _operand("workspace", workspace, torch.uint8, dev), workspace.numel(), _stream_on(dev)))
     return dx, dgu, dd

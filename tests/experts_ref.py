@@ -69,7 +69,8 @@ def ffn(x, wgu, wd, offsets, act="swiglu", dy=None):
     acc = lambda n: n * 2.0 ** -23  # noqa: E731
 
     def put(name, at, v, b):
-        out[name][0][at], out[name][1][at] = v, b + U * (v.abs() + b)
+        u = 2.0 ** -24 if name == "z" else U       # (z is fp32)
+        out[name][0][at], out[name][1][at] = v, b + u * (v.abs() + b)
 
     for e, r0, r1 in spans(offsets, P, E):
         X, W, D, r = x[r0:r1], wgu[e], wd[e], slice(r0, r1)
