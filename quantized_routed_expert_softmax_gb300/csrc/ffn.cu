@@ -24,6 +24,7 @@
 // Two accumulators alternate, so that the epilogue runs beside the next tile's MMAs.
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "pair.cuh"
 
@@ -42,21 +43,27 @@ static_assert(kFfSmem + sizeof(RowTiles) + 512 <= 227 * 1024, "ring and staging 
 static_assert((kFfThreads - 1) * 3 >= kMaxE, "the last thread has no offsets");
 
 // What is done with a tile's sums.
-enum FfEpi { kEpiBf16, kEpiF32, kEpiSwiglu, kEpiRelu2, kEpiSwigluGrad, kEpiRelu2Grad };
-// Which operands are K-major.
-enum FfOrder { kOrderKK, kOrderMK, kOrderGrad };
+enum FfEpi { kEpiNone, kEpiBf16, kEpiF32, kEpiSwiglu, kEpiRelu2, kEpiSwigluGrad, kEpiRelu2Grad };
 
+// One product.  Rows of the experts by weights, or (grad) the gradient of weights: K is the expert's rows then, N columns.
 struct FfArgs {
-    CUtensorMap ta;       // KK {k, m, expert}, SwiGLU {k, 16, half, block, expert}; MK {m, k, expert}; Grad {m, row}
-    CUtensorMap tb[4];    // KK, MK {k, row}, boxes of 16 << i rows; Grad tb[0] {n, row}
+    CUtensorMap ta;       // {k, m, expert}, SwiGLU {k, 16, half, block, expert}; M-major {m, k, expert}; grad {m, row}
+    CUtensorMap tb[4];    // {k, row}, boxes of 16 << i rows; grad tb[0] {n, row}
     const int32_t* offsets;
-    int E, P, M, N, K;    // N: Grad only.  Grad has the expert's rows for K.
+    int E, P, M, N, K;
     int f;                // neurons
     void* out;            // y, dx or the weights' gradient: rows of M values
     const float* z_in;
     float* z_out;         // may be null
     uint16_t *h_out, *dz_out;
     int32_t* err;
+};
+
+// A launch has a product over rows, a gradient of weights, or both: the two need nothing of one another, and together they
+// fill the SMs where each alone would leave some idle at its end.
+struct FfWork {
+    FfArgs rows, grad;
+    int has_rows, has_grad;
 };
 
 __device__ __forceinline__ void ff_fail(const FfArgs& g, volatile tc::Waits* waits, uint32_t rank) {
@@ -82,25 +89,56 @@ __device__ __forceinline__ float2 ff_sigmoid(float g) {
 }
 __device__ __forceinline__ float ff_relu(float z) { return z > 0.0f ? z : (z <= 0.0f ? 0.0f : z); }
 
-// The items of one role: ROWS (row tile, tile of M), GRAD (expert, tile of N, tile of M); M tiles fastest.
+// The items of one role: (row tile, tile of M) of the product over rows, then (expert, tile of N, tile of M) of the gradient;
+// M tiles fastest.
 template <bool GRAD>
 struct FfWalk {
     TileWalk w;
-    int ntiles, e, n0, n, k0, steps;   // n0, n: first row of B's tile and rows; k0, steps: GRAD, the expert's rows
-    const FfArgs& g;
-    __device__ FfWalk(const RowTiles& t, const FfArgs& g_, int first, int stride)
-        : w(t, (g_.M + 255) / 256, first, stride), ntiles((g_.N + kFfNT - 1) / kFfNT), g(g_) {}
-    __device__ bool more() const { return GRAD ? w.tile < g.E * ntiles : w.more(); }
-    __device__ void next() { w.next(); }
-    __device__ int m0() const { return w.mtile * 256; }
-    int rows = 0;   // GRAD: rows of the expert
-    __device__ void at() {
+    const FfWork& g;
+    bool grad = false;
+    int e, n0, n, steps;   // of the item: expert, first row (column) of B's tile and how many, K steps
+    int k0 = 0, rows = 0;  // grad: the expert's rows
+    int mtiles, ntiles, tile, mtile, stride_t, stride_m;
+    __device__ FfWalk(const RowTiles& t, const FfWork& g_, int first, int stride)
+        : w(t, max(1, (g_.rows.M + 255) / 256), first, stride), g(g_) {
         if constexpr (GRAD) {
-            e = w.tile / ntiles;
-            n0 = (w.tile - e * ntiles) * kFfNT;
-            n = min(kFfNT, g.N - n0);
+            mtiles = max(1, (g.grad.M + 255) / 256);
+            ntiles = (g.grad.N + kFfNT - 1) / kFfNT;
+            // this walk's first item past the product over rows
+            const int64_t before = g.has_rows ? static_cast<int64_t>(t.n_tiles) * w.mtiles : 0;
+            const int64_t skip = first < before ? (before - first + stride - 1) / stride * stride : 0;
+            const int at = static_cast<int>(first + skip - before);
+            tile = at / mtiles;
+            mtile = at - tile * mtiles;
+            stride_t = stride / mtiles;
+            stride_m = stride - stride_t * mtiles;
+        }
+    }
+    __device__ bool more() {
+        if (!grad) {
+            if (g.has_rows && w.more()) return true;
+            if (!GRAD || !g.has_grad) return false;
+            grad = true;
+        }
+        return tile < g.grad.E * ntiles;
+    }
+    __device__ void next() {
+        if (!GRAD || !grad) {
+            w.next();
+            return;
+        }
+        tile += stride_t;
+        mtile += stride_m;
+        if (mtile >= mtiles) mtile -= mtiles, ++tile;
+    }
+    __device__ int m0() const { return (GRAD && grad ? mtile : w.mtile) * 256; }
+    __device__ void at() {
+        if (GRAD && grad) {
+            e = tile / ntiles;
+            n0 = (tile - e * ntiles) * kFfNT;
+            n = min(kFfNT, g.grad.N - n0);
             int last;
-            expert_rows(g.offsets, e, g.P, &k0, &last);
+            expert_rows(g.grad.offsets, e, g.grad.P, &k0, &last);
             k0 = __shfl_sync(0xffffffffu, k0, 0);
             rows = __shfl_sync(0xffffffffu, last - k0, 0);
             steps = (rows + kFfStepK - 1) / kFfStepK;
@@ -109,18 +147,20 @@ struct FfWalk {
             e = __shfl_sync(0xffffffffu, e, 0);
             n0 = __shfl_sync(0xffffffffu, n0, 0);
             n = __shfl_sync(0xffffffffu, n, 0);
-            steps = (g.K + kFfStepK - 1) / kFfStepK;
+            steps = (g.rows.K + kFfStepK - 1) / kFfStepK;
         }
     }
     __device__ int mma_n() const { return (n + 31) & ~31; }
 };
 
-template <int EPI, int ORDER>
-__global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constant__ FfArgs g) {
-    constexpr bool kGrad = ORDER == kOrderGrad;
+// EPI: of the product over rows.  A_MN: its weights are M-major.  GEPI: of the gradient, or kEpiNone.
+template <int EPI, bool A_MN, int GEPI>
+__global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constant__ FfWork g) {
+    constexpr bool kGrad = GEPI != kEpiNone;
     constexpr bool kGated = EPI == kEpiSwiglu;   // gate and up rows interleaved in A
     constexpr bool kActGrad = EPI == kEpiSwigluGrad || EPI == kEpiRelu2Grad;
     constexpr int kHalves = EPI == kEpiSwiglu || EPI == kEpiSwigluGrad ? 2 : 1;   // z has gate and up columns
+    static_assert(!kGrad || A_MN, "both have one order of A");
     extern __shared__ __align__(16) unsigned char dsm_raw[];
     unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char* staging = ring + kFfStages * kFfStage;
@@ -135,8 +175,8 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
     const uint32_t rank = __shfl_sync(0xffffffffu, tc::cluster_rank(), 0);
 
     if (warp == 0 && lane == 0) {
-        tc::prefetch_map(&g.ta);
-        tc::prefetch_map(&g.tb[0]);
+        if (g.has_rows) tc::prefetch_map(&g.rows.ta);
+        if (kGrad && g.has_grad) tc::prefetch_map(&g.grad.ta), tc::prefetch_map(&g.grad.tb[0]);
     }
     if (warp == 3) tc::pair_alloc(&tmem_base, kFfTmemCols);
     if (tid == 0) {
@@ -156,10 +196,10 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
     }
     pdl_wait();
     if (tid == kFfThreads - 1) {
-        const long long limit = *reinterpret_cast<const volatile long long*>(g.err + kFfLimitWord);
+        const long long limit = *reinterpret_cast<const volatile long long*>(g.rows.err + kFfLimitWord);
         waits.limit_ns = limit != 0 ? limit : tc::kWaitLimitNs;
     }
-    if constexpr (!kGrad) build_row_tiles<kFfThreads>(tiles, g.offsets, g.E, g.P, kFfNT);
+    if (g.has_rows) build_row_tiles<kFfThreads>(tiles, g.rows.offsets, g.rows.E, g.rows.P, kFfNT);
     tc::fence_before();
     tc::cluster_sync();
     tc::fence_after();
@@ -178,7 +218,8 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
             const int am = walk.m0() + static_cast<int>(rank) * 128;
             int bi = 0;
             while ((16 << bi) < half) ++bi;   // the smallest box of rows of B
-            const uint32_t bytes = kFfABytes + (kGrad ? (half > 64 ? 2 : 1) * 8192 : (16 << bi) * 128);
+            const bool grad = kGrad && walk.grad;
+            const uint32_t bytes = kFfABytes + (grad ? (half > 64 ? 2 : 1) * 8192 : (16 << bi) * 128);
             for (int ks = 0; ks < walk.steps; ++ks) {
                 if (use > 0 && !tc::mbar_wait_warp(&empty[st], use - 1, &waits)) {
                     ok = false;
@@ -187,23 +228,23 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                 if (leader) {
                     const uint32_t a = ring0 + st * kFfStage, b = a + kFfABytes;
                     tc::mbar_arrive_expect_tx(&full[st], bytes);
-                    if constexpr (kGrad) {
+                    if (grad) {
                         const int k = walk.k0 + ks * kFfStepK;
-                        tc::tma_2d(a, &g.ta, am, k, &full[st]);
-                        tc::tma_2d(a + 8192, &g.ta, am + 64, k, &full[st]);
-                        tc::tma_2d(b, &g.tb[0], b0, k, &full[st]);
-                        if (half > 64) tc::tma_2d(b + 8192, &g.tb[0], b0 + 64, k, &full[st]);
+                        tc::tma_2d(a, &g.grad.ta, am, k, &full[st]);
+                        tc::tma_2d(a + 8192, &g.grad.ta, am + 64, k, &full[st]);
+                        tc::tma_2d(b, &g.grad.tb[0], b0, k, &full[st]);
+                        if (half > 64) tc::tma_2d(b + 8192, &g.grad.tb[0], b0 + 64, k, &full[st]);
                     } else {
                         const int k = ks * kFfStepK;
                         if constexpr (kGated) {
-                            tc::tma_5d(a, &g.ta, k, 0, 0, am >> 5, walk.e, &full[st]);
-                        } else if constexpr (ORDER == kOrderKK) {
-                            tc::tma_3d(a, &g.ta, k, am, walk.e, &full[st]);
+                            tc::tma_5d(a, &g.rows.ta, k, 0, 0, am >> 5, walk.e, &full[st]);
+                        } else if constexpr (!A_MN) {
+                            tc::tma_3d(a, &g.rows.ta, k, am, walk.e, &full[st]);
                         } else {
-                            tc::tma_3d(a, &g.ta, am, k, walk.e, &full[st]);
-                            tc::tma_3d(a + 8192, &g.ta, am + 64, k, walk.e, &full[st]);
+                            tc::tma_3d(a, &g.rows.ta, am, k, walk.e, &full[st]);
+                            tc::tma_3d(a + 8192, &g.rows.ta, am + 64, k, walk.e, &full[st]);
                         }
-                        tc::tma_2d(b, &g.tb[bi], k, b0, &full[st]);
+                        tc::tma_2d(b, &g.rows.tb[bi], k, b0, &full[st]);
                     }
                 }
                 if (++st == kFfStages) st = 0, ++use;
@@ -217,16 +258,15 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
         }
         if (leader) {
             issued = n_issued;
-            if (!ok) ff_fail(g, &waits, rank);
+            if (!ok) ff_fail(g.rows, &waits, rank);
         }
     } else if (warp == 1 && rank == 0) {
         // -------------------------------------------------------------------- MMA issuer
         const bool leader = tc::elect_one();
         const uint32_t ring0 = tc::s_addr(ring);
-        constexpr bool kAmn = ORDER != kOrderKK, kBmn = kGrad;
-        constexpr uint32_t kAstep = kAmn ? 128 : 2, kBstep = kBmn ? 128 : 2;   // 16 values of K, in 16 bytes
-        const uint64_t da0 = kAmn ? tc::sdesc_mn128(ring0, 8192) : tc::sdesc_k128(ring0);
-        const uint64_t db0 = kBmn ? tc::sdesc_mn128(ring0 + kFfABytes, 8192) : tc::sdesc_k128(ring0 + kFfABytes);
+        constexpr uint32_t kStepK = 2, kStepMn = 128, kAstep = A_MN ? kStepMn : kStepK;   // 16 values of K, in 16 bytes
+        const uint64_t da0 = A_MN ? tc::sdesc_mn128(ring0, 8192) : tc::sdesc_k128(ring0);
+        const uint64_t db_k = tc::sdesc_k128(ring0 + kFfABytes), db_mn = tc::sdesc_mn128(ring0 + kFfABytes, 8192);
         uint32_t st = 0, use = 0, n_acc = 0;
         bool ok = true;
         for (; walk.more() && ok; walk.next()) {
@@ -238,7 +278,9 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                 ok = false;
                 break;
             }
-            const uint32_t dt = tmem + buf * kFfNT, idesc = tc::pair_idesc(walk.mma_n(), 1, kAmn, kBmn);
+            const uint32_t dt = tmem + buf * kFfNT, idesc = tc::pair_idesc(walk.mma_n(), 1, A_MN, kGrad && walk.grad);
+            const uint64_t db0 = kGrad && walk.grad ? db_mn : db_k;
+            const uint32_t bstep = kGrad && walk.grad ? kStepMn : kStepK;
             for (int ks = 0; ks < walk.steps; ++ks) {
                 if (!tc::mbar_wait_warp(&ready[st], use, &waits)) {
                     ok = false;
@@ -249,14 +291,14 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                     const uint64_t da = da0 + st * (kFfStage >> 4), db = db0 + st * (kFfStage >> 4);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        tc::pair_mma(dt, da + kk * kAstep, db + kk * kBstep, idesc, ks > 0 || kk > 0);
+                        tc::pair_mma(dt, da + kk * kAstep, db + kk * bstep, idesc, ks > 0 || kk > 0);
                     tc::pair_commit(&empty[st]);
                     if (ks + 1 == walk.steps) tc::pair_commit(&acc_full[buf]);
                 }
                 if (++st == kFfStages) st = 0, ++use;
             }
         }
-        if (leader && !ok) ff_fail(g, &waits, rank);
+        if (leader && !ok) ff_fail(g.rows, &waits, rank);
     } else if (warp == 2) {
         // -------------------------------------------------------------------- landed tiles
         uint32_t st = 0, use = 0;
@@ -269,7 +311,7 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                     ok = false;
                     break;
                 }
-                if constexpr (kGrad) {
+                if (kGrad && walk.grad) {
                     const int valid = walk.rows - ks * kFfStepK;
                     if (valid < kFfStepK) {   // rows valid .. 63 of every box
                         unsigned char* p = ring + st * kFfStage;
@@ -285,7 +327,7 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                 if (++st == kFfStages) st = 0, ++use;
             }
         }
-        if (!ok && lane == 0) ff_fail(g, &waits, rank);
+        if (!ok && lane == 0) ff_fail(g.rows, &waits, rank);
     } else if (warp >= kFfEpi0) {
         // -------------------------------------------------------------------- epilogue
         const int q = warp & 3, grp = (warp - kFfEpi0) >> 2, t128 = tid & 127;
@@ -303,7 +345,8 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
             walk.at();
             // (an expert without rows: zeros; after a wait that ran out too, as the group's warps meet at barriers and
             // all have to come there)
-            bool none = !ok || (kGrad && walk.steps == 0);
+            const bool grad = kGrad && walk.grad;
+            bool none = !ok || walk.steps == 0;
             [[maybe_unused]] uint4 zr[4 * kHalves];
             [[maybe_unused]] auto read_z = [&](int c) {   // z of rows c .. c + 15 of the tile, 16 bytes of a row a lane
 #pragma unroll
@@ -311,11 +354,11 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                     const int i = j * 128 + t128, half = i >> 9, r = c + ((i >> 5) & 15);
                     const int m = walk.m0() + static_cast<int>(rank) * 128 + 4 * (i & 31);
                     zr[j] = make_uint4(0, 0, 0, 0);
-                    if (r < walk.n && m < g.M)
-                        zr[j] = __ldg(reinterpret_cast<const uint4*>(g.z_in + static_cast<int64_t>(walk.n0 + r) * (kHalves * g.f) + half * g.f + m));
+                    if (r < walk.n && m < g.rows.M)
+                        zr[j] = __ldg(reinterpret_cast<const uint4*>(g.rows.z_in + static_cast<int64_t>(walk.n0 + r) * (kHalves * g.rows.f) + half * g.rows.f + m));
                 }
             };
-            if constexpr (kActGrad) read_z(16 * grp);
+            if (kActGrad && !grad) read_z(16 * grp);
             const uint32_t buf = n_acc & 1;
             if (!none) {
                 ok = tc::mbar_wait_warp(&acc_full[buf], n_acc >> 1, &waits);
@@ -338,7 +381,11 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                     *reinterpret_cast<uint4*>(static_cast<char*>(to) + ((first + r) * ld + col + p * each) * elem) = v;
                 }
             };
-            if constexpr (kActGrad) {
+            auto tile = [&](auto tag, auto of_grad) {   // the item's epilogue
+            constexpr int kE = decltype(tag)::value;
+            constexpr bool kG = decltype(of_grad)::value;
+            const FfArgs& a = kG ? g.grad : g.rows;
+            if constexpr (kE == kEpiSwigluGrad || kE == kEpiRelu2Grad) {
 #pragma unroll 1
                 for (int c0 = 16 * grp; c0 < walk.n; c0 += 32) {   // 16 rows of dh
                     float v[16];   // 16 lanes' neurons, the other 16's
@@ -363,7 +410,7 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                     if (!none) tc::tmem_ld_wait(v);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        uint32_t a[4], b[4];   // rows lane / 4, + 8, + 16, + 24 of the warp's neurons, a pair of rows of dz each
+                        uint32_t wa[4], wb[4];   // rows lane / 4, + 8, + 16, + 24 of the warp's neurons, a pair of rows of dz each
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
                             const float* d = v + 8 * (m >> 1) + 4 * i + 2 * (m & 1);   // dh of the pair
@@ -373,7 +420,7 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                                 const int r = 8 * i + ncol + u, c = q * 32 + 8 * m + mrow;
                                 const uint32_t at = sb + r * 512 + ((c ^ (8 * (lane & 3))) << 2);
                                 const float z = lds_f32(at);
-                                if constexpr (EPI == kEpiSwigluGrad) {
+                                if constexpr (kE == kEpiSwigluGrad) {
                                     const float2 s = ff_sigmoid(z);
                                     const float silu = z * s.x;
                                     ga[u] = d[u] * lds_f32(at + 8192) * (s.x + silu * s.y);
@@ -382,23 +429,23 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                                     ga[u] = d[u] * (2.0f * ff_relu(z));
                                 }
                             }
-                            a[m] = ff_pack(ga[0], ga[1]);
-                            if constexpr (EPI == kEpiSwigluGrad) b[m] = ff_pack(gb[0], gb[1]);
+                            wa[m] = ff_pack(ga[0], ga[1]);
+                            if constexpr (kE == kEpiSwigluGrad) wb[m] = ff_pack(gb[0], gb[1]);
                         }
-                        tc::stsm4_t(at256 + 16384 + i * 2048, a[0], a[1], a[2], a[3]);
-                        if constexpr (EPI == kEpiSwigluGrad) tc::stsm4_t(at256 + 20480 + i * 2048, b[0], b[1], b[2], b[3]);
+                        tc::stsm4_t(at256 + 16384 + i * 2048, wa[0], wa[1], wa[2], wa[3]);
+                        if constexpr (kE == kEpiSwigluGrad) tc::stsm4_t(at256 + 20480 + i * 2048, wb[0], wb[1], wb[2], wb[3]);
                     }
                     tc::named_sync(1 + grp, 128);   // (the next rows' z goes where z has been read, their dz behind a barrier)
                     const int64_t row0 = walk.n0 + c0;
-                    copy(sb + 16384, 16, g.dz_out, row0, left, kHalves * g.f, am, g.f - am, 256, 2);
-                    if (kHalves == 2) copy(sb + 20480, 16, g.dz_out, row0, left, 2 * g.f, g.f + am, g.f - am, 256, 2);
+                    copy(sb + 16384, 16, a.dz_out, row0, left, kHalves * a.f, am, a.f - am, 256, 2);
+                    if (kHalves == 2) copy(sb + 20480, 16, a.dz_out, row0, left, 2 * a.f, a.f + am, a.f - am, 256, 2);
                 }
             } else {
 #pragma unroll 1
             for (int c0 = 32 * grp; c0 < walk.n; c0 += 64) {
                 float lo[16], hi[16];
                 const int left = walk.n - c0;   // rows of the result from c0 on
-                const int64_t row0 = (kGrad ? static_cast<int64_t>(walk.e) * g.N : 0) + walk.n0 + c0;
+                const int64_t row0 = (kG ? static_cast<int64_t>(walk.e) * a.N : 0) + walk.n0 + c0;
                 if (none) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) lo[i] = hi[i] = 0.0f;
@@ -407,20 +454,20 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                     tc::tmem_ld_frag(tb + (16u << 16) + c0, hi);
                 }
                 if (!none) tc::tmem_wait32(lo, hi);
-                if constexpr (EPI == kEpiBf16) {
+                if constexpr (kE == kEpiBf16) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         tc::stsm4_t(at256 + i * 2048, ff_pack(lo[4 * i], lo[4 * i + 1]), ff_pack(lo[4 * i + 2], lo[4 * i + 3]),
                                     ff_pack(hi[4 * i], hi[4 * i + 1]), ff_pack(hi[4 * i + 2], hi[4 * i + 3]));
-                } else if constexpr (EPI == kEpiF32) {
+                } else if constexpr (kE == kEpiF32) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {   // (column ^ 8 * row / 2: the lanes of a store meet all banks)
                         const float v = j < 16 ? lo[j] : hi[j - 16];
                         const int i = (j & 15) >> 2, r = 8 * i + ncol + (j & 1), c = q * 32 + (j >> 4) * 16 + ((j >> 1) & 1) * 8 + mrow;
                         asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + r * 512 + ((c ^ (8 * (lane & 3))) << 2)), "f"(v) : "memory");
                     }
-                } else if constexpr (EPI == kEpiSwiglu) {
-                    if (g.z_out) {
+                } else if constexpr (kE == kEpiSwiglu) {
+                    if (a.z_out) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {   // gate, up
                             const float v = j < 16 ? lo[j] : hi[j - 16];
@@ -435,8 +482,8 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                     for (int i = 0; i < 4; i += 2)
                         tc::stsm4_t(at128 + (i + (lane >> 4)) * 1024, ff_pack(lo[4 * i], lo[4 * i + 1]), ff_pack(lo[4 * i + 2], lo[4 * i + 3]),
                                     ff_pack(lo[4 * i + 4], lo[4 * i + 5]), ff_pack(lo[4 * i + 6], lo[4 * i + 7]));
-                } else if constexpr (EPI == kEpiRelu2) {
-                    if (g.z_out) {
+                } else if constexpr (kE == kEpiRelu2) {
+                    if (a.z_out) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             const float v = j < 16 ? lo[j] : hi[j - 16];
@@ -455,23 +502,30 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                                     ff_pack(hi[4 * i], hi[4 * i + 1]), ff_pack(hi[4 * i + 2], hi[4 * i + 3]));
                 }
                 tc::named_sync(1 + grp, 128);
-                if constexpr (EPI == kEpiBf16) {
-                    copy(sb, 32, g.out, row0, left, g.M, am, g.M - am, 256, 2);
-                } else if constexpr (EPI == kEpiF32) {
-                    copy(sb, 32, g.out, row0, left, g.M, am, g.M - am, 512, 4);
-                } else if constexpr (EPI == kEpiSwiglu) {
+                if constexpr (kE == kEpiBf16) {
+                    copy(sb, 32, a.out, row0, left, a.M, am, a.M - am, 256, 2);
+                } else if constexpr (kE == kEpiF32) {
+                    copy(sb, 32, a.out, row0, left, a.M, am, a.M - am, 512, 4);
+                } else if constexpr (kE == kEpiSwiglu) {
                     const int j0 = am >> 1;   // the CTA's first neuron
-                    copy(sb, 32, g.h_out, row0, left, g.f, j0, g.f - j0, 128, 2);
-                    if (g.z_out) {
-                        copy(sb + 4096, 32, g.z_out, row0, left, 2 * g.f, j0, g.f - j0, 256, 4);
-                        copy(sb + 12288, 32, g.z_out, row0, left, 2 * g.f, g.f + j0, g.f - j0, 256, 4);
+                    copy(sb, 32, a.h_out, row0, left, a.f, j0, a.f - j0, 128, 2);
+                    if (a.z_out) {
+                        copy(sb + 4096, 32, a.z_out, row0, left, 2 * a.f, j0, a.f - j0, 256, 4);
+                        copy(sb + 12288, 32, a.z_out, row0, left, 2 * a.f, a.f + j0, a.f - j0, 256, 4);
                     }
                 } else {
-                    copy(sb, 32, g.h_out, row0, left, g.f, am, g.f - am, 256, 2);
-                    if (g.z_out) copy(sb + 8192, 32, g.z_out, row0, left, g.f, am, g.f - am, 512, 4);
+                    copy(sb, 32, a.h_out, row0, left, a.f, am, a.f - am, 256, 2);
+                    if (a.z_out) copy(sb + 8192, 32, a.z_out, row0, left, a.f, am, a.f - am, 512, 4);
                 }
                 tc::named_sync(1 + grp, 128);   // the staging is free again
             }
+            }
+            };
+            if constexpr (kGrad) {
+                if (grad) tile(std::integral_constant<int, GEPI>{}, std::true_type{});
+                else tile(std::integral_constant<int, EPI>{}, std::false_type{});
+            } else {
+                tile(std::integral_constant<int, EPI>{}, std::false_type{});
             }
             if (!none) {
                 tc::fence_before();
@@ -479,7 +533,7 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                 if (lane == 0) tc::mbar_arrive_cluster(acc0 + buf * 8);
             }
         }
-        if (!ok && lane == 0) ff_fail(g, &waits, rank);
+        if (!ok && lane == 0) ff_fail(g.rows, &waits, rank);
     }
 
     // Every copy and MMA of the pair has landed before its memories are given back: the producers waited for the MMAs, the
@@ -521,34 +575,51 @@ cudaError_t ff_map_rows(FfArgs& g, const uint16_t* rows, int64_t P, int64_t cols
     return e;
 }
 
-template <int EPI, int ORDER>
-cudaError_t ff_launch(const FfArgs& g, int num_sms, cudaStream_t s) {
-    const int64_t mt = (g.M + 255) / 256;
-    const int64_t rows = ORDER == kOrderGrad ? static_cast<int64_t>(g.E) * ((g.N + kFfNT - 1) / kFfNT)
-                                             : std::min(g.E, g.P) + g.P / kFfNT;
-    const int pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms / 2, mt * rows)));
-    return launch_pairs(ffn_kernel<EPI, ORDER>, pairs, kFfThreads, kFfSmem, s, g);
+template <int EPI, bool A_MN, int GEPI>
+cudaError_t ff_launch(const FfWork& g, int num_sms, cudaStream_t s) {
+    int64_t items = 0;
+    if (g.has_rows) items += (g.rows.M + 255) / 256 * static_cast<int64_t>(std::min(g.rows.E, g.rows.P) + g.rows.P / kFfNT);
+    if (g.has_grad) items += (g.grad.M + 255) / 256 * static_cast<int64_t>(g.grad.E) * ((g.grad.N + kFfNT - 1) / kFfNT);
+    const int pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms / 2, items)));
+    return launch_pairs(ffn_kernel<EPI, A_MN, GEPI>, pairs, kFfThreads, kFfSmem, s, g);
 }
 
-template <int EPI, int ORDER>
+template <int EPI, bool A_MN, int GEPI>
 cudaError_t ff_configure() {
-    const void* fn = reinterpret_cast<const void*>(&ffn_kernel<EPI, ORDER>);
+    const void* fn = reinterpret_cast<const void*>(&ffn_kernel<EPI, A_MN, GEPI>);
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFfSmem));
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     return e;
 }
 
+FfWork ff_work(int64_t P, int64_t E, int64_t f, const int32_t* offsets, int32_t* err) {
+    FfWork g;
+    std::memset(&g, 0, sizeof(g));
+    for (FfArgs* a : {&g.rows, &g.grad})
+        a->offsets = offsets, a->E = static_cast<int>(E), a->P = static_cast<int>(P), a->f = static_cast<int>(f), a->err = err;
+    return g;
+}
+
+// The gradient [E][n][m] of weights from rows a [P][m] and b [P][n].
+cudaError_t ff_set_grad(FfWork& g, const uint16_t* a, int64_t m, const uint16_t* b, int64_t n, int64_t P, void* out) {
+    g.has_grad = 1;
+    g.grad.M = static_cast<int>(m), g.grad.N = static_cast<int>(n), g.grad.out = out;
+    const cudaError_t e = ff_map(&g.grad.ta, 2, a, {m, P}, {m}, {64, kFfStepK});
+    return e != cudaSuccess ? e : ff_map(&g.grad.tb[0], 2, b, {n, P}, {n}, {64, kFfStepK});
+}
+
 }  // namespace
 
 cudaError_t configure_ffn_kernels() {
-    cudaError_t e = ff_configure<kEpiSwiglu, kOrderKK>();
-    if (e == cudaSuccess) e = ff_configure<kEpiRelu2, kOrderKK>();
-    if (e == cudaSuccess) e = ff_configure<kEpiBf16, kOrderKK>();
-    if (e == cudaSuccess) e = ff_configure<kEpiSwigluGrad, kOrderMK>();
-    if (e == cudaSuccess) e = ff_configure<kEpiRelu2Grad, kOrderMK>();
-    if (e == cudaSuccess) e = ff_configure<kEpiBf16, kOrderMK>();
-    if (e == cudaSuccess) e = ff_configure<kEpiBf16, kOrderGrad>();
-    if (e == cudaSuccess) e = ff_configure<kEpiF32, kOrderGrad>();
+    cudaError_t e = ff_configure<kEpiSwiglu, false, kEpiNone>();
+    if (e == cudaSuccess) e = ff_configure<kEpiRelu2, false, kEpiNone>();
+    if (e == cudaSuccess) e = ff_configure<kEpiBf16, false, kEpiNone>();
+    if (e == cudaSuccess) e = ff_configure<kEpiSwigluGrad, true, kEpiBf16>();
+    if (e == cudaSuccess) e = ff_configure<kEpiSwigluGrad, true, kEpiF32>();
+    if (e == cudaSuccess) e = ff_configure<kEpiRelu2Grad, true, kEpiBf16>();
+    if (e == cudaSuccess) e = ff_configure<kEpiRelu2Grad, true, kEpiF32>();
+    if (e == cudaSuccess) e = ff_configure<kEpiBf16, true, kEpiBf16>();
+    if (e == cudaSuccess) e = ff_configure<kEpiBf16, true, kEpiF32>();
     return e;
 }
 
@@ -562,60 +633,59 @@ cudaError_t launch_ffn_forward(const uint16_t* x, int64_t P, const uint16_t* wgu
         const cudaError_t r = launch_stream_bf16(x, P, wgu, E, act == MOE_ACT_SWIGLU ? 2 * f : f, d, offsets, act, h, z, num_sms, s);
         return r == cudaSuccess ? launch_stream_bf16(h, P, wd, E, d, f, offsets, MOE_ACT_NONE, y, nullptr, num_sms, s) : r;
     }
-    FfArgs g;
-    std::memset(&g, 0, sizeof(g));
-    g.offsets = offsets, g.E = static_cast<int>(E), g.P = static_cast<int>(P), g.f = static_cast<int>(f), g.err = err;
-    g.z_out = z, g.h_out = h;
-    g.K = static_cast<int>(d);
-    cudaError_t e = ff_map_rows(g, x, P, d);
+    FfWork g = ff_work(P, E, f, offsets, err);
+    g.has_rows = 1;
+    g.rows.z_out = z, g.rows.h_out = h;
+    g.rows.K = static_cast<int>(d);
+    cudaError_t e = ff_map_rows(g.rows, x, P, d);
     if (e == cudaSuccess) {
         if (act == MOE_ACT_SWIGLU) {   // 16 gate rows, the same neurons' 16 up rows, four times
-            g.M = static_cast<int>(2 * f);
-            e = ff_map(&g.ta, 5, wgu, {d, 16, 2, f / 16, E}, {d, f * d, 16 * d, 2 * f * d}, {kFfStepK, 16, 2, 4, 1});
-            if (e == cudaSuccess) e = ff_launch<kEpiSwiglu, kOrderKK>(g, num_sms, s);
+            g.rows.M = static_cast<int>(2 * f);
+            e = ff_map(&g.rows.ta, 5, wgu, {d, 16, 2, f / 16, E}, {d, f * d, 16 * d, 2 * f * d}, {kFfStepK, 16, 2, 4, 1});
+            if (e == cudaSuccess) e = ff_launch<kEpiSwiglu, false, kEpiNone>(g, num_sms, s);
         } else {
-            g.M = static_cast<int>(f);
-            e = ff_map(&g.ta, 3, wgu, {d, f, E}, {d, f * d}, {kFfStepK, 128, 1});
-            if (e == cudaSuccess) e = ff_launch<kEpiRelu2, kOrderKK>(g, num_sms, s);
+            g.rows.M = static_cast<int>(f);
+            e = ff_map(&g.rows.ta, 3, wgu, {d, f, E}, {d, f * d}, {kFfStepK, 128, 1});
+            if (e == cudaSuccess) e = ff_launch<kEpiRelu2, false, kEpiNone>(g, num_sms, s);
         }
     }
-    if (e == cudaSuccess) e = ff_map_rows(g, h, P, f);
-    if (e == cudaSuccess) e = ff_map(&g.ta, 3, wd, {f, d, E}, {f, d * f}, {kFfStepK, 128, 1});
-    g.M = static_cast<int>(d), g.K = static_cast<int>(f), g.out = y;
-    if (e == cudaSuccess) e = ff_launch<kEpiBf16, kOrderKK>(g, num_sms, s);
+    if (e == cudaSuccess) e = ff_map_rows(g.rows, h, P, f);
+    if (e == cudaSuccess) e = ff_map(&g.rows.ta, 3, wd, {f, d, E}, {f, d * f}, {kFfStepK, 128, 1});
+    g.rows.M = static_cast<int>(d), g.rows.K = static_cast<int>(f), g.rows.out = y;
+    if (e == cudaSuccess) e = ff_launch<kEpiBf16, false, kEpiNone>(g, num_sms, s);
     return e;
 }
 
+// Two launches: dz beside the gradient of w_down, then dx beside that of w_gate_up.
 cudaError_t launch_ffn_backward(const uint16_t* dy, const uint16_t* x, int64_t P, const uint16_t* wgu, const uint16_t* wd, int64_t E,
                                 int64_t d, int64_t f, const int32_t* offsets, int act, const float* z, const uint16_t* h,
                                 uint16_t* dz, uint16_t* dx, void* dwgu, void* dwd, int gt, int32_t* err, int num_sms, cudaStream_t s) {
     const int64_t nz = act == MOE_ACT_SWIGLU ? 2 * f : f;
-    FfArgs g;
-    std::memset(&g, 0, sizeof(g));
-    g.offsets = offsets, g.E = static_cast<int>(E), g.P = static_cast<int>(P), g.f = static_cast<int>(f), g.err = err;
     cudaError_t e = cudaSuccess;
+    FfWork g = ff_work(P, E, f, offsets, err);
     if (dx || dwgu) {
-        g.M = static_cast<int>(f), g.K = static_cast<int>(d), g.z_in = z, g.dz_out = dz;
-        e = ff_map_rows(g, dy, P, d);
-        if (e == cudaSuccess) e = ff_map(&g.ta, 3, wd, {f, d, E}, {f, d * f}, {64, kFfStepK, 1});
-        if (e == cudaSuccess)
-            e = act == MOE_ACT_SWIGLU ? ff_launch<kEpiSwigluGrad, kOrderMK>(g, num_sms, s) : ff_launch<kEpiRelu2Grad, kOrderMK>(g, num_sms, s);
+        g.has_rows = 1;
+        g.rows.M = static_cast<int>(f), g.rows.K = static_cast<int>(d), g.rows.z_in = z, g.rows.dz_out = dz;
+        e = ff_map_rows(g.rows, dy, P, d);
+        if (e == cudaSuccess) e = ff_map(&g.rows.ta, 3, wd, {f, d, E}, {f, d * f}, {64, kFfStepK, 1});
     }
+    if (dwd && e == cudaSuccess) e = ff_set_grad(g, h, f, dy, d, P, dwd);
+    if ((g.has_rows || g.has_grad) && e == cudaSuccess) {
+        if (act == MOE_ACT_SWIGLU)
+            e = gt == MOE_F32 ? ff_launch<kEpiSwigluGrad, true, kEpiF32>(g, num_sms, s) : ff_launch<kEpiSwigluGrad, true, kEpiBf16>(g, num_sms, s);
+        else
+            e = gt == MOE_F32 ? ff_launch<kEpiRelu2Grad, true, kEpiF32>(g, num_sms, s) : ff_launch<kEpiRelu2Grad, true, kEpiBf16>(g, num_sms, s);
+    }
+    g = ff_work(P, E, f, offsets, err);
     if (dx && e == cudaSuccess) {
-        g.M = static_cast<int>(d), g.K = static_cast<int>(nz), g.out = dx;
-        e = ff_map_rows(g, dz, P, nz);
-        if (e == cudaSuccess) e = ff_map(&g.ta, 3, wgu, {d, nz, E}, {d, nz * d}, {64, kFfStepK, 1});
-        if (e == cudaSuccess) e = ff_launch<kEpiBf16, kOrderMK>(g, num_sms, s);
+        g.has_rows = 1;
+        g.rows.M = static_cast<int>(d), g.rows.K = static_cast<int>(nz), g.rows.out = dx;
+        e = ff_map_rows(g.rows, dz, P, nz);
+        if (e == cudaSuccess) e = ff_map(&g.rows.ta, 3, wgu, {d, nz, E}, {d, nz * d}, {64, kFfStepK, 1});
     }
-    auto grad = [&](const uint16_t* a, int64_t m, const uint16_t* b, int64_t n, void* out) {
-        g.M = static_cast<int>(m), g.N = static_cast<int>(n), g.out = out;
-        cudaError_t r = ff_map(&g.ta, 2, a, {m, P}, {m}, {64, kFfStepK});
-        if (r == cudaSuccess) r = ff_map(&g.tb[0], 2, b, {n, P}, {n}, {64, kFfStepK});
-        if (r == cudaSuccess) r = gt == MOE_F32 ? ff_launch<kEpiF32, kOrderGrad>(g, num_sms, s) : ff_launch<kEpiBf16, kOrderGrad>(g, num_sms, s);
-        return r;
-    };
-    if (dwgu && e == cudaSuccess) e = grad(x, d, dz, nz, dwgu);
-    if (dwd && e == cudaSuccess) e = grad(h, f, dy, d, dwd);
+    if (dwgu && e == cudaSuccess) e = ff_set_grad(g, x, d, dz, nz, P, dwgu);
+    if ((g.has_rows || g.has_grad) && e == cudaSuccess)
+        e = gt == MOE_F32 ? ff_launch<kEpiBf16, true, kEpiF32>(g, num_sms, s) : ff_launch<kEpiBf16, true, kEpiBf16>(g, num_sms, s);
     return e;
 }
 

