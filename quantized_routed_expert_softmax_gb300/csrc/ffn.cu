@@ -51,6 +51,7 @@ struct FfArgs {
     CUtensorMap tb[4];    // {k, row}, boxes of 16 << i rows; grad tb[0] {n, row}
     const int32_t* offsets;
     int E, P, M, N, K;
+    int block;            // tiles of M of a block (rows)
     int f;                // neurons
     void* out;            // y, dx or the weights' gradient: rows of M values
     const float* z_in;
@@ -100,7 +101,7 @@ struct FfWalk {
     int k0 = 0, rows = 0;  // grad: the expert's rows
     int mtiles, ntiles, tile, mtile, stride_t, stride_m;
     __device__ FfWalk(const RowTiles& t, const FfWork& g_, int first, int stride)
-        : w(t, max(1, (g_.rows.M + 255) / 256), first, stride), g(g_) {
+        : w(t, max(1, (g_.rows.M + 255) / 256), max(1, g_.rows.block), first, stride), g(g_) {
         if constexpr (GRAD) {
             mtiles = max(1, (g.grad.M + 255) / 256);
             ntiles = (g.grad.N + kFfNT - 1) / kFfNT;
@@ -131,7 +132,7 @@ struct FfWalk {
         mtile += stride_m;
         if (mtile >= mtiles) mtile -= mtiles, ++tile;
     }
-    __device__ int m0() const { return (GRAD && grad ? mtile : w.mtile) * 256; }
+    __device__ int m0() const { return (GRAD && grad ? mtile : w.mtile()) * 256; }
     __device__ void at() {
         if (GRAD && grad) {
             e = tile / ntiles;
@@ -576,8 +577,9 @@ cudaError_t ff_map_rows(FfArgs& g, const uint16_t* rows, int64_t P, int64_t cols
 }
 
 template <int EPI, bool A_MN, int GEPI>
-cudaError_t ff_launch(const FfWork& g, int num_sms, cudaStream_t s) {
+cudaError_t ff_launch(FfWork& g, int num_sms, cudaStream_t s) {
     int64_t items = 0;
+    g.rows.block = tile_block((g.rows.M + 255) / 256);
     if (g.has_rows) items += (g.rows.M + 255) / 256 * static_cast<int64_t>(std::min(g.rows.E, g.rows.P) + g.rows.P / kFfNT);
     if (g.has_grad) items += (g.grad.M + 255) / 256 * static_cast<int64_t>(g.grad.E) * ((g.grad.N + kFfNT - 1) / kFfNT);
     const int pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms / 2, items)));

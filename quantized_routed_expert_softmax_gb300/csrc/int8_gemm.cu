@@ -55,7 +55,8 @@ struct I8Args {
     int64_t w_mat;   // bytes between weight matrices
     const int32_t* offsets;
     int E, P, N, K;
-    int nt;   // rows of a tile at most: 64 or 128
+    int nt;      // rows of a tile at most: 64 or 128
+    int block;   // weight tiles of a block
     void* out;
     int32_t* err;
 };
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
     tc::cluster_sync();
     tc::fence_after();
     const uint32_t tmem = tmem_base;
-    TileWalk walk(tiles, (g.N + 255) / 256, blockIdx.x >> 1, gridDim.x >> 1);
+    TileWalk walk(tiles, (g.N + 255) / 256, g.block, blockIdx.x >> 1, gridDim.x >> 1);
     const int ksteps = (g.K + kI8StepK - 1) / kI8StepK;
     const int width = kGated ? g.N / 2 : g.N;
     int e = 0, n0 = 0, n = 0;
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
         bool ok = true;
         for (; walk.more(); walk.next()) {
             item();
-            const int col0 = walk.mtile * (kGated ? 128 : 256) + static_cast<int>(rank) * (kGated ? 64 : 128);
+            const int col0 = walk.mtile() * (kGated ? 128 : 256) + static_cast<int>(rank) * (kGated ? 64 : 128);
             float sw[4];   // rows mrow, + 8, + 16, + 24 of the warp's (SwiGLU: gate, gate + 8, up, up + 8)
             {
                 const float* ws = reinterpret_cast<const float*>(g.wq + e * g.w_mat);
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
             for (; walk.more() && ok; walk.next()) {
                 item();
                 const int half = mma_n() >> 1, before = static_cast<int>(rank) * half;
-                const int col = walk.mtile * (kGated ? 128 : 256) + static_cast<int>(rank) * (kGated ? 64 : 128);   // of the result
+                const int col = walk.mtile() * (kGated ? 128 : 256) + static_cast<int>(rank) * (kGated ? 64 : 128);   // of the result
                 int bi = 0;
                 while ((16 << bi) < half) ++bi;   // the smallest box of rows
                 for (int ks = 0; ks < ksteps; ++ks) {
@@ -531,6 +532,7 @@ cudaError_t launch_int8_matmul(const void* xq, int64_t P, const void* wq, int64_
     g.E = static_cast<int>(E), g.P = static_cast<int>(P), g.N = static_cast<int>(N), g.K = static_cast<int>(K);
     g.out = out;
     g.err = err;
+    g.block = tile_block(static_cast<int>((N + 255) / 256));
     // codes as 8-byte elements, four a row and panel: a box takes 64 rows of a panel as one run
     cudaError_t e = tensor_map(&g.tw, CU_TENSOR_MAP_DATA_TYPE_INT64, CU_TENSOR_MAP_SWIZZLE_NONE, 3, g.wq + i8_scale_bytes(N), {4 * N, K / 32, E},
                                {32 * N, g.w_mat}, {256, 4, 1});

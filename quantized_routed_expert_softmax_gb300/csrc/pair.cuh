@@ -157,20 +157,42 @@ __device__ __forceinline__ void build_row_tiles(RowTiles& t, const int32_t* offs
     __syncthreads();
 }
 
-// One role's walk over the items (row tile, weight tile), weight tiles fastest, from item `first` in steps of `stride`.
+// One role's walk over the items (weight tiles in blocks of `block`, row tile, weight tile of the block), weight tiles fastest,
+// from item `first` in steps of `stride`.  Blocks make the tiles that are at work at a time share weights and rows alike
+// (tile_block).
 struct TileWalk {
     const RowTiles& t;
-    int mtiles, lane, stride_t, stride_m, tile, mtile, slot = 0;
-    __device__ TileWalk(const RowTiles& table, int mtiles_, int first, int stride)
-        : t(table), mtiles(mtiles_), lane(threadIdx.x & 31), stride_t(stride / mtiles_), stride_m(stride % mtiles_),
-          tile(first / mtiles_), mtile(first % mtiles_) {}
+    int mtiles, block, stride, lane;
+    int b = 0, width, tile, m, stride_t, stride_m, slot = 0;   // block, its weight tiles; row tile and weight tile in it
+    __device__ TileWalk(const RowTiles& table, int mtiles_, int block_, int first, int stride_)
+        : t(table), mtiles(mtiles_), block(block_), stride(stride_), lane(threadIdx.x & 31) {
+        enter(first);
+        leave();
+    }
+    __device__ void enter(int item) {   // item of block b
+        width = min(block, mtiles - b * block);
+        tile = item / width;
+        m = item - tile * width;
+        stride_t = stride / width;
+        stride_m = stride - stride_t * width;
+        slot = 0;
+    }
+    __device__ void leave() {           // on to the block that the item is in
+        while (tile >= t.n_tiles && (b + 1) * block < mtiles) {
+            const int item = (tile - t.n_tiles) * width + m;
+            ++b;
+            enter(item);
+        }
+    }
     __device__ bool more() const { return tile < t.n_tiles; }
     __device__ void next() {
         tile += stride_t;
-        mtile += stride_m;
-        if (mtile >= mtiles) mtile -= mtiles, ++tile;
+        m += stride_m;
+        if (m >= width) m -= width, ++tile;
+        leave();
     }
-    // The item's expert, first row and rows (the whole warp; tiles are asked for in increasing order).
+    __device__ int mtile() const { return b * block + m; }
+    // The item's expert, first row and rows (the whole warp; a block's tiles are asked for in increasing order).
     __device__ void at(int* e, int* r_first, int* n) {
         for (;;) {
             const int i = slot + 1 + lane;
@@ -185,6 +207,14 @@ struct TileWalk {
         *n = min(h, r.y - *r_first);
     }
 };
+
+// Weight tiles of a block: about ten, as 76 pairs at work on 10 by 8 tiles read least (weight tiles and row tiles 18 in all,
+// 44 by 2 take 46).  Gate and up of 8191 rows, 2816 -> 2 x 5632, z saved, read 815 MB from memory in one block of 44, as the
+// results drive the weights out of L2.
+inline int tile_block(int mtiles) {
+    const int blocks = mtiles <= 12 ? 1 : (mtiles + 9) / 10;
+    return (mtiles + blocks - 1) / blocks;
+}
 
 // A tiled tensor map (strides in bytes, one fewer than dimensions); what lies outside the tensor reads as zero.  The driver's
 // encoder is looked up at run time (pair.cu).
