@@ -27,10 +27,11 @@ __device__ __forceinline__ float silu_fast(float g) {
 }
 
 // Whether a call's rows are few enough to stream the weights through mma.sync (stream.cu).  us, streamed / by CTA pairs:
-// int8 gate.up (2816 -> 2 x 704), 8 rows of 8 experts 11.0 / 14.9, 64 rows of 48 48 / 41, 256 of 101 116 / 74; one matrix
-// (2816 -> 4224) 1 row 6.3 / 14.5, 8 rows 8.3 / 14.4.  bf16 block (2816, 2112) 1 row 8.7 / 19.7, 8 rows 12.9 / 20.1, of 128
-// experts (2816, 704) 8 rows 22.7 / 22.7.
-inline bool stream_rows(int64_t P) { return P <= 8; }
+//   int8 gate.up (2816 -> 2 x 704): 8 rows of 8 experts 9.3 / 14.9, 16 of 16 18 / 24, 24 of 24 32 / 25, 64 of 48 48 / 41
+//   int8, one matrix (2816 -> 2 x 2112): 1 row 5.2 / 14.5, 8 rows 6.2 / 14.4, 16 rows 11.0 / 15.7, 24 rows 16.0 / 15.9
+//   bf16 block (2816, 2112): 1 row 8.8 / 19.7, 16 rows 17.5 / 20.9, 24 rows 23.8 / 20.9; (2816, 704), 16 rows of 16 experts
+//   33 / 46, 24 of 24 55 / 52
+inline bool stream_rows(int64_t P) { return P <= 16; }
 
 // The sorted rows [first, last) of expert e.  Offsets are the caller's device data: whatever they hold, the range stays
 // inside [0, P] (an expert whose range is reversed has no rows).

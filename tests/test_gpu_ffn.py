@@ -68,7 +68,7 @@ def test_block_and_gradients(counts, d, f, act):
     _run(sum(counts), len(counts), d, f, counts, act, seed=d + f)
 
 
-@pytest.mark.parametrize("P", [1, 2, 5, 8, 9, 17, 33, 64, 65, 200, 1000])
+@pytest.mark.parametrize("P", [1, 2, 5, 8, 9, 16, 17, 33, 64, 65, 200, 1000])
 def test_dense_block(P):
     _run(P, 1, 176, 336, None, seed=P)
 
