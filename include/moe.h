@@ -99,7 +99,7 @@ typedef enum { MOE_LAYOUT_CANONICAL = 0, MOE_LAYOUT_DEVICE = 1, MOE_LAYOUT_NEURO
 /* Which expert kernels moe_layer_forward uses.  GEMV: weight-streaming matrix-vector
  * kernels (a few tokens per expert).  GEMM: grouped GEMMs on the tensor cores (tcgen05),
  * which need f a multiple of 64 (128 for ReLU^2) and Q8_0 or NVFP4 weights; forcing GEMM on
- * another shape or format returns MOE_ERR_UNSUPPORTED (AUTO runs INT8PC weights on the GEMV
+ * another shape or format returns MOE_ERR_UNSUPPORTED (AUTO runs INT8PC weights, inputs uncoded, on the GEMV
  * kernels at every T).  AUTO takes GEMM when T*k >= 8*E and the shape allows it; for ONE
  * token with Q8_0 SwiGLU (k*f <= 16384) or NVFP4 ReLU^2 experts (d <= 8192) it runs the whole
  * layer as a single cooperative kernel, one CTA per SM, when the device supports cooperative
@@ -418,9 +418,9 @@ typedef struct {
                                      layer's expert weights stream -- in a stack, the next layer's
                                      router weights, so its routing does not wait on HBM.  A hint:
                                      never read by the layer's arithmetic; 16-byte aligned (MXFP4
-                                     experts: checked, not used) */
+                                     experts, int8 inputs: checked, not used) */
     int64_t l2_prefetch_bytes;    /* bytes at l2_prefetch (rounded down to a multiple of 16) */
-    int32_t act_quant;            /* moe_act_quant (MOE_ACTQ_Q8_0 needs Q8_0 weights) */
+    int32_t act_quant;            /* moe_act_quant (MOE_ACTQ_Q8_0 needs Q8_0 weights, MOE_ACTQ_INT8 INT8PC) */
     int32_t flags;                /* MOE_FLAG_* bits, 0 for the default */
 } moe_layer_desc;
 
@@ -453,7 +453,7 @@ typedef struct {
     int32_t* perm;     /* [T*k]: pair id (t*k+j) at each sorted row */
     int32_t* pos;      /* [T*k]: sorted row of each pair */
     float* h;          /* [T*k][f] activations in sorted-row order (MOE_ACTQ_Q8_0: the coded values
-                          the down projection read; MXFP4: before the coding) */
+                          the down projection read; MXFP4, MOE_ACTQ_INT8: before the coding) */
     void* stage_events[5];
 } moe_trace;
 
