@@ -414,15 +414,16 @@ def ffn_workspace(rows: int, f: int, act: str = "swiglu", backward: bool = False
 
 def _ffn_shape(x, w_gate_up, w_down, act: str):
     """(P, E, d, f, columns of z) of the block's operands."""
-    P, d = x.shape
-    if w_gate_up.dim() not in (2, 3) or w_down.dim() != w_gate_up.dim():
+    (P, d), gu, dn = x.shape, w_gate_up.shape, w_down.shape
+    n = len(dn)
+    if n not in (2, 3) or len(gu) != n or (n == 3 and gu[0] != dn[0]):
         raise ValueError("the weights must be [E, rows, cols] each, or one matrix each")
-    E, f = (w_down.shape[0] if w_down.dim() == 3 else 1), w_down.shape[-1]
+    f = dn[-1]
     nz = 2 * f if act == "swiglu" else f
-    if tuple(w_down.shape[-2:]) != (d, f) or tuple(w_gate_up.shape[-2:]) != (nz, d):
+    if dn[-2] != d or gu[-1] != d or gu[-2] != nz:
         raise ValueError(f"rows of {d} values and act {act!r} need w_gate_up [{nz}, {d}] and w_down [{d}, {f}] matrices, "
-                         f"not {tuple(w_gate_up.shape)} and {tuple(w_down.shape)}")
-    return P, E, d, f, nz
+                         f"not {tuple(gu)} and {tuple(dn)}")
+    return P, dn[0] if n == 3 else 1, d, f, nz
 
 
 @_on_stream

@@ -141,3 +141,67 @@ def test_layer_descriptor_refusals(L):
         d=512, f=96, E=16, k=3, act=0, wfmt=2, path=0, router_w=FAKE, w_gate_up=FAKE, w_down=FAKE, act_quant=3), **kw})), FAKE, 1, 4, None, None, FAKE,
         FAKE, 1 << 30, None, None)
     assert F(wfmt=0) == 5 and F(path=1) == 5 and F(flags=2) == 5 and F(act_quant=4) == 1
+
+
+class OnDevice:
+    """What the binding asks of a tensor, with a device number of its own: no GPU here."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, device):
+        self.shape, self.dtype, self.number, self.device = torch.Size(shape), dtype, device, f"cuda:{device}"
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.shape.numel()
+
+    def get_device(self):
+        return self.number
+
+    def data_ptr(self):
+        return 0x10000
+
+
+def _calls(dev):
+    """Every call with its operands on the devices of `dev` (0 for the rest)."""
+    u8, i32, f32, bf = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+    t = lambda name, shape, dtype: OnDevice(shape, dtype, dev.get(name, 0))  # noqa: E731
+    xq, wq = ref.bytes_of(4, 64), ref.bytes_of(64, 64)
+    ws = t("workspace", (4096,), u8)
+    block = lambda: (t("x", (4, 32), bf), t("w_gate_up", (2, 96, 32), bf), t("w_down", (2, 32, 48), bf))  # noqa: E731
+    return {
+        "quantize": lambda: native.quantize_int8(t("x", (4, 64), f32), rows=t("rows", (4,), i32), out=t("out", (1, xq), u8)),
+        "dequantize": lambda: native.dequantize_int8(t("q", (xq,), u8), 4, 64, out=t("out", (4, 64), f32)),
+        "matmul": lambda: native.int8_matmul(t("xq", (xq,), u8), t("wq", (2, wq), u8), t("offsets", (3,), i32), 4, 64, 64,
+                                             out=t("out", (4, 64), f32), workspace=ws),
+        "forward": lambda: native.ffn_forward(*block(), t("offsets", (3,), i32), out=t("out", (4, 32), bf), workspace=ws),
+        "backward": lambda: native.ffn_backward(t("grad", (4, 32), bf), *block(), (t("z", (4, 96), f32), t("h", (4, 48), bf)),
+                                                t("offsets", (3,), i32), workspace=ws),
+    }
+
+
+OPERANDS = {"quantize": ["x", "rows", "out"], "dequantize": ["q", "out"], "matmul": ["xq", "wq", "offsets", "out", "workspace"],
+            "forward": ["x", "w_gate_up", "w_down", "offsets", "out", "workspace"],
+            "backward": ["grad", "x", "w_gate_up", "w_down", "z", "h", "offsets", "workspace"]}
+
+
+@pytest.mark.parametrize("call,operand", [(c, o) for c, names in OPERANDS.items() for o in names] + [(c, None) for c in OPERANDS])
+def test_operands_of_another_device_are_refused(monkeypatch, call, operand):
+    monkeypatch.setattr(native, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype=torch.float32, device="cuda:0": OnDevice(
+        (shape,) if isinstance(shape, int) else shape, dtype, int(str(device).split(":")[1])))
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: 256 if name.endswith("bytes") else 0
+    monkeypatch.setattr(native, "lib", lambda: Lib())
+    if operand is None:
+        _calls({})[call]()                                             # all on the current device
+        everything = {name: 1 for name in OPERANDS[call]}
+        with pytest.raises(ValueError, match="current device"):
+            _calls(everything)[call]()
+    else:
+        with pytest.raises(ValueError, match="device"):
+            _calls({operand: 1})[call]()
