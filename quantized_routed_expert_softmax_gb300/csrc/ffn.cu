@@ -47,16 +47,26 @@ constexpr int kFfThreads = 384;
 constexpr int kFfEpi0 = 4;              // first epilogue warp
 constexpr int kFfNT = 256;              // rows of B of a tile
 constexpr int kFfStepK = 64;            // 128 bytes of bf16
-constexpr int kFfABytes = 128 * 128, kFfStage = 2 * kFfABytes, kFfStages = 5;
-constexpr int kFfEpiBytes = 24 * 1024;  // staging of an epilogue group
+constexpr int kFfABytes = 128 * 128, kFfStage = 2 * kFfABytes;
 constexpr uint32_t kFfTmemCols = 512;
 constexpr int kFfLimitWord = 8;         // the waits' limit in ns (int64) in the workspace: 0 means a second
-constexpr size_t kFfSmem = 1024 + kFfStages * kFfStage + 2 * kFfEpiBytes;
-static_assert(kFfSmem + sizeof(RowTiles) + 512 <= 227 * 1024, "ring and staging fit beside the table");
 static_assert((kFfThreads - 1) * 3 >= kMaxE, "the last thread has no offsets");
 
-// What is done with a tile's sums.
-enum FfEpi { kEpiNone, kEpiBf16, kEpiF32, kEpiSwiglu, kEpiRelu2, kEpiSwigluGrad, kEpiRelu2Grad };
+// What is done with a tile's sums (kEpiSwiglu: h alone, kEpiSwigluZ: z too).
+enum FfEpi { kEpiNone, kEpiBf16, kEpiF32, kEpiSwiglu, kEpiSwigluZ, kEpiRelu2, kEpiSwigluGrad, kEpiRelu2Grad };
+
+// Staging of an epilogue group, and as many stages of operands as fit beside it.
+constexpr int ff_staging(int epi) {
+    return epi == kEpiNone ? 0 : epi == kEpiSwiglu ? 4096 : epi == kEpiBf16 ? 8192 : epi == kEpiF32 ? 16384 : epi == kEpiSwigluZ || epi == kEpiRelu2Grad ? 20480 : 24576;
+}
+template <int EPI, int GEPI>
+struct FfCfg {
+    static constexpr int kEpiBytes = ff_staging(EPI) > ff_staging(GEPI) ? ff_staging(EPI) : ff_staging(GEPI);
+    static constexpr int kRoom = 227 * 1024 - static_cast<int>(sizeof(RowTiles)) - 512 - 1024 - 2 * kEpiBytes;
+    static constexpr int kStages = kRoom / kFfStage < 6 ? kRoom / kFfStage : 6;
+    static constexpr size_t kSmem = 1024 + kStages * kFfStage + 2 * kEpiBytes;
+    static_assert(kStages >= 5, "ring");
+};
 
 // One product.  Rows of the experts by weights, or (grad) the gradient of weights: K is the expert's rows then, N columns.
 struct FfArgs {
@@ -171,9 +181,10 @@ struct FfWalk {
 template <int EPI, bool A_MN, int GEPI>
 __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constant__ FfWork g) {
     constexpr bool kGrad = GEPI != kEpiNone;
-    constexpr bool kGated = EPI == kEpiSwiglu;   // gate and up rows interleaved in A
+    constexpr int kFfStages = FfCfg<EPI, GEPI>::kStages, kFfEpiBytes = FfCfg<EPI, GEPI>::kEpiBytes;
+    constexpr bool kGated = EPI == kEpiSwiglu || EPI == kEpiSwigluZ;   // gate and up rows interleaved in A
     constexpr bool kActGrad = EPI == kEpiSwigluGrad || EPI == kEpiRelu2Grad;
-    constexpr int kHalves = EPI == kEpiSwiglu || EPI == kEpiSwigluGrad ? 2 : 1;   // z has gate and up columns
+    constexpr int kHalves = kGated || EPI == kEpiSwigluGrad ? 2 : 1;   // z has gate and up columns
     static_assert(!kGrad || A_MN, "both have one order of A");
     extern __shared__ __align__(16) unsigned char dsm_raw[];
     unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -480,8 +491,8 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                         const int i = (j & 15) >> 2, r = 8 * i + ncol + (j & 1), c = q * 32 + (j >> 4) * 16 + ((j >> 1) & 1) * 8 + mrow;
                         asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + r * 512 + ((c ^ (8 * (lane & 3))) << 2)), "f"(v) : "memory");
                     }
-                } else if constexpr (kE == kEpiSwiglu) {
-                    if (a.z_out) {
+                } else if constexpr (kE == kEpiSwiglu || kE == kEpiSwigluZ) {
+                    if constexpr (kE == kEpiSwigluZ) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {   // gate, up
                             const float v = j < 16 ? lo[j] : hi[j - 16];
@@ -520,10 +531,10 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                     copy(sb, 32, a.out, row0, left, a.M, am, a.M - am, 256, 2);
                 } else if constexpr (kE == kEpiF32) {
                     copy(sb, 32, a.out, row0, left, a.M, am, a.M - am, 512, 4);
-                } else if constexpr (kE == kEpiSwiglu) {
+                } else if constexpr (kE == kEpiSwiglu || kE == kEpiSwigluZ) {
                     const int j0 = am >> 1;   // the CTA's first neuron
                     copy(sb, 32, a.h_out, row0, left, a.f, j0, a.f - j0, 128, 2);
-                    if (a.z_out) {
+                    if constexpr (kE == kEpiSwigluZ) {
                         copy(sb + 4096, 32, a.z_out, row0, left, 2 * a.f, j0, a.f - j0, 256, 4);
                         copy(sb + 12288, 32, a.z_out, row0, left, 2 * a.f, a.f + j0, a.f - j0, 256, 4);
                     }
@@ -596,13 +607,13 @@ cudaError_t ff_launch(FfWork& g, int num_sms, cudaStream_t s) {
     if (g.has_rows) items += (g.rows.M + 255) / 256 * static_cast<int64_t>(std::min(g.rows.E, g.rows.P) + g.rows.P / kFfNT);
     if (g.has_grad) items += (g.grad.M + 255) / 256 * static_cast<int64_t>(g.grad.E) * ((g.grad.N + kFfNT - 1) / kFfNT);
     const int pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms / 2, items)));
-    return launch_pairs(ffn_kernel<EPI, A_MN, GEPI>, pairs, kFfThreads, kFfSmem, s, g);
+    return launch_pairs(ffn_kernel<EPI, A_MN, GEPI>, pairs, kFfThreads, FfCfg<EPI, GEPI>::kSmem, s, g);
 }
 
 template <int EPI, bool A_MN, int GEPI>
 cudaError_t ff_configure() {
     const void* fn = reinterpret_cast<const void*>(&ffn_kernel<EPI, A_MN, GEPI>);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFfSmem));
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(FfCfg<EPI, GEPI>::kSmem));
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     return e;
 }
@@ -627,6 +638,7 @@ cudaError_t ff_set_grad(FfWork& g, const uint16_t* a, int64_t m, const uint16_t*
 
 cudaError_t configure_ffn_kernels() {
     cudaError_t e = ff_configure<kEpiSwiglu, false, kEpiNone>();
+    if (e == cudaSuccess) e = ff_configure<kEpiSwigluZ, false, kEpiNone>();
     if (e == cudaSuccess) e = ff_configure<kEpiRelu2, false, kEpiNone>();
     if (e == cudaSuccess) e = ff_configure<kEpiBf16, false, kEpiNone>();
     if (e == cudaSuccess) e = ff_configure<kEpiSwigluGrad, true, kEpiBf16>();
@@ -657,7 +669,7 @@ cudaError_t launch_ffn_forward(const uint16_t* x, int64_t P, const uint16_t* wgu
         if (act == MOE_ACT_SWIGLU) {   // 16 gate rows, the same neurons' 16 up rows, four times
             g.rows.M = static_cast<int>(2 * f);
             e = ff_map(&g.rows.ta, 5, wgu, {d, 16, 2, f / 16, E}, {d, f * d, 16 * d, 2 * f * d}, {kFfStepK, 16, 2, 4, 1});
-            if (e == cudaSuccess) e = ff_launch<kEpiSwiglu, false, kEpiNone>(g, num_sms, s);
+            if (e == cudaSuccess) e = z ? ff_launch<kEpiSwigluZ, false, kEpiNone>(g, num_sms, s) : ff_launch<kEpiSwiglu, false, kEpiNone>(g, num_sms, s);
         } else {
             g.rows.M = static_cast<int>(f);
             e = ff_map(&g.rows.ta, 3, wgu, {d, f, E}, {d, f * d}, {kFfStepK, 128, 1});
