@@ -36,21 +36,23 @@ namespace moe {
 
 constexpr int kI8Threads = 896;
 constexpr int kI8ConvA0 = 4, kI8ConvB0 = 12, kI8Epi0 = 20;   // first warps of the roles
-constexpr int kI8NT = 128, kI8StepK = 128;   // rows of a tile at most
+constexpr int kI8StepK = 128;
 constexpr int kI8SegSteps = 1024 / kI8StepK;
-constexpr int kI8RawA = 128 * kI8StepK, kI8ConvStages = 4, kI8MaxRawStages = 7;
-// Bytes of a stage of codes and of converted rows, for tiles of up to nt rows (half of them in a CTA).
+constexpr int kI8RawA = 128 * kI8StepK, kI8MaxRawStages = 7;
+// For tiles of up to nt rows, 64, 128 or 192 (half of them in a CTA): bytes of a stage of codes and of converted rows, and how
+// many of both.  Tensor memory has two accumulators of 128 columns (192) and A's stages of 64 behind them.
 __host__ __device__ constexpr int i8_raw(int nt) { return kI8RawA + nt / 2 * kI8StepK; }
 __host__ __device__ constexpr int i8_conv_b(int nt) { return nt / 2 * 2 * kI8StepK; }
 __host__ __device__ constexpr int i8_raw_stages(int nt) { return nt > 64 ? 4 : 7; }
+__host__ __device__ constexpr int i8_conv_stages(int nt) { return nt > 128 ? 2 : 4; }
 constexpr int kI8EpiBytes = 16 * 1024;
-constexpr uint32_t kI8ACol = 2 * kI8NT, kI8TmemCols = 512;   // A's stages of 64 columns behind the two accumulators
+constexpr uint32_t kI8TmemCols = 512;
 constexpr int kI8LimitWord = 8;   // the waits' limit in ns (int64) in the workspace: 0 means a second
-constexpr size_t i8_smem(int nt) { return 1024 + kI8ConvStages * i8_conv_b(nt) + i8_raw_stages(nt) * i8_raw(nt) + 2 * kI8EpiBytes; }
-constexpr size_t kI8Smem = i8_smem(128) > i8_smem(64) ? i8_smem(128) : i8_smem(64);
-static_assert(kI8ACol + 64 * kI8ConvStages <= kI8TmemCols, "tensor memory");
+constexpr size_t i8_smem(int nt) { return 1024 + i8_conv_stages(nt) * i8_conv_b(nt) + i8_raw_stages(nt) * i8_raw(nt) + 2 * kI8EpiBytes; }
+constexpr size_t i8_max(size_t a, size_t b) { return a > b ? a : b; }
+constexpr size_t kI8Smem = i8_max(i8_smem(192), i8_max(i8_smem(128), i8_smem(64)));
+static_assert(2 * 128 + 64 * i8_conv_stages(128) <= kI8TmemCols && 2 * 192 + 64 * i8_conv_stages(192) <= kI8TmemCols, "tensor memory");
 static_assert(kI8Smem + sizeof(RowTiles) + 512 <= 227 * 1024, "rings and staging fit beside the table");
-static_assert(kI8ConvStages % 2 == 0, "the two groups of converting warps have stages of their own");
 static_assert((kI8Threads - 1) * 2 >= kMaxE, "the last thread has no offsets");
 // Sums of more than 1024 columns: the epilogue's warps hold their segments' sums in registers, which the other warps give
 // up (twenty warps of 48 and eight of 128 are less than the 28 of 72 that the block starts with).
@@ -60,12 +62,12 @@ static_assert(20 * kI8RegsOther + 8 * kI8RegsEpi <= 28 * kI8RegsLaunch, "registe
 
 struct I8Args {
     CUtensorMap tw;      // codes of the weights {8 bytes, panel, matrix}, boxes of 64 rows by 4 panels
-    CUtensorMap tx[3];   // codes of the rows {8 bytes, panel}, boxes of 16 << i rows by 4 panels
+    CUtensorMap tx[3];   // codes of the rows {8 bytes, panel}, boxes of 16 << i rows by 4 panels (96 rows: 64 and 32)
     const uint8_t *xq, *wq;
     int64_t w_mat;   // bytes between weight matrices
     const int32_t* offsets;
     int E, P, N, K;
-    int nt;      // rows of a tile at most: 64 or 128
+    int nt;      // rows of a tile at most: 64, 128 or 192
     int block;   // weight tiles of a block
     void* out;
     int32_t* err;
@@ -110,9 +112,14 @@ __device__ __forceinline__ uint32_t i8_pack(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int ACT, bool F32, bool MULTI>
+// MULTI: sums of more than 1024 columns.  NT: 128 (also 64, by g.nt), or 192.
+template <int ACT, bool F32, bool MULTI, int NT>
 __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_constant__ I8Args g) {
     constexpr bool kGated = ACT == MOE_ACT_SWIGLU;
+    constexpr int kI8ConvStages = i8_conv_stages(NT);
+    constexpr uint32_t kI8ACol = 2 * NT;
+    static_assert(!MULTI || NT == 128, "the epilogue's registers hold two times 32 rows");
+    static_assert(kI8ConvStages % 2 == 0, "the two groups of converting warps have stages of their own");
     extern __shared__ __align__(16) unsigned char dsm_raw[];
     unsigned char* convb = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t raw_bytes = i8_raw(g.nt), raw_stages = i8_raw_stages(g.nt), convb_bytes = i8_conv_b(g.nt);
@@ -210,20 +217,20 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                 tc::fence_after();
                 const bool last = seg + 1 == segs;
 #pragma unroll (MULTI ? 2 : 1)
-                for (int ch = 0; ch < 2; ++ch) {
+                for (int ch = 0; ch < NT / 64; ++ch) {
                     const int c0 = 32 * grp + 64 * ch;
                     if (c0 >= n) continue;
                     float* lo = sums[MULTI ? ch : 0];
                     float* hi = lo + 16;
                     if (!MULTI || seg == 0) {
-                        tc::tmem_ld_frag(tq + buf * kI8NT + c0, lo);
-                        tc::tmem_ld_frag(tq + (16u << 16) + buf * kI8NT + c0, hi);
+                        tc::tmem_ld_frag(tq + buf * NT + c0, lo);
+                        tc::tmem_ld_frag(tq + (16u << 16) + buf * NT + c0, hi);
                         tc::tmem_wait32(lo, hi);
                     } else {
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             float v[16];
-                            tc::tmem_ld_frag(tq + (u ? 16u << 16 : 0u) + buf * kI8NT + c0, v);
+                            tc::tmem_ld_frag(tq + (u ? 16u << 16 : 0u) + buf * NT + c0, v);
                             tc::tmem_ld_wait(v);
 #pragma unroll
                             for (int j = 0; j < 16; ++j) lo[16 * u + j] += v[j];
@@ -308,7 +315,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                 const int half = mma_n() >> 1, before = static_cast<int>(rank) * half;
                 const int col = walk.mtile() * (kGated ? 128 : 256) + static_cast<int>(rank) * (kGated ? 64 : 128);   // of the result
                 int bi = 0;
-                while ((16 << bi) < half) ++bi;   // the smallest box of rows
+                while (bi < 2 && (16 << bi) < half) ++bi;   // the smallest box of rows; more than 64: and one of 32
+            const bool more = NT > 128 && half > 64;
                 for (int ks = 0; ks < ksteps; ++ks) {
                     if (use > 0 && !tc::mbar_wait_warp(&raw_empty[st], use - 1, &waits)) {
                         ok = false;
@@ -317,10 +325,11 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                     if (leader) {
                         // (rows and panels past a matrix's end arrive as zeros)
                         const uint32_t dst = raw0 + st * raw_bytes;
-                        tc::mbar_arrive_expect_tx(&raw_full[st], kI8RawA + (16 << bi) * kI8StepK);
+                        tc::mbar_arrive_expect_tx(&raw_full[st], kI8RawA + ((16 << bi) + (more ? 32 : 0)) * kI8StepK);
                         tc::tma_3d(dst, &g.tw, 4 * col, 4 * ks, e, &raw_full[st]);
                         tc::tma_3d(dst + kI8RawA / 2, &g.tw, 4 * (col + (kGated ? width : 64)), 4 * ks, e, &raw_full[st]);
                         tc::tma_2d(dst + kI8RawA, &g.tx[bi], 4 * (n0 + before), 4 * ks, &raw_full[st]);
+                    if (more) tc::tma_2d(dst + kI8RawA + 8192, &g.tx[1], 4 * (n0 + before + 64), 4 * ks, &raw_full[st]);
                     }
                     if (++st == raw_stages) st = 0, ++use;
                 }
@@ -361,7 +370,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)   // (64 columns of B's rows, then the next 64)
                             if (kk < 4 || two)
-                                i8_mma(tmem + buf * kI8NT, ta + 8 * kk, db + (kk >> 2) * (convb_bytes >> 5) + 2 * (kk & 3), idesc, in_seg > 0 || kk > 0);
+                                i8_mma(tmem + buf * NT, ta + 8 * kk, db + (kk >> 2) * (convb_bytes >> 5) + 2 * (kk & 3), idesc, in_seg > 0 || kk > 0);
                         seen = tc::mbar_test_wait(&ready[st1], use1 & 1u);   // beside the MMAs
                         tc::pair_commit(&empty[st]);
                         if (last) tc::pair_commit(&acc_full[buf]);
@@ -394,8 +403,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                 item();
                 const int half = mma_n() >> 1;
                 int bi = 0;
-                while ((16 << bi) < half) ++bi;
-                const uint32_t pstride = 32u * (16 << bi);   // of the panels of the rows' box
+                while (bi < 2 && (16 << bi) < half) ++bi;
+                const uint32_t pstride = 32u * (16 << bi);   // of the panels of the rows' (first) box
                 for (; ks < ksteps; ks += by) {
                     if (!tc::mbar_wait_warp(&raw_full[rs], ruse, &waits)) {
                         ok = false;
@@ -453,6 +462,24 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                                 sts128(row + (((c + 2) ^ (brow & 7)) << 4), h + 4);
                             }
                         }
+                        if (NT > 128 && half > 64) {   // rows 64 .. 95, a panel a lane
+                            const int r = t128 & 31, panel = t128 >> 5, hf = (r >> 2) & 1;
+                            if (64 + r < half && (two || panel < 2)) {
+                                const uint32_t row = conv0 + cs * convb_bytes + (panel >> 1) * (convb_bytes >> 1) + (64 + r) * 128;
+                                const uint32_t from = src + kI8RawA + 8192 + panel * 1024 + r * 32;
+                                uint4 v[2];
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) v[j] = lds128(from + (hf ^ j) * 16);
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const int c = (panel & 1) * 4 + (hf ^ j);
+                                    uint32_t h[8];
+                                    i8_f16(v[j].x, h), i8_f16(v[j].z, h + 2), i8_f16(v[j].y, h + 4), i8_f16(v[j].w, h + 6);
+                                    sts128(row + ((c ^ (r & 7)) << 4), h);
+                                    sts128(row + (((c + 2) ^ (r & 7)) << 4), h + 4);
+                                }
+                            }
+                        }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
                     __syncwarp();
@@ -503,11 +530,15 @@ namespace {
 
 using I8Kernel = void (*)(I8Args);
 
-template <bool MULTI>
+template <bool MULTI, int NT>
 I8Kernel i8_kernel(int act, bool f32) {
-    if (act == MOE_ACT_SWIGLU) return f32 ? int8_gemm_kernel<MOE_ACT_SWIGLU, true, MULTI> : int8_gemm_kernel<MOE_ACT_SWIGLU, false, MULTI>;
-    if (act == MOE_ACT_RELU2) return f32 ? int8_gemm_kernel<MOE_ACT_RELU2, true, MULTI> : int8_gemm_kernel<MOE_ACT_RELU2, false, MULTI>;
-    return f32 ? int8_gemm_kernel<MOE_ACT_NONE, true, MULTI> : int8_gemm_kernel<MOE_ACT_NONE, false, MULTI>;
+    if (act == MOE_ACT_SWIGLU) return f32 ? int8_gemm_kernel<MOE_ACT_SWIGLU, true, MULTI, NT> : int8_gemm_kernel<MOE_ACT_SWIGLU, false, MULTI, NT>;
+    if (act == MOE_ACT_RELU2) return f32 ? int8_gemm_kernel<MOE_ACT_RELU2, true, MULTI, NT> : int8_gemm_kernel<MOE_ACT_RELU2, false, MULTI, NT>;
+    return f32 ? int8_gemm_kernel<MOE_ACT_NONE, true, MULTI, NT> : int8_gemm_kernel<MOE_ACT_NONE, false, MULTI, NT>;
+}
+I8Kernel i8_kernel(bool multi, int nt, int act, bool f32) {
+    if (multi) return i8_kernel<true, 128>(act, f32);
+    return nt > 128 ? i8_kernel<false, 192>(act, f32) : i8_kernel<false, 128>(act, f32);
 }
 
 }  // namespace
@@ -516,8 +547,9 @@ cudaError_t configure_int8_kernels() {
     cudaError_t e = cudaSuccess;
     for (int act : {MOE_ACT_SWIGLU, MOE_ACT_RELU2, MOE_ACT_NONE})
         for (bool f32 : {false, true})
-            for (bool multi : {false, true}) {
-                const void* fn = reinterpret_cast<const void*>(multi ? i8_kernel<true>(act, f32) : i8_kernel<false>(act, f32));
+            for (int kind = 0; kind < 3; ++kind) {
+                const bool multi = kind == 2;
+                const void* fn = reinterpret_cast<const void*>(i8_kernel(multi, kind == 1 ? 192 : 128, act, f32));
                 if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kI8Smem));
                 if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
                 // (with fewer registers at launch the epilogue's warps would wait for theirs for ever)
@@ -552,11 +584,13 @@ cudaError_t launch_int8_matmul(const void* xq, int64_t P, const void* wq, int64_
     if (e != cudaSuccess) return e;
     // Tiles of up to 64 rows where experts have few: smaller stages leave room for more of them, and what is on its way from
     // memory bounds the kernel then.
-    g.nt = P / std::min(E, P) <= 48 ? 64 : 128;
+    // Sums of up to 1024 columns in tiles of 192 rows where experts have many: weights are converted once for each row tile.
+    const int64_t avg = P / std::min(E, P);
+    const bool multi = K > kI8SegSteps * kI8StepK;
+    g.nt = avg <= 48 ? 64 : (avg < 160 || multi ? 128 : 192);
     const int64_t bound = (N + 255) / 256 * (std::min(E, P) + P / g.nt);
     const int pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms / 2, bound)));
-    return launch_pairs(K > kI8SegSteps * kI8StepK ? i8_kernel<true>(act, ot == MOE_F32) : i8_kernel<false>(act, ot == MOE_F32), pairs, kI8Threads,
-                        i8_smem(g.nt), s, g);
+    return launch_pairs(i8_kernel(multi, g.nt, act, ot == MOE_F32), pairs, kI8Threads, i8_smem(g.nt), s, g);
 }
 
 }  // namespace moe

@@ -165,7 +165,8 @@ def _check(P, E, N, K, counts, act, dtype, seed=0, full=False, before=0):
                                        ("swiglu", torch.float32), ("relu2", torch.float32), ("relu2", torch.bfloat16)])
 @pytest.mark.parametrize("counts,N,K", [
     ([1], 64, 32), ([1, 0, 0, 2], 128, 64), ([5, 0, 1, 9], 192, 96), ([0, 16], 64, 2848), ([11, 5], 128, 4128), ([9, 0, 7, 1], 128, 96), ([0, 0, 3], 64, 704), ([17, 33, 0, 64, 130], 320, 160),
-    ([128, 127, 129, 1], 256, 1024), ([300, 0, 70], 192, 1056), ([257, 256, 255], 64, 2816), ([1] * 40, 128, 2816), ([8] * 20, 64, 2080)])
+    ([128, 127, 129, 1], 256, 1024), ([300, 0, 70], 192, 1056), ([257, 256, 255], 64, 2816), ([1] * 40, 128, 2816), ([8] * 20, 64, 2080),
+    ([400, 150, 0, 290], 320, 1024), ([193], 64, 96), ([389, 0, 160, 2], 128, 704), ([161, 224], 576, 32)])
 def test_product(counts, N, K, act, dtype):
     _check(sum(counts), len(counts), N, K, counts, act, dtype, seed=N + K)
 
