@@ -6,7 +6,7 @@
 // 1024 columns is below 2^24 and exact; longer sums are cut into segments of 1024 whose exact sums are added in fp32, in the
 // epilogue's registers.
 //
-// Weights are the MMA's M (256 a pair of CTAs), an expert's rows its N (32 .. 128), so that an expert with few rows does not
+// Weights are the MMA's M (256 a pair of CTAs), an expert's rows its N (32 .. 192), so that an expert with few rows does not
 // pay for a full tile.  A persistent grid of CTA pairs; warps have fixed roles, linked by mbarriers:
 //   warp 0       TMA: per K step of 128, the CTA's 128 weight rows and half of the tile's rows.  A panel of 32 columns holds
 //                the codes of consecutive rows side by side, so a box takes a panel's 64 rows as one run of 2 KB;
@@ -18,15 +18,15 @@
 //                memory in 16-byte pieces of whole rows to memory.
 // Two accumulators alternate.
 //
-// Measured: 512 tokens' gate.up (32 rows an expert, 2816 -> 2 x 704) 102 us, 5.1 TB/s of weights, bound by HBM and by the
-// chain load -> convert -> MMA of the stages; 65528 rows, 704 -> 2816, 252 us, 1,030 TFLOP/s, gate.up 451 us, 1,150;
-// 8192^3 695 us, 1,580.  Many rows are bound by issuing instructions (72 % of the slots: five a 4-code word to convert,
-// weights again for every row tile, and the epilogue) and by shared memory (63 %), the tensor cores are at work 43 % of
-// the time.
+// Measured: 512 tokens' gate.up (32 rows an expert, 2816 -> 2 x 704) 100 us, 5.2 TB/s of weights, bound by HBM and by the
+// chain load -> convert -> MMA of the stages; 65528 rows, 704 -> 2816, 229 us, 1,130 TFLOP/s, gate.up 444 us, 1,170;
+// 8192^3 693 us, 1,590.  Many rows are bound by issuing instructions: five a 4-code word to convert (weights again for every row
+// tile), and the epilogue.
 // What it took, us for 65528 rows 704 -> 2816 / 8192^3: K steps of 64 by bulk copies 426 / 1382; TMA tiles of 128 columns,
 // segment sums in registers 316 / 941; codes as fragments, without bank conflicts, read ahead 296 / 820; eight warps for the
-// rows 259 / 746; blocks of weight tiles 252 / 695.  Dropped: stores of A of 32 columns (848 against 820), commits one step
-// later (no change).
+// rows 259 / 746; blocks of weight tiles 252 / 695; row tiles of 192 232 / 695; addresses by xor, scales by shuffle and two
+// staging buffers 229 / 693 (gate.up 452 -> 444).  Dropped: stores of A of 32 columns (848 against 820), commits one step later
+// (no change).
 #include <algorithm>
 #include <cstring>
 
@@ -190,12 +190,19 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
         const int r8 = lane & 7;
         const int piece = kGated ? q * 2 + ((lane >> 3) & 1) : q * 4 + (lane >> 3);   // stmatrix (bf16): this lane's 16 bytes
         const uint32_t at = sb + r8 * kRow + ((piece ^ r8) << 4) + (kGated ? (lane >> 4) * 8 * kRow : 0);
+        // whole rows from shared memory to memory, 16 bytes a lane: this lane's piece of every kStep-th row.  (The rows' xor is the
+        // same for all of them, but for fp32 rows of 512 bytes, where every other one has bit 2 of the piece turned.)
+        constexpr int kElem = F32 ? 4 : 2, kPer = kRow / 16, kEach = 16 / kElem, kStep = 128 / kPer;
+        constexpr bool kTwo = kRow * 32 * 2 <= kI8EpiBytes;   // two buffers, so that one barrier a chunk will do
+        const int crow = t128 / kPer, cpiece = t128 % kPer;
+        const uint32_t cfrom = sb + crow * kRow + ((F32 ? cpiece ^ (2 * ((crow >> 1) & 3)) : cpiece ^ (crow & 7)) << 4);
         const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
         const float* sx = reinterpret_cast<const float*>(g.xq);
         const bool wide = width % (F32 ? 4 : 8) == 0;
         const int segs = (ksteps + kI8SegSteps - 1) / kI8SegSteps;
         uint32_t n_acc = 0;
         bool ok = true;
+        uint32_t turn = 0;   // the buffer whose turn it is, bytes from the first
         for (; walk.more(); walk.next()) {
             item();
             const int col0 = walk.mtile() * (kGated ? 128 : 256) + static_cast<int>(rank) * (kGated ? 64 : 128);
@@ -220,6 +227,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                 for (int ch = 0; ch < NT / 64; ++ch) {
                     const int c0 = 32 * grp + 64 * ch;
                     if (c0 >= n) continue;
+                    const float scale = __ldg(sx + n0 + min(c0 + lane, n - 1));   // of row c0 + lane
                     float* lo = sums[MULTI ? ch : 0];
                     float* hi = lo + 16;
                     if (!MULTI || seg == 0) {
@@ -237,14 +245,18 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                         }
                     }
                     if (MULTI && !last) continue;
-                    float s[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s[j] = __ldg(sx + n0 + min(c0 + 8 * (j >> 1) + ncol + (j & 1), n - 1));
+                    for (int i = 0; i < 4; ++i) {
+                        const uint64_t t = pack_f32x2(__shfl_sync(0xffffffffu, scale, 8 * i + ncol), __shfl_sync(0xffffffffu, scale, 8 * i + ncol + 1));
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {   // rows mrow, + 8, + 16, + 24 of the warp's: two columns each
+                            float* z = (u < 2 ? lo : hi) + 4 * i + 2 * (u & 1);
+                            const float2 v = unpack_f32x2(mul_f32x2(pack_f32x2(z[0], z[1]), mul_f32x2(t, pack_f32x2(sw[u], sw[u]))));
+                            z[0] = v.x, z[1] = v.y;
+                        }
+                    }
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float t = s[2 * (j >> 2) + (j & 1)];
-                        lo[j] *= t * sw[(j >> 1) & 1];
-                        hi[j] *= t * sw[2 + ((j >> 1) & 1)];
                         if (kGated) lo[j] = silu_fast(lo[j]) * hi[j];
                         if (ACT == MOE_ACT_RELU2) {
                             lo[j] = lo[j] > 0.0f ? lo[j] * lo[j] : (lo[j] <= 0.0f ? 0.0f : lo[j]);
@@ -257,44 +269,45 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                             const float v = j < 16 ? lo[j] : hi[j - 16];
                             const int r = 8 * ((j & 15) >> 2) + ncol + (j & 1);
                             const int c = q * (kGated ? 16 : 32) + (j >> 4) * 16 + ((j >> 1) & 1) * 8 + mrow;
-                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + r * kRow + ((c ^ (8 * (lane & 3))) << 2)), "f"(v) : "memory");
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + turn + r * kRow + ((c ^ (8 * (lane & 3))) << 2)), "f"(v) : "memory");
                         }
                     } else if constexpr (kGated) {
 #pragma unroll
                         for (int i = 0; i < 4; i += 2)
-                            tc::stsm4_t(at + i * 8 * kRow, i8_pack(lo[4 * i], lo[4 * i + 1]), i8_pack(lo[4 * i + 2], lo[4 * i + 3]),
+                            tc::stsm4_t(at + turn + i * 8 * kRow, i8_pack(lo[4 * i], lo[4 * i + 1]), i8_pack(lo[4 * i + 2], lo[4 * i + 3]),
                                         i8_pack(lo[4 * i + 4], lo[4 * i + 5]), i8_pack(lo[4 * i + 6], lo[4 * i + 7]));
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            tc::stsm4_t(at + i * 8 * kRow, i8_pack(lo[4 * i], lo[4 * i + 1]), i8_pack(lo[4 * i + 2], lo[4 * i + 3]),
+                            tc::stsm4_t(at + turn + i * 8 * kRow, i8_pack(lo[4 * i], lo[4 * i + 1]), i8_pack(lo[4 * i + 2], lo[4 * i + 3]),
                                         i8_pack(hi[4 * i], hi[4 * i + 1]), i8_pack(hi[4 * i + 2], hi[4 * i + 3]));
                     }
                     tc::named_sync(1 + grp, 128);
                     const int left = n - c0, cols = width - col0;
                     const int64_t o0 = static_cast<int64_t>(n0 + c0) * width + col0;
-                    constexpr int kElem = F32 ? 4 : 2, kPer = kRow / 16, kEach = 16 / kElem;
-                    if (wide) {   // whole rows, 16 bytes a lane
+                    if (wide) {
+                        char* to = static_cast<char*>(g.out) + (o0 + static_cast<int64_t>(crow) * width + cpiece * kEach) * kElem;
+                        const int64_t pitch = static_cast<int64_t>(kStep) * width * kElem;
+                        const int rows = cpiece * kEach < cols ? left - crow : 0;
 #pragma unroll
-                        for (int j = 0; j < kRow * 32 / 16 / 128; ++j) {
-                            const int i = j * 128 + t128, r = i / kPer, p = i % kPer;
-                            const int place = F32 ? p ^ (2 * ((r >> 1) & 3)) : p ^ (r & 7);
-                            if (r >= left || p * kEach >= cols) continue;
-                            *reinterpret_cast<uint4*>(static_cast<char*>(g.out) + (o0 + static_cast<int64_t>(r) * width + p * kEach) * kElem) =
-                                lds128(sb + r * kRow + (place << 4));
-                        }
+                        for (int j = 0; j < 32 / kStep; ++j, to += pitch)
+                            if (j * kStep < rows) *reinterpret_cast<uint4*>(to) = lds128((cfrom ^ (F32 && !kGated && (j & 1) ? 64 : 0)) + turn + j * kStep * kRow);
                     } else {   // rows that start anywhere: a value a lane
                         for (int i = t128; i < 32 * kPer * kEach; i += 128) {
                             const int r = i / (kPer * kEach), c = i % (kPer * kEach);
                             if (r >= left || c >= cols) continue;
                             const int place = F32 ? (c / kEach) ^ (2 * ((r >> 1) & 3)) : (c / kEach) ^ (r & 7);
-                            const unsigned char* p = staging + grp * kI8EpiBytes + r * kRow + (place << 4) + (c % kEach) * kElem;
+                            const unsigned char* p = staging + grp * kI8EpiBytes + turn + r * kRow + (place << 4) + (c % kEach) * kElem;
                             const int64_t o = o0 + static_cast<int64_t>(r) * width + c;
                             if (F32) static_cast<float*>(g.out)[o] = *reinterpret_cast<const float*>(p);
                             else static_cast<uint16_t*>(g.out)[o] = *reinterpret_cast<const uint16_t*>(p);
                         }
                     }
-                    tc::named_sync(1 + grp, 128);   // the staging is free again
+                    if constexpr (kTwo) {
+                        turn ^= kI8EpiBytes / 2;
+                    } else {
+                        tc::named_sync(1 + grp, 128);   // the staging is free again
+                    }
                 }
                 tc::fence_before();
                 __syncwarp();
@@ -396,6 +409,9 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
             // B: this lane's row and half of the step's columns; lanes 4-7 of 8 begin with the second 16 bytes of a panel, so
             // that 8 lanes meet all banks, here and in the swizzled stores.
             const int brow = t128 & 63, bset = t128 >> 6, bhalf = (brow >> 2) & 1;
+            // (a piece's place in its row of 128 bytes is xored with the row; the rest of the address leaves those bits alone)
+            const uint32_t bto = bset * (convb_bytes >> 1) + brow * 128 + ((bhalf ^ (brow & 7)) << 4);
+            const uint32_t bfrom = kI8RawA + brow * 32 + bhalf * 16;
             uint32_t rs = first, cs = first, ruse = 0, cuse = 0;
             int ks = static_cast<int>(first);   // of the step in its item
             bool ok = true;
@@ -448,35 +464,33 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                             break;
                         }
                         if (brow < half && (two || bset == 0)) {
-                            const uint32_t row = conv0 + cs * convb_bytes + bset * (convb_bytes >> 1) + brow * 128;
-                            const uint32_t from = src + kI8RawA + bset * 2 * pstride + brow * 32;
+                            const uint32_t to = conv0 + cs * convb_bytes + bto, from = src + bfrom + bset * 2 * pstride;
                             uint4 v[4];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) v[j] = lds128(from + (j >> 1) * pstride + (bhalf ^ (j & 1)) * 16);
+                            for (int j = 0; j < 4; ++j) v[j] = lds128((from + (j >> 1) * pstride) ^ ((j & 1) * 16));
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int c = (j >> 1) * 4 + (bhalf ^ (j & 1));   // (words 0 2 of the half to piece c, 1 3 to piece c + 2)
+                            for (int j = 0; j < 4; ++j) {   // (words 0 2 of 16 bytes to their piece, 1 3 to the piece two on)
                                 uint32_t h[8];
                                 i8_f16(v[j].x, h), i8_f16(v[j].z, h + 2), i8_f16(v[j].y, h + 4), i8_f16(v[j].w, h + 6);
-                                sts128(row + ((c ^ (brow & 7)) << 4), h);
-                                sts128(row + (((c + 2) ^ (brow & 7)) << 4), h + 4);
+                                sts128(to ^ (((j >> 1) * 4 + (j & 1)) << 4), h);
+                                sts128(to ^ (((j >> 1) * 4 + (j & 1) + 2) << 4), h + 4);
                             }
                         }
                         if (NT > 128 && half > 64) {   // rows 64 .. 95, a panel a lane
                             const int r = t128 & 31, panel = t128 >> 5, hf = (r >> 2) & 1;
                             if (64 + r < half && (two || panel < 2)) {
-                                const uint32_t row = conv0 + cs * convb_bytes + (panel >> 1) * (convb_bytes >> 1) + (64 + r) * 128;
-                                const uint32_t from = src + kI8RawA + 8192 + panel * 1024 + r * 32;
+                                const uint32_t to = conv0 + cs * convb_bytes + (panel >> 1) * (convb_bytes >> 1) + (64 + r) * 128 +
+                                                    ((((panel & 1) * 4 + hf) ^ (r & 7)) << 4);
+                                const uint32_t from = src + kI8RawA + 8192 + panel * 1024 + r * 32 + hf * 16;
                                 uint4 v[2];
 #pragma unroll
-                                for (int j = 0; j < 2; ++j) v[j] = lds128(from + (hf ^ j) * 16);
+                                for (int j = 0; j < 2; ++j) v[j] = lds128(from ^ (j * 16));
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {
-                                    const int c = (panel & 1) * 4 + (hf ^ j);
                                     uint32_t h[8];
                                     i8_f16(v[j].x, h), i8_f16(v[j].z, h + 2), i8_f16(v[j].y, h + 4), i8_f16(v[j].w, h + 6);
-                                    sts128(row + ((c ^ (r & 7)) << 4), h);
-                                    sts128(row + (((c + 2) ^ (r & 7)) << 4), h + 4);
+                                    sts128(to ^ (j << 4), h);
+                                    sts128(to ^ ((j + 2) << 4), h + 4);
                                 }
                             }
                         }
