@@ -2,12 +2,16 @@
 // any number of rows), and its inverse.
 //
 // Per row: s = amax / 127, q = round-half-away(x / s), both divisions correctly rounded in fp32, as the per-channel
-// weight packer has them.  A division a value would bound the kernel by instructions, so the quotient is taken as x * (1 / s),
-// and an exact comparison decides where that lies close to the middle between two codes (i8_codes).
+// weight packer has them.  A division a value would bound the kernel by instructions, so the quotient is taken as x * (1 / s).
+// For bf16 rows the factor is chosen so that this always gives the same code (i8_factor); for fp32 an exact comparison decides
+// where the quotient lies close to the middle between two codes (i8_codes).
 //
-// Measured: quantising 45056 x 2816 fp32 105 us, 6.0 TB/s read and written; 32764 x 2816 bf16 82 us, gathered from 4097 rows
-// in L2 58 us, 1.96 TB/s, bound by instructions; one row 2.6 us.  The decode to fp32 113 us, 5.6 TB/s, of 32764 x 2816 to bf16
-// 46 us, 6.0 TB/s.
+// Measured: quantising 45056 x 2816 fp32 96 us, 6.6 TB/s read and written; 32768 x 2816 bf16 45 us, 6.1 TB/s, gathered from
+// 4097 rows in L2 34 us; one row 2.5 us.  Bound by HBM, the gathered rows by their stores.  Where rows mod 8 is 1 .. 4 the
+// panels start 16 bytes off a sector and each store meets two: 32764 rows 68 us, gathered 39.
+// What it took, us for 32764 gathered bf16 rows: rows in registers 82; read again from L1 58; held in shared memory 52; one
+// decision a row for values close to a middle, in place of one a value, 39 (a quarter of a warp's steps had such a value).
+// The decode to fp32 113 us, 5.6 TB/s, of 32764 x 2816 to bf16 46 us, 6.0 TB/s.
 #include <algorithm>
 
 #include "int8.cuh"
@@ -42,61 +46,108 @@ __device__ __forceinline__ void i8_values(const uint32_t* raw, float* v) {
     }
 }
 // The larger of m and the magnitudes of eight values, as bits (non-negative floats order like their bit patterns, NaN above
-// Inf); bf16: of both halves of a word at once.
+// Inf); bf16: of both halves of a word at once, a NaN stays, the signs mean nothing.
 template <bool F32>
 __device__ __forceinline__ uint32_t i8_amax(uint32_t m, const uint32_t* raw) {
 #pragma unroll
-    for (int i = 0; i < (F32 ? 8 : 4); ++i) m = F32 ? max(m, raw[i] & 0x7fffffffu) : __vmaxu2(m, raw[i] & 0x7fff7fffu);
+    for (int i = 0; i < (F32 ? 8 : 4); ++i) {
+        if (F32) m = max(m, raw[i] & 0x7fffffffu);
+        else asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(raw[i]));
+    }
     return m;
 }
 template <bool F32>
-__device__ __forceinline__ uint32_t i8_amax_bits(uint32_t m) { return F32 ? m : max(m << 16, m & 0xffff0000u); }
+__device__ __forceinline__ uint32_t i8_amax_bits(uint32_t m) { return F32 ? m : max((m & 0x7fffu) << 16, m & 0x7fff0000u); }
 
-// Eight codes of a row with scale s, inv about 1 / s, or 0 where s is too small for what follows.  Adding 1.5 * 2^23 rounds
-// to an integer and leaves its two's complement in the low byte; what that took off tells how near the quotient is to the
-// middle m between two codes.  There the rounded quotient decides: it is at least m if |v| / s is at least m less half of
-// fp32's step below m, and |v| - m s, a small difference of numbers of 24 and 32 bits, is exact.  (bf16 rows come to such
-// places often, as v / amax is a ratio of two 8-bit numbers.)
-constexpr float kNearTie = 0.49997f;
+constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: added, it rounds to an integer and leaves its two's complement in the low byte
+
+// The factor for a row's codes, about 1 / s, or 0 where s is so small that they are divided.
+// bf16: the codes are x * inv rounded to the nearest integer, so inv has to be such that no product falls on the other side of
+// the middle m between two codes than the rounded quotient.  s comes from a bf16 maximum, one of 128 mantissas: but for
+// two cases no bf16 number lies within 2^-16 of a middle m s, relatively (all of them were gone through).  One is amax / 2, whose
+// m is 63.5: inv is moved by three steps, if need be, to the side that the exact comparison (i8_codes) asks for.  The other is s = a
+// power of two, where x / s meets middles exactly and they go away from zero: inv is the number above 1 / s.
+template <bool F32>
+__device__ __forceinline__ float i8_factor(float amax, float s) {
+    if (!(s >= 1e-27f)) return 0.0f;
+    const float inv = __frcp_rn(s);   // (s is 2.7e36 at most)
+    if (F32) return inv;
+    const float half = 0.5f * amax, want = fmaf(-63.5f, s, half) >= -0x1p-19f * s ? 64.0f : 63.0f;
+    int steps = 0;
+    if ((__float_as_uint(s) & 0x7fffffu) == 0) steps = 1;
+    else if (fmaf(half, inv, kMagic) - kMagic != want) steps = want == 64.0f ? 3 : -3;
+    return __uint_as_float(__float_as_uint(inv) + steps);
+}
+
+// Eight codes of a row with scale s and that factor.  fp32: what the rounding took off tells how near the quotient is to a
+// middle m.  There the rounded quotient decides: it is at least m if |v| / s is at least m less half of fp32's step below m,
+// and |v| - m s, a small difference of numbers of 24 and 32 bits, is exact.
+constexpr float kNearTie = 0.49997f;   // (the roundings of v inv and inv: 2^-23 of 127 at most, 1.6e-5)
 template <bool F32>
 __device__ __forceinline__ uint2 i8_codes(const uint32_t* raw, float s, float inv) {
-    constexpr float kMagic = 12582912.0f;
     float v[8];
     i8_values<F32>(raw, v);
     uint32_t b[8];
-    float worst = 0.0f;
+    float d[8], worst = 0.0f;
+    const uint64_t up = pack_f32x2(inv, inv), minus = pack_f32x2(-kMagic, -kMagic), magic = pack_f32x2(kMagic, kMagic);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float r = fmaf(v[i], inv, kMagic);
-        worst = fmaxf(worst, fabsf(fmaf(v[i], inv, kMagic - r)));
-        b[i] = __float_as_uint(r);
-    }
-    if (worst >= kNearTie) {   // (the roundings of v inv and inv: 2^-23 of 127 at most, 1.6e-5)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float n = __uint_as_float(b[i]) - kMagic, d = fmaf(v[i], inv, -n);
-            if (fabsf(d) >= kNearTie) {
-                const float m = fabsf(n + copysignf(0.5f, d));
-                const float step = m == 0.5f ? 0x1p-26f : __uint_as_float((__float_as_uint(m) & 0x7f800000u) - (24u << 23));
-                const float code = fmaf(-m, s, fabsf(v[i])) >= -step * s ? m + 0.5f : m - 0.5f;
-                b[i] = __float_as_uint(copysignf(code, v[i]) + kMagic);
-            }
+    for (int i = 0; i < 8; i += 2) {   // two values at a time; fp32: the rounded quotients negative, the same low bytes
+        const uint64_t w = pack_f32x2(v[i], v[i + 1]);
+        uint64_t r = F32 ? minus : magic;
+        fma_f32x2(r, w, F32 ? pack_f32x2(-inv, -inv) : up);
+        const float2 rf = unpack_f32x2(r);
+        b[i] = __float_as_uint(rf.x), b[i + 1] = __float_as_uint(rf.y);
+        if (F32) {
+            uint64_t t = add_f32x2(r, magic);
+            fma_f32x2(t, w, up);
+            const float2 df = unpack_f32x2(t);
+            d[i] = fabsf(df.x), d[i + 1] = fabsf(df.y);
+            asm("max.f32 %0, %0, %1, %2;" : "+f"(worst) : "f"(d[i]), "f"(d[i + 1]));
         }
     }
-    if (inv == 0.0f) {
+    uint2 out = make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                           __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+    if (worst >= kNearTie || inv == 0.0f) {
+        // value by value, so that lanes whose values are at different places go through this together
+        uint32_t left = 0xff;
+        if (F32 && inv != 0.0f) {
+            left = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            b[i] = static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(roundf(__fdiv_rn(v[i], s)), -127.0f), 127.0f)));
+            for (int i = 0; i < 8; ++i) left |= d[i] >= kNearTie ? 1u << i : 0u;
+        }
+        while (left) {
+            const int i = __ffs(left) - 1;
+            left &= left - 1;
+            const float lo = i & 2 ? (i & 1 ? v[3] : v[2]) : (i & 1 ? v[1] : v[0]);
+            const float hi = i & 2 ? (i & 1 ? v[7] : v[6]) : (i & 1 ? v[5] : v[4]);
+            const float x = i & 4 ? hi : lo;
+            float code;
+            if (F32 && inv != 0.0f) {
+                const float n = fmaf(x, inv, kMagic) - kMagic;
+                const float m = fabsf(n + copysignf(0.5f, fmaf(x, inv, -n)));
+                const float step = m == 0.5f ? 0x1p-26f : __uint_as_float((__float_as_uint(m) & 0x7f800000u) - (24u << 23));
+                code = copysignf(fmaf(-m, s, fabsf(x)) >= -step * s ? m + 0.5f : m - 0.5f, x);
+            } else {
+                code = fminf(fmaxf(roundf(__fdiv_rn(x, s)), -127.0f), 127.0f);
+            }
+            const uint32_t byte = (__float_as_uint(code + kMagic) & 0xffu) << (8 * (i & 3)), keep = ~(0xffu << (8 * (i & 3)));
+            if (i & 4) out.y = (out.y & keep) | byte;
+            else out.x = (out.x & keep) | byte;
+        }
     }
-    return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
-                      __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+    return out;
 }
 
 constexpr int kQRow = 256;   // columns that a warp covers at a time, eight a lane
 
-// `split` warps a row, 8 / split consecutive rows a CTA, so that a panel's codes of a CTA's rows lie side by side.  ITERS: a
-// lane holds its part of the row, eight values each time, between the search for the largest and the coding; 0: it reads
-// the row again.
+__device__ __forceinline__ void i8_copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// `split` warps a row, 8 / split consecutive rows a CTA, so that a panel's codes of a CTA's rows lie side by side.  Between
+// the search for the largest and the coding a lane holds its part of the row, eight values each time: ITERS times in
+// registers (fp32), kHeld (bf16): in shared memory, where each lane reads what it copied itself; 0: it reads the row again.
+constexpr int kHeld = -1, kMaxIters = 12;
 template <bool F32, int ITERS>
 __global__ void __launch_bounds__(256, F32 ? 2 : 4) int8_quantize_kernel(const char* __restrict__ x, int64_t x_rows,
                                                             const int32_t* __restrict__ src_rows, int src_div, int64_t n_mat,
@@ -104,6 +155,7 @@ __global__ void __launch_bounds__(256, F32 ? 2 : 4) int8_quantize_kernel(const c
                                                             uint8_t* __restrict__ dst) {
     constexpr int kElem = F32 ? 4 : 2, kRaw = F32 ? 8 : 4;
     __shared__ uint32_t largest[8];
+    extern __shared__ uint4 held[];
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp & (split - 1), lead = warp - sub;
     const int per = 8 / split, step = split * kQRow, c0 = sub * kQRow + lane * 8;
@@ -123,7 +175,18 @@ __global__ void __launch_bounds__(256, F32 ? 2 : 4) int8_quantize_kernel(const c
             const char* src = x + (sr * cols + c0) * kElem;
             uint32_t raw[ITERS > 0 ? ITERS : 1][kRaw];
             uint32_t amax = 0;
-            if constexpr (ITERS > 0) {
+            const int times = (cols - c0 + step - 1) / step;   // that this lane has eight values
+            uint4* mine = held + warp * ((cols + step - 1) / step) * 32 + lane;
+            if constexpr (ITERS == kHeld) {
+                if (has) {
+                    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+                    const char* from = src;
+                    for (int u = 0; u < times; ++u, from += step * kElem) i8_copy16(to + u * 512, from);
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 4
+                    for (int u = 0; u < times; ++u) amax = i8_amax<F32>(amax, reinterpret_cast<const uint32_t*>(mine + 32 * u));
+                }
+            } else if constexpr (ITERS > 0) {
 #pragma unroll
                 for (int u = 0; u < ITERS; ++u) {
 #pragma unroll
@@ -155,11 +218,22 @@ __global__ void __launch_bounds__(256, F32 ? 2 : 4) int8_quantize_kernel(const c
             if (!live) continue;
             const bool bad = amax >= 0x7f800000u;
             const float s = __fdiv_rn(__uint_as_float(amax), 127.0f);
-            const float inv = s >= 1e-27f ? __frcp_rn(s) : 0.0f;   // (s is 2.7e36 at most)
+            const float inv = i8_factor<F32>(__uint_as_float(amax), s);
             const bool code = has && !bad && s > 0.0f;
             uint8_t* o = out + i8_scale_bytes(rows) + (static_cast<int64_t>(c0 >> 5) * rows + r) * 32 + (c0 & 31);
             const int64_t o_step = static_cast<int64_t>(step >> 5) * rows * 32;
-            if constexpr (ITERS > 0) {
+            if constexpr (ITERS == kHeld) {
+                if (code) {
+#pragma unroll 2
+                    for (int u = 0; u < times; ++u, o += o_step) {
+                        const uint4 w = mine[32 * u];
+                        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+                        *reinterpret_cast<uint2*>(o) = i8_codes<F32>(v, s, inv);
+                    }
+                } else {
+                    for (int u = 0; u < times; ++u, o += o_step) *reinterpret_cast<uint2*>(o) = make_uint2(0, 0);
+                }
+            } else if constexpr (ITERS > 0) {
 #pragma unroll
                 for (int u = 0; u < ITERS; ++u)
                     if (c0 + u * step < cols)
@@ -227,16 +301,21 @@ namespace {
 
 using QuantizeKernel = void (*)(const char*, int64_t, const int32_t*, int, int64_t, int64_t, int, int, bool, uint8_t*);
 
-// bf16 rows are read again (from L1): held in registers, the unrolled coding is too much code for the instruction caches
-// (32764 gathered rows of 2816 82 us, read again 57; fp32 rows are bound by memory either way).
+// (bf16 rows longer than shared memory has room for are read again)
 QuantizeKernel quantize_kernel(bool f32, int iters) {
-    if (!f32) return int8_quantize_kernel<false, 0>;
+    if (!f32) return iters <= kMaxIters ? int8_quantize_kernel<false, kHeld> : int8_quantize_kernel<false, 0>;
     if (iters <= 3) return int8_quantize_kernel<true, 3>;
     if (iters <= 6) return int8_quantize_kernel<true, 6>;
-    return iters <= 12 ? int8_quantize_kernel<true, 12> : int8_quantize_kernel<true, 0>;
+    return iters <= kMaxIters ? int8_quantize_kernel<true, kMaxIters> : int8_quantize_kernel<true, 0>;
 }
 
 }  // namespace
+
+cudaError_t configure_int8_codec() {
+    const void* fn = reinterpret_cast<const void*>(int8_quantize_kernel<false, kHeld>);
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxIters * 8 * 512);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+}
 
 cudaError_t launch_int8_quantize(const void* x, int xt, int64_t x_rows, const int32_t* src_rows, int src_div, int64_t n_mat,
                                  int64_t rows, int64_t cols, void* dst, int num_sms, cudaStream_t s) {
@@ -244,11 +323,12 @@ cudaError_t launch_int8_quantize(const void* x, int xt, int64_t x_rows, const in
     // and a warp more than 256 columns.
     int split = 1;
     auto iters = [&] { return static_cast<int>((cols + split * kQRow - 1) / (split * kQRow)); };
-    while (split < 8 && (iters() > 12 || (iters() > 1 && n_mat * rows * split < 4ll * num_sms))) split *= 2;
+    while (split < 8 && (iters() > kMaxIters || (iters() > 1 && n_mat * rows * split < 4ll * num_sms))) split *= 2;
     const int64_t groups = (rows * split + 7) / 8, ctas = 8ll * num_sms;
     const int64_t gx = std::min<int64_t>(groups, ctas);
     const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(std::min<int64_t>(n_mat, std::max<int64_t>(1, ctas / gx))));
-    return launch_pdl(quantize_kernel(xt == MOE_F32, iters()), grid, dim3(256), 0, s,
+    const size_t held = xt == MOE_F32 || iters() > kMaxIters ? 0 : 8 * 512 * static_cast<size_t>(iters());
+    return launch_pdl(quantize_kernel(xt == MOE_F32, iters()), grid, dim3(256), held, s,
                       static_cast<const char*>(x), x_rows, src_rows, src_div, n_mat, rows, static_cast<int>(cols), split,
                       (reinterpret_cast<uintptr_t>(x) & 31u) == 0, static_cast<uint8_t*>(dst));
 }

@@ -557,8 +557,10 @@ I8Kernel i8_kernel(bool multi, int nt, int act, bool f32) {
 
 }  // namespace
 
+cudaError_t configure_int8_codec();
+
 cudaError_t configure_int8_kernels() {
-    cudaError_t e = cudaSuccess;
+    cudaError_t e = configure_int8_codec();
     for (int act : {MOE_ACT_SWIGLU, MOE_ACT_RELU2, MOE_ACT_NONE})
         for (bool f32 : {false, true})
             for (int kind = 0; kind < 3; ++kind) {

@@ -57,6 +57,28 @@ def test_codec_bit_for_bit(rows, cols, dtype):
         assert back.dtype == out and np.array_equal(_host(back), _host(torch.from_numpy(v).to(out)), equal_nan=True)
 
 
+@pytest.mark.parametrize("exponent", [-130, -90, -83, -20, 0, 100, 127])
+def test_codec_of_every_bf16_maximum(exponent):
+    """A row for each mantissa of its maximum, with all bf16 numbers of both signs in the eleven octaves below it."""
+    top = (min(max(exponent + 127, 0), 254) << 7) + np.arange(128, dtype=np.int64)
+    bits = np.maximum(top[:, None] - np.arange(11 * 128), 0)
+    bits = np.concatenate([bits, bits | 0x8000], 1)
+    g = np.random.default_rng(exponent + 200)
+    x = torch.from_numpy(g.permuted(bits, axis=1).astype(np.uint16).view(np.int16)).cuda().view(torch.bfloat16)
+    want, known = ref.pack(*ref.quantize(_host(x)))
+    assert np.array_equal(native.quantize_int8(x)[0].cpu().numpy()[known], want[known])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_codec_finds_what_is_not_finite_wherever_it_is(dtype):
+    x = torch.randn(96, 544, device="cuda", generator=torch.Generator("cuda").manual_seed(2)).to(dtype)
+    for i, v in enumerate([float("nan"), float("inf"), -float("inf")] * 32):
+        x[i, 17 * i % 544 if i % 2 else 543 - i] = v
+    x[::6] = -x[::6]        # NaNs of the other sign
+    q = native.quantize_int8(x)[0].cpu().numpy()
+    assert np.isnan(q[: 4 * 96].view("<f4")).all() and (q[4 * 96 :] == 0).all()
+
+
 def test_codec_of_a_stack_and_of_gathered_rows():
     x = _codec_rows(30, 96, 3, torch.float32).view(6, 5, 96)
     q = native.quantize_int8(x)
