@@ -7,10 +7,10 @@
 // where the quotient lies close to the middle between two codes (i8_codes).
 //
 // Measured: quantising 45056 x 2816 fp32 96 us, 6.6 TB/s read and written; 32768 x 2816 bf16 45 us, 6.1 TB/s, gathered from
-// 4097 rows in L2 34 us; one row 2.5 us.  Bound by HBM, the gathered rows by their stores.  Where rows mod 8 is 1 .. 4 the
-// panels start 16 bytes off a sector and each store meets two: 32764 rows 68 us, gathered 39.
+// 4097 rows in L2 34 us, 32764 rows 44 and 38; one row 2.5 us.  Bound by HBM, the gathered rows by their stores.
 // What it took, us for 32764 gathered bf16 rows: rows in registers 82; read again from L1 58; held in shared memory 52; one
-// decision a row for values close to a middle, in place of one a value, 39 (a quarter of a warp's steps had such a value).
+// decision a row for values close to a middle, in place of one a value, 39 (a quarter of a warp's steps had such a value).  Not
+// gathered 82, 69 by then, and 44 by panels.
 // The decode to fp32 113 us, 5.6 TB/s, of 32764 x 2816 to bf16 46 us, 6.0 TB/s.
 #include <algorithm>
 
@@ -146,8 +146,10 @@ __device__ __forceinline__ void i8_copy16(uint32_t dst, const void* src) {
 
 // `split` warps a row, 8 / split consecutive rows a CTA, so that a panel's codes of a CTA's rows lie side by side.  Between
 // the search for the largest and the coding a lane holds its part of the row, eight values each time: ITERS times in
-// registers (fp32), kHeld (bf16): in shared memory, where each lane reads what it copied itself; 0: it reads the row again.
-constexpr int kHeld = -1, kMaxIters = 12;
+// registers (fp32), or in shared memory (bf16); 0: it reads the row again.  kHeldPanels: the codes go through shared memory too,
+// and 16 bytes a lane to their panels.
+constexpr int kHeld = -1, kHeldPanels = -2, kMaxIters = 12;
+__host__ __device__ constexpr int held_row(int iters) { return iters * 512 + 32; }   // (32: the rows of a panel lie in different banks)
 template <bool F32, int ITERS>
 __global__ void __launch_bounds__(256, F32 ? 2 : 4) int8_quantize_kernel(const char* __restrict__ x, int64_t x_rows,
                                                             const int32_t* __restrict__ src_rows, int src_div, int64_t n_mat,
@@ -155,10 +157,10 @@ __global__ void __launch_bounds__(256, F32 ? 2 : 4) int8_quantize_kernel(const c
                                                             uint8_t* __restrict__ dst) {
     constexpr int kElem = F32 ? 4 : 2, kRaw = F32 ? 8 : 4;
     __shared__ uint32_t largest[8];
-    extern __shared__ uint4 held[];
+    extern __shared__ __align__(16) unsigned char held[];
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp & (split - 1), lead = warp - sub;
-    const int per = 8 / split, step = split * kQRow, c0 = sub * kQRow + lane * 8;
+    const int per = 8 / split, split_log = __ffs(split) - 1, per_log = 3 - split_log, step = split * kQRow, c0 = sub * kQRow + lane * 8;
     const int64_t groups = (rows + per - 1) / per;
     for (int64_t m = blockIdx.y; m < n_mat; m += gridDim.y) {
         uint8_t* out = dst + m * i8_bytes(rows, cols);
@@ -176,15 +178,16 @@ __global__ void __launch_bounds__(256, F32 ? 2 : 4) int8_quantize_kernel(const c
             uint32_t raw[ITERS > 0 ? ITERS : 1][kRaw];
             uint32_t amax = 0;
             const int times = (cols - c0 + step - 1) / step;   // that this lane has eight values
-            uint4* mine = held + warp * ((cols + step - 1) / step) * 32 + lane;
-            if constexpr (ITERS == kHeld) {
+            const int iters = (cols + step - 1) / step;
+            unsigned char* mine = held + warp * held_row(iters);
+            if constexpr (ITERS < 0) {
                 if (has) {
-                    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+                    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(mine)) + lane * 16;
                     const char* from = src;
                     for (int u = 0; u < times; ++u, from += step * kElem) i8_copy16(to + u * 512, from);
                     asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 4
-                    for (int u = 0; u < times; ++u) amax = i8_amax<F32>(amax, reinterpret_cast<const uint32_t*>(mine + 32 * u));
+                    for (int u = 0; u < times; ++u) amax = i8_amax<F32>(amax, reinterpret_cast<const uint32_t*>(mine + u * 512 + lane * 16));
                 }
             } else if constexpr (ITERS > 0) {
 #pragma unroll
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(256, F32 ? 2 : 4) int8_quantize_kernel(const c
                 for (int i = 0; i < split; ++i) amax = max(amax, largest[lead + i]);
                 __syncthreads();
             }
-            if (!live) continue;
+            if (ITERS != kHeldPanels && !live) continue;
             const bool bad = amax >= 0x7f800000u;
             const float s = __fdiv_rn(__uint_as_float(amax), 127.0f);
             const float inv = i8_factor<F32>(__uint_as_float(amax), s);
@@ -223,15 +226,24 @@ __global__ void __launch_bounds__(256, F32 ? 2 : 4) int8_quantize_kernel(const c
             uint8_t* o = out + i8_scale_bytes(rows) + (static_cast<int64_t>(c0 >> 5) * rows + r) * 32 + (c0 & 31);
             const int64_t o_step = static_cast<int64_t>(step >> 5) * rows * 32;
             if constexpr (ITERS == kHeld) {
-                if (code) {
 #pragma unroll 2
-                    for (int u = 0; u < times; ++u, o += o_step) {
-                        const uint4 w = mine[32 * u];
+                for (int u = 0; u < times; ++u, o += o_step) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(mine + u * 512 + lane * 16);
+                    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+                    *reinterpret_cast<uint2*>(o) = code ? i8_codes<F32>(v, s, inv) : make_uint2(0, 0);
+                }
+            } else if constexpr (ITERS == kHeldPanels) {
+                // the codes over the values, which all lanes have read by then
+#pragma unroll 2
+                for (int u = 0; u < iters; ++u) {
+                    uint2 c = make_uint2(0, 0);
+                    if (code && u < times) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(mine + u * 512 + lane * 16);
                         const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-                        *reinterpret_cast<uint2*>(o) = i8_codes<F32>(v, s, inv);
+                        c = i8_codes<F32>(v, s, inv);
                     }
-                } else {
-                    for (int u = 0; u < times; ++u, o += o_step) *reinterpret_cast<uint2*>(o) = make_uint2(0, 0);
+                    __syncwarp();
+                    *reinterpret_cast<uint2*>(mine + u * 256 + lane * 8) = c;
                 }
             } else if constexpr (ITERS > 0) {
 #pragma unroll
@@ -244,7 +256,21 @@ __global__ void __launch_bounds__(256, F32 ? 2 : 4) int8_quantize_kernel(const c
                     *reinterpret_cast<uint2*>(o) = code ? i8_codes<F32>(raw[0], s, inv) : make_uint2(0, 0);
                 }
             }
-            if (sub == 0 && lane == 0) reinterpret_cast<float*>(out)[r] = bad ? __uint_as_float(0x7fffffffu) : s;
+            if (live && sub == 0 && lane == 0) reinterpret_cast<float*>(out)[r] = bad ? __uint_as_float(0x7fffffffu) : s;
+            if constexpr (ITERS == kHeldPanels) {   // a panel's codes of the CTA's rows, 16 bytes a lane
+                const int64_t r0 = grp * per;
+                const int pieces = 2 * static_cast<int>(min(static_cast<int64_t>(per), rows - r0));
+                uint8_t* to = out + i8_scale_bytes(rows) + r0 * 32;
+                __syncthreads();
+                for (int i = threadIdx.x; i < (cols >> 5) * 2 * per; i += 256) {
+                    const int panel = i >> (per_log + 1), j = i & (2 * per - 1), set = panel >> 3;
+                    if (j >= pieces) continue;
+                    const unsigned char* from = held + ((j >> 1) * split + (set & (split - 1))) * held_row(iters);
+                    from += (set >> split_log) * 256 + (panel & 7) * 32 + (j & 1) * 16;
+                    *reinterpret_cast<uint4*>(to + static_cast<int64_t>(panel) * rows * 32 + j * 16) = *reinterpret_cast<const uint4*>(from);
+                }
+                __syncthreads();
+            }
         }
     }
 }
@@ -301,9 +327,12 @@ namespace {
 
 using QuantizeKernel = void (*)(const char*, int64_t, const int32_t*, int, int64_t, int64_t, int, int, bool, uint8_t*);
 
-// (bf16 rows longer than shared memory has room for are read again)
-QuantizeKernel quantize_kernel(bool f32, int iters) {
-    if (!f32) return iters <= kMaxIters ? int8_quantize_kernel<false, kHeld> : int8_quantize_kernel<false, 0>;
+// bf16 by panels: where these start 16 bytes off a sector each store of a lane's codes would meet two (32764 rows of 2816: 68 us,
+// by panels 44); where they do not, the barriers of the panels cost more (32768 rows 43 against 45, gathered 38 against 34,
+// 100000 rows of 704 52 against 46).  Rows longer than shared memory has room for are read again.
+QuantizeKernel quantize_kernel(bool f32, int iters, bool panels) {
+    if (!f32 && iters > kMaxIters) return int8_quantize_kernel<false, 0>;
+    if (!f32) return panels ? int8_quantize_kernel<false, kHeldPanels> : int8_quantize_kernel<false, kHeld>;
     if (iters <= 3) return int8_quantize_kernel<true, 3>;
     if (iters <= 6) return int8_quantize_kernel<true, 6>;
     return iters <= kMaxIters ? int8_quantize_kernel<true, kMaxIters> : int8_quantize_kernel<true, 0>;
@@ -312,9 +341,13 @@ QuantizeKernel quantize_kernel(bool f32, int iters) {
 }  // namespace
 
 cudaError_t configure_int8_codec() {
-    const void* fn = reinterpret_cast<const void*>(int8_quantize_kernel<false, kHeld>);
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxIters * 8 * 512);
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    cudaError_t e = cudaSuccess;
+    for (bool panels : {false, true}) {
+        const void* fn = reinterpret_cast<const void*>(quantize_kernel(false, 1, panels));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * held_row(kMaxIters));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    }
+    return e;
 }
 
 cudaError_t launch_int8_quantize(const void* x, int xt, int64_t x_rows, const int32_t* src_rows, int src_div, int64_t n_mat,
@@ -324,11 +357,14 @@ cudaError_t launch_int8_quantize(const void* x, int xt, int64_t x_rows, const in
     int split = 1;
     auto iters = [&] { return static_cast<int>((cols + split * kQRow - 1) / (split * kQRow)); };
     while (split < 8 && (iters() > kMaxIters || (iters() > 1 && n_mat * rows * split < 4ll * num_sms))) split *= 2;
-    const int64_t groups = (rows * split + 7) / 8, ctas = 8ll * num_sms;
+    const bool in_shared = xt != MOE_F32 && iters() <= kMaxIters, panels = in_shared && i8_scale_bytes(rows) % 32 != 0;
+    const int64_t groups = (rows * split + 7) / 8;
+    // (by panels: a CTA for about kMaxIters steps, so that its barriers meet other CTAs' work: 32764 rows 47 -> 44 us)
+    const int64_t ctas = std::max<int64_t>(8ll * num_sms, panels ? groups / (kMaxIters / iters()) : 0);
     const int64_t gx = std::min<int64_t>(groups, ctas);
     const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(std::min<int64_t>(n_mat, std::max<int64_t>(1, ctas / gx))));
-    const size_t held = xt == MOE_F32 || iters() > kMaxIters ? 0 : 8 * 512 * static_cast<size_t>(iters());
-    return launch_pdl(quantize_kernel(xt == MOE_F32, iters()), grid, dim3(256), held, s,
+    const size_t held = in_shared ? 8 * static_cast<size_t>(held_row(iters())) : 0;
+    return launch_pdl(quantize_kernel(xt == MOE_F32, iters(), panels), grid, dim3(256), held, s,
                       static_cast<const char*>(x), x_rows, src_rows, src_div, n_mat, rows, static_cast<int>(cols), split,
                       (reinterpret_cast<uintptr_t>(x) & 31u) == 0, static_cast<uint8_t*>(dst));
 }
