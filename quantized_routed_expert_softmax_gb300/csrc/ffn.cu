@@ -27,12 +27,14 @@
 // now 0.0024; one rounding is 0.0017), for 8191 rows of 2816 x 5632 it costs 30 us of 430 in the forward pass.  h and dz are
 // bf16 because the next product's MMA takes them so.
 //
-// Many rows an expert are bound by the MMAs: 8191 rows of 2816 x 5632 forward 398 us, 1,955 TFLOP/s (a library product of
-// 8192^3 does 1,932), with z saved 431, backward 890, 1,750 TFLOP/s.  Few rows are bound by the weights' bytes: 4096 rows of 128
-// experts, 2816 and 704, forward 255 us, 6.1 TB/s; their gradients by writing as many bytes: 1.0 GB of dWgu in 213 us.
+// Many rows an expert are bound by the MMAs: 8191 rows of 2816 x 5632 forward 403 us, 1,930 TFLOP/s (a library product of
+// 8192^3 does 1,932), with z saved 435, backward 890, 1,750 TFLOP/s.  Few rows are bound by the weights' bytes: 4096 rows of 128
+// experts, 2816 and 704, forward 255 us, 6.1 TB/s; their gradients by writing as many bytes: 1.0 GB of dWgu in 198 us, 5.1 TB/s
+// (a library's fill of a gigabyte writes 4.1).  32768 rows: forward 334 us, z saved 371, backward 775.
 // What it took, forward us of the dense block: barriers with release and acquire over the cluster 1288, without 406 (see
 // pair.cuh), blocks of weight tiles 398 (z saved 466 -> 431).  Backward: 2926, 932; z read a step ahead 890 (dz 223 -> 174);
-// two launches in place of four 967 -> 889 (fp32 z between).
+// two launches in place of four 967 -> 889 (fp32 z between).  A sixth stage of operands: 32768 rows 350 -> 334 forward.  Addresses
+// of the result's rows by steps: backward of 4096 rows 593 -> 567, 8192 601 -> 577, 16384 638 -> 628, but 32768 769 -> 777.
 // Tried and dropped: streaming stores for z and the weights' gradients (no change); fences over the cluster behind the
 // cleared rows (dWgu of 32768 rows of 128 experts 259 -> 370 us).
 #include <algorithm>
@@ -395,15 +397,17 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
             const int am = walk.m0() + static_cast<int>(rank) * 128;
             // whole rows from shared memory to memory, 16 bytes a lane
             auto copy = [&](uint32_t from, int n_rows, void* to, int64_t first, int left, int64_t ld, int col, int cols, int row_bytes, int elem) {
-                const int per = row_bytes / 16, each = 16 / elem;
+                const int per = row_bytes / 16, each = 16 / elem, step = 128 / per, r = t128 / per, p = t128 % per;
+                const uint32_t place = elem == 4 ? p ^ (2 * ((r >> 1) & 3)) : p ^ (r & 7), at = from + r * row_bytes + (place << 4);
+                char* d = static_cast<char*>(to) + ((first + r) * ld + col + p * each) * elem;
+                const int rows = p * each < cols ? left - r : 0;
 #pragma unroll
-                for (int j = 0; j < n_rows * per / 128; ++j) {
-                    const int i = j * 128 + t128, r = i / per, p = i % per;
-                    const int place = elem == 4 ? p ^ (2 * ((r >> 1) & 3)) : p ^ (r & 7);
-                    if (r >= left || p * each >= cols) continue;
-                    uint4 v;
-                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from + r * row_bytes + (place << 4)));
-                    *reinterpret_cast<uint4*>(static_cast<char*>(to) + ((first + r) * ld + col + p * each) * elem) = v;
+                for (int j = 0; j < n_rows / step; ++j, d += step * ld * elem) {
+                    if (j * step >= rows) continue;
+                    uint4 v;   // (fp32 rows of 512 bytes: every other of a lane's has bit 2 of its place turned)
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "r"((at ^ (elem == 4 && step == 4 && (j & 1) ? 64u : 0u)) + j * step * row_bytes));
+                    *reinterpret_cast<uint4*>(d) = v;
                 }
             };
             auto tile = [&](auto tag, auto of_grad) {   // the item's epilogue
