@@ -117,6 +117,9 @@ template <int ACT, bool F32, bool MULTI, int NT>
 __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_constant__ I8Args g) {
     constexpr bool kGated = ACT == MOE_ACT_SWIGLU;
     constexpr int kI8ConvStages = i8_conv_stages(NT);
+    // The two halves of a converted stage, 64 columns each, are handed over one by one where each group of converting warps has
+    // one stage alone, so that it converts a half while the MMAs of the other run.
+    constexpr int kParts = kI8ConvStages > 2 ? 1 : 2;
     constexpr uint32_t kI8ACol = 2 * NT;
     static_assert(!MULTI || NT == 128, "the epilogue's registers hold two times 32 rows");
     static_assert(kI8ConvStages % 2 == 0, "the two groups of converting warps have stages of their own");
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
     const uint32_t raw_bytes = i8_raw(g.nt), raw_stages = i8_raw_stages(g.nt), convb_bytes = i8_conv_b(g.nt);
     unsigned char* raw = convb + kI8ConvStages * convb_bytes;
     unsigned char* staging = raw + raw_stages * raw_bytes;
-    __shared__ uint64_t raw_full[kI8MaxRawStages], raw_empty[kI8MaxRawStages], ready[kI8ConvStages], empty[kI8ConvStages];
+    __shared__ uint64_t raw_full[kI8MaxRawStages], raw_empty[kI8MaxRawStages], ready[kI8ConvStages * kParts], empty[kI8ConvStages * kParts];
     __shared__ uint64_t acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t issued, tmem_base;
     __shared__ volatile tc::Waits waits;
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
             tc::mbar_init(&raw_full[s], 1);
             tc::mbar_init(&raw_empty[s], 8);   // four warps for A, four for B
         }
-        for (int s = 0; s < kI8ConvStages; ++s) {
+        for (int s = 0; s < kI8ConvStages * kParts; ++s) {
             tc::mbar_init(&ready[s], 16);      // the same of both CTAs
             tc::mbar_init(&empty[s], 1);
         }
@@ -368,26 +371,31 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                         ok = false;
                         break;
                     }
-                    if (!__any_sync(0xffffffffu, seen) && !tc::mbar_wait_warp(&ready[st], use, &waits)) {
-                        ok = false;
-                        break;
-                    }
                     const uint32_t st1 = st + 1 == kI8ConvStages ? 0 : st + 1, use1 = use + (st1 == 0);
                     const bool last = in_seg + 1 == kI8SegSteps || ks + 1 == ksteps;
                     const bool two = g.K - ks * kI8StepK > kI8StepK / 2;
-                    seen = false;
-                    tc::fence_after();
-                    if (leader) {
-                        const uint64_t db = db0 + st * (convb_bytes >> 4);
-                        const uint32_t ta = tmem + kI8ACol + 64 * st;
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)   // (64 columns of B's rows, then the next 64)
-                            if (kk < 4 || two)
-                                i8_mma(tmem + buf * NT, ta + 8 * kk, db + (kk >> 2) * (convb_bytes >> 5) + 2 * (kk & 3), idesc, in_seg > 0 || kk > 0);
-                        seen = tc::mbar_test_wait(&ready[st1], use1 & 1u);   // beside the MMAs
-                        tc::pair_commit(&empty[st]);
-                        if (last) tc::pair_commit(&acc_full[buf]);
+                    for (int part = 0; part < kParts; ++part) {
+                        if (!__any_sync(0xffffffffu, seen) && !tc::mbar_wait_warp(&ready[st * kParts + part], use, &waits)) {
+                            ok = false;
+                            break;
+                        }
+                        seen = false;
+                        tc::fence_after();
+                        if (leader) {
+                            const bool end = part + 1 == kParts;
+                            const uint64_t db = db0 + st * (convb_bytes >> 4);
+                            const uint32_t ta = tmem + kI8ACol + 64 * st;
+#pragma unroll
+                            for (int kk = part * 8 / kParts; kk < (part + 1) * 8 / kParts; ++kk)   // (64 columns of B's rows, then the next 64)
+                                if (kk < 4 || two)
+                                    i8_mma(tmem + buf * NT, ta + 8 * kk, db + (kk >> 2) * (convb_bytes >> 5) + 2 * (kk & 3), idesc, in_seg > 0 || kk > 0);
+                            seen = tc::mbar_test_wait(&ready[end ? st1 * kParts : st * kParts + part + 1], (end ? use1 : use) & 1u);   // beside the MMAs
+                            tc::pair_commit(&empty[st * kParts + part]);
+                            if (end && last) tc::pair_commit(&acc_full[buf]);
+                        }
                     }
+                    if (!ok) break;
                     if (last) ++n_acc;
                     st = st1;
                     use = use1;
@@ -410,8 +418,14 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
             // that 8 lanes meet all banks, here and in the swizzled stores.
             const int brow = t128 & 63, bset = t128 >> 6, bhalf = (brow >> 2) & 1;
             // (a piece's place in its row of 128 bytes is xored with the row; the rest of the address leaves those bits alone)
-            const uint32_t bto = bset * (convb_bytes >> 1) + brow * 128 + ((bhalf ^ (brow & 7)) << 4);
+            const uint32_t bto = brow * 128 + ((bhalf ^ (brow & 7)) << 4);
             const uint32_t bfrom = kI8RawA + brow * 32 + bhalf * 16;
+            auto store = [&](uint32_t to, int j, uint4 v) {   // half j of a panel: words 0 2 of 16 bytes to their piece, 1 3 to the piece two on
+                uint32_t h[8];
+                i8_f16(v.x, h), i8_f16(v.z, h + 2), i8_f16(v.y, h + 4), i8_f16(v.w, h + 6);
+                sts128(to ^ (j << 4), h);
+                sts128(to ^ ((j + 2) << 4), h + 4);
+            };
             uint32_t rs = first, cs = first, ruse = 0, cuse = 0;
             int ks = static_cast<int>(first);   // of the step in its item
             bool ok = true;
@@ -436,70 +450,78 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                             v[2] = lds64(src + p * 2048 + ahi), v[3] = lds64(src + p * 2048 + ahi + 256);
                         };
                         read(0, r[0]);
-                        if (cuse > 0 && !tc::mbar_wait_warp(&empty[cs], cuse - 1, &waits)) {
-                            ok = false;
-                            break;
-                        }
-                        tc::fence_after();
                         const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + kI8ACol + 64 * cs;
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) {
-                            if (p == 2 && !two) break;
-                            if (p < 3) read(p + 1, r[(p + 1) & 1]);
-                            const uint2* v = r[p & 1];
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                uint32_t h[8];
-                                i8_f16(v[2 * u].x, h), i8_f16(v[2 * u + 1].x, h + 2), i8_f16(v[2 * u].y, h + 4), i8_f16(v[2 * u + 1].y, h + 6);
-                                tmem_st_frag16(t + (static_cast<uint32_t>(16 * u) << 16) + 16 * p, h);
+                        for (int part = 0; part < kParts; ++part) {
+                            if (cuse > 0 && !tc::mbar_wait_warp(&empty[cs * kParts + part], cuse - 1, &waits)) {
+                                ok = false;
+                                break;
                             }
-                        }
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&raw_empty[rs]);
-                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                        tc::fence_before();
-                    } else {
-                        if (cuse > 0 && !tc::mbar_wait_warp(&empty[cs], cuse - 1, &waits)) {
-                            ok = false;
-                            break;
-                        }
-                        if (brow < half && (two || bset == 0)) {
-                            const uint32_t to = conv0 + cs * convb_bytes + bto, from = src + bfrom + bset * 2 * pstride;
-                            uint4 v[4];
+                            tc::fence_after();
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) v[j] = lds128((from + (j >> 1) * pstride) ^ ((j & 1) * 16));
+                            for (int p = part * 4 / kParts; p < (part + 1) * 4 / kParts; ++p) {
+                                if (p == 2 && !two) break;
+                                if (p < 3) read(p + 1, r[(p + 1) & 1]);
+                                const uint2* v = r[p & 1];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {   // (words 0 2 of 16 bytes to their piece, 1 3 to the piece two on)
-                                uint32_t h[8];
-                                i8_f16(v[j].x, h), i8_f16(v[j].z, h + 2), i8_f16(v[j].y, h + 4), i8_f16(v[j].w, h + 6);
-                                sts128(to ^ (((j >> 1) * 4 + (j & 1)) << 4), h);
-                                sts128(to ^ (((j >> 1) * 4 + (j & 1) + 2) << 4), h + 4);
-                            }
-                        }
-                        if (NT > 128 && half > 64) {   // rows 64 .. 95, a panel a lane
-                            const int r = t128 & 31, panel = t128 >> 5, hf = (r >> 2) & 1;
-                            if (64 + r < half && (two || panel < 2)) {
-                                const uint32_t to = conv0 + cs * convb_bytes + (panel >> 1) * (convb_bytes >> 1) + (64 + r) * 128 +
-                                                    ((((panel & 1) * 4 + hf) ^ (r & 7)) << 4);
-                                const uint32_t from = src + kI8RawA + 8192 + panel * 1024 + r * 32 + hf * 16;
-                                uint4 v[2];
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) v[j] = lds128(from ^ (j * 16));
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) {
+                                for (int u = 0; u < 2; ++u) {
                                     uint32_t h[8];
-                                    i8_f16(v[j].x, h), i8_f16(v[j].z, h + 2), i8_f16(v[j].y, h + 4), i8_f16(v[j].w, h + 6);
-                                    sts128(to ^ (j << 4), h);
-                                    sts128(to ^ ((j + 2) << 4), h + 4);
+                                    i8_f16(v[2 * u].x, h), i8_f16(v[2 * u + 1].x, h + 2), i8_f16(v[2 * u].y, h + 4), i8_f16(v[2 * u + 1].y, h + 6);
+                                    tmem_st_frag16(t + (static_cast<uint32_t>(16 * u) << 16) + 16 * p, h);
                                 }
                             }
+                            __syncwarp();
+                            if (part + 1 == kParts && lane == 0) tc::mbar_arrive(&raw_empty[rs]);
+                            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                            tc::fence_before();
+                            if (part + 1 < kParts) {
+                                __syncwarp();
+                                if (lane == 0) tc::mbar_arrive_cluster(ready0 + (cs * kParts + part) * 8);
+                            }
                         }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    } else {
+#pragma unroll
+                        for (int part = 0; part < kParts; ++part) {
+                            if (cuse > 0 && !tc::mbar_wait_warp(&empty[cs * kParts + part], cuse - 1, &waits)) {
+                                ok = false;
+                                break;
+                            }
+                            if (kParts == 1 && brow < half && (two || bset == 0)) {   // two panels a lane
+                                const uint32_t to = conv0 + cs * convb_bytes + bset * (convb_bytes >> 1) + bto, from = src + bfrom + bset * 2 * pstride;
+                                uint4 v[4];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) v[j] = lds128((from + (j >> 1) * pstride) ^ ((j & 1) * 16));
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) store(to ^ ((j >> 1) << 6), j & 1, v[j]);
+                            }
+                            if (kParts == 2 && (part == 0 || two)) {
+                                const uint32_t ph = conv0 + cs * convb_bytes + part * (convb_bytes >> 1);
+                                if (brow < half) {   // a panel a lane
+                                    const uint32_t from = src + bfrom + (2 * part + bset) * pstride, to = (ph + bto) ^ (bset << 6);
+                                    const uint4 v0 = lds128(from), v1 = lds128(from ^ 16);
+                                    store(to, 0, v0), store(to, 1, v1);
+                                }
+                                // rows 64 .. 95: two of the warps, the other two the next half of the columns
+                                const int r = 64 + (t128 & 31), hf = (r >> 2) & 1;
+                                if (part == bset && r < half) {
+                                    const uint32_t from = src + kI8RawA + 8192 + (t128 >> 5) * 1024 + (r - 64) * 32 + hf * 16;
+                                    const uint32_t to = (ph + r * 128 + ((hf ^ (r & 7)) << 4)) ^ (((t128 >> 5) & 1) << 6);
+                                    const uint4 v0 = lds128(from), v1 = lds128(from ^ 16);
+                                    store(to, 0, v0), store(to, 1, v1);
+                                }
+                            }
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            if (part + 1 < kParts) {
+                                __syncwarp();
+                                if (lane == 0) tc::mbar_arrive_cluster(ready0 + (cs * kParts + part) * 8);
+                            }
+                        }
                     }
+                    if (!ok) break;
                     __syncwarp();
                     if (lane == 0) {
                         if (!is_a) tc::mbar_arrive(&raw_empty[rs]);
-                        tc::mbar_arrive_cluster(ready0 + cs * 8);
+                        tc::mbar_arrive_cluster(ready0 + (cs * kParts + kParts - 1) * 8);
                     }
                     rs += by, cs += by;
                     if (rs >= raw_stages) rs -= raw_stages, ++ruse;
@@ -509,7 +531,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
             }
             // the MMAs' last arrivals on this CTA's barriers, which have to land before it ends (the warps for B: each group its stages)
             for (int i = 0; i < kI8ConvStages / 2 && ok && !is_a; ++i) {
-                if (cuse > 0) ok = tc::mbar_wait_warp(&empty[cs], cuse - 1, &waits);
+                for (int part = 0; part < kParts && ok && cuse > 0; ++part) ok = tc::mbar_wait_warp(&empty[cs * kParts + part], cuse - 1, &waits);
                 cs += by;
                 if (cs >= kI8ConvStages) cs -= kI8ConvStages, ++cuse;
             }
