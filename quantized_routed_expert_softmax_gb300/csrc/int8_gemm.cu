@@ -19,14 +19,14 @@
 // Two accumulators alternate.
 //
 // Measured: 512 tokens' gate.up (32 rows an expert, 2816 -> 2 x 704) 100 us, 5.2 TB/s of weights, bound by HBM and by the
-// chain load -> convert -> MMA of the stages; 65528 rows, 704 -> 2816, 229 us, 1,130 TFLOP/s, gate.up 444 us, 1,170;
-// 8192^3 693 us, 1,590.  Many rows are bound by issuing instructions: five a 4-code word to convert (weights again for every row
-// tile), and the epilogue.
+// chain load -> convert -> MMA of the stages; 65528 rows, 704 -> 2816, 227 us, 1,140 TFLOP/s, gate.up 439 us, 1,180;
+// 8192^3 687 us, 1,600.  Many rows are bound by no one part: the MMA issuer, the converters (five instructions a 4-code word, weights
+// again for every row tile) and the epilogue are each at work for 60 to 85 % of the time, the issue slots 55 %.
 // What it took, us for 65528 rows 704 -> 2816 / 8192^3: K steps of 64 by bulk copies 426 / 1382; TMA tiles of 128 columns,
 // segment sums in registers 316 / 941; codes as fragments, without bank conflicts, read ahead 296 / 820; eight warps for the
 // rows 259 / 746; blocks of weight tiles 252 / 695; row tiles of 192 232 / 695; addresses by xor, scales by shuffle and two
-// staging buffers 229 / 693 (gate.up 452 -> 444).  Dropped: stores of A of 32 columns (848 against 820), commits one step later
-// (no change).
+// staging buffers 229 / 693 (gate.up 452 -> 444); converted stages by halves 227 / 687 (gate.up 439).  Dropped: stores of A of
+// 32 columns (848 against 820), commits one step later (no change).
 #include <algorithm>
 #include <cstring>
 
