@@ -30,7 +30,7 @@
 // Many rows an expert are bound by the MMAs: 8191 rows of 2816 x 5632 forward 403 us, 1,930 TFLOP/s (a library product of
 // 8192^3 does 1,932), with z saved 435, backward 890, 1,750 TFLOP/s.  Few rows are bound by the weights' bytes: 4096 rows of 128
 // experts, 2816 and 704, forward 255 us, 6.1 TB/s; their gradients by writing as many bytes: 1.0 GB of dWgu in 198 us, 5.1 TB/s
-// (a library's fill of a gigabyte writes 4.1).  32768 rows: forward 334 us, z saved 371, backward 775.
+// (a library's fill of a gigabyte writes 4.1).  32768 rows: forward 334 us, z saved 372, backward 780.
 // What it took, forward us of the dense block: barriers with release and acquire over the cluster 1288, without 406 (see
 // pair.cuh), blocks of weight tiles 398 (z saved 466 -> 431).  Backward: 2926, 932; z read a step ahead 890 (dz 223 -> 174);
 // two launches in place of four 967 -> 889 (fp32 z between).  A sixth stage of operands: 32768 rows 350 -> 334 forward.  Addresses
@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
         issued = 0;
     }
     pdl_wait();
+    pdl_trigger();   // the next product's pairs come as this one's go (32 to 128 rows dense 20.9 -> 19.3 us, a step of four launches 27.8 -> 25.4)
     if (tid == kFfThreads - 1) {
         const long long limit = *reinterpret_cast<const volatile long long*>(g.rows.err + kFfLimitWord);
         waits.limit_ns = limit != 0 ? limit : tc::kWaitLimitNs;

@@ -84,7 +84,7 @@ __global__ void __maxnreg__(80) stream_kernel(const StreamArgs g) {
     const int r0 = blockIdx.y;   // a block works if a group of 8 rows of an expert begins with its row
     if (tid == 0) owner = g.E;
     __syncthreads();
-    pdl_wait();
+    pdl_wait();   // (no early trigger: the next kernel's blocks would take places unevenly, 8 rows of 8 experts 11.3 -> 12.1 us)
     for (int e = tid; e < g.E; e += blockDim.x) {
         int first, last;
         expert_rows(g.offsets, e, g.P, &first, &last);
