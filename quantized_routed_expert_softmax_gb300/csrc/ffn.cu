@@ -47,7 +47,7 @@ namespace moe {
 
 constexpr int kFfThreads = 384;
 constexpr int kFfEpi0 = 4;              // first epilogue warp
-constexpr int kFfNT = 256;              // rows of B of a tile
+constexpr int kFfNT = 256;              // rows of B of a tile at most
 constexpr int kFfStepK = 64;            // 128 bytes of bf16
 constexpr int kFfABytes = 128 * 128, kFfStage = 2 * kFfABytes;
 constexpr uint32_t kFfTmemCols = 512;
@@ -77,6 +77,8 @@ struct FfArgs {
     const int32_t* offsets;
     int E, P, M, N, K;
     int block;            // tiles of M of a block (rows)
+    int log_nt;           // rows of B of a tile at most, a power of two (ff_launch; a shift, as more code before the first tile costs
+                          // a small launch half a microsecond)
     int f;                // neurons
     void* out;            // y, dx or the weights' gradient: rows of M values
     const float* z_in;
@@ -129,7 +131,7 @@ struct FfWalk {
         : w(t, max(1, (g_.rows.M + 255) / 256), max(1, g_.rows.block), first, stride), g(g_) {
         if constexpr (GRAD) {
             mtiles = max(1, (g.grad.M + 255) / 256);
-            ntiles = (g.grad.N + kFfNT - 1) / kFfNT;
+            ntiles = (g.grad.N + (1 << g.grad.log_nt) - 1) >> g.grad.log_nt;
             // this walk's first item past the product over rows
             const int64_t before = g.has_rows ? static_cast<int64_t>(t.n_tiles) * w.mtiles : 0;
             const int64_t skip = first < before ? (before - first + stride - 1) / stride * stride : 0;
@@ -161,8 +163,8 @@ struct FfWalk {
     __device__ void at() {
         if (GRAD && grad) {
             e = tile / ntiles;
-            n0 = (tile - e * ntiles) * kFfNT;
-            n = min(kFfNT, g.grad.N - n0);
+            n0 = (tile - e * ntiles) << g.grad.log_nt;
+            n = min(1 << g.grad.log_nt, g.grad.N - n0);
             int last;
             expert_rows(g.grad.offsets, e, g.grad.P, &k0, &last);
             k0 = __shfl_sync(0xffffffffu, k0, 0);
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
         const long long limit = *reinterpret_cast<const volatile long long*>(g.rows.err + kFfLimitWord);
         waits.limit_ns = limit != 0 ? limit : tc::kWaitLimitNs;
     }
-    if (g.has_rows) build_row_tiles<kFfThreads>(tiles, g.rows.offsets, g.rows.E, g.rows.P, kFfNT);
+    if (g.has_rows) build_row_tiles<kFfThreads>(tiles, g.rows.offsets, g.rows.E, g.rows.P, [&](int n) { return (n + (1 << g.rows.log_nt) - 1) >> g.rows.log_nt; });
     tc::fence_before();
     tc::cluster_sync();
     tc::fence_after();
@@ -605,12 +607,36 @@ cudaError_t ff_map_rows(FfArgs& g, const uint16_t* rows, int64_t P, int64_t cols
     return e;
 }
 
+// The tiles' height (its logarithm, `least` to 8) for `rows` in `groups`: as many rounds of the pairs as it takes, each about 128 (the
+// weights' side of a step) and the height long.  So calls whose tiles would leave most pairs idle take lower ones: dense blocks,
+// forward and backward, with tiles of 256 / these: 245 rows of 2272 x 2208 88 / 65 us, 194 of 1600 x 432 47 / 35, 2078 of 800 x 256
+// 51 / 41, 10056 of 880 x 272 143 / 123; where tiles fill the pairs anyway nothing changes.
+int ff_tile_log(int64_t mtiles, int64_t groups, int64_t rows, int least, int64_t pairs) {
+    int best = 8;
+    int64_t best_cost = INT64_MAX;
+    for (int log = 8; log >= least; --log) {
+        const int64_t each = (rows + groups - 1) / groups, n = (each + (1 << log) - 1) >> log, high = ((each + n - 1) / n + 31) / 32 * 32;
+        const int64_t tiles = mtiles * (groups * n + (groups > 1 ? groups / 2 : 0));   // (groups are not alike)
+        const int64_t cost = (tiles + pairs - 1) / pairs * (128 + high);
+        if (cost < best_cost) best_cost = cost, best = log;
+    }
+    return best;
+}
+
 template <int EPI, bool A_MN, int GEPI>
 cudaError_t ff_launch(FfWork& g, int num_sms, cudaStream_t s) {
     int64_t items = 0;
-    g.rows.block = tile_block((g.rows.M + 255) / 256);
-    if (g.has_rows) items += (g.rows.M + 255) / 256 * static_cast<int64_t>(std::min(g.rows.E, g.rows.P) + g.rows.P / kFfNT);
-    if (g.has_grad) items += (g.grad.M + 255) / 256 * static_cast<int64_t>(g.grad.E) * ((g.grad.N + kFfNT - 1) / kFfNT);
+    if (g.has_rows) {
+        const int64_t mtiles = (g.rows.M + 255) / 256, groups = std::min(g.rows.E, g.rows.P);
+        g.rows.block = tile_block(static_cast<int>(mtiles));
+        g.rows.log_nt = ff_tile_log(mtiles, groups, g.rows.P, 5, num_sms / 2);
+        items += mtiles * (groups + (g.rows.P >> g.rows.log_nt));
+    }
+    if (g.has_grad) {   // (its B comes in boxes of 64 for each CTA)
+        const int64_t mtiles = (g.grad.M + 255) / 256 * static_cast<int64_t>(g.grad.E);
+        g.grad.log_nt = ff_tile_log(mtiles, 1, g.grad.N, 7, num_sms / 2);
+        items += mtiles * ((g.grad.N + (1 << g.grad.log_nt) - 1) >> g.grad.log_nt);
+    }
     const int pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms / 2, items)));
     return launch_pairs(ffn_kernel<EPI, A_MN, GEPI>, pairs, kFfThreads, FfCfg<EPI, GEPI>::kSmem, s, g);
 }

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
         const long long limit = *reinterpret_cast<const volatile long long*>(g.err + kI8LimitWord);
         waits.limit_ns = limit != 0 ? limit : tc::kWaitLimitNs;
     }
-    build_row_tiles<kI8Threads>(tiles, g.offsets, g.E, g.P, g.nt);
+    build_row_tiles<kI8Threads>(tiles, g.offsets, g.E, g.P, [&](int n) { return (n + g.nt - 1) / g.nt; });
     tc::fence_before();
     tc::cluster_sync();
     tc::fence_after();

@@ -105,7 +105,7 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 }  // namespace tc
 
 // The row tiles of the experts that have rows, in shared memory.  An expert's tiles are equally high, a multiple of 32
-// (a pair's MMA takes N in steps of 32) and at most `nt`.
+// (a pair's MMA takes N in steps of 32).
 struct RowTiles {
     int prefix[kMaxE];   // first tile of a slot
     int2 rows[kMaxE];    // first row, last row + 1
@@ -114,9 +114,9 @@ struct RowTiles {
     int n_slots, n_tiles;
 };
 
-// By all THREADS threads of the CTA; ends with a __syncthreads().
-template <int THREADS>
-__device__ __forceinline__ void build_row_tiles(RowTiles& t, const int32_t* offsets, int E, int P, int nt) {
+// By all THREADS threads of the CTA; ends with a __syncthreads().  tiles_of(n): how many tiles n rows take.
+template <int THREADS, typename TilesOf>
+__device__ __forceinline__ void build_row_tiles(RowTiles& t, const int32_t* offsets, int E, int P, TilesOf tiles_of) {
     constexpr int kPer = (kMaxE + THREADS - 1) / THREADS;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int first[kPer], last[kPer], tiles = 0, live = 0;
@@ -124,7 +124,7 @@ __device__ __forceinline__ void build_row_tiles(RowTiles& t, const int32_t* offs
     for (int i = 0; i < kPer; ++i) {
         first[i] = last[i] = 0;
         if (tid * kPer + i < E) expert_rows(offsets, tid * kPer + i, P, &first[i], &last[i]);
-        tiles += (last[i] - first[i] + nt - 1) / nt;
+        tiles += tiles_of(last[i] - first[i]);
         live += last[i] > first[i];
     }
     int t_incl = tiles, l_incl = live;
@@ -141,7 +141,7 @@ __device__ __forceinline__ void build_row_tiles(RowTiles& t, const int32_t* offs
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         if (last[i] > first[i]) {
-            const int n = last[i] - first[i], n_tiles = (n + nt - 1) / nt;
+            const int n = last[i] - first[i], n_tiles = tiles_of(n);
             t.prefix[slot] = run;
             t.height[slot] = static_cast<uint16_t>(((n + n_tiles - 1) / n_tiles + 31) & ~31);
             t.rows[slot] = make_int2(first[i], last[i]);

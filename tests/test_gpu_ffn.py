@@ -73,6 +73,17 @@ def test_dense_block(P):
     _run(P, 1, 176, 336, None, seed=P)
 
 
+@pytest.mark.parametrize("P,d,f", [(2600, 272, 1040), (1500, 1040, 272), (700, 528, 528), (300, 1040, 1552), (4100, 1296, 640)])
+def test_dense_block_in_tiles_of_every_height(P, d, f):
+    _run(P, 1, d, f, None, seed=P, act="swiglu" if P % 200 else "relu2")
+
+
+@pytest.mark.parametrize("counts", [[int(n) for n in np.random.default_rng(3).integers(0, 600, 48)], [3000] + [1] * 20 + [0, 900],
+                                    [255, 256, 257, 512, 513, 511, 128, 129] * 6])
+def test_many_row_tiles_an_expert(counts):
+    _run(sum(counts), len(counts), 272, 144, counts, seed=len(counts))
+
+
 def test_layer_shapes():
     _run(70, 4, 2816, 704, [9, 0, 60, 1], seed=1)
     _run(40, 3, 1024, 2688, [13, 1, 26], act="relu2", seed=2)
