@@ -39,7 +39,7 @@ constexpr int kI8ConvA0 = 4, kI8ConvB0 = 12, kI8Epi0 = 20;   // first warps of t
 constexpr int kI8StepK = 128;
 constexpr int kI8SegSteps = 1024 / kI8StepK;
 constexpr int kI8RawA = 128 * kI8StepK, kI8MaxRawStages = 7;
-// For tiles of up to nt rows, 64, 128 or 192 (half of them in a CTA): bytes of a stage of codes and of converted rows, and how
+// For tiles of up to nt rows, 32, 64, 128 or 192 (half of them in a CTA): bytes of a stage of codes and of converted rows, and how
 // many of both.  Tensor memory has two accumulators of 128 columns (192) and A's stages of 64 behind them.
 __host__ __device__ constexpr int i8_raw(int nt) { return kI8RawA + nt / 2 * kI8StepK; }
 __host__ __device__ constexpr int i8_conv_b(int nt) { return nt / 2 * 2 * kI8StepK; }
@@ -50,7 +50,7 @@ constexpr uint32_t kI8TmemCols = 512;
 constexpr int kI8LimitWord = 8;   // the waits' limit in ns (int64) in the workspace: 0 means a second
 constexpr size_t i8_smem(int nt) { return 1024 + i8_conv_stages(nt) * i8_conv_b(nt) + i8_raw_stages(nt) * i8_raw(nt) + 2 * kI8EpiBytes; }
 constexpr size_t i8_max(size_t a, size_t b) { return a > b ? a : b; }
-constexpr size_t kI8Smem = i8_max(i8_smem(192), i8_max(i8_smem(128), i8_smem(64)));
+constexpr size_t kI8Smem = i8_max(i8_smem(192), i8_max(i8_smem(128), i8_smem(64)));   // (tiles of 32 rows take less)
 static_assert(2 * 128 + 64 * i8_conv_stages(128) <= kI8TmemCols && 2 * 192 + 64 * i8_conv_stages(192) <= kI8TmemCols, "tensor memory");
 static_assert(kI8Smem + sizeof(RowTiles) + 512 <= 227 * 1024, "rings and staging fit beside the table");
 static_assert((kI8Threads - 1) * 2 >= kMaxE, "the last thread has no offsets");
@@ -67,7 +67,7 @@ struct I8Args {
     int64_t w_mat;   // bytes between weight matrices
     const int32_t* offsets;
     int E, P, N, K;
-    int nt;      // rows of a tile at most: 64, 128 or 192
+    int nt;      // rows of a tile at most: 32, 64, 128 or 192
     int block;   // weight tiles of a block
     void* out;
     int32_t* err;
@@ -623,9 +623,21 @@ cudaError_t launch_int8_matmul(const void* xq, int64_t P, const void* wq, int64_
     // Tiles of up to 64 rows where experts have few: smaller stages leave room for more of them, and what is on its way from
     // memory bounds the kernel then.
     // Sums of up to 1024 columns in tiles of 192 rows where experts have many: weights are converted once for each row tile.
-    const int64_t avg = P / std::min(E, P);
+    // In between as many rounds of the pairs as it takes, each about 128 (the weights) and the height long, so that calls whose tiles
+    // would leave most pairs idle take lower ones (one matrix: 674 rows, 672 -> 640, 16.1 -> 10.5 us; 114 rows, 1728 -> 1472, 14.0
+    // -> 12.1; 4728 rows, 384 -> 896, 13.2 -> 11.5).
+    const int64_t groups = std::min(E, P), avg = P / groups, mtiles = (N + 255) / 256;
     const bool multi = K > kI8SegSteps * kI8StepK;
-    g.nt = avg <= 48 ? 64 : (avg < 160 || multi ? 128 : 192);
+    g.nt = 64;
+    if (avg > 48) {
+        int64_t least = INT64_MAX;
+        for (int nt = multi || avg < 160 ? 128 : 192; nt >= 32; nt = nt > 64 ? nt - 64 : nt / 2) {
+            const int64_t n = (avg + nt - 1) / nt, high = ((avg + n - 1) / n + 31) / 32 * 32;
+            const int64_t tiles = mtiles * (groups * n + (groups > 1 ? groups / 2 : 0));   // (experts are not alike)
+            const int64_t cost = (tiles + num_sms / 2 - 1) / (num_sms / 2) * (128 + high);
+            if (cost < least) least = cost, g.nt = nt;
+        }
+    }
     const int64_t bound = (N + 255) / 256 * (std::min(E, P) + P / g.nt);
     const int pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms / 2, bound)));
     return launch_pairs(i8_kernel(multi, g.nt, act, ot == MOE_F32), pairs, kI8Threads, i8_smem(g.nt), s, g);

@@ -200,6 +200,21 @@ def test_product_odd_widths(P, N):
     _check(P, 1, N, 224, None, "relu2", torch.bfloat16, seed=P + N + 1)
 
 
+@pytest.mark.parametrize("act,dtype", [("none", torch.bfloat16), ("none", torch.float32), ("swiglu", torch.bfloat16),
+                                       ("swiglu", torch.float32), ("relu2", torch.bfloat16), ("relu2", torch.float32)])
+@pytest.mark.parametrize("most,E,K", [(700, 24, 704), (700, 24, 1056), (160, 40, 96), (60, 60, 224)])
+def test_product_of_more_tiles_than_pairs(most, E, K, act, dtype):
+    """(Fewer are cut lower: these take tiles of 192, 128, 128 and 64 rows at most.)"""
+    counts = [int(n) for n in np.random.default_rng(most + K).integers(0, most, E)]
+    _check(sum(counts), E, 1088, K, counts, act, dtype, seed=K)
+
+
+@pytest.mark.parametrize("P", [64, 96, 129, 700, 4097])
+def test_product_of_one_matrix_in_low_tiles(P):
+    _check(P, 1, 584, 736, None, "none", torch.float32, seed=P)
+    _check(P, 1, 320, 1088, None, "swiglu", torch.bfloat16, seed=P + 1)
+
+
 @pytest.mark.parametrize("P", [2, 100])
 def test_product_of_the_largest_codes_is_exact_by_integers(P):
     # every product 127 * 127 at K = 65536: 1.06e9, far past 24 bits
