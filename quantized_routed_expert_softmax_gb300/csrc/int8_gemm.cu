@@ -18,15 +18,17 @@
 //                memory in 16-byte pieces of whole rows to memory.
 // Two accumulators alternate.
 //
-// Measured: 512 tokens' gate.up (32 rows an expert, 2816 -> 2 x 704) 100 us, 5.2 TB/s of weights, bound by HBM and by the
-// chain load -> convert -> MMA of the stages; 65528 rows, 704 -> 2816, 227 us, 1,140 TFLOP/s, gate.up 439 us, 1,180;
-// 8192^3 687 us, 1,600.  Many rows are bound by no one part: the MMA issuer, the converters (five instructions a 4-code word, weights
-// again for every row tile) and the epilogue are each at work for 60 to 85 % of the time, the issue slots 55 %.
+// Measured: 512 tokens' gate.up (32 rows an expert, 2816 -> 2 x 704) 95 us, 5.5 TB/s of weights, bound by HBM and by the
+// chain load -> convert -> MMA of the stages; 65528 rows, 704 -> 2816, 227 us, 1,140 TFLOP/s (2817 columns, which no row
+// begins aligned for, 345), gate.up 424 us, 1,230; 8192^3 659 us, 1,670.  Many rows are bound by no one part: the MMA issuer,
+// the converters (five instructions a 4-code word, weights again for every row tile) and the epilogue are each at work for 60 to
+// 85 % of the time, the issue slots 55 %.
 // What it took, us for 65528 rows 704 -> 2816 / 8192^3: K steps of 64 by bulk copies 426 / 1382; TMA tiles of 128 columns,
 // segment sums in registers 316 / 941; codes as fragments, without bank conflicts, read ahead 296 / 820; eight warps for the
 // rows 259 / 746; blocks of weight tiles 252 / 695; row tiles of 192 232 / 695; addresses by xor, scales by shuffle and two
-// staging buffers 229 / 693 (gate.up 452 -> 444); converted stages by halves 227 / 687 (gate.up 439).  Dropped: stores of A of
-// 32 columns (848 against 820), commits one step later (no change).
+// staging buffers 229 / 693 (gate.up 452 -> 444); converted stages by halves 227 / 687 (gate.up 439); rows of any
+// alignment in 16-byte pieces (65528 rows to 2817 columns 404 -> 345), which also freed registers of the other forms 227 / 659
+// (gate.up 424).  Dropped: stores of A of 32 columns (848 against 820), commits one step later (no change).
 #include <algorithm>
 #include <cstring>
 
@@ -73,6 +75,11 @@ struct I8Args {
     int32_t* err;
 };
 
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -295,15 +302,39 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
 #pragma unroll
                         for (int j = 0; j < 32 / kStep; ++j, to += pitch)
                             if (j * kStep < rows) *reinterpret_cast<uint4*>(to) = lds128((cfrom ^ (F32 && !kGated && (j & 1) ? 64 : 0)) + turn + j * kStep * kRow);
-                    } else {   // rows that start anywhere: a value a lane
-                        for (int i = t128; i < 32 * kPer * kEach; i += 128) {
-                            const int r = i / (kPer * kEach), c = i % (kPer * kEach);
-                            if (r >= left || c >= cols) continue;
-                            const int place = F32 ? (c / kEach) ^ (2 * ((r >> 1) & 3)) : (c / kEach) ^ (r & 7);
-                            const unsigned char* p = staging + grp * kI8EpiBytes + turn + r * kRow + (place << 4) + (c % kEach) * kElem;
-                            const int64_t o = o0 + static_cast<int64_t>(r) * width + c;
-                            if (F32) static_cast<float*>(g.out)[o] = *reinterpret_cast<const float*>(p);
-                            else static_cast<uint16_t*>(g.out)[o] = *reinterpret_cast<const uint16_t*>(p);
+                    } else {   // rows that start anywhere: memory's whole pieces of 16 bytes, then the columns before and behind them
+                        const int w = min(cols, kPer * kEach);
+                        auto row = [&](int r) { return static_cast<char*>(g.out) + (o0 + static_cast<int64_t>(r) * width) * kElem; };
+                        auto head = [&](const char* to) { return static_cast<int>((0 - reinterpret_cast<uintptr_t>(to)) & 15) / kElem; };
+                        auto place = [&](int r, int byte) {   // in shared memory
+                            return sb + turn + r * kRow + (((byte >> 4) ^ (F32 ? 2 * ((r >> 1) & 3) : r & 7)) << 4) + (byte & 15);
+                        };
+                        for (int i = t128; i < 32 * kPer; i += 128) {
+                            const int r = i / kPer;
+                            if (r >= left) break;
+                            char* to = row(r);
+                            const int c = head(to) + i % kPer * kEach, at4 = c * kElem & ~3;
+                            if (c + kEach > w) continue;
+                            uint32_t v[5];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) v[j] = lds32(place(r, at4 + 4 * j));
+                            if (!F32 && (c & 1)) {   // two bytes on
+                                v[4] = lds32(place(r, at4 + 16));
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) v[j] = __byte_perm(v[j], v[j + 1], 0x5432);
+                            }
+                            *reinterpret_cast<uint4*>(to + c * kElem) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                        for (int i = t128; i < 64 * kEach; i += 128) {
+                            const int r = i / (2 * kEach), j = i % (2 * kEach);
+                            if (r >= left) break;
+                            char* to = row(r);
+                            const int h = min(head(to), w), behind = h + (w - h) / kEach * kEach;
+                            const int c = j < kEach ? j : behind + j - kEach;
+                            if (c >= (j < kEach ? h : w)) continue;
+                            const uint32_t v = lds32(place(r, c * kElem & ~3));
+                            if (F32) *reinterpret_cast<uint32_t*>(to + c * kElem) = v;
+                            else *reinterpret_cast<uint16_t*>(to + c * kElem) = static_cast<uint16_t>(c & 1 ? v >> 16 : v);
                         }
                     }
                     if constexpr (kTwo) {
