@@ -115,7 +115,6 @@ __device__ __forceinline__ float2 ff_sigmoid(float g) {
     const float e = __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + e), t = e * r;
     return g < 0.0f ? make_float2(t, r) : make_float2(r, t);
 }
-__device__ __forceinline__ float ff_relu(float z) { return z > 0.0f ? z : (z <= 0.0f ? 0.0f : z); }
 
 // The items of one role: (row tile, tile of M) of the product over rows, then (expert, tile of N, tile of M) of the gradient;
 // M tiles fastest.
@@ -458,7 +457,7 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                                     ga[u] = d[u] * lds_f32(at + 8192) * (s.x + silu * s.y);
                                     gb[u] = d[u] * silu;
                                 } else {
-                                    ga[u] = d[u] * (2.0f * ff_relu(z));
+                                    ga[u] = d[u] * (2.0f * relu_nan(z));
                                 }
                             }
                             wa[m] = ff_pack(ga[0], ga[1]);
@@ -525,8 +524,8 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        lo[j] = ff_relu(lo[j]) * ff_relu(lo[j]);
-                        hi[j] = ff_relu(hi[j]) * ff_relu(hi[j]);
+                        lo[j] = relu_nan(lo[j]) * relu_nan(lo[j]);
+                        hi[j] = relu_nan(hi[j]) * relu_nan(hi[j]);
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i)

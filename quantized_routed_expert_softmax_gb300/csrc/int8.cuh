@@ -10,6 +10,13 @@ namespace moe {
 __host__ __device__ inline int64_t i8_scale_bytes(int64_t rows) { return (4 * rows + 15) / 16 * 16; }
 __host__ __device__ inline int64_t i8_bytes(int64_t rows, int64_t cols) { return i8_scale_bytes(rows) + rows * cols; }
 
+// max(z, 0), a NaN stays.  (As a choice by comparisons it becomes branches on the data.)
+__device__ __forceinline__ float relu_nan(float z) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(z));
+    return r;
+}
+
 // Four codes -> two pairs of f16, exactly: 0x64 in front of the byte c + 128 is the f16 value 1152 + c, and subtracting 1152
 // leaves c; two values an instruction.
 __device__ __forceinline__ void i8_f16(uint32_t w, uint32_t* h) {

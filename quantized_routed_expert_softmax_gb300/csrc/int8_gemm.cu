@@ -19,7 +19,7 @@
 // Two accumulators alternate.
 //
 // Measured: 512 tokens' gate.up (32 rows an expert, 2816 -> 2 x 704) 95 us, 5.5 TB/s of weights, bound by HBM and by the
-// chain load -> convert -> MMA of the stages; 65528 rows, 704 -> 2816, 227 us, 1,140 TFLOP/s (2817 columns, which no row
+// chain load -> convert -> MMA of the stages; 65528 rows, 704 -> 2816, 221 us, 1,180 TFLOP/s (2817 columns, which no row
 // begins aligned for, 345), gate.up 424 us, 1,230; 8192^3 659 us, 1,670.  Many rows are bound by no one part: the MMA issuer,
 // the converters (five instructions a 4-code word, weights again for every row tile) and the epilogue are each at work for 60 to
 // 85 % of the time, the issue slots 55 %.
@@ -28,7 +28,8 @@
 // rows 259 / 746; blocks of weight tiles 252 / 695; row tiles of 192 232 / 695; addresses by xor, scales by shuffle and two
 // staging buffers 229 / 693 (gate.up 452 -> 444); converted stages by halves 227 / 687 (gate.up 439); rows of any
 // alignment in 16-byte pieces (65528 rows to 2817 columns 404 -> 345), which also freed registers of the other forms 227 / 659
-// (gate.up 424).  Dropped: stores of A of 32 columns (848 against 820), commits one step later (no change).
+// (gate.up 424); scales before the wait, groups in turn 221; ReLU^2 without branches on the data (relu_nan; 40040 rows of 512
+// experts, 256 -> 520, 92 -> 44, 65528 rows 704 -> 2816 into fp32 436 -> 268).  Dropped: stores of A of 32 columns (848 against 820), commits one step later (no change).
 #include <algorithm>
 #include <cstring>
 
@@ -211,6 +212,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
         const bool wide = width % (F32 ? 4 : 8) == 0;
         const int segs = (ksteps + kI8SegSteps - 1) / kI8SegSteps;
         uint32_t n_acc = 0;
+        [[maybe_unused]] uint32_t turns = 0;
         bool ok = true;
         uint32_t turn = 0;   // the buffer whose turn it is, bytes from the first
         for (; walk.more(); walk.next()) {
@@ -225,6 +227,13 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                     sw[i] = __ldg(ws + (kGated && i >= 2 ? width : 0) + min(c, width - 1));
                 }
             }
+            // Short sums are bound by the epilogue: the group that begins changes from tile to tile, as an odd number of chunks is more
+            // for one of them, and the scales of the chunks' rows from + lane, + 64 .. are asked for at once, before the wait.
+            const int from = 32 * (MULTI ? grp : grp ^ static_cast<int>(turns++ & 1));
+            [[maybe_unused]] float scales[NT / 64];
+            if constexpr (!MULTI)
+#pragma unroll
+                for (int ch = 0; ch < NT / 64; ++ch) scales[ch] = __ldg(sx + n0 + min(from + 64 * ch + lane, n - 1));
             float sums[MULTI ? 2 : 1][32];   // of 32 rows (two times, SwiGLU: gate and up rows): 16 lanes, the other 16
             for (int seg = 0; seg < segs; ++seg) {
                 // (after a wait that ran out the group's warps go on, as they meet at barriers; the sums are not valid then)
@@ -235,9 +244,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                 const bool last = seg + 1 == segs;
 #pragma unroll (MULTI ? 2 : 1)
                 for (int ch = 0; ch < NT / 64; ++ch) {
-                    const int c0 = 32 * grp + 64 * ch;
+                    const int c0 = from + 64 * ch;
                     if (c0 >= n) continue;
-                    const float scale = __ldg(sx + n0 + min(c0 + lane, n - 1));   // of row c0 + lane
                     float* lo = sums[MULTI ? ch : 0];
                     float* hi = lo + 16;
                     if (!MULTI || seg == 0) {
@@ -255,6 +263,10 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                         }
                     }
                     if (MULTI && !last) continue;
+                    const float scale = MULTI     ? __ldg(sx + n0 + min(c0 + lane, n - 1))
+                                        : ch == 0 ? scales[0]
+                                        : ch == 1 ? scales[1]
+                                                  : scales[NT / 64 - 1];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint64_t t = pack_f32x2(__shfl_sync(0xffffffffu, scale, 8 * i + ncol), __shfl_sync(0xffffffffu, scale, 8 * i + ncol + 1));
@@ -269,8 +281,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                     for (int j = 0; j < 16; ++j) {
                         if (kGated) lo[j] = silu_fast(lo[j]) * hi[j];
                         if (ACT == MOE_ACT_RELU2) {
-                            lo[j] = lo[j] > 0.0f ? lo[j] * lo[j] : (lo[j] <= 0.0f ? 0.0f : lo[j]);
-                            hi[j] = hi[j] > 0.0f ? hi[j] * hi[j] : (hi[j] <= 0.0f ? 0.0f : hi[j]);
+                            lo[j] = relu_nan(lo[j]), hi[j] = relu_nan(hi[j]);
+                            lo[j] *= lo[j], hi[j] *= hi[j];
                         }
                     }
                     if constexpr (F32) {

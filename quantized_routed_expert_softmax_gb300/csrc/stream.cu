@@ -188,7 +188,7 @@ __global__ void __maxnreg__(80) stream_kernel(const StreamArgs g) {
             if (kGated) v[0] = silu_fast(v[0]) * v[1];
 #pragma unroll
             for (int u = 0; u < (kGated ? 1 : 2); ++u) {
-                if (ACT == MOE_ACT_RELU2) v[u] = v[u] > 0.0f ? v[u] * v[u] : (v[u] <= 0.0f ? 0.0f : v[u]);
+                if (ACT == MOE_ACT_RELU2) v[u] = relu_nan(v[u]) * relu_nan(v[u]);
                 if (c[u] >= width) continue;
                 if (g.f32) static_cast<float*>(g.out)[row * width + c[u]] = v[u];
                 else static_cast<__nv_bfloat16*>(g.out)[row * width + c[u]] = __float2bfloat16_rn(v[u]);
