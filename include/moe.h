@@ -284,7 +284,8 @@ moe_status moe_dequantize_int8(const void* src, int64_t n_mat, int64_t rows, int
  * moe_int8_matmul -- the expert-indexed product of int8 rows with per-channel int8 weights, the activation
  * fused:
  *   z[r][n] = sx[r] * sw[e(r)][n] * sum_i xq[r][i] * wq[e(r)][n][i]
- * (the code products of up to 1024 columns summed exactly, those sums in fp32), then NONE, SWIGLU or RELU2
+ * (the code products of up to 1024 columns summed exactly, those sums in fp32; the sum times one scale, then the
+ * other, so that no z which fp32 can hold is lost to the product of the scales), then NONE, SWIGLU or RELU2
  * as in moe_mxfp4_matmul.
  * xq       device, one int8 matrix [P][K]: the rows sorted by expert.
  * wq       device, E int8 matrices [N][K] back to back (SWIGLU: rows 0..N/2-1 gate, the rest up).

@@ -26,6 +26,14 @@ __device__ __forceinline__ void i8_f16(uint32_t w, uint32_t* h) {
         : "=r"(h[0]), "=r"(h[1])
         : "r"(u), "r"(k1152), "r"(0x64646464u));
 }
+// A sum of codes meets its two scales one after the other: their product alone may be too small or too large for fp32 where the
+// result is not.  A sum is 0 or 1 to 2^30 in magnitude, so it loses nothing to a scale however small (whole numbers of a subnormal
+// step), and a scale of up to kI8LargeScale takes it to 2^127 at most.  The channel's scale comes first, or, where it is larger,
+// the row's: if that overflows, the result does.  (Scales are not negative.)
+constexpr float kI8LargeScale = 0x1p97f;
+__device__ __forceinline__ float i8_scaled(float z, float row, float channel) {
+    return channel > kI8LargeScale ? z * row * channel : z * channel * row;
+}
 // SiLU to a few units in the last place at any gate: exp(-|g|) is at most 1, so that the divisor of the fast division lies
 // in [1, 2], where it is good to 2 units.
 __device__ __forceinline__ float silu_fast(float g) {

@@ -32,6 +32,7 @@
 // experts, 256 -> 520, 92 -> 44, 65528 rows 704 -> 2816 into fp32 436 -> 268).  Dropped: stores of A of 32 columns (848 against 820), commits one step later (no change).
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "pair.cuh"
 
@@ -227,6 +228,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                     sw[i] = __ldg(ws + (kGated && i >= 2 ? width : 0) + min(c, width - 1));
                 }
             }
+            // (the choice once a tile; in every product it cost 65528 rows 704 -> 2816 6 us of 221)
+            const bool large = __any_sync(0xffffffffu, max(max(sw[0], sw[1]), max(sw[2], sw[3])) > kI8LargeScale);
             // Short sums are bound by the epilogue: the group that begins changes from tile to tile, as an odd number of chunks is more
             // for one of them, and the scales of the chunks' rows from + lane, + 64 .. are asked for at once, before the wait.
             const int from = 32 * (MULTI ? grp : grp ^ static_cast<int>(turns++ & 1));
@@ -267,16 +270,24 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                                         : ch == 0 ? scales[0]
                                         : ch == 1 ? scales[1]
                                                   : scales[NT / 64 - 1];
+                    auto scaled = [&](auto slow) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint64_t t = pack_f32x2(__shfl_sync(0xffffffffu, scale, 8 * i + ncol), __shfl_sync(0xffffffffu, scale, 8 * i + ncol + 1));
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 t = make_float2(__shfl_sync(0xffffffffu, scale, 8 * i + ncol), __shfl_sync(0xffffffffu, scale, 8 * i + ncol + 1));
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {   // rows mrow, + 8, + 16, + 24 of the warp's: two columns each
-                            float* z = (u < 2 ? lo : hi) + 4 * i + 2 * (u & 1);
-                            const float2 v = unpack_f32x2(mul_f32x2(pack_f32x2(z[0], z[1]), mul_f32x2(t, pack_f32x2(sw[u], sw[u]))));
-                            z[0] = v.x, z[1] = v.y;
+                            for (int u = 0; u < 4; ++u) {   // rows mrow, + 8, + 16, + 24 of the warp's: two columns each
+                                float* z = (u < 2 ? lo : hi) + 4 * i + 2 * (u & 1);
+                                if constexpr (decltype(slow)::value) {
+                                    z[0] = i8_scaled(z[0], t.x, sw[u]), z[1] = i8_scaled(z[1], t.y, sw[u]);
+                                } else {   // i8_scaled, two at a time
+                                    const float2 v = unpack_f32x2(mul_f32x2(mul_f32x2(pack_f32x2(z[0], z[1]), pack_f32x2(sw[u], sw[u])), pack_f32x2(t.x, t.y)));
+                                    z[0] = v.x, z[1] = v.y;
+                                }
+                            }
                         }
-                    }
+                    };
+                    if (large) scaled(std::true_type{});
+                    else scaled(std::false_type{});
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         if (kGated) lo[j] = silu_fast(lo[j]) * hi[j];

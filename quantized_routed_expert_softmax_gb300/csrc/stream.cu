@@ -170,7 +170,7 @@ __global__ void __maxnreg__(80) stream_kernel(const StreamArgs g) {
             const float swa = __ldg(sw + ra), swb = __ldg(sw + rb);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                z[i] = static_cast<float>(zi[i]) * (__ldg(g.sx + r0 + min(2 * t + (i & 1), rows - 1)) * (i < 2 ? swa : swb));
+                z[i] = i8_scaled(static_cast<float>(zi[i]), __ldg(g.sx + r0 + min(2 * t + (i & 1), rows - 1)), i < 2 ? swa : swb);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {   // rows 2 t, 2 t + 1
