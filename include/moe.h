@@ -299,7 +299,8 @@ moe_status moe_dequantize_int8(const void* src, int64_t n_mat, int64_t rows, int
  * The same inputs give the same bits.  P = 0 returns MOE_OK, launches nothing and touches no buffer.
  * Errors: INVALID_ARG (NULL, bad enum, offsets NULL with E > 1), SHAPE (K a positive multiple of 32 up to
  * 65536; P up to 2^25; N from 1 to 131072, for SWIGLU a multiple of 64; E up to 1024), ALIGNMENT, WORKSPACE,
- * CUDA.
+ * CUDA (more than 16 rows of more than 1024 columns: also where the library was compiled to fewer registers
+ * than that kernel needs).
  */
 size_t moe_int8_matmul_workspace_bytes(void);
 moe_status moe_int8_matmul(const void* xq, int64_t P, const void* wq, int64_t E, int64_t N, int64_t K,

@@ -31,6 +31,7 @@
 // (gate.up 424); scales before the wait, groups in turn 221; ReLU^2 without branches on the data (relu_nan; 40040 rows of 512
 // experts, 256 -> 520, 92 -> 44, 65528 rows 704 -> 2816 into fp32 436 -> 268).  Dropped: stores of A of 32 columns (848 against 820), commits one step later (no change).
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <type_traits>
 
@@ -61,7 +62,7 @@ static_assert((kI8Threads - 1) * 2 >= kMaxE, "the last thread has no offsets");
 // Sums of more than 1024 columns: the epilogue's warps hold their segments' sums in registers, which the other warps give
 // up (twenty warps of 48 and eight of 128 are less than the 28 of 72 that the block starts with).
 constexpr int kI8RegsOther = 48, kI8RegsEpi = 128;
-constexpr int kI8RegsLaunch = 72;   // of a thread as the block is launched; checked when the kernels are configured
+constexpr int kI8RegsLaunch = 72;   // of a thread as the block is launched; with fewer a kernel is not launched (i8_short)
 static_assert(20 * kI8RegsOther + 8 * kI8RegsEpi <= 28 * kI8RegsLaunch, "registers of the block");
 
 struct I8Args {
@@ -631,6 +632,10 @@ I8Kernel i8_kernel(bool multi, int nt, int act, bool f32) {
     return nt > 128 ? i8_kernel<false, 192>(act, f32) : i8_kernel<false, 128>(act, f32);
 }
 
+// Which kernels for sums of more than 1024 columns, by activation and type, were compiled to fewer registers than they redistribute:
+// the epilogue's warps would wait for theirs for ever, so these are not launched.
+std::atomic<bool> i8_short[3][2];
+
 }  // namespace
 
 cudaError_t configure_int8_codec();
@@ -644,10 +649,9 @@ cudaError_t configure_int8_kernels() {
                 const void* fn = reinterpret_cast<const void*>(i8_kernel(multi, kind == 1 ? 192 : 128, act, f32));
                 if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kI8Smem));
                 if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-                // (with fewer registers at launch the epilogue's warps would wait for theirs for ever)
                 cudaFuncAttributes attr{};
                 if (e == cudaSuccess && multi) e = cudaFuncGetAttributes(&attr, fn);
-                if (e == cudaSuccess && multi && attr.numRegs < kI8RegsLaunch) e = cudaErrorInvalidConfiguration;
+                if (e == cudaSuccess && multi) i8_short[act][f32] = attr.numRegs < kI8RegsLaunch;
             }
     return e;
 }
@@ -657,6 +661,8 @@ cudaError_t launch_stream_int8(const void*, int64_t, const void*, int64_t, int64
 cudaError_t launch_int8_matmul(const void* xq, int64_t P, const void* wq, int64_t E, int64_t N, int64_t K, const int32_t* offsets,
                                int act, void* out, int ot, int32_t* err, int num_sms, cudaStream_t s) {
     if (stream_rows(P)) return launch_stream_int8(xq, P, wq, E, N, K, offsets, act, out, ot, num_sms, s);
+    const bool multi = K > kI8SegSteps * kI8StepK;
+    if (multi && i8_short[act][ot == MOE_F32]) return cudaErrorInvalidConfiguration;
     I8Args g;
     std::memset(&g, 0, sizeof(g));
     g.xq = static_cast<const uint8_t*>(xq);
@@ -681,7 +687,6 @@ cudaError_t launch_int8_matmul(const void* xq, int64_t P, const void* wq, int64_
     // would leave most pairs idle take lower ones (one matrix: 674 rows, 672 -> 640, 16.1 -> 10.5 us; 114 rows, 1728 -> 1472, 14.0
     // -> 12.1; 4728 rows, 384 -> 896, 13.2 -> 11.5).
     const int64_t groups = std::min(E, P), avg = P / groups, mtiles = (N + 255) / 256;
-    const bool multi = K > kI8SegSteps * kI8StepK;
     g.nt = 64;
     if (avg > 48) {
         int64_t least = INT64_MAX;
