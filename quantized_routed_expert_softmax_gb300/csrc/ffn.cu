@@ -413,144 +413,144 @@ __global__ void __launch_bounds__(kFfThreads, 1) ffn_kernel(const __grid_constan
                 }
             };
             auto tile = [&](auto tag, auto of_grad) {   // the item's epilogue
-            constexpr int kE = decltype(tag)::value;
-            constexpr bool kG = decltype(of_grad)::value;
-            const FfArgs& a = kG ? g.grad : g.rows;
-            if constexpr (kE == kEpiSwigluGrad || kE == kEpiRelu2Grad) {
+                constexpr int kE = decltype(tag)::value;
+                constexpr bool kG = decltype(of_grad)::value;
+                const FfArgs& a = kG ? g.grad : g.rows;
+                if constexpr (kE == kEpiSwigluGrad || kE == kEpiRelu2Grad) {
 #pragma unroll 1
-                for (int c0 = 16 * grp; c0 < walk.n; c0 += 32) {   // 16 rows of dh
-                    float v[16];   // 16 lanes' neurons, the other 16's
-                    const int left = walk.n - c0;
-                    if (none) {
+                    for (int c0 = 16 * grp; c0 < walk.n; c0 += 32) {   // 16 rows of dh
+                        float v[16];   // 16 lanes' neurons, the other 16's
+                        const int left = walk.n - c0;
+                        if (none) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-                    } else {
-                        tc::tmem_ld_frag16(tb + c0, v);
-                        tc::tmem_ld_frag16(tb + (16u << 16) + c0, v + 8);
-                    }
-                    // z of these rows and neurons into shared memory, the next rows' on their way to registers
-#pragma unroll
-                    for (int j = 0; j < 4 * kHalves; ++j) {
-                        const int i = j * 128 + t128, half = i >> 9, r = (i >> 5) & 15, p = i & 31;
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sb + half * 8192 + r * 512 + ((p ^ (2 * ((r >> 1) & 3))) << 4)),
-                                     "r"(zr[j].x), "r"(zr[j].y), "r"(zr[j].z), "r"(zr[j].w)
-                                     : "memory");
-                    }
-                    if (left > 32) read_z(c0 + 32);
-                    tc::named_sync(1 + grp, 128);
-                    if (!none) tc::tmem_ld_wait(v);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t wa[4], wb[4];   // rows lane / 4, + 8, + 16, + 24 of the warp's neurons, a pair of rows of dz each
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const float* d = v + 8 * (m >> 1) + 4 * i + 2 * (m & 1);   // dh of the pair
-                            float ga[2], gb[2];
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const int r = 8 * i + ncol + u, c = q * 32 + 8 * m + mrow;
-                                const uint32_t at = sb + r * 512 + ((c ^ (8 * (lane & 3))) << 2);
-                                const float z = lds_f32(at);
-                                if constexpr (kE == kEpiSwigluGrad) {
-                                    const float2 s = ff_sigmoid(z);
-                                    const float silu = z * s.x;
-                                    ga[u] = d[u] * lds_f32(at + 8192) * (s.x + silu * s.y);
-                                    gb[u] = d[u] * silu;
-                                } else {
-                                    ga[u] = d[u] * (2.0f * relu_nan(z));
-                                }
-                            }
-                            wa[m] = ff_pack(ga[0], ga[1]);
-                            if constexpr (kE == kEpiSwigluGrad) wb[m] = ff_pack(gb[0], gb[1]);
+                            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                        } else {
+                            tc::tmem_ld_frag16(tb + c0, v);
+                            tc::tmem_ld_frag16(tb + (16u << 16) + c0, v + 8);
                         }
-                        tc::stsm4_t(at256 + 16384 + i * 2048, wa[0], wa[1], wa[2], wa[3]);
-                        if constexpr (kE == kEpiSwigluGrad) tc::stsm4_t(at256 + 20480 + i * 2048, wb[0], wb[1], wb[2], wb[3]);
-                    }
-                    tc::named_sync(1 + grp, 128);   // (the next rows' z goes where z has been read, their dz behind a barrier)
-                    const int64_t row0 = walk.n0 + c0;
-                    copy(sb + 16384, 16, a.dz_out, row0, left, kHalves * a.f, am, a.f - am, 256, 2);
-                    if (kHalves == 2) copy(sb + 20480, 16, a.dz_out, row0, left, 2 * a.f, a.f + am, a.f - am, 256, 2);
-                }
-            } else {
-#pragma unroll 1
-            for (int c0 = 32 * grp; c0 < walk.n; c0 += 64) {
-                float lo[16], hi[16];
-                const int left = walk.n - c0;   // rows of the result from c0 on
-                const int64_t row0 = (kG ? static_cast<int64_t>(walk.e) * a.N : 0) + walk.n0 + c0;
-                if (none) {
+                        // z of these rows and neurons into shared memory, the next rows' on their way to registers
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) lo[i] = hi[i] = 0.0f;
-                } else {
-                    tc::tmem_ld_frag(tb + c0, lo);
-                    tc::tmem_ld_frag(tb + (16u << 16) + c0, hi);
-                }
-                if (!none) tc::tmem_wait32(lo, hi);
-                if constexpr (kE == kEpiBf16) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        tc::stsm4_t(at256 + i * 2048, ff_pack(lo[4 * i], lo[4 * i + 1]), ff_pack(lo[4 * i + 2], lo[4 * i + 3]),
-                                    ff_pack(hi[4 * i], hi[4 * i + 1]), ff_pack(hi[4 * i + 2], hi[4 * i + 3]));
-                } else if constexpr (kE == kEpiF32) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {   // (column ^ 8 * row / 2: the lanes of a store meet all banks)
-                        const float v = j < 16 ? lo[j] : hi[j - 16];
-                        const int i = (j & 15) >> 2, r = 8 * i + ncol + (j & 1), c = q * 32 + (j >> 4) * 16 + ((j >> 1) & 1) * 8 + mrow;
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + r * 512 + ((c ^ (8 * (lane & 3))) << 2)), "f"(v) : "memory");
-                    }
-                } else if constexpr (kE == kEpiSwiglu || kE == kEpiSwigluZ) {
-                    if constexpr (kE == kEpiSwigluZ) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {   // gate, up
-                            const float v = j < 16 ? lo[j] : hi[j - 16];
-                            const int r = 8 * ((j & 15) >> 2) + ncol + (j & 1), c = q * 16 + ((j >> 1) & 1) * 8 + mrow;
-                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + 4096 + (j >> 4) * 8192 + r * 256 + ((c ^ (8 * (lane & 3))) << 2)), "f"(v)
+                        for (int j = 0; j < 4 * kHalves; ++j) {
+                            const int i = j * 128 + t128, half = i >> 9, r = (i >> 5) & 15, p = i & 31;
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sb + half * 8192 + r * 512 + ((p ^ (2 * ((r >> 1) & 3))) << 4)),
+                                         "r"(zr[j].x), "r"(zr[j].y), "r"(zr[j].z), "r"(zr[j].w)
                                          : "memory");
                         }
-                    }
+                        if (left > 32) read_z(c0 + 32);
+                        tc::named_sync(1 + grp, 128);
+                        if (!none) tc::tmem_ld_wait(v);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) lo[j] = lo[j] * ff_sigmoid(lo[j]).x * hi[j];
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t wa[4], wb[4];   // rows lane / 4, + 8, + 16, + 24 of the warp's neurons, a pair of rows of dz each
 #pragma unroll
-                    for (int i = 0; i < 4; i += 2)
-                        tc::stsm4_t(at128 + (i + (lane >> 4)) * 1024, ff_pack(lo[4 * i], lo[4 * i + 1]), ff_pack(lo[4 * i + 2], lo[4 * i + 3]),
-                                    ff_pack(lo[4 * i + 4], lo[4 * i + 5]), ff_pack(lo[4 * i + 6], lo[4 * i + 7]));
-                } else if constexpr (kE == kEpiRelu2) {
-                    if (a.z_out) {
+                            for (int m = 0; m < 4; ++m) {
+                                const float* d = v + 8 * (m >> 1) + 4 * i + 2 * (m & 1);   // dh of the pair
+                                float ga[2], gb[2];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float v = j < 16 ? lo[j] : hi[j - 16];
-                            const int r = 8 * ((j & 15) >> 2) + ncol + (j & 1), c = q * 32 + (j >> 4) * 16 + ((j >> 1) & 1) * 8 + mrow;
-                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + 8192 + r * 512 + ((c ^ (8 * (lane & 3))) << 2)), "f"(v) : "memory");
+                                for (int u = 0; u < 2; ++u) {
+                                    const int r = 8 * i + ncol + u, c = q * 32 + 8 * m + mrow;
+                                    const uint32_t at = sb + r * 512 + ((c ^ (8 * (lane & 3))) << 2);
+                                    const float z = lds_f32(at);
+                                    if constexpr (kE == kEpiSwigluGrad) {
+                                        const float2 s = ff_sigmoid(z);
+                                        const float silu = z * s.x;
+                                        ga[u] = d[u] * lds_f32(at + 8192) * (s.x + silu * s.y);
+                                        gb[u] = d[u] * silu;
+                                    } else {
+                                        ga[u] = d[u] * (2.0f * relu_nan(z));
+                                    }
+                                }
+                                wa[m] = ff_pack(ga[0], ga[1]);
+                                if constexpr (kE == kEpiSwigluGrad) wb[m] = ff_pack(gb[0], gb[1]);
+                            }
+                            tc::stsm4_t(at256 + 16384 + i * 2048, wa[0], wa[1], wa[2], wa[3]);
+                            if constexpr (kE == kEpiSwigluGrad) tc::stsm4_t(at256 + 20480 + i * 2048, wb[0], wb[1], wb[2], wb[3]);
                         }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        lo[j] = relu_nan(lo[j]) * relu_nan(lo[j]);
-                        hi[j] = relu_nan(hi[j]) * relu_nan(hi[j]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        tc::stsm4_t(at256 + i * 2048, ff_pack(lo[4 * i], lo[4 * i + 1]), ff_pack(lo[4 * i + 2], lo[4 * i + 3]),
-                                    ff_pack(hi[4 * i], hi[4 * i + 1]), ff_pack(hi[4 * i + 2], hi[4 * i + 3]));
-                }
-                tc::named_sync(1 + grp, 128);
-                if constexpr (kE == kEpiBf16) {
-                    copy(sb, 32, a.out, row0, left, a.M, am, a.M - am, 256, 2);
-                } else if constexpr (kE == kEpiF32) {
-                    copy(sb, 32, a.out, row0, left, a.M, am, a.M - am, 512, 4);
-                } else if constexpr (kE == kEpiSwiglu || kE == kEpiSwigluZ) {
-                    const int j0 = am >> 1;   // the CTA's first neuron
-                    copy(sb, 32, a.h_out, row0, left, a.f, j0, a.f - j0, 128, 2);
-                    if constexpr (kE == kEpiSwigluZ) {
-                        copy(sb + 4096, 32, a.z_out, row0, left, 2 * a.f, j0, a.f - j0, 256, 4);
-                        copy(sb + 12288, 32, a.z_out, row0, left, 2 * a.f, a.f + j0, a.f - j0, 256, 4);
+                        tc::named_sync(1 + grp, 128);   // (the next rows' z goes where z has been read, their dz behind a barrier)
+                        const int64_t row0 = walk.n0 + c0;
+                        copy(sb + 16384, 16, a.dz_out, row0, left, kHalves * a.f, am, a.f - am, 256, 2);
+                        if (kHalves == 2) copy(sb + 20480, 16, a.dz_out, row0, left, 2 * a.f, a.f + am, a.f - am, 256, 2);
                     }
                 } else {
-                    copy(sb, 32, a.h_out, row0, left, a.f, am, a.f - am, 256, 2);
-                    if (a.z_out) copy(sb + 8192, 32, a.z_out, row0, left, a.f, am, a.f - am, 512, 4);
+#pragma unroll 1
+                    for (int c0 = 32 * grp; c0 < walk.n; c0 += 64) {
+                        float lo[16], hi[16];
+                        const int left = walk.n - c0;   // rows of the result from c0 on
+                        const int64_t row0 = (kG ? static_cast<int64_t>(walk.e) * a.N : 0) + walk.n0 + c0;
+                        if (none) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) lo[i] = hi[i] = 0.0f;
+                        } else {
+                            tc::tmem_ld_frag(tb + c0, lo);
+                            tc::tmem_ld_frag(tb + (16u << 16) + c0, hi);
+                        }
+                        if (!none) tc::tmem_wait32(lo, hi);
+                        if constexpr (kE == kEpiBf16) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                tc::stsm4_t(at256 + i * 2048, ff_pack(lo[4 * i], lo[4 * i + 1]), ff_pack(lo[4 * i + 2], lo[4 * i + 3]),
+                                            ff_pack(hi[4 * i], hi[4 * i + 1]), ff_pack(hi[4 * i + 2], hi[4 * i + 3]));
+                        } else if constexpr (kE == kEpiF32) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {   // (column ^ 8 * row / 2: the lanes of a store meet all banks)
+                                const float v = j < 16 ? lo[j] : hi[j - 16];
+                                const int i = (j & 15) >> 2, r = 8 * i + ncol + (j & 1), c = q * 32 + (j >> 4) * 16 + ((j >> 1) & 1) * 8 + mrow;
+                                asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + r * 512 + ((c ^ (8 * (lane & 3))) << 2)), "f"(v) : "memory");
+                            }
+                        } else if constexpr (kE == kEpiSwiglu || kE == kEpiSwigluZ) {
+                            if constexpr (kE == kEpiSwigluZ) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) {   // gate, up
+                                    const float v = j < 16 ? lo[j] : hi[j - 16];
+                                    const int r = 8 * ((j & 15) >> 2) + ncol + (j & 1), c = q * 16 + ((j >> 1) & 1) * 8 + mrow;
+                                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + 4096 + (j >> 4) * 8192 + r * 256 + ((c ^ (8 * (lane & 3))) << 2)), "f"(v)
+                                                 : "memory");
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) lo[j] = lo[j] * ff_sigmoid(lo[j]).x * hi[j];
+#pragma unroll
+                            for (int i = 0; i < 4; i += 2)
+                                tc::stsm4_t(at128 + (i + (lane >> 4)) * 1024, ff_pack(lo[4 * i], lo[4 * i + 1]), ff_pack(lo[4 * i + 2], lo[4 * i + 3]),
+                                            ff_pack(lo[4 * i + 4], lo[4 * i + 5]), ff_pack(lo[4 * i + 6], lo[4 * i + 7]));
+                        } else if constexpr (kE == kEpiRelu2) {
+                            if (a.z_out) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) {
+                                    const float v = j < 16 ? lo[j] : hi[j - 16];
+                                    const int r = 8 * ((j & 15) >> 2) + ncol + (j & 1), c = q * 32 + (j >> 4) * 16 + ((j >> 1) & 1) * 8 + mrow;
+                                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + 8192 + r * 512 + ((c ^ (8 * (lane & 3))) << 2)), "f"(v) : "memory");
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                lo[j] = relu_nan(lo[j]) * relu_nan(lo[j]);
+                                hi[j] = relu_nan(hi[j]) * relu_nan(hi[j]);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                tc::stsm4_t(at256 + i * 2048, ff_pack(lo[4 * i], lo[4 * i + 1]), ff_pack(lo[4 * i + 2], lo[4 * i + 3]),
+                                            ff_pack(hi[4 * i], hi[4 * i + 1]), ff_pack(hi[4 * i + 2], hi[4 * i + 3]));
+                        }
+                        tc::named_sync(1 + grp, 128);
+                        if constexpr (kE == kEpiBf16) {
+                            copy(sb, 32, a.out, row0, left, a.M, am, a.M - am, 256, 2);
+                        } else if constexpr (kE == kEpiF32) {
+                            copy(sb, 32, a.out, row0, left, a.M, am, a.M - am, 512, 4);
+                        } else if constexpr (kE == kEpiSwiglu || kE == kEpiSwigluZ) {
+                            const int j0 = am >> 1;   // the CTA's first neuron
+                            copy(sb, 32, a.h_out, row0, left, a.f, j0, a.f - j0, 128, 2);
+                            if constexpr (kE == kEpiSwigluZ) {
+                                copy(sb + 4096, 32, a.z_out, row0, left, 2 * a.f, j0, a.f - j0, 256, 4);
+                                copy(sb + 12288, 32, a.z_out, row0, left, 2 * a.f, a.f + j0, a.f - j0, 256, 4);
+                            }
+                        } else {
+                            copy(sb, 32, a.h_out, row0, left, a.f, am, a.f - am, 256, 2);
+                            if (a.z_out) copy(sb + 8192, 32, a.z_out, row0, left, a.f, am, a.f - am, 512, 4);
+                        }
+                        tc::named_sync(1 + grp, 128);   // the staging is free again
+                    }
                 }
-                tc::named_sync(1 + grp, 128);   // the staging is free again
-            }
-            }
             };
             if constexpr (kGrad) {
                 if (grad) tile(std::integral_constant<int, GEPI>{}, std::true_type{});

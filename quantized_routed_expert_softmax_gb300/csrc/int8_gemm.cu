@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                 const int col = walk.mtile() * (kGated ? 128 : 256) + static_cast<int>(rank) * (kGated ? 64 : 128);   // of the result
                 int bi = 0;
                 while (bi < 2 && (16 << bi) < half) ++bi;   // the smallest box of rows; more than 64: and one of 32
-            const bool more = NT > 128 && half > 64;
+                const bool more = NT > 128 && half > 64;
                 for (int ks = 0; ks < ksteps; ++ks) {
                     if (use > 0 && !tc::mbar_wait_warp(&raw_empty[st], use - 1, &waits)) {
                         ok = false;
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                         tc::tma_3d(dst, &g.tw, 4 * col, 4 * ks, e, &raw_full[st]);
                         tc::tma_3d(dst + kI8RawA / 2, &g.tw, 4 * (col + (kGated ? width : 64)), 4 * ks, e, &raw_full[st]);
                         tc::tma_2d(dst + kI8RawA, &g.tx[bi], 4 * (n0 + before), 4 * ks, &raw_full[st]);
-                    if (more) tc::tma_2d(dst + kI8RawA + 8192, &g.tx[1], 4 * (n0 + before + 64), 4 * ks, &raw_full[st]);
+                        if (more) tc::tma_2d(dst + kI8RawA + 8192, &g.tx[1], 4 * (n0 + before + 64), 4 * ks, &raw_full[st]);
                     }
                     if (++st == raw_stages) st = 0, ++use;
                 }

@@ -152,7 +152,7 @@ __device__ __forceinline__ void build_row_tiles(RowTiles& t, const int32_t* offs
     }
     if (tid == THREADS - 1) {
         t.n_slots = slot;
-        t.n_tiles = run;   // (2^17 and a few an expert at most: 32 bits hold even the sum of overlapping ranges)
+        t.n_tiles = run;   // (2^25 rows in tiles of 32 at least: 2^20 an expert, 2^30 were the ranges of 1024 experts to overlap)
     }
     __syncthreads();
 }
