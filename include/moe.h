@@ -275,7 +275,7 @@ moe_status moe_quantize_int8(const void* x, moe_dtype xt, int64_t x_rows, const 
 
 /*
  * moe_dequantize_int8 -- the values q * s that the codes of n_mat int8 matrices stand for, [n_mat][rows][cols]
- * in fp32 or bf16 (ot), rounded once.  Errors: as moe_quantize_int8.
+ * in fp32 (ot; the product rounded) or bf16 (that fp32 value rounded).  Errors: as moe_quantize_int8.
  */
 moe_status moe_dequantize_int8(const void* src, int64_t n_mat, int64_t rows, int64_t cols, void* out, moe_dtype ot,
                                moe_stream_t stream);
@@ -296,7 +296,8 @@ moe_status moe_dequantize_int8(const void* src, int64_t n_mat, int64_t rows, int
  * workspace  device, moe_int8_matmul_workspace_bytes() bytes, zero-filled before its first use: an error word
  *          that moe_get_device_status() reads and clears (2: a wait ran past its limit, a second unless the
  *          int64 at byte 32 is not 0; out is not valid).  Calls that may overlap can share it.
- * The same inputs give the same bits.  P = 0 returns MOE_OK, launches nothing and touches no buffer.
+ * The same call gives the same bits; a row's last bits depend on P too, as up to 16 rows sum every column's codes in
+ * integers.  P = 0 returns MOE_OK, launches nothing and touches no buffer.
  * Errors: INVALID_ARG (NULL, bad enum, offsets NULL with E > 1), SHAPE (K a positive multiple of 32 up to
  * 65536; P up to 2^25; N from 1 to 131072, for SWIGLU a multiple of 64; E up to 1024), ALIGNMENT, WORKSPACE,
  * CUDA (more than 16 rows of more than 1024 columns: also where the library was compiled to fewer registers
@@ -315,7 +316,8 @@ moe_status moe_int8_matmul(const void* xq, int64_t P, const void* wq, int64_t E,
  * Backward, from dy:  dh = Wd^T dy;  dz = dh * dh/dz;  dx = Wgu^T dz;
  *   dWgu[e] = sum over the expert's rows of dz x^T;  dWd[e] = sum of dy h^T  (0 for an expert without rows).
  * Sums are fp32, z is kept in fp32; h, y, dz and dx are rounded to bf16 once each (h and dz as the products' operands).
- * No atomics: the same inputs give the same bits.
+ * No atomics: the same call gives the same bits (a row's last bits depend on P too: up to 16 rows stream the weights,
+ * which adds in another order).
  * x, y, dy, dx   device bf16 [P][d], rows sorted by expert.   w_gate_up  device bf16 [E][2f][d] (RELU2:
  *           [E][f][d]).   w_down  device bf16 [E][d][f].
  * z, h      device fp32 [P][2f] (RELU2: [P][f]) and bf16 [P][f]: kept by the forward pass for the backward one.

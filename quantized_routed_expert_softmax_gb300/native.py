@@ -431,7 +431,8 @@ def ffn_forward(x, w_gate_up, w_down, offsets=None, act: str = "swiglu", save: b
     """moe_ffn_forward: x bf16 [P, d] sorted by expert, w_gate_up bf16 [E, 2f, d] (act "relu2": [E, f, d]),
     w_down bf16 [E, d, f], offsets int32 [E + 1] (None with one expert) -> y bf16 [P, d]; with save
     (y, saved), saved = (z fp32, h bf16) for ffn_backward.  Rows that no expert owns are left as they are (in `out`;
-    a result that the call makes is not initialised there)."""
+    a result that the call makes is not initialised there).  Without a workspace the call makes one, which takes its
+    error word with it: pass one (ffn_workspace) to be able to ask device_status."""
     P, E, d, f, nz = _ffn_shape(x, w_gate_up, w_down, act)
     bf, dev, where = torch.bfloat16, x.get_device(), x.device
     xp = _operand("x", x, bf, dev)
@@ -455,7 +456,8 @@ def ffn_backward(grad, x, w_gate_up, w_down, saved, offsets=None, act: str = "sw
                  need=(True, True, True), workspace=None):
     """moe_ffn_backward: grad bf16 [P, d], the operands of ffn_forward and its saved (z, h) -> (dx bf16 [P, d],
     dw_gate_up, dw_down), the weights' gradients in dtype bfloat16 (the default) or float32.  need: which of the
-    three are computed (None in the place of the others)."""
+    three are computed (None in the place of the others).  Rows of dx that no expert owns are not initialised.  The
+    workspace: as in ffn_forward."""
     P, E, d, f, nz = _ffn_shape(x, w_gate_up, w_down, act)
     bf, dev, where = torch.bfloat16, x.get_device(), x.device
     z, h = saved
