@@ -29,7 +29,7 @@
 //
 // Many rows an expert are bound by the MMAs: 8191 rows of 2816 x 5632 forward 403 us, 1,930 TFLOP/s (a library product of
 // 8192^3 does 1,932), with z saved 435, backward 890, 1,750 TFLOP/s.  Few rows are bound by the weights' bytes: 4096 rows of 128
-// experts, 2816 and 704, forward 255 us, 6.1 TB/s; their gradients by writing as many bytes: 1.0 GB of dWgu in 198 us, 5.1 TB/s
+// experts, 2816 and 704, forward 251 us, 6.2 TB/s; their gradients by writing as many bytes: 1.0 GB of dWgu in 198 us, 5.1 TB/s
 // (a library's fill of a gigabyte writes 4.1).  32768 rows: forward 334 us, z saved 372, backward 780.
 // What it took, forward us of the dense block: barriers with release and acquire over the cluster 1288, without 406 (see
 // pair.cuh), blocks of weight tiles 398 (z saved 466 -> 431).  Backward: 2926, 932; z read a step ahead 890 (dz 223 -> 174);
