@@ -7,7 +7,8 @@
 // where the quotient lies close to the middle between two codes (i8_codes).
 //
 // Measured: quantising 45056 x 2816 fp32 96 us, 6.6 TB/s read and written; 32768 x 2816 bf16 45 us, 6.1 TB/s, gathered from
-// 4097 rows in L2 34 us, 32764 rows 44 and 38; one row 2.5 us.  Bound by HBM, the gathered rows by their stores.
+// 4097 rows in L2 34 us, 32764 rows 44 and 38; one row 2.5 us.  Bound by HBM; the gathered rows, at half its
+// rate, by a row's copy, search and coding one after the other or by their stores, which of these has not been measured.
 // What it took, us for 32764 gathered bf16 rows: rows in registers 82; read again from L1 58; held in shared memory 52; one
 // decision a row for values close to a middle, in place of one a value, 39 (a quarter of a warp's steps had such a value).  Not
 // gathered 82, 69 by then, and 44 by panels.
